@@ -23,7 +23,9 @@ __all__ = ["dr_chunk_fwd", "dr_decode_step", "dr_chunk_fwd_ex", "dr_chunk_fwd_no
            "chunk_fwd", "delta_rule", "decode_step", "chunk_bwd", "chunk_fwd_plan", "chunk_fwd_plan_ex", "snapshot_count",
            "check_offsets",
            "library_path",
-           "load_library", "VARIANTS", "DeltaRuleError"]
+           "load_library", "VARIANTS", "DeltaRuleError",
+           "dr_decay_fwd", "dr_decay_step", "decay_fwd", "decay_step",
+           "dr_state_pack", "dr_state_unpack", "state_pack", "state_unpack"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "lib", "libdeltarule.so")
@@ -136,6 +138,8 @@ def load_library(path: Optional[str] = None):
     lib.dr_chunk_fwd_plan.restype = ip
     lib.dr_chunk_fwd_plan_ex.argtypes = [ctypes.POINTER(_Dims), ip, ip, ctypes.POINTER(_Plan)]
     lib.dr_chunk_fwd_plan_ex.restype = ip
+    if hasattr(lib, "dr_decay_fwd"):  # (a host-only build of api.cpp has the entry points of deltarule.h alone)
+        _decay.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -554,3 +558,8 @@ def delta_rule(q, k, v, alpha, erase, write=None, variant: str = "kda", S0=None,
     ``checkpoint=False`` keeps no states from the forward (the backward then recomputes them,
     at about 5% of its time, with identical results)."""
     return _DeltaRule.apply(q, k, v, alpha, erase, write, S0, cu_seqlens, variant, checkpoint)
+
+
+from . import _decay  # noqa: E402  (its functions use the helpers above)
+from ._decay import (decay_fwd, decay_step, dr_decay_fwd, dr_decay_step, dr_state_pack, dr_state_unpack,  # noqa: E402,F401
+                     state_pack, state_unpack)

@@ -1,0 +1,236 @@
+"""Binding of the decayed linear attention and the 8-bit state cache (``include/deltarule_decay.h``).
+
+Argument marshalling only, as for the gated delta rule: shapes, dtypes and layouts are checked, raw pointers and
+the current stream go to the library, a non-zero status raises. The ``dr_*`` functions write into the
+caller's tensors; ``decay_fwd``, ``decay_step``, ``decay_bwd``, ``state_pack`` and ``state_unpack`` allocate;
+``decay_attention`` wires the prefill and its backward into torch autograd.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import (_DT, _Opts, _capturing, _check, _need, _need_rows, _opts, _ptr, _stream, check_offsets, load_library,
+               snapshot_count)
+
+# code types of the state cache (dr_cache_format)
+CACHE_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
+
+
+class _DecayDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("num_heads", ctypes.c_int64),
+                ("num_k_heads", ctypes.c_int64), ("head_dim_k", ctypes.c_int64), ("head_dim_v", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int64), ("in_dtype", ctypes.c_int32), ("decay_layout", ctypes.c_int32),
+                ("strided", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_token_stride", ctypes.c_int64), ("q_batch_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_batch_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_batch_stride", ctypes.c_int64)]
+
+
+class _CacheDims(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("num_states", ctypes.c_int64), ("num_slots", ctypes.c_int64),
+                ("num_heads", ctypes.c_int64), ("head_dim_k", ctypes.c_int64), ("head_dim_v", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def declare(lib):
+    """Signatures of this part of the library."""
+    vp, ip = ctypes.c_void_p, ctypes.c_int
+    dp, op, cp = ctypes.POINTER(_DecayDims), ctypes.POINTER(_Opts), ctypes.POINTER(_CacheDims)
+    lib.dr_decay_fwd.argtypes = [vp] * 8 + [dp, op, vp]
+    lib.dr_decay_step.argtypes = [vp] * 6 + [dp, op, vp]
+    lib.dr_state_pack.argtypes = [vp] * 5 + [cp, vp]
+    lib.dr_state_unpack.argtypes = [vp] * 5 + [cp, vp]
+    for f in (lib.dr_decay_fwd, lib.dr_decay_step, lib.dr_state_pack, lib.dr_state_unpack):
+        f.restype = ip
+
+
+def _inputs(q, k, v, alpha, lead):
+    """Checks q, k, v, alpha with ``lead`` leading dimensions (2: batch and token, 1: sequence) and returns the sizes
+    block without num_seqs."""
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} dimensions, got {q.dim()} and {v.dim()}")
+    dev, first = q.device, tuple(q.shape[:lead])
+    Hk, dk = q.shape[lead:]
+    H, dv = v.shape[lead:]
+    if q.dtype not in _DT:
+        raise ValueError(f"q dtype {q.dtype} is not float32 or bfloat16")
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError(f"{H} value heads are not a multiple of {Hk} query/key heads")
+    sq = _need_rows(q, "q", first + (Hk, dk), lead, q.dtype, dev)
+    sk = _need_rows(k, "k", first + (Hk, dk), lead, q.dtype, dev)
+    sv = _need_rows(v, "v", first + (H, dv), lead, q.dtype, dev)
+    per_head = alpha is not None and alpha.dim() == 1
+    _need(alpha, "alpha", (H,) if per_head else first + (H,), torch.float32, dev)
+    d = _DecayDims(first[0], first[1] if lead == 2 else 1, H, Hk, dk, dv, first[0], _DT[q.dtype], int(per_head), 0, 0)
+    if not all(x.is_contiguous() for x in (q, k, v)):
+        d.strided = 1
+        (d.q_token_stride, d.q_batch_stride), (d.k_token_stride, d.k_batch_stride), \
+            (d.v_token_stride, d.v_batch_stride) = [((s[1], s[0]) if lead == 2 else (0, s[0])) for s in (sq, sk, sv)]
+    return d
+
+
+def _offsets(cu_seqlens, d, dev):
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be a vector of num_seqs + 1 offsets")
+        _need(cu_seqlens, "cu_seqlens", (cu_seqlens.shape[0],), torch.int32, dev)
+        d.num_seqs = cu_seqlens.shape[0] - 1
+
+
+def dr_decay_fwd(q, k, v, alpha, S0, cu_seqlens, o, S_T, state_idx=None, snapshots=None,
+                 snapshot_every: int = 0) -> None:
+    """Prefill of the decayed linear attention into ``o`` [B,T,H,dv] and ``S_T`` [N,H,dk,dv] (fp32, either may be
+    None). q, k [B,T,Hk,dk] and v [B,T,H,dv] (fp32 or bf16, views with free batch and token strides), alpha fp32
+    [B,T,H] or [H]. ``S0``, ``cu_seqlens``, ``state_idx`` and ``snapshots`` as for ``dr_chunk_fwd_ex``; the offsets
+    are clamped on the device and not read on the host."""
+    lib = load_library()
+    d = _inputs(q, k, v, alpha, 2)
+    dev, B, T, H, dk, dv = q.device, d.batch, d.seqlen, d.num_heads, d.head_dim_k, d.head_dim_v
+    _offsets(cu_seqlens, d, dev)
+    rows = d.num_seqs
+    if state_idx is not None:
+        _need(state_idx, "state_idx", (d.num_seqs,), torch.int32, dev)
+        pools = [t for t in (S0, S_T) if t is not None]
+        rows = pools[0].shape[0] if pools else 0
+    for t, name in ((S0, "S0"), (S_T, "S_T")):
+        if t is not None:
+            _need(t, name, (rows, H, dk, dv), torch.float32, dev)
+    if snapshots is not None:
+        if not snapshot_every or snapshot_every <= 0:
+            raise ValueError("snapshots need a positive snapshot_every")
+        if cu_seqlens is None:
+            rows_s = B * (T // int(snapshot_every))
+        elif not _capturing():
+            rows_s = snapshot_count(check_offsets(cu_seqlens, T), snapshot_every)
+        else:
+            rows_s = snapshots.shape[0]
+        _need(snapshots, "snapshots", (rows_s, H, dk, dv), torch.float32, dev)
+    if o is not None:
+        _need(o, "o", (B, T, H, dv), torch.float32, dev)
+    opts = _opts(state_idx, rows, snapshots, snapshot_every)
+    with torch.cuda.device(dev):  # the library launches on the current device
+        st = lib.dr_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(cu_seqlens), _ptr(o), _ptr(S_T),
+                              ctypes.byref(d), ctypes.byref(opts), _stream(dev))
+    _check(lib, st, "dr_decay_fwd")
+
+
+def decay_fwd(q, k, v, alpha, S0=None, cu_seqlens=None, output_final_state: bool = True, state_idx=None,
+              snapshot_every: Optional[int] = None, output: bool = True):
+    """Allocates ``o`` (and ``S_T``) and runs ``dr_decay_fwd``. Returns (o, S_T or None), plus the snapshots when
+    ``snapshot_every`` is given. With ``state_idx``, S0 is a pool that is updated in place and returned as S_T.
+    Rows of ``o`` past the last packed sequence are not written."""
+    B, T, _, dk = q.shape
+    H, dv = v.shape[-2:]
+    N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    new = lambda *s: torch.empty(s, dtype=torch.float32, device=q.device)  # noqa: E731
+    if state_idx is not None and S0 is None:
+        raise ValueError("state_idx needs the pool of states as S0")
+    S_T = S0 if state_idx is not None else (new(N, H, dk, dv) if output_final_state else None)
+    snaps = None
+    if snapshot_every is not None:
+        if cu_seqlens is None:
+            lens = [T] * B
+        elif _capturing():
+            raise ValueError("snapshots of packed sequences need cu_seqlens on the host: not inside a graph capture")
+        else:
+            lens = check_offsets(cu_seqlens, T)
+        snaps = new(snapshot_count(lens, snapshot_every), H, dk, dv)
+    o = new(B, T, H, dv) if output else None
+    dr_decay_fwd(q, k, v, alpha, S0, cu_seqlens, o, S_T, state_idx, snaps, snapshot_every or 0)
+    return (o, S_T) if snapshot_every is None else (o, S_T, snaps)
+
+
+def dr_decay_step(q, k, v, alpha, S, o, state_idx=None) -> None:
+    """One token for each sequence, in place on ``S`` [N,H,dk,dv] fp32 (or, with ``state_idx`` [N] int32, on the rows
+    it names of a pool); writes ``o`` [N,H,dv] fp32. q, k [N,Hk,dk]; v [N,H,dv]; alpha fp32 [N,H] or [H]."""
+    lib = load_library()
+    d = _inputs(q, k, v, alpha, 1)
+    dev, N, H, dk, dv = q.device, d.batch, d.num_heads, d.head_dim_k, d.head_dim_v
+    rows = N
+    if state_idx is not None:
+        _need(state_idx, "state_idx", (N,), torch.int32, dev)
+        rows = S.shape[0]
+    _need(S, "S", (rows, H, dk, dv), torch.float32, dev)
+    _need(o, "o", (N, H, dv), torch.float32, dev)
+    opts = _opts(state_idx, rows)
+    with torch.cuda.device(dev):
+        st = lib.dr_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S), _ptr(o), ctypes.byref(d),
+                               ctypes.byref(opts), _stream(dev))
+    _check(lib, st, "dr_decay_step")
+
+
+def decay_step(q, k, v, alpha, S, state_idx=None):
+    """Allocates ``o`` and runs ``dr_decay_step`` (S, or its rows ``state_idx``, updated in place). Returns o."""
+    o = torch.empty(tuple(v.shape), dtype=torch.float32, device=q.device)
+    dr_decay_step(q, k, v, alpha, S, o, state_idx)
+    return o
+
+
+def _cache_dims(S, codes, scales, state_idx, slot_idx):
+    if S.dim() != 4 or codes.dim() != 4:
+        raise ValueError("S and codes must have 4 dimensions: rows, heads, d_k, d_v")
+    dev = S.device
+    rows, H, dk, dv = S.shape
+    slots = codes.shape[0]
+    fmt = [f for f, t in CACHE_FORMATS.values() if t == codes.dtype]
+    if not fmt:
+        raise ValueError(f"codes have dtype {codes.dtype}, expected int8 or float8_e4m3fn")
+    _need(S, "S", (rows, H, dk, dv), torch.float32, dev)
+    _need(codes, "codes", (slots, H, dk, dv), codes.dtype, dev)
+    _need(scales, "scales", (slots, H, dk), torch.float32, dev)
+    count = None
+    for t, name in ((state_idx, "state_idx"), (slot_idx, "slot_idx")):
+        if t is not None:
+            if t.dim() != 1:
+                raise ValueError(f"{name} must be a vector")
+            _need(t, name, (t.shape[0] if count is None else count,), torch.int32, dev)
+            count = t.shape[0]
+    if count is None and rows != slots:
+        raise ValueError(f"{rows} states and {slots} slots: give state_idx or slot_idx")
+    return _CacheDims(rows if count is None else count, rows, slots, H, dk, dv, fmt[0], 0)
+
+
+def dr_state_pack(S, codes, scales, slot_idx=None, state_idx=None) -> None:
+    """Writes states ``S`` [R,H,dk,dv] fp32 (rows ``state_idx``) in 8 bits to the rows ``slot_idx`` of the cache:
+    ``codes`` [P,H,dk,dv] int8 or float8_e4m3fn, ``scales`` [P,H,dk] fp32. A state row outside S is the zero state, a
+    slot outside the cache is skipped; other slots are left as they are."""
+    lib = load_library()
+    d = _cache_dims(S, codes, scales, state_idx, slot_idx)
+    dev = S.device
+    with torch.cuda.device(dev):
+        st = lib.dr_state_pack(_ptr(S), _ptr(state_idx), _ptr(codes), _ptr(scales), _ptr(slot_idx), ctypes.byref(d),
+                               _stream(dev))
+    _check(lib, st, "dr_state_pack")
+
+
+def dr_state_unpack(codes, scales, S, slot_idx=None, state_idx=None) -> None:
+    """Reads the rows ``slot_idx`` of the cache into the rows ``state_idx`` of ``S``: the inverse of
+    ``dr_state_pack``. A slot outside the cache gives the zero state, a state row outside S is skipped."""
+    lib = load_library()
+    d = _cache_dims(S, codes, scales, state_idx, slot_idx)
+    dev = S.device
+    with torch.cuda.device(dev):
+        st = lib.dr_state_unpack(_ptr(codes), _ptr(scales), _ptr(slot_idx), _ptr(S), _ptr(state_idx), ctypes.byref(d),
+                                 _stream(dev))
+    _check(lib, st, "dr_state_unpack")
+
+
+def state_pack(S, fmt: str = "int8"):
+    """``S`` [N,H,dk,dv] in 8 bits: (codes, scales), a cache of N slots."""
+    if fmt not in CACHE_FORMATS:
+        raise ValueError(f"unknown cache format {fmt!r}")
+    codes = torch.empty(tuple(S.shape), dtype=CACHE_FORMATS[fmt][1], device=S.device)
+    scales = torch.empty(tuple(S.shape[:-1]), dtype=torch.float32, device=S.device)
+    dr_state_pack(S, codes, scales)
+    return codes, scales
+
+
+def state_unpack(codes, scales, slot_idx=None):
+    """The states held by a cache (or by its rows ``slot_idx``), fp32."""
+    rows = codes.shape[0] if slot_idx is None else slot_idx.shape[0]
+    S = torch.empty((rows,) + tuple(codes.shape[1:]), dtype=torch.float32, device=codes.device)
+    dr_state_unpack(codes, scales, S, slot_idx=slot_idx)
+    return S

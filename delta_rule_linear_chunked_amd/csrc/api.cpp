@@ -11,6 +11,7 @@
 
 #include "../../include/deltarule.h"
 #include "common.hpp"
+#include "host.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -189,6 +190,28 @@ int check_offsets(const int32_t* cu, int64_t nseq, int64_t tokens, hipStream_t s
 }
 
 }  // namespace
+
+namespace dr {
+
+void host_clear_error() { g_last_error.clear(); }
+
+int host_fail(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return status;
+}
+
+hipError_t host_workspace(size_t bytes, hipStream_t stream, void** ptr) { return workspace_alloc(bytes, stream, ptr); }
+
+int host_check_offsets(const int32_t* cu, int64_t nseq, int64_t tokens, hipStream_t stream) {
+  return cu != nullptr && debug_validate() ? check_offsets(cu, nseq, tokens, stream) : DR_OK;
+}
+
+}  // namespace dr
 
 extern "C" {
 

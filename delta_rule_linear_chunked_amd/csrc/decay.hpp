@@ -1,0 +1,290 @@
+// Decayed linear attention (a scalar decay for each head): parameter block, launch plan and the
+// device building blocks that its forward and backward kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace dr {
+
+constexpr int DCH = 64;  // tokens per chunk
+
+// Sequences are cut into segments of `seg` tokens (a multiple of 64; one segment when that fills the
+// chip): a slot is one segment of one sequence. Fixed length: slot n * nseg + j. Packed: the plan pass
+// writes the table.
+struct DecayParams {
+  const void* q;         // [B, T, Hk, d_k]
+  const void* k;
+  const void* v;         // [B, T, H, d_v]
+  const float* alpha;    // [B, T, H], or [H] when !a_tok
+  const float* S0;       // initial states (may be null)
+  const int32_t* cu;     // packed offsets; past the plan pass its clamped copy
+  float* o;              // may be null
+  float* S;              // final states (may be null); step: states in and out
+  int64_t T;             // tokens per batch row
+  int64_t q_ts, q_bs, k_ts, k_bs, v_ts, v_bs;  // element strides (token, batch row)
+  int32_t H, Hk, DK, DV;
+  int32_t a_tok;
+  int32_t nseq;
+  int32_t seg;           // tokens per segment
+  int32_t nseg;          // fixed length: segments per sequence
+  int32_t slots;         // slots (packed: an upper bound)
+  int32_t grid;          // logical workgroups of the launch
+  int32_t ncb;           // value-column blocks of the launch
+  const int32_t* sidx;   // slot of each sequence in the state buffers (null: row n)
+  int64_t nslots;
+  float* snap;           // states after every snap_chunks chunks (may be null)
+  int32_t snap_chunks;
+  // packed: written by the plan pass
+  int32_t* cu_ok;        // [nseq + 1] offsets clamped to [0, T] and non-decreasing
+  int32_t* slot_seq;     // [slots] sequence of the slot (-1: unused)
+  int32_t* slot_first;   // [nseq + 1] first slot of each sequence
+  int32_t* snap_first;   // [nseq] first snapshot row of each sequence
+  // segments: each slot's own contribution to the state behind it, then the state at its start
+  float* part;           // [slots, H, d_k, d_v]
+  float* gpart;          // [slots, H] product of the slot's decays
+  // backward
+  const float* dO;       // [B, T, H, d_v]
+  const float* dST;      // may be null
+  float* cs;             // [chunk slots, H, d_k, d_v] state at each chunk's start
+  float* ds;             // [chunk slots, H, d_k, d_v] state gradient at each chunk's end
+  float* rpart;          // segments of the reverse pass, as part / gpart
+  int32_t* chunk_seq;    // packed: [cslots] sequence of the chunk slot (-1: unused)
+  int32_t* chunk_first;  // packed: [nseq + 1]
+  int32_t cslots;
+  float* dq;             // [B, T, Hk, d_k] or, with shared heads, per-head partial sums [B, T, H, d_k]
+  float* dk;
+  float* dv;
+  float* dalpha;         // [B, T, H]
+  float* dS0;
+};
+
+// What the host decides for a call.
+struct DecayPlan {
+  int ct;              // column tiles of 16 per workgroup of the main pass (1, 2 or 4)
+  int64_t seg;         // tokens per segment
+  int64_t nseg;        // fixed length: segments per sequence; packed: more than 1 if any may have more
+  int64_t slots;
+  int64_t workspace;   // bytes
+  int64_t off_part, off_gpart, off_tab;
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// The fp32 values x cut into three bf16 terms whose sum is x exactly (8 + 8 + 8 significand bits,
+// by truncation, so that nothing overflows): an MFMA over the three terms against a bf16 operand is
+// an fp32-grade product at three bf16 rates (the fp32 MFMA runs at a sixteenth of one).
+struct Tri {
+  bf16x8 t[3];
+};
+__device__ __forceinline__ Tri split3(const float (&x)[8]) {
+  uint32_t w[3][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = x[2 * j], b = x[2 * j + 1];
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+      w[t][j] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);  // the upper halves of both
+      if (t < 2) {
+        a -= __builtin_bit_cast(float, ua & 0xffff0000u);
+        b -= __builtin_bit_cast(float, ub & 0xffff0000u);
+      }
+    }
+  }
+  Tri r;
+#pragma unroll
+  for (int t = 0; t < 3; ++t) r.t[t] = __builtin_bit_cast(bf16x8, w[t]);
+  return r;
+}
+
+// Operand of one 32-deep slice: NP bf16 terms (1: bf16 data as they are, 3: fp32 data).
+template <int NP>
+struct Op {
+  bf16x8 t[NP];
+};
+// acc += A B over the term pairs that reach fp32's significand (p + q <= 2), smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]) {
+#pragma unroll
+  for (int sum = NA + NB - 2 < 2 ? NA + NB - 2 : 2; sum >= 0; --sum)
+#pragma unroll
+    for (int p = 0; p < NA; ++p)
+#pragma unroll
+      for (int q = 0; q < NB; ++q)
+        if (p + q == sum) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], b[q], acc, 0, 0, 0);
+}
+
+// LDS tile of 64 token rows x W bf16 channels (W 32, 64 or 128), 16-byte pieces permuted within a row
+// so that both kinds of read are free of bank conflicts: a fragment along the channels (16 rows, one
+// piece each) and a transposing read (4 consecutive rows, 4 pieces of 8 bytes each).
+template <int W>
+__device__ __forceinline__ int swz(int row, int piece) {
+  constexpr int CPR = W / 8;
+  if constexpr (CPR == 16) return row * 16 + (piece ^ (((row & 3) << 2) | ((row >> 2) & 3)));
+  if constexpr (CPR == 8) return row * 8 + (piece ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3)));
+  return row * 4 + (piece ^ ((row >> 2) & 3));
+}
+
+// Fragment with token rows on the lanes: row row0 + l % 16, channels 32 u + 8 (l / 16) .. + 7.
+template <int W>
+__device__ __forceinline__ bf16x8 frag_rows(const unsigned char* tile, int row0, int u, int lane) {
+  return *reinterpret_cast<const bf16x8*>(tile + 16 * swz<W>(row0 + (lane & 15), 4 * u + (lane >> 4)));
+}
+__device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
+  union {
+    s16x4 h[2];
+    bf16x8 v;
+  } x;
+  x.h[0] = a;
+  x.h[1] = b;
+  return x.v;
+}
+// Fragment with channels on the lanes and tokens along the product: tokens 32 u + 16 a + 4 (l / 16) + b
+// at item 4 a + b. ds_read_b64_tr_b16 transposes a 4 x 16 block per 16 lanes: lane p names 4 consecutive
+// elements of row p / 4, columns 4 (p % 4) ..; it receives column l of the four rows. Lane l's channel of
+// channel tile 2 w + e is 32 w + 8 ((l % 16) / 4) + 4 e + l % 4: the accumulators of a product with such
+// rows hold, in a lane, channels 32 w + 8 (l / 16) + 4 e + i, and the two tiles e = 0, 1 together are the
+// eight consecutive channels of a fragment along the channels.
+template <int W>
+__device__ __forceinline__ bf16x8 frag_chan(const unsigned char* tile, int w, int e, int u, int lane) {
+  const int g = lane >> 4, p = lane & 15;
+  const int r = 32 * u + 4 * g + (p >> 2), piece = 4 * w + (p & 3);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + 16 * swz<W>(r, piece) + 8 * e));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + 16 * swz<W>(r + 16, piece) + 8 * e));
+  return join(a, b);
+}
+// The same for a tile of CW columns in order, no swizzle: lane l's column is n0 + l % 16.
+template <int CW>
+__device__ __forceinline__ bf16x8 frag_cols(const unsigned char* tile, int n0, int u, int lane) {
+  const int g = lane >> 4, p = lane & 15;
+  const unsigned char* at = tile + ((32 * u + 4 * g + (p >> 2)) * CW + n0 + 4 * (p & 3)) * 2;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * CW * 2));
+  return join(a, b);
+}
+
+// ---------------------------------------------------------------------------
+// Products of a chunk's decays. ratio(r, s) = a_{s+1} ... a_r is formed as a product of products, never
+// as a quotient or from logarithms: zero and negative decays are exact and nothing overflows that the
+// recurrence itself would not. Per tile of 16 tokens: the inclusive products from the tile's start (pre),
+// the products behind a token up to the tile's end (suf), the tile's whole product, and the 16 x 16
+// products within the tile. Across tiles ratio(r, s) = pre_r * (tiles between) * suf_s.
+// ---------------------------------------------------------------------------
+constexpr int LDP = 20;  // row pitch of the 16 x 16 products (floats; 16-byte reads of a row's 4 columns)
+struct DecayTab {
+  float pre[DCH];
+  float suf[DCH];
+  float tile[4];
+  float in[4][16 * LDP];  // [r][s], s <= r (the rest is not written)
+};
+template <int D>
+__device__ __forceinline__ float row_shl(float x) {
+  return dpp_or<0x100 + D>(1.f, x);  // lane l takes lane l + D of its 16, 1 past the end
+}
+// Wave w fills tile w; a: the decay of token 16 w + l % 16 in every lane.
+__device__ __forceinline__ void decay_table(DecayTab& t, int w, float a, int lane) {
+  const int s = lane & 15, g = lane >> 4;
+  const float pre = row_prefix_prod(a), suf = row_suffix_prod_excl(a);
+  if (g == 0) {
+    t.pre[16 * w + s] = pre;
+    t.suf[16 * w + s] = suf;
+    if (s == 15) t.tile[w] = pre;
+  }
+  // lane group g: rows r = s + 4 g .. + 3 of column s, from the products over 4, 8 and 12 tokens
+  const float p1 = row_shl<1>(a);
+  const float p2 = p1 * row_shl<1>(p1);
+  const float p4 = p2 * row_shl<2>(p2);
+  const float p8 = p4 * row_shl<4>(p4);
+  const float p12 = p8 * row_shl<8>(p4);
+  const float x0 = p1, x1 = row_shl<4>(p1), x2 = row_shl<8>(p1), x3 = row_shl<12>(p1);
+  float v = g == 0 ? 1.f : g == 1 ? p4 : g == 2 ? p8 : p12;
+  float nx = g == 0 ? x0 : g == 1 ? x1 : g == 2 ? x2 : x3;  // a_{s + 4 g + 1}
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = s + 4 * g + i;
+    if (r < 16) t.in[w][r * LDP + s] = v;
+    v *= nx;
+    nx = row_shl<1>(nx);
+  }
+}
+
+// One slot's sequence and token span.
+struct Span {
+  int n;         // sequence (-1: unused slot)
+  int64_t b;     // batch row
+  int64_t row0;  // first token of the segment within the batch row
+  int len;       // tokens of the segment
+  int t0;        // first token of the segment within the sequence
+  int total;     // tokens of the sequence
+};
+__device__ __forceinline__ Span slot_span(const DecayParams& p, int slot) {
+  Span x;
+  if (p.cu) {
+    x.n = p.slot_seq[slot];
+    if (x.n < 0) return x;
+    const int j = slot - p.slot_first[x.n];
+    const int c0 = p.cu[x.n];
+    x.total = p.cu[x.n + 1] - c0;
+    x.t0 = j * p.seg;
+    x.b = 0;
+    x.row0 = (int64_t)c0 + x.t0;
+  } else {
+    x.n = slot / p.nseg;
+    x.t0 = (slot - x.n * p.nseg) * p.seg;
+    x.total = (int)p.T;
+    x.b = x.n;
+    x.row0 = x.t0;
+  }
+  x.len = x.total - x.t0 < p.seg ? x.total - x.t0 : p.seg;
+  return x;
+}
+
+// 8 channels of one token row: raw bits as loaded, zeroed when the row does not exist, then the bf16
+// terms in LDS (fp32 data: three tiles `plane` bytes apart).
+template <typename InT>
+struct Piece;
+template <>
+struct Piece<__bf16> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const __bf16* p, bool ok) {
+    v = *reinterpret_cast<const u32x4*>(p);
+    if (!ok) v = u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void store(unsigned char* at, int) const { *reinterpret_cast<u32x4*>(at) = v; }
+};
+template <>
+struct Piece<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p, bool ok) {
+    a = *reinterpret_cast<const f32x4*>(p);
+    b = *reinterpret_cast<const f32x4*>(p + 4);
+    if (!ok) zero();
+  }
+  __device__ __forceinline__ void zero() { a = b = f32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void store(unsigned char* at, int plane) const {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    const Tri t = split3(x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(at + i * plane) = t.t[i];
+  }
+};
+template <typename InT>
+struct Terms {
+  static constexpr int N = 3;
+};
+template <>
+struct Terms<__bf16> {
+  static constexpr int N = 1;
+};
+
+hipError_t launch_decay_plan(const DecayParams& p, hipStream_t s);
+hipError_t launch_decay_fwd(DecayParams p, const DecayPlan& pl, bool bf16, hipStream_t s);
+hipError_t launch_decay_step(const DecayParams& p, bool bf16, hipStream_t s);
+hipError_t launch_decay_bwd(DecayParams p, const DecayPlan& pl, bool bf16, hipStream_t s);
+
+}  // namespace dr

@@ -1,0 +1,322 @@
+// C ABI of the decayed linear attention and the 8-bit state cache: argument checks, launch planning
+// and dispatch. Every check runs on the host before any launch; no device memory is read here.
+#include <climits>
+#include <cstdint>
+#include <cstdlib>
+#include <initializer_list>
+#include <utility>
+
+#include "../../include/deltarule_decay.h"
+#include "decay.hpp"
+#include "host.hpp"
+#include "state_cache.hpp"
+
+using dr::host_fail;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool head_dim_ok(int64_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
+using Named = std::pair<const void*, const char*>;
+int check_ptrs(std::initializer_list<Named> required, std::initializer_list<Named> optional) {
+  for (const Named& x : required)
+    if (x.first == nullptr) return host_fail(DR_ERR_NULL, "`%s` is NULL", x.second);
+  for (const auto* list : {&required, &optional})
+    for (const Named& x : *list)
+      if (!aligned16(x.first)) return host_fail(DR_ERR_LAYOUT, "`%s` is not 16-byte aligned", x.second);
+  return DR_OK;
+}
+
+int check_dims(const dr_decay_dims* d, const int32_t* cu, bool decode) {
+  if (d == nullptr) return host_fail(DR_ERR_NULL, "dims is NULL");
+  if (d->in_dtype != DR_F32 && d->in_dtype != DR_BF16)
+    return host_fail(DR_ERR_DTYPE, "in_dtype %d is neither DR_F32 nor DR_BF16", d->in_dtype);
+  if (d->decay_layout != DR_DECAY_TOKEN && d->decay_layout != DR_DECAY_HEAD)
+    return host_fail(DR_ERR_SHAPE, "decay_layout %d is neither DR_DECAY_TOKEN nor DR_DECAY_HEAD", d->decay_layout);
+  if ((d->strided != 0 && d->strided != 1) || d->reserved != 0)
+    return host_fail(DR_ERR_SHAPE, "strided must be 0 or 1 and reserved 0");
+  if (d->batch < 0 || d->seqlen < 0 || d->num_heads < 1 || d->num_k_heads < 1 || d->num_seqs < 0)
+    return host_fail(DR_ERR_SHAPE, "bad sizes: batch=%lld seqlen=%lld heads=%lld key heads=%lld seqs=%lld",
+                     (long long)d->batch, (long long)d->seqlen, (long long)d->num_heads, (long long)d->num_k_heads,
+                     (long long)d->num_seqs);
+  if (d->num_heads % d->num_k_heads != 0)
+    return host_fail(DR_ERR_SHAPE, "num_heads (%lld) is not a multiple of num_k_heads (%lld)", (long long)d->num_heads,
+                     (long long)d->num_k_heads);
+  if (!head_dim_ok(d->head_dim_k) || !head_dim_ok(d->head_dim_v))
+    return host_fail(DR_ERR_UNSUPPORTED, "head sizes d_k=%lld d_v=%lld: each must be 16, 32, 64 or 128",
+                     (long long)d->head_dim_k, (long long)d->head_dim_v);
+  // (each factor is bounded first, so that the products below stay within 64 bits)
+  const int64_t lim = (int64_t)1 << 31;
+  if (d->num_heads >= lim || d->num_seqs >= lim || d->batch >= lim || d->seqlen >= lim ||
+      d->num_seqs * d->num_heads >= lim || d->batch * d->seqlen >= lim)
+    return host_fail(DR_ERR_SHAPE, "problem too large for 32-bit token or head counts");
+  if (d->strided) {
+    const int64_t st[6] = {d->q_token_stride, d->q_batch_stride, d->k_token_stride,
+                           d->k_batch_stride, d->v_token_stride, d->v_batch_stride};
+    static const char* names[6] = {"q token", "q batch", "k token", "k batch", "v token", "v batch"};
+    const int64_t esz = d->in_dtype == DR_BF16 ? 2 : 4;
+    for (int i = 0; i < 6; ++i) {
+      if (st[i] < 0) return host_fail(DR_ERR_SHAPE, "%s stride %lld is negative", names[i], (long long)st[i]);
+      if (st[i] > ((int64_t)1 << 40) || (st[i] * esz) % 16 != 0)
+        return host_fail(DR_ERR_LAYOUT, "%s stride %lld is not a multiple of 16 bytes (or is beyond 2^40)", names[i],
+                         (long long)st[i]);
+    }
+  }
+  if (decode) {
+    if (d->num_seqs != d->batch || d->seqlen != 1)
+      return host_fail(DR_ERR_SHAPE, "a step has num_seqs equal to batch and seqlen 1, got %lld, %lld and %lld",
+                       (long long)d->num_seqs, (long long)d->batch, (long long)d->seqlen);
+  } else if (cu != nullptr) {
+    if (d->batch != 1)
+      return host_fail(DR_ERR_SHAPE, "packed sequences (cu_seqlens) need batch == 1, got %lld", (long long)d->batch);
+  } else if (d->num_seqs != d->batch) {
+    return host_fail(DR_ERR_SHAPE, "num_seqs (%lld) must equal batch (%lld) without cu_seqlens", (long long)d->num_seqs,
+                     (long long)d->batch);
+  }
+  return DR_OK;
+}
+
+int check_opts(const dr_opts* o, bool prefill) {
+  if (o == nullptr) return DR_OK;
+  if (o->l2norm_qk != 0 || o->alpha_dtype != DR_F32 || o->alpha_act != DR_ACT_NONE || o->gate_act != DR_ACT_NONE)
+    return host_fail(DR_ERR_UNSUPPORTED, "the decayed linear attention takes its inputs as they are: no input preparation");
+  if (o->state_idx) {
+    if (!aligned16(o->state_idx)) return host_fail(DR_ERR_LAYOUT, "state_idx must be 16-byte aligned");
+    if (o->num_slots < 0) return host_fail(DR_ERR_SHAPE, "num_slots (%lld) is negative", (long long)o->num_slots);
+    if (o->num_slots > INT32_MAX) return host_fail(DR_ERR_UNSUPPORTED, "num_slots above 2^31 - 1");
+  }
+  if (o->snapshots) {
+    if (!prefill) return host_fail(DR_ERR_SHAPE, "snapshots are a prefill option");
+    if (!aligned16(o->snapshots)) return host_fail(DR_ERR_LAYOUT, "snapshots must be 16-byte aligned");
+    if (o->snapshot_every <= 0 || o->snapshot_every % 64 != 0)
+      return host_fail(DR_ERR_SHAPE, "snapshot_every (%lld) must be a positive multiple of 64", (long long)o->snapshot_every);
+    if (o->snapshot_every > INT32_MAX) return host_fail(DR_ERR_UNSUPPORTED, "snapshot_every too large");
+  }
+  return DR_OK;
+}
+
+void set_dims(dr::DecayParams& p, const dr_decay_dims* d) {
+  p.T = d->seqlen;
+  p.H = (int32_t)d->num_heads;
+  p.Hk = (int32_t)d->num_k_heads;
+  p.DK = (int32_t)d->head_dim_k;
+  p.DV = (int32_t)d->head_dim_v;
+  p.a_tok = d->decay_layout == DR_DECAY_TOKEN;
+  p.nseq = (int32_t)d->num_seqs;
+  if (d->strided) {
+    p.q_ts = d->q_token_stride; p.q_bs = d->q_batch_stride;
+    p.k_ts = d->k_token_stride; p.k_bs = d->k_batch_stride;
+    p.v_ts = d->v_token_stride; p.v_bs = d->v_batch_stride;
+  } else {
+    p.q_ts = p.k_ts = d->num_k_heads * d->head_dim_k;
+    p.v_ts = d->num_heads * d->head_dim_v;
+    p.q_bs = p.k_bs = d->seqlen * p.q_ts;
+    p.v_bs = d->seqlen * p.v_ts;
+  }
+}
+
+// An integer from the environment, for tuning and tests (0: not set).
+int64_t env_int(const char* name) {
+  const char* e = getenv(name);
+  return e ? atoll(e) : 0;
+}
+
+// Segments and column blocks (the same for the forward and for the backward's state passes).
+dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
+  dr::DecayPlan pl{};
+  const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads;
+  pl.ct = tiles >= 2 ? 2 : 1;
+  if (const int64_t c = env_int("DR_DECAY_CT"))
+    if ((c == 1 || c == 2 || c == 4) && c <= tiles) pl.ct = (int)c;
+  const int64_t wide = tiles / pl.ct;  // workgroups per segment and head
+  // enough segments for 512 workgroups, none shorter than 512 tokens
+  int64_t seg;
+  if (packed) {
+    seg = d->seqlen * d->num_heads * wide / 512;
+  } else {
+    const int64_t have = pairs * wide;
+    const int64_t want = have >= 256 || have == 0 ? 1 : (512 + have - 1) / have;
+    seg = (d->seqlen + want - 1) / want;
+  }
+  if (seg < 512) seg = 512;
+  if (const int64_t s = env_int("DR_DECAY_SEG"))
+    if (s > 0) seg = s;
+  seg = (seg + 63) / 64 * 64;
+  pl.nseg = (d->seqlen + seg - 1) / seg;
+  if (pl.nseg < 1) pl.nseg = 1;
+  pl.seg = seg;
+  pl.slots = packed ? d->seqlen / seg + d->num_seqs : d->num_seqs * pl.nseg;
+  return pl;
+}
+
+// Lays out a workspace: offsets of 256-byte aligned pieces.
+struct Layout {
+  int64_t size = 0;
+  int64_t take(int64_t bytes) {
+    const int64_t at = size;
+    size += round256(bytes);
+    return at;
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
+                 const int32_t* cu_seqlens, float* o, float* S_T, const dr_decay_dims* dims, const dr_opts* opts,
+                 hipStream_t stream) {
+  dr::host_clear_error();
+  int st = check_dims(dims, cu_seqlens, false);
+  if (st) return st;
+  if (dims->batch * dims->seqlen > 0) {
+    st = check_ptrs({{q, "q"}, {k, "k"}, {v, "v"}, {alpha, "alpha"}}, {{o, "o"}});
+    if (st) return st;
+  }
+  st = check_ptrs({}, {{S0, "S0"}, {S_T, "S_T"}, {cu_seqlens, "cu_seqlens"}});
+  if (st) return st;
+  st = check_opts(opts, true);
+  if (st) return st;
+  st = dr::host_check_offsets(cu_seqlens, dims->num_seqs, dims->seqlen, stream);
+  if (st) return st;
+  if (dims->num_seqs == 0) return DR_OK;
+  const bool packed = cu_seqlens != nullptr;
+  const dr::DecayPlan pl = plan_decay(dims, packed, false);
+  dr::DecayParams p{};
+  set_dims(p, dims);
+  p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.cu = cu_seqlens; p.o = o; p.S = S_T;
+  if (opts) {
+    p.sidx = opts->state_idx;
+    p.nslots = opts->num_slots;
+    p.snap = opts->snapshots;
+    p.snap_chunks = opts->snapshots ? (int32_t)(opts->snapshot_every / 64) : 0;
+  }
+  if (pl.slots * dims->num_heads * (dims->head_dim_v / 16) > INT32_MAX - 8 || pl.seg > INT32_MAX)
+    return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
+  p.seg = (int32_t)pl.seg;
+  p.nseg = (int32_t)pl.nseg;
+  p.slots = (int32_t)pl.slots;
+  const int64_t nh = pl.slots * dims->num_heads;
+  Layout lay;
+  const bool segs = pl.nseg > 1;
+  const int64_t off_part = segs ? lay.take(nh * dims->head_dim_k * dims->head_dim_v * 4) : 0;
+  const int64_t off_g = segs ? lay.take(nh * 4) : 0;
+  const int64_t off_tab = packed ? lay.take((pl.slots + 3 * dims->num_seqs + 2) * 4) : 0;
+  unsigned char* ws = nullptr;
+  hipError_t e = hipSuccess;
+  if (lay.size > 0) {
+    void* mem = nullptr;
+    e = dr::host_workspace((size_t)lay.size, stream, &mem);
+    if (e != hipSuccess)
+      return host_fail(DR_ERR_HIP, "decay prefill workspace (%lld bytes) allocation failed: %s", (long long)lay.size,
+                       hipGetErrorString(e));
+    ws = static_cast<unsigned char*>(mem);
+  }
+  if (segs) {
+    p.part = reinterpret_cast<float*>(ws + off_part);
+    p.gpart = reinterpret_cast<float*>(ws + off_g);
+  }
+  if (packed) {
+    p.slot_seq = reinterpret_cast<int32_t*>(ws + off_tab);
+    p.slot_first = p.slot_seq + pl.slots;
+    p.cu_ok = p.slot_first + dims->num_seqs + 1;
+    p.snap_first = p.cu_ok + dims->num_seqs + 1;
+  }
+  e = dr::launch_decay_fwd(p, pl, dims->in_dtype == DR_BF16, stream);
+  const hipError_t ef = ws ? hipFreeAsync(ws, stream) : hipSuccess;
+  if (e != hipSuccess) return host_fail(DR_ERR_HIP, "decay prefill launch failed: %s", hipGetErrorString(e));
+  if (ef != hipSuccess) return host_fail(DR_ERR_HIP, "decay prefill workspace release failed: %s", hipGetErrorString(ef));
+  return DR_OK;
+}
+
+int dr_decay_step(const void* q, const void* k, const void* v, const float* alpha, float* S, float* o,
+                  const dr_decay_dims* dims, const dr_opts* opts, hipStream_t stream) {
+  dr::host_clear_error();
+  int st = check_dims(dims, nullptr, true);
+  if (st) return st;
+  st = check_opts(opts, false);
+  if (st) return st;
+  if (dims->num_seqs == 0) return DR_OK;
+  st = check_ptrs({{q, "q"}, {k, "k"}, {v, "v"}, {alpha, "alpha"}, {S, "S"}, {o, "o"}}, {});
+  if (st) return st;
+  dr::DecayParams p{};
+  set_dims(p, dims);
+  p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S = S; p.o = o;
+  if (opts) {
+    p.sidx = opts->state_idx;
+    p.nslots = opts->num_slots;
+  }
+  if (dims->num_seqs * dims->num_heads * (dims->head_dim_v / 16) > INT32_MAX)
+    return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
+  const hipError_t e = dr::launch_decay_step(p, dims->in_dtype == DR_BF16, stream);
+  if (e != hipSuccess) return host_fail(DR_ERR_HIP, "decay step launch failed: %s", hipGetErrorString(e));
+  return DR_OK;
+}
+
+static int cache_checks(const void* S, const int32_t* state_idx, const void* codes, const float* scales,
+                        const int32_t* slot_idx, const dr_cache_dims* d) {
+  if (d == nullptr) return host_fail(DR_ERR_NULL, "dims is NULL");
+  if (d->format != DR_CACHE_INT8 && d->format != DR_CACHE_E4M3)
+    return host_fail(DR_ERR_DTYPE, "format %d is neither DR_CACHE_INT8 nor DR_CACHE_E4M3", d->format);
+  if (d->reserved != 0) return host_fail(DR_ERR_SHAPE, "reserved must be 0");
+  if (d->count < 0 || d->num_states < 0 || d->num_slots < 0 || d->num_heads < 1)
+    return host_fail(DR_ERR_SHAPE, "bad sizes: count=%lld states=%lld slots=%lld heads=%lld", (long long)d->count,
+                     (long long)d->num_states, (long long)d->num_slots, (long long)d->num_heads);
+  if (!head_dim_ok(d->head_dim_k) || !head_dim_ok(d->head_dim_v))
+    return host_fail(DR_ERR_UNSUPPORTED, "head sizes d_k=%lld d_v=%lld: each must be 16, 32, 64 or 128",
+                     (long long)d->head_dim_k, (long long)d->head_dim_v);
+  if (d->num_states > INT32_MAX || d->num_slots > INT32_MAX || d->num_heads > INT32_MAX || d->count > INT32_MAX ||
+      d->count * d->num_heads > INT32_MAX / 4)
+    return host_fail(DR_ERR_UNSUPPORTED, "too many states for one call");
+  if (state_idx == nullptr && d->num_states < d->count)
+    return host_fail(DR_ERR_SHAPE, "%lld states for a count of %lld", (long long)d->num_states, (long long)d->count);
+  if (slot_idx == nullptr && d->num_slots < d->count)
+    return host_fail(DR_ERR_SHAPE, "%lld slots for a count of %lld", (long long)d->num_slots, (long long)d->count);
+  int st = DR_OK;
+  if (d->count > 0) st = check_ptrs({{S, "S"}, {codes, "codes"}, {scales, "scales"}}, {});
+  if (st) return st;
+  return check_ptrs({}, {{state_idx, "state_idx"}, {slot_idx, "slot_idx"}});
+}
+
+static dr::CacheParams cache_params(const float* S, const int32_t* state_idx, const uint8_t* codes, const float* scales,
+                                    const int32_t* slot_idx, const dr_cache_dims* d) {
+  dr::CacheParams p{};
+  p.S = const_cast<float*>(S);
+  p.codes = const_cast<uint8_t*>(codes);
+  p.scales = const_cast<float*>(scales);
+  p.state_idx = state_idx;
+  p.slot_idx = slot_idx;
+  p.count = d->count;
+  p.nstates = d->num_states;
+  p.nslots = d->num_slots;
+  p.H = (int32_t)d->num_heads;
+  p.DK = (int32_t)d->head_dim_k;
+  p.DV = (int32_t)d->head_dim_v;
+  return p;
+}
+
+int dr_state_pack(const float* S, const int32_t* state_idx, uint8_t* codes, float* scales, const int32_t* slot_idx,
+                  const dr_cache_dims* dims, hipStream_t stream) {
+  dr::host_clear_error();
+  const int st = cache_checks(S, state_idx, codes, scales, slot_idx, dims);
+  if (st || dims->count == 0) return st;
+  const hipError_t e = dr::launch_state_pack(cache_params(S, state_idx, codes, scales, slot_idx, dims),
+                                             dims->format == DR_CACHE_E4M3, stream);
+  if (e != hipSuccess) return host_fail(DR_ERR_HIP, "state pack launch failed: %s", hipGetErrorString(e));
+  return DR_OK;
+}
+
+int dr_state_unpack(const uint8_t* codes, const float* scales, const int32_t* slot_idx, float* S,
+                    const int32_t* state_idx, const dr_cache_dims* dims, hipStream_t stream) {
+  dr::host_clear_error();
+  const int st = cache_checks(S, state_idx, codes, scales, slot_idx, dims);
+  if (st || dims->count == 0) return st;
+  const hipError_t e = dr::launch_state_unpack(cache_params(S, state_idx, codes, scales, slot_idx, dims),
+                                               dims->format == DR_CACHE_E4M3, stream);
+  if (e != hipSuccess) return host_fail(DR_ERR_HIP, "state unpack launch failed: %s", hipGetErrorString(e));
+  return DR_OK;
+}
+
+}  // extern "C"
