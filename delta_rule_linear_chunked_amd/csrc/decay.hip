@@ -104,7 +104,7 @@ struct MainShape {
 };
 
 // One chunk of a wave: row tiles R..., column tile at column n0 of the block.
-template <int W, int CT, typename InT, int... R>
+template <int W, int CT, typename InT, bool OUT, int... R>
 __device__ __forceinline__ void main_chunk(const unsigned char* buf, const DecayTab& tb, f32x4 (&st)[W / 16], int n0,
                                            float* o, int64_t o_ts, int rows, int lane) {
   using Sh = MainShape<W, CT, InT>;
@@ -129,7 +129,7 @@ __device__ __forceinline__ void main_chunk(const unsigned char* buf, const Decay
 #pragma unroll
     for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_cols<16 * CT>(Vt + i * Sh::VB, n0, u, lane);
 
-  if (o) {
+  if constexpr (OUT) {
     Op<NP> qf[NR][U];
 #pragma unroll
     for (int n = 0; n < NR; ++n)
@@ -161,16 +161,15 @@ __device__ __forceinline__ void main_chunk(const unsigned char* buf, const Decay
     }
     // ((Q K^T) . ratio) V over the 32-token halves that reach the row tiles
 #pragma unroll
-    for (int u = 0; u <= RMAX / 2; ++u) {
+    for (int u = 0; u < RMAX / 2 + 1; ++u) {
       f32x4 sc[NR][2];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         const int S = 2 * u + a;
-        if (S > RMAX) continue;
 #pragma unroll
         for (int n = 0; n < NR; ++n) sc[n][a] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < U; ++w) {
+        for (int w = 0; w < (S <= RMAX ? U : 0); ++w) {
           Op<NP> kf;
 #pragma unroll
           for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(Kt + i * Sh::QK, 16 * S, w, lane);
@@ -181,7 +180,6 @@ __device__ __forceinline__ void main_chunk(const unsigned char* buf, const Decay
       }
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        if (RL[n] < 2 * u) continue;
         float x[8];
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
@@ -201,8 +199,10 @@ __device__ __forceinline__ void main_chunk(const unsigned char* buf, const Decay
             for (int i = 0; i < 4; ++i) x[4 * a + i] = 0.f;
           }
         }
-        const Tri pf = split3(x);
-        mma(oa[n], vf[u].t, pf.t);
+        if (RL[n] >= 2 * u) {
+          const Tri pf = split3(x);
+          mma(oa[n], vf[u].t, pf.t);
+        }
       }
     }
 #pragma unroll
@@ -247,7 +247,45 @@ __device__ __forceinline__ void main_chunk(const unsigned char* buf, const Decay
   }
 }
 
-// 64 x W tile of an input: each thread's pieces of a chunk, loaded and then put into LDS.
+// Column `col` of a d_k x d_v state in a lane's accumulators of NT channel tiles, the first of them t0 (see
+// frag_chan). Only d_k = 16 has fewer channels than its accumulators (W = 32).
+template <int W>
+__device__ __forceinline__ int chan_of(int t, int i, int lane) {
+  return 32 * (t >> 1) + 8 * (lane >> 4) + 4 * (t & 1) + i;
+}
+template <int W, int NT>
+__device__ __forceinline__ void state_load(f32x4 (&st)[NT], const float* src, int t0, int DK, int DV, int col, int lane) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
+  if (src == nullptr) return;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ch = chan_of<W>(t0 + t, i, lane);
+      st[t][i] = src[(W == 32 && ch >= DK ? 0 : ch) * DV + col];
+    }
+  if (W == 32) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (chan_of<W>(t0 + t, i, lane) >= DK) st[t][i] = 0.f;
+  }
+}
+template <int W, int NT>
+__device__ __forceinline__ void state_store(const f32x4 (&st)[NT], float* dst, int t0, int DK, int DV, int col, int lane) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ch = chan_of<W>(t0 + t, i, lane);
+      if (W > 32 || ch < DK) dst[ch * DV + col] = st[t][i];
+    }
+}
+
+// 64 x W tile of an input: each thread's pieces of a chunk, loaded (rows past the end from the last one) and
+// then put into LDS (those rows, and channels past d_k, as zeros).
 template <int W, typename InT>
 struct Stage {
   static constexpr int CPR = W / 8, NPC = DCH * CPR / 256;
@@ -255,13 +293,18 @@ struct Stage {
   __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int d, int tid) {
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
-      const int idx = tid + 256 * i, row = idx / CPR, pc = idx % CPR;
-      const int t = c0 + row;
-      const bool ok = t < len && pc * 8 < d;
-      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (pc * 8 < d ? pc * 8 : 0), ok);
+      const int idx = tid + 256 * i, pc = idx % CPR, t = c0 + idx / CPR;
+      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (pc * 8 < d ? pc * 8 : 0));
     }
   }
-  __device__ __forceinline__ void store(unsigned char* tile, int plane, int tid) const {
+  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int d, int tid) {
+    if (c0 + DCH > len || d < W) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) {
+        const int idx = tid + 256 * i;
+        if (c0 + idx / CPR >= len || (idx % CPR) * 8 >= d) x[i].zero();
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
       const int idx = tid + 256 * i;
@@ -277,12 +320,19 @@ struct StageCols {
   __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int tid) {
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
-      const int idx = (tid + 256 * i) % (DCH * CPR), row = idx / CPR, pc = idx % CPR;
-      const int t = c0 + row;
-      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + pc * 8, t < len);
+      const int idx = (tid + 256 * i) % (DCH * CPR), t = c0 + idx / CPR;
+      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (idx % CPR) * 8);
     }
   }
-  __device__ __forceinline__ void store(unsigned char* tile, int plane, int tid) const {
+  __device__ __forceinline__ void mask(int c0, int len, int tid) {
+    if (c0 + DCH > len) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i)
+        if (c0 + ((tid + 256 * i) % (DCH * CPR)) / CPR >= len) x[i].zero();
+    }
+  }
+  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int tid) {
+    mask(c0, len, tid);
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
       const int idx = tid + 256 * i;
@@ -291,7 +341,7 @@ struct StageCols {
   }
 };
 
-template <int W, int CT, typename InT>
+template <int W, int CT, typename InT, bool OUT>
 __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   using Sh = MainShape<W, CT, InT>;
   constexpr int NB = Sh::NB;
@@ -314,7 +364,7 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   const float* al = p.alpha + (p.a_tok ? trow * p.H : 0) + h;
   const int64_t a_ts = p.a_tok ? p.H : 0;
   const int64_t o_ts = (int64_t)p.H * p.DV;
-  float* o = p.o ? p.o + trow * o_ts + (int64_t)h * p.DV + cb * 16 * CT : nullptr;
+  float* o = OUT ? p.o + trow * o_ts + (int64_t)h * p.DV + cb * 16 * CT : nullptr;
 
   // the state at the segment's start: lane's column l % 16, rows 32 u + 8 (l / 16) + 4 e + i
   const int col = cb * 16 * CT + 16 * ct + (lane & 15);
@@ -327,13 +377,7 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   const float* src = p.part ? p.part + ((int64_t)slot * p.H + h) * hsz
                             : (p.S0 && srow >= 0 ? p.S0 + (srow * p.H + h) * hsz : nullptr);
   f32x4 st[W / 16];
-#pragma unroll
-  for (int t = 0; t < W / 16; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ch = 32 * (t >> 1) + 8 * (lane >> 4) + 4 * (t & 1) + i;
-      st[t][i] = src && ch < p.DK ? src[(int64_t)ch * p.DV + col] : 0.f;
-    }
+  state_load<W>(st, src, 0, p.DK, p.DV, col, lane);
 
   Stage<W, InT> sq, sk;
   StageCols<16 * CT, InT> sv;
@@ -341,19 +385,19 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   const int nc = (sp.len + DCH - 1) / DCH;
   auto fetch = [&](int c) {
     const int c0 = c * DCH;
-    if (o) sq.load(q, p.q_ts, c0, sp.len, p.DK, tid);
+    if constexpr (OUT) sq.load(q, p.q_ts, c0, sp.len, p.DK, tid);
     sk.load(k, p.k_ts, c0, sp.len, p.DK, tid);
     sv.load(v, p.v_ts, c0, sp.len, tid);
     const int t = c0 + 16 * wave + (lane & 15);
     a_next = al[(int64_t)(t < sp.len ? t : sp.len - 1) * a_ts];
-    if (t >= sp.len) a_next = 1.f;
   };
   auto put = [&](int c) {
+    const int c0 = c * DCH;
     unsigned char* buf = smem + (c % NB) * Sh::BUF;
-    if (o) sq.store(buf, Sh::QK, tid);
-    sk.store(buf + Sh::NP * Sh::QK, Sh::QK, tid);
-    sv.store(buf + 2 * Sh::NP * Sh::QK, Sh::VB, tid);
-    decay_table(tabs[c % NB], wave, a_next, lane);
+    if constexpr (OUT) sq.store(buf, Sh::QK, c0, sp.len, p.DK, tid);
+    sk.store(buf + Sh::NP * Sh::QK, Sh::QK, c0, sp.len, p.DK, tid);
+    sv.store(buf + 2 * Sh::NP * Sh::QK, Sh::VB, c0, sp.len, tid);
+    decay_table(tabs[c % NB], wave, c0 + 16 * wave + (lane & 15) < sp.len ? a_next : 1.f, lane);
   };
   if (nc > 0) {
     fetch(0);
@@ -365,50 +409,35 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
     __syncthreads();
     const unsigned char* buf = smem + (c % NB) * Sh::BUF;
     const DecayTab& tb = tabs[c % NB];
-    float* oc = o ? o + (int64_t)c * DCH * o_ts : nullptr;
+    float* oc = OUT ? o + (int64_t)c * DCH * o_ts : nullptr;
     const int rows = sp.len - c * DCH;
     if constexpr (CT == 4) {
-      main_chunk<W, CT, InT, 0, 1, 2, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+      main_chunk<W, CT, InT, OUT, 0, 1, 2, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
     } else if constexpr (CT == 2) {
       if (m == 0)
-        main_chunk<W, CT, InT, 0, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+        main_chunk<W, CT, InT, OUT, 0, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
       else
-        main_chunk<W, CT, InT, 1, 2>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+        main_chunk<W, CT, InT, OUT, 1, 2>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
     } else {
       if (m == 0)
-        main_chunk<W, CT, InT, 0>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+        main_chunk<W, CT, InT, OUT, 0>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
       else if (m == 1)
-        main_chunk<W, CT, InT, 1>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+        main_chunk<W, CT, InT, OUT, 1>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
       else if (m == 2)
-        main_chunk<W, CT, InT, 2>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+        main_chunk<W, CT, InT, OUT, 2>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
       else
-        main_chunk<W, CT, InT, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+        main_chunk<W, CT, InT, OUT, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
     }
     if (p.snap && m == 0 && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
       const int64_t per = p.T / DCH / p.snap_chunks;  // fixed length: snapshots per sequence
       const int64_t row = (p.cu ? p.snap_first[sp.n] : sp.n * per) + (first_chunk + c + 1) / p.snap_chunks - 1;
-      float* dst = p.snap + (row * p.H + h) * hsz;
-#pragma unroll
-      for (int t = 0; t < W / 16; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ch = 32 * (t >> 1) + 8 * (lane >> 4) + 4 * (t & 1) + i;
-          if (ch < p.DK) dst[(int64_t)ch * p.DV + col] = st[t][i];
-        }
+      state_store<W>(st, p.snap + (row * p.H + h) * hsz, 0, p.DK, p.DV, col, lane);
     }
     if constexpr (NB == 1) __syncthreads();
     if (c + 1 < nc) put(c + 1);
   }
-  if (p.S && m == 0 && srow >= 0 && sp.t0 + sp.len >= sp.total) {
-    float* dst = p.S + (srow * p.H + h) * hsz;
-#pragma unroll
-    for (int t = 0; t < W / 16; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ch = 32 * (t >> 1) + 8 * (lane >> 4) + 4 * (t & 1) + i;
-        if (ch < p.DK) dst[(int64_t)ch * p.DV + col] = st[t][i];
-      }
-  }
+  if (p.S && m == 0 && srow >= 0 && sp.t0 + sp.len >= sp.total)
+    state_store<W>(st, p.S + (srow * p.H + h) * hsz, 0, p.DK, p.DV, col, lane);
 }
 
 template <int W, int CT, typename InT>
@@ -417,7 +446,11 @@ static hipError_t launch_main_t(DecayParams p, hipStream_t s) {
   const int64_t grid = (int64_t)p.slots * p.H * p.ncb;
   if (grid > INT32_MAX - 8) return hipErrorInvalidValue;
   p.grid = (int32_t)grid;
-  hipLaunchKernelGGL((decay_main_kernel<W, CT, InT>), dim3((unsigned)((grid + 7) / 8 * 8)), dim3(256), 0, s, p);
+  const dim3 blocks((unsigned)((grid + 7) / 8 * 8));
+  if (p.o)
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 template <int W, typename InT>
@@ -479,30 +512,14 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
     else if (REV ? p.dST != nullptr : p.S0 != nullptr)
       src = (REV ? p.dST : p.S0) + ((int64_t)sp.n * p.H + h) * hsz;
   }
-  f32x4 st[TI][TC];
-  auto at = [&](int ti, int tc, int i) {
-    const int t = wi * TI + ti, ch = 32 * (t >> 1) + 8 * (lane >> 4) + 4 * (t & 1) + i;
-    return active && ch < p.DK ? (int64_t)ch * p.DV + cb * 16 * CT + 16 * (wc * TC + tc) + (lane & 15) : (int64_t)-1;
-  };
+  f32x4 st[TC][TI];
+  const int t0 = wi * TI, col0 = cb * 16 * CT + 16 * wc * TC + (lane & 15);
 #pragma unroll
-  for (int ti = 0; ti < TI; ++ti)
-#pragma unroll
-    for (int tc = 0; tc < TC; ++tc)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t e = at(ti, tc, i);
-        st[ti][tc][i] = src && e >= 0 ? src[e] : 0.f;
-      }
+  for (int tc = 0; tc < TC; ++tc) state_load<W>(st[tc], active ? src : nullptr, t0, p.DK, p.DV, col0 + 16 * tc, lane);
   auto save = [&](float* dst) {
+    if (!active) return;
 #pragma unroll
-    for (int ti = 0; ti < TI; ++ti)
-#pragma unroll
-      for (int tc = 0; tc < TC; ++tc)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t e = at(ti, tc, i);
-          if (e >= 0) dst[e] = st[ti][tc][i];
-        }
+    for (int tc = 0; tc < TC; ++tc) state_store<W>(st[tc], dst, t0, p.DK, p.DV, col0 + 16 * tc, lane);
   };
 
   Stage<W, XT> sx;
@@ -516,11 +533,13 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
     sy.load(y, y_ts, c0, sp.len, tid);
     const int t = c0 + lane;
     a_next = al[(int64_t)(t < sp.len ? t : sp.len - 1) * a_ts];
-    if (t >= sp.len) a_next = 1.f;
   };
   auto put = [&](int i) {
+    const int c0 = chunk_of(i) * DCH;
     unsigned char* buf = smem + (i % NB) * BUF;
-    sx.store(buf, XB, tid);
+    sx.store(buf, XB, c0, sp.len, p.DK, tid);
+    sy.mask(c0, sp.len, tid);
+    if (c0 + lane >= sp.len) a_next = 1.f;
     // lane t: the weight of token t, from its tile's products and the whole tiles before or behind it
     const float pre = row_prefix_prod(a_next), suf = row_suffix_prod_excl(a_next);
     float P[4];
@@ -580,14 +599,14 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
 #pragma unroll
         for (int tc = 0; tc < TC; ++tc)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st[ti][tc][e] *= G;
+          for (int e = 0; e < 4; ++e) st[tc][ti][e] *= G;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           bf16x8 xf[NPX];
 #pragma unroll
           for (int e = 0; e < NPX; ++e) xf[e] = frag_chan<W>(buf + e * XB, t >> 1, t & 1, u, lane);
 #pragma unroll
-          for (int tc = 0; tc < TC; ++tc) mma(st[ti][tc], xf, yf[tc][u]);
+          for (int tc = 0; tc < TC; ++tc) mma(st[tc][ti], xf, yf[tc][u]);
         }
       }
     }

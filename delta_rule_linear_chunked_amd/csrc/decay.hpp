@@ -243,27 +243,23 @@ __device__ __forceinline__ Span slot_span(const DecayParams& p, int slot) {
   return x;
 }
 
-// 8 channels of one token row: raw bits as loaded, zeroed when the row does not exist, then the bf16
-// terms in LDS (fp32 data: three tiles `plane` bytes apart).
+// 8 channels of one token row: raw bits as loaded (zeroed only when they are put away, so that nothing
+// waits for the load before), then the bf16 terms in LDS (fp32 data: three tiles `plane` bytes apart).
 template <typename InT>
 struct Piece;
 template <>
 struct Piece<__bf16> {
   u32x4 v;
-  __device__ __forceinline__ void load(const __bf16* p, bool ok) {
-    v = *reinterpret_cast<const u32x4*>(p);
-    if (!ok) v = u32x4{0, 0, 0, 0};
-  }
+  __device__ __forceinline__ void load(const __bf16* p) { v = *reinterpret_cast<const u32x4*>(p); }
   __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void store(unsigned char* at, int) const { *reinterpret_cast<u32x4*>(at) = v; }
 };
 template <>
 struct Piece<float> {
   f32x4 a, b;
-  __device__ __forceinline__ void load(const float* p, bool ok) {
+  __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const f32x4*>(p);
     b = *reinterpret_cast<const f32x4*>(p + 4);
-    if (!ok) zero();
   }
   __device__ __forceinline__ void zero() { a = b = f32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void store(unsigned char* at, int plane) const {
