@@ -24,7 +24,7 @@ __all__ = ["dr_chunk_fwd", "dr_decode_step", "dr_chunk_fwd_ex", "dr_chunk_fwd_no
            "check_offsets",
            "library_path",
            "load_library", "VARIANTS", "DeltaRuleError",
-           "dr_decay_fwd", "dr_decay_step", "decay_fwd", "decay_step",
+           "dr_decay_fwd", "dr_decay_step", "dr_decay_bwd", "decay_fwd", "decay_step", "decay_bwd", "decay_attention",
            "dr_state_pack", "dr_state_unpack", "state_pack", "state_unpack"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -561,5 +561,5 @@ def delta_rule(q, k, v, alpha, erase, write=None, variant: str = "kda", S0=None,
 
 
 from . import _decay  # noqa: E402  (its functions use the helpers above)
-from ._decay import (decay_fwd, decay_step, dr_decay_fwd, dr_decay_step, dr_state_pack, dr_state_unpack,  # noqa: E402,F401
-                     state_pack, state_unpack)
+from ._decay import (decay_attention, decay_bwd, decay_fwd, decay_step, dr_decay_bwd, dr_decay_fwd,  # noqa: E402,F401
+                     dr_decay_step, dr_state_pack, dr_state_unpack, state_pack, state_unpack)

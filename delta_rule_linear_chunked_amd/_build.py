@@ -21,7 +21,7 @@ LIB = os.path.join(LIBDIR, "libdeltarule.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "plan.cpp", "scratch.hip", "decode.hip", "prefill.hip", "prefill_state.hip", "backward.hip",
-           "backward_chunked.hip", "decay_api.cpp", "decay.hip", "decay_step.hip", "state_cache.hip"]
+           "backward_chunked.hip", "decay_api.cpp", "decay.hip", "decay_bwd.hip", "decay_step.hip", "state_cache.hip"]
 
 # Packed-fp32 instructions are disabled for every device compile; hipcc's host
 # pass does not know the feature and says so, which is harmless.

@@ -43,7 +43,8 @@ def declare(lib):
     lib.dr_decay_step.argtypes = [vp] * 6 + [dp, op, vp]
     lib.dr_state_pack.argtypes = [vp] * 5 + [cp, vp]
     lib.dr_state_unpack.argtypes = [vp] * 5 + [cp, vp]
-    for f in (lib.dr_decay_fwd, lib.dr_decay_step, lib.dr_state_pack, lib.dr_state_unpack):
+    lib.dr_decay_bwd.argtypes = [vp] * 13 + [dp, vp]
+    for f in (lib.dr_decay_fwd, lib.dr_decay_step, lib.dr_decay_bwd, lib.dr_state_pack, lib.dr_state_unpack):
         f.restype = ip
 
 
@@ -167,6 +168,69 @@ def decay_step(q, k, v, alpha, S, state_idx=None):
     o = torch.empty(tuple(v.shape), dtype=torch.float32, device=q.device)
     dr_decay_step(q, k, v, alpha, S, o, state_idx)
     return o
+
+
+def dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dalpha, dS0) -> None:
+    """Gradients of ``dr_decay_fwd`` into caller-provided fp32 tensors: dq, dk [B,T,Hk,dk] (summed over the value heads
+    that share them), dv [B,T,H,dv], dalpha in alpha's shape, dS0 [N,H,dk,dv] or None; dS_T may be None (zero)."""
+    lib = load_library()
+    d = _inputs(q, k, v, alpha, 2)
+    dev, B, T, H, dk_, dv_ = q.device, d.batch, d.seqlen, d.num_heads, d.head_dim_k, d.head_dim_v
+    _offsets(cu_seqlens, d, dev)
+    for t, name in ((S0, "S0"), (dS_T, "dS_T"), (dS0, "dS0")):
+        if t is not None:
+            _need(t, name, (d.num_seqs, H, dk_, dv_), torch.float32, dev)
+    for t, name, shape in ((dO, "dO", (B, T, H, dv_)), (dq, "dq", tuple(q.shape)), (dk, "dk", tuple(q.shape)),
+                           (dv, "dv", (B, T, H, dv_)), (dalpha, "dalpha", tuple(alpha.shape))):
+        _need(t, name, shape, torch.float32, dev)
+    with torch.cuda.device(dev):
+        st = lib.dr_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T),
+                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dalpha), _ptr(dS0), ctypes.byref(d), _stream(dev))
+    _check(lib, st, "dr_decay_bwd")
+
+
+def decay_bwd(q, k, v, alpha, S0=None, cu_seqlens=None, dO=None, dS_T=None, need_dS0: bool = True):
+    """Allocates the gradients and runs ``dr_decay_bwd``. Returns a dict with dq, dk, dv, dalpha and dS0 (None unless
+    ``need_dS0``). Rows past the last packed sequence are not written."""
+    new = lambda s: torch.empty(tuple(s), dtype=torch.float32, device=q.device)  # noqa: E731
+    N = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    g = dict(dq=new(q.shape), dk=new(k.shape), dv=new(v.shape), dalpha=new(alpha.shape),
+             dS0=new((N, v.shape[2], q.shape[3], v.shape[3])) if need_dS0 else None)
+    dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, dS_T, g["dq"], g["dk"], g["dv"], g["dalpha"], g["dS0"])
+    return g
+
+
+class _DecayAttention(torch.autograd.Function):
+    """``decay_fwd`` as an autograd node; both directions are the library's kernels."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, alpha, S0, cu_seqlens):
+        ctx.set_materialize_grads(False)  # an output that the loss does not use gets no gradient
+        N = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+        # rows that no packed sequence holds are zeros, and so are their gradients
+        new = torch.empty if cu_seqlens is None else torch.zeros
+        o = new(tuple(v.shape), dtype=torch.float32, device=q.device)
+        S_T = torch.empty((N, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=q.device)
+        dr_decay_fwd(q, k, v, alpha, S0, cu_seqlens, o, S_T)
+        ctx.save_for_backward(q, k, v, alpha, S0, cu_seqlens)
+        return o, S_T
+
+    @staticmethod
+    def backward(ctx, dO, dS_T):
+        q, k, v, alpha, S0, cu_seqlens = ctx.saved_tensors
+        new = torch.empty if cu_seqlens is None else torch.zeros
+        like = lambda x: new(tuple(x.shape), dtype=torch.float32, device=x.device)  # noqa: E731
+        dO = torch.zeros(tuple(v.shape), dtype=torch.float32, device=q.device) if dO is None else dO.contiguous()
+        dq, dk, dv, da = like(q), like(k), like(v), like(alpha)
+        dS0 = torch.empty_like(S0) if S0 is not None and ctx.needs_input_grad[4] else None
+        dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, None if dS_T is None else dS_T.contiguous(), dq, dk, dv, da, dS0)
+        return dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), da, dS0, None
+
+
+def decay_attention(q, k, v, alpha, S0=None, cu_seqlens=None):
+    """The prefill with gradients through torch autograd: returns (o, S_T) as ``decay_fwd``; ``backward()`` fills the
+    ``.grad`` of q, k, v, alpha and S0 (gradients of bf16 inputs are computed in fp32 and returned in bf16)."""
+    return _DecayAttention.apply(q, k, v, alpha, S0, cu_seqlens)
 
 
 def _cache_dims(S, codes, scales, state_idx, slot_idx):

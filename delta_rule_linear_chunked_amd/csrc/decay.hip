@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void decay_plan_kernel(DecayParams p) {
   fill_slots(p.nseq, tid, p.slot_first, p.slot_seq, p.slots, s_carry);
   __syncthreads();
   if (p.cslots > 0) {
-    scan_table(p.nseq, s_scan, &s_carry, tid, p.chunk_first, p.cu_ok, DCH, true);
+    scan_table(p.nseq, s_scan, &s_carry, tid, p.chunk_first, p.cu_ok, p.bwd_chunk, true);
     fill_slots(p.nseq, tid, p.chunk_first, p.chunk_seq, p.cslots, s_carry);
     __syncthreads();
   }
@@ -284,63 +284,6 @@ __device__ __forceinline__ void state_store(const f32x4 (&st)[NT], float* dst, i
     }
 }
 
-// 64 x W tile of an input: each thread's pieces of a chunk, loaded (rows past the end from the last one) and
-// then put into LDS (those rows, and channels past d_k, as zeros).
-template <int W, typename InT>
-struct Stage {
-  static constexpr int CPR = W / 8, NPC = DCH * CPR / 256;
-  Piece<InT> x[NPC];
-  __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int d, int tid) {
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = tid + 256 * i, pc = idx % CPR, t = c0 + idx / CPR;
-      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (pc * 8 < d ? pc * 8 : 0));
-    }
-  }
-  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int d, int tid) {
-    if (c0 + DCH > len || d < W) {
-#pragma unroll
-      for (int i = 0; i < NPC; ++i) {
-        const int idx = tid + 256 * i;
-        if (c0 + idx / CPR >= len || (idx % CPR) * 8 >= d) x[i].zero();
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = tid + 256 * i;
-      x[i].store(tile + 16 * swz<W>(idx / CPR, idx % CPR), plane);
-    }
-  }
-};
-// 64 x CW tile (CW 16, 32 or 64), rows in order
-template <int CW, typename InT>
-struct StageCols {
-  static constexpr int CPR = CW / 8, NPC = (DCH * CPR + 255) / 256;
-  Piece<InT> x[NPC];
-  __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int tid) {
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = (tid + 256 * i) % (DCH * CPR), t = c0 + idx / CPR;
-      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (idx % CPR) * 8);
-    }
-  }
-  __device__ __forceinline__ void mask(int c0, int len, int tid) {
-    if (c0 + DCH > len) {
-#pragma unroll
-      for (int i = 0; i < NPC; ++i)
-        if (c0 + ((tid + 256 * i) % (DCH * CPR)) / CPR >= len) x[i].zero();
-    }
-  }
-  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int tid) {
-    mask(c0, len, tid);
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = tid + 256 * i;
-      if (idx < DCH * CPR) x[i].store(tile + idx * 16, plane);
-    }
-  }
-};
-
 template <int W, int CT, typename InT, bool OUT>
 __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   using Sh = MainShape<W, CT, InT>;
@@ -444,6 +387,7 @@ template <int W, int CT, typename InT>
 static hipError_t launch_main_t(DecayParams p, hipStream_t s) {
   p.ncb = p.DV / (16 * CT);
   const int64_t grid = (int64_t)p.slots * p.H * p.ncb;
+  if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX - 8) return hipErrorInvalidValue;
   p.grid = (int32_t)grid;
   const dim3 blocks((unsigned)((grid + 7) / 8 * 8));
@@ -475,11 +419,11 @@ static hipError_t launch_main(const DecayParams& p, const DecayPlan& pl, hipStre
 //   CHUNKS: the state at each chunk's start (reverse: the gradient at its end) into cs / ds, from the
 //           segment's start state
 // ---------------------------------------------------------------------------
-template <int W, int CT, typename XT, typename YT, bool REV>
+template <int W, int CT, int DC, typename XT, typename YT, bool REV>
 __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, int local) {
   constexpr int NPX = Terms<XT>::N;
   constexpr int IW = W / 16 < 4 ? W / 16 : 4, TI = W / 16 / IW, CW = 4 / IW, TC = CT / CW > 0 ? CT / CW : 1;
-  constexpr int XB = DCH * W * 2, YB = DCH * CT * 32, BUF = NPX * XB + 3 * YB;
+  constexpr int XB = DC * W * 2, YB = DC * CT * 32, BUF = NPX * XB + 3 * YB;
   constexpr int NB = NPX == 1 ? 2 : 1;
   __shared__ __align__(16) unsigned char smem[NB * BUF];
   __shared__ float s_gam[NB];
@@ -522,24 +466,24 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
     for (int tc = 0; tc < TC; ++tc) state_store<W>(st[tc], dst, t0, p.DK, p.DV, col0 + 16 * tc, lane);
   };
 
-  Stage<W, XT> sx;
-  StageCols<16 * CT, YT> sy;
+  Stage<W, XT, DC> sx;
+  StageCols<16 * CT, YT, DC> sy;
   float a_next = 1.f;
-  const int nc = (sp.len + DCH - 1) / DCH;
+  const int nc = (sp.len + DC - 1) / DC;
   auto chunk_of = [&](int i) { return REV ? nc - 1 - i : i; };
   auto fetch = [&](int i) {
-    const int c0 = chunk_of(i) * DCH;
+    const int c0 = chunk_of(i) * DC;
     sx.load(x, x_ts, c0, sp.len, p.DK, tid);
     sy.load(y, y_ts, c0, sp.len, tid);
-    const int t = c0 + lane;
+    const int t = c0 + (lane & (DC - 1));
     a_next = al[(int64_t)(t < sp.len ? t : sp.len - 1) * a_ts];
   };
   auto put = [&](int i) {
-    const int c0 = chunk_of(i) * DCH;
+    const int c0 = chunk_of(i) * DC;
     unsigned char* buf = smem + (i % NB) * BUF;
     sx.store(buf, XB, c0, sp.len, p.DK, tid);
     sy.mask(c0, sp.len, tid);
-    if (c0 + lane >= sp.len) a_next = 1.f;
+    if (lane >= DC || c0 + lane >= sp.len) a_next = 1.f;
     // lane t: the weight of token t, from its tile's products and the whole tiles before or behind it
     const float pre = row_prefix_prod(a_next), suf = row_suffix_prod_excl(a_next);
     float P[4];
@@ -550,12 +494,12 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
 #pragma unroll
     for (int j = 0; j < 4; ++j) wt *= (REV ? j < (lane >> 4) : j > (lane >> 4)) ? P[j] : 1.f;
     if (tid == 0) s_gam[i % NB] = P[0] * P[1] * P[2] * P[3];
-    constexpr int CPR = StageCols<16 * CT, YT>::CPR;
+    constexpr int CPR = StageCols<16 * CT, YT, DC>::CPR;
 #pragma unroll
-    for (int j = 0; j < StageCols<16 * CT, YT>::NPC; ++j) {
+    for (int j = 0; j < StageCols<16 * CT, YT, DC>::NPC; ++j) {
       const int idx = tid + 256 * j;
-      const float f = __shfl(wt, (idx / CPR) & 63);
-      if (idx < DCH * CPR) {
+      const float f = __shfl(wt, (idx / CPR) & (DC - 1));
+      if (idx < DC * CPR) {
         float z[8];
         if constexpr (sizeof(YT) == 2) {
           const bf16x8 b = __builtin_bit_cast(bf16x8, sy.x[j].v);
@@ -575,7 +519,7 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
     fetch(0);
     put(0);
   }
-  const int64_t cslot0 = (p.cu ? (local ? 0 : p.chunk_first[sp.n]) : (int64_t)sp.n * ((p.T + DCH - 1) / DCH)) + sp.t0 / DCH;
+  const int64_t cslot0 = (p.cu ? (local ? 0 : p.chunk_first[sp.n]) : (int64_t)sp.n * ((p.T + DC - 1) / DC)) + sp.t0 / DC;
   float gall = 1.f;
   for (int i = 0; i < nc; ++i) {
     if (i + 1 < nc) fetch(i + 1);
@@ -585,11 +529,11 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
     const float G = s_gam[i % NB];
     gall *= G;
     if (active) {
-      bf16x8 yf[TC][2][3];
+      bf16x8 yf[TC][DC / 32][3];
 #pragma unroll
       for (int tc = 0; tc < TC; ++tc)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < DC / 32; ++u)
 #pragma unroll
           for (int e = 0; e < 3; ++e)
             yf[tc][u][e] = frag_cols<16 * CT>(buf + NPX * XB + e * YB, 16 * (wc * TC + tc), u, lane);
@@ -601,7 +545,7 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
 #pragma unroll
           for (int e = 0; e < 4; ++e) st[tc][ti][e] *= G;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < DC / 32; ++u) {
           bf16x8 xf[NPX];
 #pragma unroll
           for (int e = 0; e < NPX; ++e) xf[e] = frag_chan<W>(buf + e * XB, t >> 1, t & 1, u, lane);
@@ -661,33 +605,38 @@ __global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p, in
   }
 }
 
-template <int W, int CT, typename XT, typename YT, bool REV>
+template <int W, int CT, int DC, typename XT, typename YT, bool REV>
 static hipError_t launch_state_t(DecayParams p, int local, hipStream_t s) {
   p.ncb = p.DV / (16 * CT);
   const int64_t grid = (int64_t)p.slots * p.H * p.ncb;
+  if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX - 8) return hipErrorInvalidValue;
   p.grid = (int32_t)grid;
-  hipLaunchKernelGGL((decay_state_kernel<W, CT, XT, YT, REV>), dim3((unsigned)((grid + 7) / 8 * 8)), dim3(256), 0, s, p, local);
+  hipLaunchKernelGGL((decay_state_kernel<W, CT, DC, XT, YT, REV>), dim3((unsigned)((grid + 7) / 8 * 8)), dim3(256), 0, s, p,
+                     local);
   return hipGetLastError();
 }
-template <int W, typename XT, typename YT, bool REV>
+template <int W, int DC, typename XT, typename YT, bool REV>
 static hipError_t launch_state_w(const DecayParams& p, int local, hipStream_t s) {
-  return p.DV >= 32 ? launch_state_t<W, 2, XT, YT, REV>(p, local, s) : launch_state_t<W, 1, XT, YT, REV>(p, local, s);
+  return p.DV >= 32 ? launch_state_t<W, 2, DC, XT, YT, REV>(p, local, s) : launch_state_t<W, 1, DC, XT, YT, REV>(p, local, s);
 }
-template <typename XT, typename YT, bool REV>
+template <int DC, typename XT, typename YT, bool REV>
 static hipError_t launch_state(const DecayParams& p, int local, hipStream_t s) {
-  if (p.DK == 128) return launch_state_w<128, XT, YT, REV>(p, local, s);
-  if (p.DK == 64) return launch_state_w<64, XT, YT, REV>(p, local, s);
-  return launch_state_w<32, XT, YT, REV>(p, local, s);
+  if (p.DK == 128) return launch_state_w<128, DC, XT, YT, REV>(p, local, s);
+  if (p.DK == 64) return launch_state_w<64, DC, XT, YT, REV>(p, local, s);
+  return launch_state_w<32, DC, XT, YT, REV>(p, local, s);
 }
 
+// (the contribution of whole segments does not depend on the chunk length)
 hipError_t launch_decay_states(const DecayParams& p, bool bf16, bool rev, int local, hipStream_t s) {
-  if (rev) return bf16 ? launch_state<__bf16, float, true>(p, local, s) : launch_state<float, float, true>(p, local, s);
-  return bf16 ? launch_state<__bf16, __bf16, false>(p, local, s) : launch_state<float, float, false>(p, local, s);
+  constexpr int CB = decay_bwd_chunk(true), CF = decay_bwd_chunk(false);
+  if (rev) return bf16 ? launch_state<CB, __bf16, float, true>(p, local, s) : launch_state<CF, float, float, true>(p, local, s);
+  return bf16 ? launch_state<CB, __bf16, __bf16, false>(p, local, s) : launch_state<CF, float, float, false>(p, local, s);
 }
 hipError_t launch_decay_join(const DecayParams& p, int rev, hipStream_t s) {
   const int64_t hsz = (int64_t)p.DK * p.DV;
   const int64_t grid = (int64_t)p.nseq * p.H * ((hsz / 4 + 255) / 256);
+  if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)grid), dim3(256), 0, s, p, rev);
   return hipGetLastError();

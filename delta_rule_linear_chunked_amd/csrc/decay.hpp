@@ -54,11 +54,17 @@ struct DecayParams {
   int32_t* chunk_seq;    // packed: [cslots] sequence of the chunk slot (-1: unused)
   int32_t* chunk_first;  // packed: [nseq + 1]
   int32_t cslots;
+  int32_t bwd_chunk;     // tokens per chunk slot
   float* dq;             // [B, T, Hk, d_k] or, with shared heads, per-head partial sums [B, T, H, d_k]
   float* dk;
   float* dv;
   float* dalpha;         // [B, T, H]
   float* dS0;
+  float* pq;             // shared heads: partial sums [B, T, H, d_k]
+  float* pk;
+  float* head_da;        // one decay per head: its gradient [H] (dalpha is then a workspace)
+  int32_t dq_heads;      // heads of dq and dk as the gradient kernel writes them
+  int32_t nbatch;        // batch rows
 };
 
 // What the host decides for a call.
@@ -157,7 +163,7 @@ __device__ __forceinline__ bf16x8 frag_chan(const unsigned char* tile, int w, in
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + 16 * swz<W>(r + 16, piece) + 8 * e));
   return join(a, b);
 }
-// The same for a tile of CW columns in order, no swizzle: lane l's column is n0 + l % 16.
+// The same for a tile with rows of CW elements in order, no swizzle: lane l's column is n0 + l % 16.
 template <int CW>
 __device__ __forceinline__ bf16x8 frag_cols(const unsigned char* tile, int n0, int u, int lane) {
   const int g = lane >> 4, p = lane & 15;
@@ -278,9 +284,70 @@ struct Terms<__bf16> {
   static constexpr int N = 1;
 };
 
+// DC x W tile of an input: each thread's pieces of a chunk, loaded (rows past the end from the last one) and
+// then put into LDS (those rows, and channels past d_k, as zeros).
+template <int W, typename InT, int DC = DCH>
+struct Stage {
+  static constexpr int CPR = W / 8, NPC = (DC * CPR + 255) / 256;
+  Piece<InT> x[NPC];
+  __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int d, int tid) {
+#pragma unroll
+    for (int i = 0; i < NPC; ++i) {
+      const int idx = (tid + 256 * i) % (DC * CPR), pc = idx % CPR, t = c0 + idx / CPR;
+      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (pc * 8 < d ? pc * 8 : 0));
+    }
+  }
+  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int d, int tid) {
+    if (c0 + DC > len || d < W) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) {
+        const int idx = (tid + 256 * i) % (DC * CPR);
+        if (c0 + idx / CPR >= len || (idx % CPR) * 8 >= d) x[i].zero();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NPC; ++i) {
+      const int idx = tid + 256 * i;
+      if (idx < DC * CPR) x[i].store(tile + 16 * swz<W>(idx / CPR, idx % CPR), plane);
+    }
+  }
+};
+// DC x CW tile (CW 16, 32 or 64), rows in order
+template <int CW, typename InT, int DC = DCH>
+struct StageCols {
+  static constexpr int CPR = CW / 8, NPC = (DC * CPR + 255) / 256;
+  Piece<InT> x[NPC];
+  __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int tid) {
+#pragma unroll
+    for (int i = 0; i < NPC; ++i) {
+      const int idx = (tid + 256 * i) % (DC * CPR), t = c0 + idx / CPR;
+      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (idx % CPR) * 8);
+    }
+  }
+  __device__ __forceinline__ void mask(int c0, int len, int tid) {
+    if (c0 + DC > len) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i)
+        if (c0 + ((tid + 256 * i) % (DC * CPR)) / CPR >= len) x[i].zero();
+    }
+  }
+  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int tid) {
+    mask(c0, len, tid);
+#pragma unroll
+    for (int i = 0; i < NPC; ++i) {
+      const int idx = tid + 256 * i;
+      if (idx < DC * CPR) x[i].store(tile + idx * 16, plane);
+    }
+  }
+};
+
 hipError_t launch_decay_plan(const DecayParams& p, hipStream_t s);
 hipError_t launch_decay_fwd(DecayParams p, const DecayPlan& pl, bool bf16, hipStream_t s);
 hipError_t launch_decay_step(const DecayParams& p, bool bf16, hipStream_t s);
 hipError_t launch_decay_bwd(DecayParams p, const DecayPlan& pl, bool bf16, hipStream_t s);
+// Tokens per chunk of the backward: its chunk holds q, k, v and dO in LDS, fp32 data three times as large.
+constexpr int decay_bwd_chunk(bool bf16) { return bf16 ? 64 : 32; }
+hipError_t launch_decay_states(const DecayParams& p, bool bf16, bool rev, int local, hipStream_t s);
+hipError_t launch_decay_join(const DecayParams& p, int rev, hipStream_t s);
 
 }  // namespace dr

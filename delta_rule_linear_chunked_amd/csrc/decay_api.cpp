@@ -255,6 +255,88 @@ int dr_decay_step(const void* q, const void* k, const void* v, const float* alph
   return DR_OK;
 }
 
+int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
+                 const int32_t* cu_seqlens, const float* dO, const float* dS_T, float* dq, float* dk, float* dv,
+                 float* dalpha, float* dS0, const dr_decay_dims* dims, hipStream_t stream) {
+  dr::host_clear_error();
+  int st = check_dims(dims, cu_seqlens, false);
+  if (st) return st;
+  const int64_t tokens = dims->batch * dims->seqlen, H = dims->num_heads, N = dims->num_seqs;
+  if (tokens > 0) {
+    st = check_ptrs({{q, "q"}, {k, "k"}, {v, "v"}, {alpha, "alpha"}, {dO, "dO"}, {dq, "dq"}, {dk, "dk"}, {dv, "dv"}}, {});
+    if (st) return st;
+  }
+  const bool per_head = dims->decay_layout == DR_DECAY_HEAD;
+  if (tokens > 0 || per_head) {
+    st = check_ptrs({{dalpha, "dalpha"}}, {});
+    if (st) return st;
+  }
+  st = check_ptrs({}, {{S0, "S0"}, {cu_seqlens, "cu_seqlens"}, {dS_T, "dS_T"}, {dS0, "dS0"}});
+  if (st) return st;
+  st = dr::host_check_offsets(cu_seqlens, N, dims->seqlen, stream);
+  if (st) return st;
+  const bool packed = cu_seqlens != nullptr, bf16 = dims->in_dtype == DR_BF16;
+  if (N == 0 && !per_head) return DR_OK;
+  const dr::DecayPlan pl = plan_decay(dims, packed, true);
+  const int64_t chunk = dr::decay_bwd_chunk(bf16);
+  const int64_t cslots = packed ? dims->seqlen / chunk + N : N * ((dims->seqlen + chunk - 1) / chunk);
+  if (pl.slots * H * (dims->head_dim_v / 16) > INT32_MAX - 8 || cslots * H > INT32_MAX - 8 || pl.seg > INT32_MAX ||
+      tokens * dims->num_k_heads * (dims->head_dim_k / 4) / 256 >= INT32_MAX)
+    return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
+  dr::DecayParams p{};
+  set_dims(p, dims);
+  p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.cu = cu_seqlens;
+  p.dO = dO; p.dST = dS_T; p.dq = dq; p.dk = dk; p.dv = dv; p.dalpha = dalpha; p.dS0 = dS0;
+  p.seg = (int32_t)pl.seg;
+  p.nseg = (int32_t)pl.nseg;
+  p.slots = (int32_t)pl.slots;
+  p.cslots = (int32_t)cslots;
+  p.bwd_chunk = (int32_t)chunk;
+  p.nbatch = (int32_t)dims->batch;
+  const int64_t hsz = dims->head_dim_k * dims->head_dim_v;
+  Layout lay;
+  const bool segs = pl.nseg > 1, shared = dims->num_k_heads != H;
+  const int64_t off_cs = lay.take(cslots * H * hsz * 4), off_ds = lay.take(cslots * H * hsz * 4);
+  const int64_t off_part = segs ? lay.take(pl.slots * H * hsz * 4) : 0, off_g = segs ? lay.take(pl.slots * H * 4) : 0;
+  const int64_t off_pq = shared ? lay.take(tokens * H * dims->head_dim_k * 4) : 0;
+  const int64_t off_pk = shared ? lay.take(tokens * H * dims->head_dim_k * 4) : 0;
+  const int64_t off_da = per_head ? lay.take(tokens * H * 4) : 0;
+  const int64_t off_tab = packed ? lay.take((pl.slots + cslots + 4 * N + 3) * 4) : 0;
+  void* mem = nullptr;
+  hipError_t e = dr::host_workspace((size_t)(lay.size > 0 ? lay.size : 256), stream, &mem);
+  if (e != hipSuccess)
+    return host_fail(DR_ERR_HIP, "decay backward workspace (%lld bytes) allocation failed: %s", (long long)lay.size,
+                     hipGetErrorString(e));
+  unsigned char* ws = static_cast<unsigned char*>(mem);
+  auto f = [&](int64_t off) { return reinterpret_cast<float*>(ws + off); };
+  p.cs = f(off_cs);
+  p.ds = f(off_ds);
+  if (segs) {
+    p.part = p.rpart = f(off_part);  // (the reverse passes run after the forward ones)
+    p.gpart = f(off_g);
+  }
+  if (shared) {
+    p.pq = f(off_pq);
+    p.pk = f(off_pk);
+  }
+  if (per_head) {
+    p.head_da = dalpha;
+    p.dalpha = f(off_da);
+  }
+  if (packed) {
+    p.slot_seq = reinterpret_cast<int32_t*>(ws + off_tab);
+    p.slot_first = p.slot_seq + pl.slots;
+    p.cu_ok = p.slot_first + N + 1;
+    p.chunk_first = p.cu_ok + N + 1;
+    p.chunk_seq = p.chunk_first + N + 1;
+  }
+  e = dr::launch_decay_bwd(p, pl, bf16, stream);
+  const hipError_t ef = hipFreeAsync(mem, stream);
+  if (e != hipSuccess) return host_fail(DR_ERR_HIP, "decay backward launch failed: %s", hipGetErrorString(e));
+  if (ef != hipSuccess) return host_fail(DR_ERR_HIP, "decay backward workspace release failed: %s", hipGetErrorString(ef));
+  return DR_OK;
+}
+
 static int cache_checks(const void* S, const int32_t* state_idx, const void* codes, const float* scales,
                         const int32_t* slot_idx, const dr_cache_dims* d) {
   if (d == nullptr) return host_fail(DR_ERR_NULL, "dims is NULL");
