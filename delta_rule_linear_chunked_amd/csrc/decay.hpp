@@ -80,9 +80,9 @@ struct DecayPlan {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// The fp32 values x cut into three bf16 terms whose sum is x exactly (8 + 8 + 8 significand bits,
-// by truncation, so that nothing overflows): an MFMA over the three terms against a bf16 operand is
-// an fp32-grade product at three bf16 rates (the fp32 MFMA runs at a sixteenth of one).
+// The fp32 values x as three bf16 terms, each the remainder rounded to nearest: the sum is x to 2^-26, so an
+// MFMA over the three terms against a bf16 operand is an fp32-grade product at three bf16 rates (the fp32
+// MFMA runs at a sixteenth of one). Magnitudes from about 3.39e38 up round to infinity.
 struct Tri {
   bf16x8 t[3];
 };
@@ -93,11 +93,10 @@ __device__ __forceinline__ Tri split3(const float (&x)[8]) {
     float a = x[2 * j], b = x[2 * j + 1];
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
-      const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
-      w[t][j] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);  // the upper halves of both
+      w[t][j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
       if (t < 2) {
-        a -= __builtin_bit_cast(float, ua & 0xffff0000u);
-        b -= __builtin_bit_cast(float, ub & 0xffff0000u);
+        a -= __builtin_bit_cast(float, w[t][j] << 16);
+        b -= __builtin_bit_cast(float, w[t][j] & 0xffff0000u);
       }
     }
   }
@@ -105,6 +104,23 @@ __device__ __forceinline__ Tri split3(const float (&x)[8]) {
 #pragma unroll
   for (int t = 0; t < 3; ++t) r.t[t] = __builtin_bit_cast(bf16x8, w[t]);
   return r;
+}
+// Four values' terms to LDS, `plane` bytes apart.
+__device__ __forceinline__ void split_store4(unsigned char* at, int plane, const f32x4& v) {
+  float x[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    uint2 w;
+    w.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2));
+    w.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2], x[3]}, bf16x2));
+    *reinterpret_cast<uint2*>(at + t * plane) = w;
+    if (t < 2) {
+      x[0] -= __builtin_bit_cast(float, w.x << 16);
+      x[1] -= __builtin_bit_cast(float, w.x & 0xffff0000u);
+      x[2] -= __builtin_bit_cast(float, w.y << 16);
+      x[3] -= __builtin_bit_cast(float, w.y & 0xffff0000u);
+    }
+  }
 }
 
 // Operand of one 32-deep slice: NP bf16 terms (1: bf16 data as they are, 3: fp32 data).

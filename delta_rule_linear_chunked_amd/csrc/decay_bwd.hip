@@ -62,23 +62,6 @@ __device__ __forceinline__ f32x4 ratio_col(const DecayTab& tb, const float (&P)[
   return x;
 }
 
-__device__ __forceinline__ void split_store4(unsigned char* at, int plane, const f32x4& v) {
-  const float x[8] = {v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
-  const Tri t = split3(x);
-#pragma unroll
-  for (int e = 0; e < 3; ++e) {
-    union {
-      bf16x8 v;
-      u32x4 w;
-    } y;
-    y.v = t.t[e];
-    uint2 z;
-    z.x = y.w[0];
-    z.y = y.w[1];
-    *reinterpret_cast<uint2*>(at + e * plane) = z;
-  }
-}
-
 // Rows of tile R: P = (Q K^T) . ratio and E = (dO V^T) . ratio as bf16 terms into LDS, and their path sums
 // sum_r ratio(r, t) sum_{s<t} ratio(t-1, s) A[r, s] for the tile's rows r. R is a template argument so that no branch
 // stands between an MFMA and the first use of its result: where one did, the compiler left out the
