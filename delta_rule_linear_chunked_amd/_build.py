@@ -45,7 +45,8 @@ def _hipcc() -> str:
 # architectural VGPRs (rather than AGPRs) speed up both prefill passes.
 _ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 _MFMA_VGPR = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-FILE_FLAGS = {"prefill.hip": _MFMA_VGPR, "prefill_state.hip": _ILP + _MFMA_VGPR, "backward.hip": _ILP}
+FILE_FLAGS = {"prefill.hip": _MFMA_VGPR, "prefill_state.hip": _ILP + _MFMA_VGPR, "backward.hip": _ILP,
+              "decay.hip": _MFMA_VGPR, "decay_bwd.hip": _MFMA_VGPR}
 
 
 def _compile(src: str) -> str:

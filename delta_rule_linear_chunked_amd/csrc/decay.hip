@@ -5,8 +5,8 @@
 //
 //   O = Gamma . (Q S0) + ((Q K^T) . ratio) V,     S <- Gamma_C S0 + K^T (ratio(C, .) . V)
 //
-// One workgroup of 4 waves carries 16 CT value columns of one head through one segment of a sequence;
-// a wave holds the d_k x 16 state of one column tile in its accumulators for the whole segment. The
+// One workgroup of 8 waves carries 16 CT value columns of one head through one segment of a sequence; the
+// waves of a column tile hold its d_k x 16 state in their accumulators for the whole segment. The
 // layouts are chosen so that nothing but the inputs goes through LDS: the accumulators of K^T V are, lane
 // for lane, the S^T operand of Q S0, and the accumulators of K Q^T are the P^T operand of P V (common
 // index orders of the 32-deep products, see decay.hpp), so O^T comes out with 4 consecutive columns per
@@ -94,155 +94,180 @@ __global__ __launch_bounds__(256) void decay_plan_kernel(DecayParams p) {
 // ---------------------------------------------------------------------------
 // Main pass
 // ---------------------------------------------------------------------------
+// The eight waves are CT column tiles x G = 8 / CT waves each. The G waves of a column split its channels in
+// IS parts (whole 32-channel slices) and repeat them D times: a wave forms its channels' part of Q S0 for the row
+// tiles of its repeat, hands the parts of row tiles that it does not finish to their owner, and updates its channels
+// of the state.
+constexpr int MAIN_WAVES = 8;
+template <int W, int CT>
+struct Split {
+  static constexpr int G = MAIN_WAVES / CT, IS = G < W / 32 ? G : W / 32, D = G / IS < 4 ? G / IS : 4;
+  static constexpr int U = W / 32 / IS;           // 32-channel slices of a wave
+  static constexpr int RT = 4 / D;                // row tiles of a repeat
+  static constexpr int RO = (RT + IS - 1) / IS;   // of them finished by each part (the first RT / RO parts)
+  // i-th row tile of repeat d; pairs are 0 with 3 and 1 with 2, which have equal work
+  static constexpr int tile(int d, int i) {
+    if (RT == 4) return RO == 2 ? (i == 0 ? 0 : i == 1 ? 3 : i == 2 ? 1 : 2) : i;
+    if (RT == 2) return d == 0 ? (i == 0 ? 0 : 3) : (i == 0 ? 1 : 2);
+    return d;
+  }
+};
 template <int W, int CT, typename InT>
 struct MainShape {
   static constexpr int NP = Terms<InT>::N;
   static constexpr int NB = NP == 1 ? 2 : 1;  // fp32 data is held as three bf16 terms: one buffer fits
   static constexpr int QK = DCH * W * 2;      // bytes of one plane
   static constexpr int VB = DCH * CT * 32;
-  static constexpr int BUF = NP * (2 * QK + VB);
+  static constexpr int OFF_K = NP * QK, OFF_V = 2 * NP * QK, OFF_T = OFF_V + NP * VB, BUF = OFF_T + 3 * VB;
+  static constexpr int PP = DCH + 8, PB = DCH * PP * 2;  // P: row pitch free of bank conflicts, bytes of one plane
+  using Sp = Split<W, CT>;
+  static constexpr int XCH = Sp::IS > 1 ? CT * 4 * (Sp::IS - 1) * 1024 : 0;  // parts of Q S0 on their way
 };
 
-// One chunk of a wave: row tiles R..., column tile at column n0 of the block.
-template <int W, int CT, typename InT, bool OUT, int... R>
-__device__ __forceinline__ void main_chunk(const unsigned char* buf, const DecayTab& tb, f32x4 (&st)[W / 16], int n0,
-                                           float* o, int64_t o_ts, int rows, int lane) {
+// P = (Q K^T) . ratio of tile (R, S) as bf16 terms into LDS, rows r
+template <int W, int CT, typename InT, int R, int S>
+__device__ __forceinline__ void score_tile(const unsigned char* buf, const DecayTab& tb, const Op<Terms<InT>::N> (&qf)[W / 32],
+                                           unsigned char* Pt, int lane) {
   using Sh = MainShape<W, CT, InT>;
-  constexpr int NP = Sh::NP, U = W / 32;
-  constexpr int RL[] = {R...};
-  constexpr int NR = sizeof...(R);
-  constexpr int RMAX = RL[NR - 1];
-  const unsigned char* Qt = buf;
-  const unsigned char* Kt = buf + NP * Sh::QK;
-  const unsigned char* Vt = buf + 2 * NP * Sh::QK;
+  constexpr int NP = Sh::NP;
   const int g = lane >> 4, r16 = lane & 15;
-  float P[4];
-  f32x4 suf[4];
+  f32x4 sc = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    P[i] = tb.tile[i];
-    suf[i] = *reinterpret_cast<const f32x4*>(&tb.suf[16 * i + 4 * g]);
+  for (int u = 0; u < W / 32; ++u) {
+    Op<NP> kf;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(buf + Sh::OFF_K + i * Sh::QK, 16 * S, u, lane);
+    mma(sc, kf.t, qf[u].t);
   }
-  Op<NP> vf[2];
+  if constexpr (S == R) {
+    const f32x4 in = *reinterpret_cast<const f32x4*>(&tb.in[S][r16 * LDP + 4 * g]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[i] = r16 >= 4 * g + i ? sc[i] * in[i] : 0.f;
+  } else {
+    float f = tb.pre[16 * R + r16];
+#pragma unroll
+    for (int j = S + 1; j < R; ++j) f *= tb.tile[j];
+    const f32x4 suf = *reinterpret_cast<const f32x4*>(&tb.suf[16 * S + 4 * g]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[i] *= f * suf[i];
+  }
+  split_store4(Pt + ((16 * R + r16) * Sh::PP + 16 * S + 4 * g) * 2, Sh::PB, sc);
+}
+template <int W, typename InT, int R>
+__device__ __forceinline__ void score_rows(const unsigned char* buf, Op<Terms<InT>::N> (&qf)[W / 32], int lane) {
+  constexpr int NP = Terms<InT>::N;
+#pragma unroll
+  for (int u = 0; u < W / 32; ++u)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) qf[u].t[i] = frag_rows<W>(buf + i * DCH * W * 2, 16 * R, u, lane);
+}
+
+// First half of a chunk, wave WV: its part of Q S0 (kept for the row tiles that it finishes, handed on for
+// the others) and its share of the ten tiles of P.
+template <int W, int CT, typename InT, int WV>
+__device__ __forceinline__ void chunk_first(const unsigned char* buf, const DecayTab& tb, const f32x4* st,
+                                            f32x4 (&oa)[Split<W, CT>::RO], unsigned char* Pt, unsigned char* xch, int lane) {
+  using Sh = MainShape<W, CT, InT>;
+  using Sp = Split<W, CT>;
+  constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
+  Tri sf[Sp::U];
+  if constexpr (REP < Sp::D) {
+#pragma unroll
+  for (int u = 0; u < Sp::U; ++u) {
+    const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
+                        st[2 * u + 1][0], st[2 * u + 1][1], st[2 * u + 1][2], st[2 * u + 1][3]};
+    sf[u] = split3(x);
+  }
+#pragma unroll
+  for (int i = 0; i < Sp::RT; ++i) {
+    const int R = Sp::tile(REP, i), owner = i / Sp::RO;
+    f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < Sp::U; ++u) {
+      Op<NP> qf;
+#pragma unroll
+      for (int e = 0; e < NP; ++e) qf.t[e] = frag_rows<W>(buf + e * Sh::QK, 16 * R, PART * Sp::U + u, lane);
+      mma(acc, sf[u].t, qf.t);
+    }
+    if (owner == PART)
+      oa[i % Sp::RO] = acc;
+    else  // slot of this part among the owner's IS - 1 others
+      *reinterpret_cast<f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + (PART < owner ? PART : PART - 1)) * 64 + lane) * 16) = acc;
+  }
+  }
+  // (waves w and w + 4 share a SIMD)
+  Op<NP> qf[W / 32];
+  constexpr int R = WV < 4 ? 3 : WV < 7 ? 2 : 1;
+  score_rows<W, InT, R>(buf, qf, lane);
+  score_tile<W, CT, InT, R, WV < 4 ? WV : WV < 7 ? WV - 4 : 0>(buf, tb, qf, Pt, lane);
+  if constexpr (WV == 7) score_tile<W, CT, InT, 1, 1>(buf, tb, qf, Pt, lane);
+  if constexpr (WV == 4) {
+    score_rows<W, InT, 0>(buf, qf, lane);
+    score_tile<W, CT, InT, 0, 0>(buf, tb, qf, Pt, lane);
+  }
+}
+
+// Second half: the row tiles that wave WV finishes, and its channels of the state:
+// S <- Gamma_C S + K^T (tail . V).
+template <int W, int CT, typename InT, bool OUT, int WV>
+__device__ __forceinline__ void chunk_second(const unsigned char* buf, const DecayTab& tb, f32x4 (&st)[2 * Split<W, CT>::U],
+                                             f32x4 (&oa)[Split<W, CT>::RO], const unsigned char* Pt,
+                                             const unsigned char* xch, float* o, int o_ts, int rows, int lane) {
+  using Sh = MainShape<W, CT, InT>;
+  using Sp = Split<W, CT>;
+  constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
+  const int g = lane >> 4, r16 = lane & 15;
+  bf16x8 vt[2][3];
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_cols<16 * CT>(Vt + i * Sh::VB, n0, u, lane);
-
-  if constexpr (OUT) {
-    Op<NP> qf[NR][U];
+    for (int e = 0; e < 3; ++e) vt[u][e] = frag_cols<16 * CT>(buf + Sh::OFF_T + e * Sh::VB, 16 * CTI, u, lane);
+  const float G = tb.tile[0] * tb.tile[1] * tb.tile[2] * tb.tile[3];
+  if constexpr (OUT && REP < Sp::D && PART * Sp::RO < Sp::RT) {
+    // rows past the end fall outside the descriptor and are dropped
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
+    Op<NP> vf[2];
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_cols<16 * CT>(buf + Sh::OFF_V + i * Sh::VB, 16 * CTI, u, lane);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) qf[n][u].t[i] = frag_rows<W>(Qt + i * Sh::QK, 16 * RL[n], u, lane);
-    // Gamma . (Q S0), as its transpose
-    f32x4 oa[NR];
+    for (int j = 0; j < Sp::RO; ++j) {
+      const int R = Sp::tile(REP, PART * Sp::RO + j);
+      f32x4 acc = oa[j];
 #pragma unroll
-    for (int n = 0; n < NR; ++n) oa[n] = f32x4{0, 0, 0, 0};
+      for (int e = 0; e < IS - 1; ++e)
+        acc += *reinterpret_cast<const f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + e) * 64 + lane) * 16);
+      float gam = tb.pre[16 * R + r16];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
-                          st[2 * u + 1][0], st[2 * u + 1][1], st[2 * u + 1][2], st[2 * u + 1][3]};
-      const Tri sf = split3(x);
+      for (int t = 0; t < R; ++t) gam *= tb.tile[t];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) mma(oa[n], sf.t, qf[n][u].t);
-    }
-    float pre[NR];
+      for (int i = 0; i < 4; ++i) acc[i] *= gam;
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      pre[n] = tb.pre[16 * RL[n] + r16];
-      float gam = pre[n];
+      for (int u = 0; u < R / 2 + 1; ++u) {
+        bf16x8 pf[3];
 #pragma unroll
-      for (int j = 0; j < RL[n]; ++j) gam *= P[j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) oa[n][i] *= gam;
-    }
-    // ((Q K^T) . ratio) V over the 32-token halves that reach the row tiles
-#pragma unroll
-    for (int u = 0; u < RMAX / 2 + 1; ++u) {
-      f32x4 sc[NR][2];
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const int S = 2 * u + a;
-#pragma unroll
-        for (int n = 0; n < NR; ++n) sc[n][a] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < (S <= RMAX ? U : 0); ++w) {
-          Op<NP> kf;
-#pragma unroll
-          for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(Kt + i * Sh::QK, 16 * S, w, lane);
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-            if (RL[n] >= S) mma(sc[n][a], kf.t, qf[n][w].t);
+        for (int e = 0; e < 3; ++e) {
+          const unsigned char* at = Pt + e * Sh::PB + ((16 * R + r16) * Sh::PP + 32 * u + 4 * g) * 2;
+          pf[e] = join(*reinterpret_cast<const s16x4*>(at), *reinterpret_cast<const s16x4*>(at + 32));
         }
+        mma(acc, vf[u].t, pf);
       }
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        float x[8];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const int S = 2 * u + a;
-          if (S < RL[n]) {
-            float f = pre[n];
-#pragma unroll
-            for (int j = S + 1; j < RL[n]; ++j) f *= P[j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * a + i] = sc[n][a][i] * (f * suf[S][i]);
-          } else if (S == RL[n]) {
-            const f32x4 in = *reinterpret_cast<const f32x4*>(&tb.in[S][r16 * LDP + 4 * g]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * a + i] = r16 >= 4 * g + i ? sc[n][a][i] * in[i] : 0.f;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * a + i] = 0.f;
-          }
-        }
-        if (RL[n] >= 2 * u) {
-          const Tri pf = split3(x);
-          mma(oa[n], vf[u].t, pf.t);
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const int r = 16 * RL[n] + r16;
-      if (r < rows) *reinterpret_cast<f32x4*>(o + r * o_ts + n0 + 4 * g) = oa[n];
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), rsrc,
+                                             ((16 * R + r16) * o_ts + 16 * CTI + 4 * g) * 4, 0, 0);
     }
   }
-
-  // S <- Gamma_C S + K^T (ratio(C, .) . V)
-  Tri vt[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    float x[8];
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      float f = 1.f;
-#pragma unroll
-      for (int j = 2 * u + a + 1; j < 4; ++j) f *= P[j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y = 0.f;
-#pragma unroll
-        for (int t = NP - 1; t >= 0; --t) y += (float)vf[u].t[t][4 * a + i];
-        x[4 * a + i] = y * (suf[2 * u + a][i] * f);
-      }
-    }
-    vt[u] = split3(x);
-  }
-  const float G = P[0] * P[1] * P[2] * P[3];
-#pragma unroll
-  for (int t = 0; t < W / 16; ++t) {
+  for (int t = 0; t < 2 * Sp::U; ++t) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) st[t][i] *= G;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       Op<NP> kf;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) kf.t[i] = frag_chan<W>(Kt + i * Sh::QK, t >> 1, t & 1, u, lane);
-      mma(st[t], kf.t, vt[u].t);
+      for (int i = 0; i < NP; ++i)
+        kf.t[i] = frag_chan<W>(buf + Sh::OFF_K + i * Sh::QK, PART * Sp::U + (t >> 1), t & 1, u, lane);
+      mma(st[t], kf.t, vt[u]);
     }
   }
 }
@@ -284,11 +309,46 @@ __device__ __forceinline__ void state_store(const f32x4 (&st)[NT], float* dst, i
     }
 }
 
+// A chunk's token weights from its decays a (lane t: token t): the product of the decays behind the token (or, REV,
+// from the chunk's start through it) and of the whole chunk.
+template <bool REV>
+__device__ __forceinline__ float chunk_weight(float a, int lane, float& all) {
+  const float pre = row_prefix_prod(a), suf = row_suffix_prod_excl(a);
+  float P[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    P[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, pre), 16 * j + 15));
+  float wt = REV ? pre : suf;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) wt *= (REV ? j < (lane >> 4) : j > (lane >> 4)) ? P[j] : 1.f;
+  all = P[0] * P[1] * P[2] * P[3];
+  return wt;
+}
+// One piece of V or dO, its row scaled by f, as three bf16 terms into LDS
+template <typename T>
+__device__ __forceinline__ void scaled_store(const Piece<T>& x, float f, unsigned char* at, int plane) {
+  float z[8];
+  if constexpr (sizeof(T) == 2) {
+    const bf16x8 b = __builtin_bit_cast(bf16x8, x.v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = (float)b[e] * f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = (e < 4 ? x.a[e] : x.b[e - 4]) * f;
+  }
+  const Tri t = split3(z);
+#pragma unroll
+  for (int e = 0; e < 3; ++e) *reinterpret_cast<bf16x8*>(at + e * plane) = t.t[e];
+}
+
 template <int W, int CT, typename InT, bool OUT>
-__global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
+__global__ __launch_bounds__(64 * MAIN_WAVES) void decay_main_kernel(const DecayParams p) {
   using Sh = MainShape<W, CT, InT>;
-  constexpr int NB = Sh::NB;
+  using Sp = Split<W, CT>;
+  constexpr int NB = Sh::NB, NT = 2 * Sp::U, NTH = 64 * MAIN_WAVES;
   __shared__ __align__(16) unsigned char smem[NB * Sh::BUF];
+  __shared__ __align__(16) unsigned char Pt[OUT ? 3 * Sh::PB : 16];
+  __shared__ __align__(16) unsigned char xch[OUT && Sh::XCH ? Sh::XCH : 16];
   __shared__ __align__(16) DecayTab tabs[NB];
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   if (id >= p.grid) return;
@@ -298,7 +358,7 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   if (sp.n < 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ct = wave % CT, m = wave / CT;
+  const int ct = wave % CT, m = wave / CT, part = m % Sp::IS;
   const int hk = h / (p.H / p.Hk);
   const InT* q = static_cast<const InT*>(p.q) + sp.b * p.q_bs + sp.row0 * p.q_ts + (int64_t)hk * p.DK;
   const InT* k = static_cast<const InT*>(p.k) + sp.b * p.k_bs + sp.row0 * p.k_ts + (int64_t)hk * p.DK;
@@ -309,8 +369,8 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   const int64_t o_ts = (int64_t)p.H * p.DV;
   float* o = OUT ? p.o + trow * o_ts + (int64_t)h * p.DV + cb * 16 * CT : nullptr;
 
-  // the state at the segment's start: lane's column l % 16, rows 32 u + 8 (l / 16) + 4 e + i
-  const int col = cb * 16 * CT + 16 * ct + (lane & 15);
+  // the state at the segment's start: lane's column l % 16, channels 32 u + 8 (l / 16) + 4 e + i of the wave's slices
+  const int col = cb * 16 * CT + 16 * ct + (lane & 15), tile0 = part * NT;
   const int64_t hsz = (int64_t)p.DK * p.DV;
   int64_t srow = sp.n;  // row of the state buffers
   if (p.sidx) {
@@ -319,68 +379,121 @@ __global__ __launch_bounds__(256) void decay_main_kernel(const DecayParams p) {
   }
   const float* src = p.part ? p.part + ((int64_t)slot * p.H + h) * hsz
                             : (p.S0 && srow >= 0 ? p.S0 + (srow * p.H + h) * hsz : nullptr);
-  f32x4 st[W / 16];
-  state_load<W>(st, src, 0, p.DK, p.DV, col, lane);
+  f32x4 st[NT];
+  state_load<W>(st, src, tile0, p.DK, p.DV, col, lane);
 
-  Stage<W, InT> sq, sk;
-  StageCols<16 * CT, InT> sv;
+  Stage<W, InT, DCH, true, NTH> sq, sk;
+  Stage<16 * CT, InT, DCH, false, 256> sv;  // the first four waves; the others fill the decays' table
+  if constexpr (OUT) sq.init(p.q_ts, p.DK, tid);
+  sk.init(p.k_ts, p.DK, tid);
+  sv.init(p.v_ts, 16 * CT, tid & 255);
   float a_next = 1.f;
   const int nc = (sp.len + DCH - 1) / DCH;
   auto fetch = [&](int c) {
-    const int c0 = c * DCH;
-    if constexpr (OUT) sq.load(q, p.q_ts, c0, sp.len, p.DK, tid);
-    sk.load(k, p.k_ts, c0, sp.len, p.DK, tid);
-    sv.load(v, p.v_ts, c0, sp.len, tid);
-    const int t = c0 + 16 * wave + (lane & 15);
-    a_next = al[(int64_t)(t < sp.len ? t : sp.len - 1) * a_ts];
+    const int64_t c0 = (int64_t)c * DCH;
+    const int rows = sp.len - (int)c0;
+    if constexpr (OUT) sq.load(q + c0 * p.q_ts, p.q_ts, rows);
+    sk.load(k + c0 * p.k_ts, p.k_ts, rows);
+    sv.load(v + c0 * p.v_ts, p.v_ts, rows);
+    a_next = al[(c0 + (lane < rows ? lane : rows - 1)) * a_ts];
   };
   auto put = [&](int c) {
-    const int c0 = c * DCH;
+    const int rows = sp.len - c * DCH;
     unsigned char* buf = smem + (c % NB) * Sh::BUF;
-    if constexpr (OUT) sq.store(buf, Sh::QK, c0, sp.len, p.DK, tid);
-    sk.store(buf + Sh::NP * Sh::QK, Sh::QK, c0, sp.len, p.DK, tid);
-    sv.store(buf + 2 * Sh::NP * Sh::QK, Sh::VB, c0, sp.len, tid);
-    decay_table(tabs[c % NB], wave, c0 + 16 * wave + (lane & 15) < sp.len ? a_next : 1.f, lane);
+    if constexpr (OUT) sq.store(buf, Sh::QK, rows, p.DK, tid);
+    sk.store(buf + Sh::OFF_K, Sh::QK, rows, p.DK, tid);
+    if (lane >= rows) a_next = 1.f;
+    if (wave < 4) {
+      sv.mask(rows, 16 * CT, tid);
+      float all;
+      const float wt = chunk_weight<false>(a_next, lane, all);
+#pragma unroll
+      for (int i = 0; i < sv.NPC; ++i) {
+        const float f = __shfl(wt, sv.row + i * sv.STEP);
+        if (sv.mine(i, tid)) {
+          if constexpr (OUT) sv.x[i].store(buf + Sh::OFF_V + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+          scaled_store(sv.x[i], f, buf + Sh::OFF_T + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+        }
+      }
+    } else {
+      decay_table(tabs[c % NB], wave - 4, __shfl(a_next, 16 * (wave - 4) + (lane & 15)), lane);
+    }
   };
+  if constexpr (OUT) {
+    // the two tiles of P above the diagonal that the 32-token products meet
+    for (int i = tid; i < 3 * 2 * 16 * 2; i += NTH) {
+      const int e = i / 64, w = i % 64, R = (w / 32) * 2, r = (w % 32) / 2, hf = w & 1;
+      *reinterpret_cast<u32x4*>(Pt + e * Sh::PB + ((16 * R + r) * Sh::PP + 16 * (R + 1)) * 2 + 16 * hf) = u32x4{0, 0, 0, 0};
+    }
+  }
+  // Loads run two chunks ahead: a chunk's data goes from registers to LDS while the chunk before it is worked
+  // on, and the registers then wait for the chunk after it. (Past the end the last chunk is fetched again: a
+  // branch would make the loads' results merge with the old ones, and that copy waits for them.)
   if (nc > 0) {
     fetch(0);
     put(0);
+    fetch(nc > 1 ? 1 : 0);
   }
   const int first_chunk = sp.t0 / DCH;
   for (int c = 0; c < nc; ++c) {
-    if (c + 1 < nc) fetch(c + 1);
     __syncthreads();
     const unsigned char* buf = smem + (c % NB) * Sh::BUF;
     const DecayTab& tb = tabs[c % NB];
-    float* oc = OUT ? o + (int64_t)c * DCH * o_ts : nullptr;
     const int rows = sp.len - c * DCH;
-    if constexpr (CT == 4) {
-      main_chunk<W, CT, InT, OUT, 0, 1, 2, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
-    } else if constexpr (CT == 2) {
-      if (m == 0)
-        main_chunk<W, CT, InT, OUT, 0, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
-      else
-        main_chunk<W, CT, InT, OUT, 1, 2>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
-    } else {
-      if (m == 0)
-        main_chunk<W, CT, InT, OUT, 0>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
-      else if (m == 1)
-        main_chunk<W, CT, InT, OUT, 1>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
-      else if (m == 2)
-        main_chunk<W, CT, InT, OUT, 2>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
-      else
-        main_chunk<W, CT, InT, OUT, 3>(buf, tb, st, 16 * ct, oc, o_ts, rows, lane);
+    if constexpr (NB == 2) {
+      if (c + 1 < nc) put(c + 1);
+      fetch(c + 2 < nc ? c + 2 : nc - 1);
     }
-    if (p.snap && m == 0 && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
+    f32x4 oa[Sp::RO];
+    float* oc = OUT ? o + (int64_t)c * DCH * o_ts : nullptr;
+    if constexpr (OUT) {
+      if (wave == 0)
+        chunk_first<W, CT, InT, 0>(buf, tb, st, oa, Pt, xch, lane);
+      else if (wave == 1)
+        chunk_first<W, CT, InT, 1>(buf, tb, st, oa, Pt, xch, lane);
+      else if (wave == 2)
+        chunk_first<W, CT, InT, 2>(buf, tb, st, oa, Pt, xch, lane);
+      else if (wave == 3)
+        chunk_first<W, CT, InT, 3>(buf, tb, st, oa, Pt, xch, lane);
+      else if (wave == 4)
+        chunk_first<W, CT, InT, 4>(buf, tb, st, oa, Pt, xch, lane);
+      else if (wave == 5)
+        chunk_first<W, CT, InT, 5>(buf, tb, st, oa, Pt, xch, lane);
+      else if (wave == 6)
+        chunk_first<W, CT, InT, 6>(buf, tb, st, oa, Pt, xch, lane);
+      else
+        chunk_first<W, CT, InT, 7>(buf, tb, st, oa, Pt, xch, lane);
+      __syncthreads();
+    }
+    if (wave == 0)
+      chunk_second<W, CT, InT, OUT, 0>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else if (wave == 1)
+      chunk_second<W, CT, InT, OUT, 1>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else if (wave == 2)
+      chunk_second<W, CT, InT, OUT, 2>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else if (wave == 3)
+      chunk_second<W, CT, InT, OUT, 3>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else if (wave == 4)
+      chunk_second<W, CT, InT, OUT, 4>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else if (wave == 5)
+      chunk_second<W, CT, InT, OUT, 5>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else if (wave == 6)
+      chunk_second<W, CT, InT, OUT, 6>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    else
+      chunk_second<W, CT, InT, OUT, 7>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    if (p.snap && m < Sp::IS && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
       const int64_t per = p.T / DCH / p.snap_chunks;  // fixed length: snapshots per sequence
       const int64_t row = (p.cu ? p.snap_first[sp.n] : sp.n * per) + (first_chunk + c + 1) / p.snap_chunks - 1;
-      state_store<W>(st, p.snap + (row * p.H + h) * hsz, 0, p.DK, p.DV, col, lane);
+      state_store<W>(st, p.snap + (row * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
     }
-    if constexpr (NB == 1) __syncthreads();
-    if (c + 1 < nc) put(c + 1);
+    if constexpr (NB == 1) {
+      __syncthreads();
+      if (c + 1 < nc) put(c + 1);
+      fetch(c + 2 < nc ? c + 2 : nc - 1);
+    }
   }
-  if (p.S && m == 0 && srow >= 0 && sp.t0 + sp.len >= sp.total)
-    state_store<W>(st, p.S + (srow * p.H + h) * hsz, 0, p.DK, p.DV, col, lane);
+  if (p.S && m < Sp::IS && srow >= 0 && sp.t0 + sp.len >= sp.total)
+    state_store<W>(st, p.S + (srow * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
 }
 
 template <int W, int CT, typename InT>
@@ -392,20 +505,23 @@ static hipError_t launch_main_t(DecayParams p, hipStream_t s) {
   p.grid = (int32_t)grid;
   const dim3 blocks((unsigned)((grid + 7) / 8 * 8));
   if (p.o)
-    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(64 * MAIN_WAVES), 0, s, p);
   else
-    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(64 * MAIN_WAVES), 0, s, p);
   return hipGetLastError();
 }
 template <int W, typename InT>
 static hipError_t launch_main_w(const DecayParams& p, const DecayPlan& pl, hipStream_t s) {
-  if (pl.ct == 4) return launch_main_t<W, 4, InT>(p, s);
-  if (pl.ct == 2) return launch_main_t<W, 2, InT>(p, s);
-  return launch_main_t<W, 1, InT>(p, s);
+  return pl.ct == 2 ? launch_main_t<W, 2, InT>(p, s) : launch_main_t<W, 1, InT>(p, s);
 }
 template <typename InT>
 static hipError_t launch_main(const DecayParams& p, const DecayPlan& pl, hipStream_t s) {
-  if (p.DK == 128) return launch_main_w<128, InT>(p, pl, s);
+  if (p.DK == 128) {
+    if constexpr (sizeof(InT) == 4)  // (two column tiles of three-term data do not fit the LDS)
+      return launch_main_t<128, 1, InT>(p, s);
+    else
+      return launch_main_w<128, InT>(p, pl, s);
+  }
   if (p.DK == 64) return launch_main_w<64, InT>(p, pl, s);
   return launch_main_w<32, InT>(p, pl, s);
 }
@@ -467,63 +583,47 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
   };
 
   Stage<W, XT, DC> sx;
-  StageCols<16 * CT, YT, DC> sy;
+  Stage<16 * CT, YT, DC, false> sy;
+  sx.init(x_ts, p.DK, tid);
+  sy.init(y_ts, 16 * CT, tid);
   float a_next = 1.f;
   const int nc = (sp.len + DC - 1) / DC;
   auto chunk_of = [&](int i) { return REV ? nc - 1 - i : i; };
   auto fetch = [&](int i) {
-    const int c0 = chunk_of(i) * DC;
-    sx.load(x, x_ts, c0, sp.len, p.DK, tid);
-    sy.load(y, y_ts, c0, sp.len, tid);
-    const int t = c0 + (lane & (DC - 1));
-    a_next = al[(int64_t)(t < sp.len ? t : sp.len - 1) * a_ts];
+    const int64_t c0 = (int64_t)chunk_of(i) * DC;
+    const int rows = sp.len - (int)c0, t = lane & (DC - 1);
+    sx.load(x + c0 * x_ts, x_ts, rows);
+    sy.load(y + c0 * y_ts, y_ts, rows);
+    a_next = al[(c0 + (t < rows ? t : rows - 1)) * a_ts];
   };
   auto put = [&](int i) {
-    const int c0 = chunk_of(i) * DC;
+    const int rows = sp.len - chunk_of(i) * DC;
     unsigned char* buf = smem + (i % NB) * BUF;
-    sx.store(buf, XB, c0, sp.len, p.DK, tid);
-    sy.mask(c0, sp.len, tid);
-    if (lane >= DC || c0 + lane >= sp.len) a_next = 1.f;
-    // lane t: the weight of token t, from its tile's products and the whole tiles before or behind it
-    const float pre = row_prefix_prod(a_next), suf = row_suffix_prod_excl(a_next);
-    float P[4];
+    sx.store(buf, XB, rows, p.DK, tid);
+    sy.mask(rows, 16 * CT, tid);
+    if (lane >= DC || lane >= rows) a_next = 1.f;
+    float all;
+    const float wt = chunk_weight<REV>(a_next, lane, all);
+    if (tid == 0) s_gam[i % NB] = all;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      P[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, pre), 16 * j + 15));
-    float wt = REV ? pre : suf;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) wt *= (REV ? j < (lane >> 4) : j > (lane >> 4)) ? P[j] : 1.f;
-    if (tid == 0) s_gam[i % NB] = P[0] * P[1] * P[2] * P[3];
-    constexpr int CPR = StageCols<16 * CT, YT, DC>::CPR;
-#pragma unroll
-    for (int j = 0; j < StageCols<16 * CT, YT, DC>::NPC; ++j) {
-      const int idx = tid + 256 * j;
-      const float f = __shfl(wt, (idx / CPR) & (DC - 1));
-      if (idx < DC * CPR) {
-        float z[8];
-        if constexpr (sizeof(YT) == 2) {
-          const bf16x8 b = __builtin_bit_cast(bf16x8, sy.x[j].v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = (float)b[e] * f;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = (e < 4 ? sy.x[j].a[e] : sy.x[j].b[e - 4]) * f;
-        }
-        const Tri t = split3(z);
-#pragma unroll
-        for (int e = 0; e < 3; ++e) *reinterpret_cast<bf16x8*>(buf + NPX * XB + e * YB + idx * 16) = t.t[e];
-      }
+    for (int j = 0; j < sy.NPC; ++j) {
+      const float f = __shfl(wt, sy.row + j * sy.STEP);
+      if (sy.mine(j, tid)) scaled_store(sy.x[j], f, buf + NPX * XB + sy.at + j * sy.STEP * CT * 32, YB);
     }
   };
   if (nc > 0) {
     fetch(0);
     put(0);
+    fetch(nc > 1 ? 1 : 0);
   }
   const int64_t cslot0 = (p.cu ? (local ? 0 : p.chunk_first[sp.n]) : (int64_t)sp.n * ((p.T + DC - 1) / DC)) + sp.t0 / DC;
   float gall = 1.f;
   for (int i = 0; i < nc; ++i) {
-    if (i + 1 < nc) fetch(i + 1);
     __syncthreads();
+    if constexpr (NB == 2) {
+      if (i + 1 < nc) put(i + 1);
+      fetch(i + 2 < nc ? i + 2 : nc - 1);  // (always: see the main pass)
+    }
     if (!local) save((REV ? p.ds : p.cs) + ((cslot0 + chunk_of(i)) * p.H + h) * hsz);
     const unsigned char* buf = smem + (i % NB) * BUF;
     const float G = s_gam[i % NB];
@@ -554,8 +654,11 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
         }
       }
     }
-    if constexpr (NB == 1) __syncthreads();
-    if (i + 1 < nc) put(i + 1);
+    if constexpr (NB == 1) {
+      __syncthreads();
+      if (i + 1 < nc) put(i + 1);
+      fetch(i + 2 < nc ? i + 2 : nc - 1);
+    }
   }
   if (local) {
     save(part + ((int64_t)slot * p.H + h) * hsz);

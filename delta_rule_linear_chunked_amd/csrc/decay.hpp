@@ -140,15 +140,22 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
         if (p + q == sum) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], b[q], acc, 0, 0, 0);
 }
 
-// LDS tile of 64 token rows x W bf16 channels (W 32, 64 or 128), 16-byte pieces permuted within a row
-// so that both kinds of read are free of bank conflicts: a fragment along the channels (16 rows, one
-// piece each) and a transposing read (4 consecutive rows, 4 pieces of 8 bytes each).
+// The wait between an MFMA and the first use of its result behind a branch, which the compiler does not always
+// leave (seen in its output: 3 or 7 instead of 8 cycles where the two stand in different blocks).
+__device__ __forceinline__ void settle(f32x4& acc) { asm volatile("s_nop 7" : "+v"(acc)); }
+
+// LDS tile of token rows x W bf16 channels (W 32, 64 or 128), 16-byte pieces permuted within a row so that both
+// kinds of read are free of bank conflicts: a fragment along the channels (16 rows, one piece each; the
+// hardware serves rows 0-3 and 12-15 of one piece together with rows 4-11 of its neighbour) and a
+// transposing read (4 consecutive rows, 4 pieces of 8 bytes each). Measured per read and CU: 4.9 and 4.2 cycles, as
+// for linear addresses; with the row number as the permutation 4.9 and 8.1, with no regard to the pairing 8.2 and 4.2.
 template <int W>
 __device__ __forceinline__ int swz(int row, int piece) {
   constexpr int CPR = W / 8;
-  if constexpr (CPR == 16) return row * 16 + (piece ^ (((row & 3) << 2) | ((row >> 2) & 3)));
-  if constexpr (CPR == 8) return row * 8 + (piece ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3)));
-  return row * 4 + (piece ^ ((row >> 2) & 3));
+  const int x = (row >> 2) & 3, h = ((x ^ (x >> 1)) & 1) << 1 | x >> 1;  // 0, 2, 3, 1
+  if constexpr (CPR == 16) return row * 16 + (piece ^ (((row & 3) << 2) | h));
+  if constexpr (CPR == 8) return row * 8 + (piece ^ ((((row >> 1) & 1) << 2) | h));
+  return row * 4 + (piece ^ h);
 }
 
 // Fragment with token rows on the lanes: row row0 + l % 16, channels 32 u + 8 (l / 16) .. + 7.
@@ -301,59 +308,51 @@ struct Terms<__bf16> {
 };
 
 // DC x W tile of an input: each thread's pieces of a chunk, loaded (rows past the end from the last one) and
-// then put into LDS (those rows, and channels past d_k, as zeros).
-template <int W, typename InT, int DC = DCH>
+// then put into LDS (those rows, and channels past d, as zeros). A thread's pieces lie NTH / (W / 8) rows apart, a
+// multiple of 16, which the swizzle does not see. Offsets within a chunk are 32 bits (token strides are limited
+// to 2^24 elements), the chunk's base is uniform.
+template <int W, typename InT, int DC = DCH, bool SWZ = true, int NTH = 256>
 struct Stage {
-  static constexpr int CPR = W / 8, NPC = (DC * CPR + 255) / 256;
+  static constexpr int CPR = W / 8, NPC = (DC * CPR + NTH - 1) / NTH, STEP = NTH / CPR;
+  static_assert(!SWZ || STEP % 16 == 0, "the swizzle repeats every 16 rows");
   Piece<InT> x[NPC];
-  __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int d, int tid) {
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = (tid + 256 * i) % (DC * CPR), pc = idx % CPR, t = c0 + idx / CPR;
-      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (pc * 8 < d ? pc * 8 : 0));
-    }
+  uint32_t off, step, col;  // bytes: the first piece's offset, between pieces, the piece's column
+  int row, at;
+  __device__ __forceinline__ void init(int64_t ts, int d, int tid) {
+    const int pc = tid % CPR;
+    row = (tid / CPR) % DC;
+    col = pc * 8 < d ? (uint32_t)(pc * 8 * sizeof(InT)) : 0u;
+    step = (uint32_t)(STEP * ts * sizeof(InT));
+    off = (uint32_t)(row * ts * sizeof(InT)) + col;
+    at = 16 * (SWZ ? swz<W>(row, pc) : row * CPR + pc);
   }
-  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int d, int tid) {
-    if (c0 + DC > len || d < W) {
+  // base: the chunk's first row
+  __device__ __forceinline__ void load(const InT* base, int64_t ts, int rows) {
+    const char* b = reinterpret_cast<const char*>(base);
+    if (rows >= DC) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) x[i].load(reinterpret_cast<const InT*>(b + (off + i * step)));
+    } else {
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
-        const int idx = (tid + 256 * i) % (DC * CPR);
-        if (c0 + idx / CPR >= len || (idx % CPR) * 8 >= d) x[i].zero();
+        const int r = row + i * STEP;
+        x[i].load(reinterpret_cast<const InT*>(b + ((uint32_t)((r < rows ? r : rows - 1) * ts * sizeof(InT)) + col)));
       }
     }
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = tid + 256 * i;
-      if (idx < DC * CPR) x[i].store(tile + 16 * swz<W>(idx / CPR, idx % CPR), plane);
-    }
   }
-};
-// DC x CW tile (CW 16, 32 or 64), rows in order
-template <int CW, typename InT, int DC = DCH>
-struct StageCols {
-  static constexpr int CPR = CW / 8, NPC = (DC * CPR + 255) / 256;
-  Piece<InT> x[NPC];
-  __device__ __forceinline__ void load(const InT* base, int64_t ts, int c0, int len, int tid) {
-#pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = (tid + 256 * i) % (DC * CPR), t = c0 + idx / CPR;
-      x[i].load(base + (int64_t)(t < len ? t : len - 1) * ts + (idx % CPR) * 8);
-    }
-  }
-  __device__ __forceinline__ void mask(int c0, int len, int tid) {
-    if (c0 + DC > len) {
+  __device__ __forceinline__ void mask(int rows, int d, int tid) {
+    if (rows < DC || d < W) {
 #pragma unroll
       for (int i = 0; i < NPC; ++i)
-        if (c0 + ((tid + 256 * i) % (DC * CPR)) / CPR >= len) x[i].zero();
+        if (row + i * STEP >= rows || (tid % CPR) * 8 >= d) x[i].zero();
     }
   }
-  __device__ __forceinline__ void store(unsigned char* tile, int plane, int c0, int len, int tid) {
-    mask(c0, len, tid);
+  __device__ __forceinline__ bool mine(int i, int tid) const { return DC * CPR >= NTH || tid < DC * CPR; }
+  __device__ __forceinline__ void store(unsigned char* tile, int plane, int rows, int d, int tid) {
+    mask(rows, d, tid);
 #pragma unroll
-    for (int i = 0; i < NPC; ++i) {
-      const int idx = tid + 256 * i;
-      if (idx < DC * CPR) x[i].store(tile + idx * 16, plane);
-    }
+    for (int i = 0; i < NPC; ++i)
+      if (mine(i, tid)) x[i].store(tile + at + i * STEP * W * 2, plane);
   }
 };
 

@@ -49,6 +49,8 @@ int check_dims(const dr_decay_dims* d, const int32_t* cu, bool decode) {
                      (long long)d->head_dim_k, (long long)d->head_dim_v);
   // (each factor is bounded first, so that the products below stay within 64 bits)
   const int64_t lim = (int64_t)1 << 31;
+  if (d->num_heads > (int64_t)1 << 16)
+    return host_fail(DR_ERR_UNSUPPORTED, "%lld heads: at most 65536", (long long)d->num_heads);
   if (d->num_heads >= lim || d->num_seqs >= lim || d->batch >= lim || d->seqlen >= lim ||
       d->num_seqs * d->num_heads >= lim || d->batch * d->seqlen >= lim)
     return host_fail(DR_ERR_SHAPE, "problem too large for 32-bit token or head counts");
@@ -59,9 +61,11 @@ int check_dims(const dr_decay_dims* d, const int32_t* cu, bool decode) {
     const int64_t esz = d->in_dtype == DR_BF16 ? 2 : 4;
     for (int i = 0; i < 6; ++i) {
       if (st[i] < 0) return host_fail(DR_ERR_SHAPE, "%s stride %lld is negative", names[i], (long long)st[i]);
-      if (st[i] > ((int64_t)1 << 40) || (st[i] * esz) % 16 != 0)
-        return host_fail(DR_ERR_LAYOUT, "%s stride %lld is not a multiple of 16 bytes (or is beyond 2^40)", names[i],
-                         (long long)st[i]);
+      // (a chunk's rows are reached with 32-bit offsets from its first one)
+      const int64_t most = i % 2 == 0 ? (int64_t)1 << 24 : (int64_t)1 << 40;
+      if (st[i] > most || (st[i] * esz) % 16 != 0)
+        return host_fail(DR_ERR_LAYOUT, "%s stride %lld is not a multiple of 16 bytes (or is beyond %lld)", names[i],
+                         (long long)st[i], (long long)most);
     }
   }
   if (decode) {
@@ -129,7 +133,7 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads;
   pl.ct = tiles >= 2 ? 2 : 1;
   if (const int64_t c = env_int("DR_DECAY_CT"))
-    if ((c == 1 || c == 2 || c == 4) && c <= tiles) pl.ct = (int)c;
+    if ((c == 1 || c == 2) && c <= tiles) pl.ct = (int)c;
   const int64_t wide = tiles / pl.ct;  // workgroups per segment and head
   // enough segments for 512 workgroups, none shorter than 512 tokens
   int64_t seg;

@@ -188,18 +188,22 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(const DecayParams p) {
     Stage<W, InT, DC> sq, sk;
     Stage<V, InT, DC> sv;
     Stage<V, float, DC> so;
-    sq.load(static_cast<const InT*>(p.q) + b * p.q_bs + row0 * p.q_ts + (int64_t)hk * p.DK, p.q_ts, 0, len, p.DK, tid);
-    sk.load(static_cast<const InT*>(p.k) + b * p.k_bs + row0 * p.k_ts + (int64_t)hk * p.DK, p.k_ts, 0, len, p.DK, tid);
-    sv.load(static_cast<const InT*>(p.v) + b * p.v_bs + row0 * p.v_ts + (int64_t)h * p.DV, p.v_ts, 0, len, p.DV, tid);
-    so.load(p.dO + trow * o_ts + (int64_t)h * p.DV, o_ts, 0, len, p.DV, tid);
+    sq.init(p.q_ts, p.DK, tid);
+    sk.init(p.k_ts, p.DK, tid);
+    sv.init(p.v_ts, p.DV, tid);
+    so.init(o_ts, p.DV, tid);
+    sq.load(static_cast<const InT*>(p.q) + b * p.q_bs + row0 * p.q_ts + (int64_t)hk * p.DK, p.q_ts, len);
+    sk.load(static_cast<const InT*>(p.k) + b * p.k_bs + row0 * p.k_ts + (int64_t)hk * p.DK, p.k_ts, len);
+    sv.load(static_cast<const InT*>(p.v) + b * p.v_bs + row0 * p.v_ts + (int64_t)h * p.DV, p.v_ts, len);
+    so.load(p.dO + trow * o_ts + (int64_t)h * p.DV, o_ts, len);
     const int t = 16 * wave + r16;
     float a = p.alpha[(p.a_tok ? (trow + (t < len ? t : len - 1)) * p.H : 0) + h];
     if (t >= len) a = 1.f;
     decay_table(tb, wave, a, lane);
-    sq.store(sm, Sh::QK, 0, len, p.DK, tid);
-    sk.store(sm + Sh::OFF_K, Sh::QK, 0, len, p.DK, tid);
-    sv.store(sm + Sh::OFF_V, Sh::VO, 0, len, p.DV, tid);
-    so.store(sm + Sh::OFF_O, Sh::VO, 0, len, p.DV, tid);
+    sq.store(sm, Sh::QK, len, p.DK, tid);
+    sk.store(sm + Sh::OFF_K, Sh::QK, len, p.DK, tid);
+    sv.store(sm + Sh::OFF_V, Sh::VO, len, p.DV, tid);
+    so.store(sm + Sh::OFF_O, Sh::VO, len, p.DV, tid);
   }
   if (tid < 4 * DC) {
     (&s_da[0][0])[tid] = 0.f;

@@ -39,7 +39,8 @@ typedef enum dr_decay_layout {
 /* Sizes of one call. batch, seqlen, num_heads, head_dim_k, head_dim_v, num_seqs and in_dtype as in dr_dims;
  * num_heads must be a multiple of num_k_heads. strided = 0: q, k and v are dense; 1: the element strides
  * between consecutive tokens of a batch row and between batch rows (decode: between sequences) are given,
- * under the rules of dr_dims_v2 (heads and channels dense, non-negative, multiples of 16 bytes). */
+ * under the rules of dr_dims_v2 (heads and channels dense, non-negative, multiples of 16 bytes; token strides at
+ * most 2^24 elements). At most 65536 heads. */
 typedef struct dr_decay_dims {
   int64_t batch;
   int64_t seqlen;
