@@ -5,7 +5,7 @@
 //
 //   O = Gamma . (Q S0) + ((Q K^T) . ratio) V,     S <- Gamma_C S0 + K^T (ratio(C, .) . V)
 //
-// One workgroup of 8 waves carries 16 CT value columns of one head through one segment of a sequence; the
+// One workgroup of 8 waves, with 4 more to fill the LDS, carries 16 CT value columns of one head through one segment of a sequence; the
 // waves of a column tile hold its d_k x 16 state in their accumulators for the whole segment. The
 // layouts are chosen so that nothing but the inputs goes through LDS: the accumulators of K^T V are, lane
 // for lane, the S^T operand of Q S0, and the accumulators of K Q^T are the P^T operand of P V (common
@@ -94,11 +94,11 @@ __global__ __launch_bounds__(256) void decay_plan_kernel(DecayParams p) {
 // ---------------------------------------------------------------------------
 // Main pass
 // ---------------------------------------------------------------------------
-// The eight waves are CT column tiles x G = 8 / CT waves each. The G waves of a column split its channels in
+// Eight waves work on the state, as CT column tiles x G = 8 / CT waves each; four more fill the LDS and form P. The G waves of a column split its channels in
 // IS parts (whole 32-channel slices) and repeat them D times: a wave forms its channels' part of Q S0 for the row
 // tiles of its repeat, hands the parts of row tiles that it does not finish to their owner, and updates its channels
 // of the state.
-constexpr int MAIN_WAVES = 8;
+constexpr int MAIN_WAVES = 8, FILL_WAVES = 4;
 template <int W, int CT>
 struct Split {
   static constexpr int G = MAIN_WAVES / CT, IS = G < W / 32 ? G : W / 32, D = G / IS < 4 ? G / IS : 4;
@@ -118,7 +118,8 @@ struct MainShape {
   static constexpr int NB = NP == 1 ? 2 : 1;  // fp32 data is held as three bf16 terms: one buffer fits
   static constexpr int QK = DCH * W * 2;      // bytes of one plane
   static constexpr int VB = DCH * CT * 32;
-  static constexpr int OFF_K = NP * QK, OFF_V = 2 * NP * QK, OFF_T = OFF_V + NP * VB, BUF = OFF_T + 3 * VB;
+  // Q has one buffer: it is read in the first half of a chunk and filled in the second
+  static constexpr int QB = NP * QK, OFF_V = NP * QK, OFF_T = OFF_V + NP * VB, BUF = OFF_T + 3 * VB;
   static constexpr int PP = DCH + 8, PB = DCH * PP * 2;  // P: row pitch free of bank conflicts, bytes of one plane
   using Sp = Split<W, CT>;
   static constexpr int XCH = Sp::IS > 1 ? CT * 4 * (Sp::IS - 1) * 1024 : 0;  // parts of Q S0 on their way
@@ -136,7 +137,7 @@ __device__ __forceinline__ void score_tile(const unsigned char* buf, const Decay
   for (int u = 0; u < W / 32; ++u) {
     Op<NP> kf;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(buf + Sh::OFF_K + i * Sh::QK, 16 * S, u, lane);
+    for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(buf + i * Sh::QK, 16 * S, u, lane);
     mma(sc, kf.t, qf[u].t);
   }
   if constexpr (S == R) {
@@ -162,11 +163,10 @@ __device__ __forceinline__ void score_rows(const unsigned char* buf, Op<Terms<In
     for (int i = 0; i < NP; ++i) qf[u].t[i] = frag_rows<W>(buf + i * DCH * W * 2, 16 * R, u, lane);
 }
 
-// First half of a chunk, wave WV: its part of Q S0 (kept for the row tiles that it finishes, handed on for
-// the others) and its share of the ten tiles of P.
+// First half of a chunk, wave WV: its part of Q S0, kept for the row tiles that it finishes, handed on for the others.
 template <int W, int CT, typename InT, int WV>
-__device__ __forceinline__ void chunk_first(const unsigned char* buf, const DecayTab& tb, const f32x4* st,
-                                            f32x4 (&oa)[Split<W, CT>::RO], unsigned char* Pt, unsigned char* xch, int lane) {
+__device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x4* st, f32x4 (&oa)[Split<W, CT>::RO],
+                                            unsigned char* xch, int lane) {
   using Sh = MainShape<W, CT, InT>;
   using Sp = Split<W, CT>;
   constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
@@ -195,14 +195,20 @@ __device__ __forceinline__ void chunk_first(const unsigned char* buf, const Deca
       *reinterpret_cast<f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + (PART < owner ? PART : PART - 1)) * 64 + lane) * 16) = acc;
   }
   }
-  // (waves w and w + 4 share a SIMD)
-  Op<NP> qf[W / 32];
-  constexpr int R = WV < 4 ? 3 : WV < 7 ? 2 : 1;
-  score_rows<W, InT, R>(buf, qf, lane);
-  score_tile<W, CT, InT, R, WV < 4 ? WV : WV < 7 ? WV - 4 : 0>(buf, tb, qf, Pt, lane);
-  if constexpr (WV == 7) score_tile<W, CT, InT, 1, 1>(buf, tb, qf, Pt, lane);
-  if constexpr (WV == 4) {
-    score_rows<W, InT, 0>(buf, qf, lane);
+}
+
+// P by the filling waves, the ten tiles split 3, 2, 3, 2.
+template <int W, int CT, typename InT, int WV>
+__device__ __forceinline__ void scores(const unsigned char* qbuf, const unsigned char* buf, const DecayTab& tb,
+                                       unsigned char* Pt, int lane) {
+  Op<Terms<InT>::N> qf[W / 32];
+  constexpr int R = WV < 2 ? 3 : WV == 2 ? 2 : 1, S0 = WV == 1 ? 2 : 0;
+  score_rows<W, InT, R>(qbuf, qf, lane);
+  score_tile<W, CT, InT, R, S0>(buf, tb, qf, Pt, lane);
+  score_tile<W, CT, InT, R, S0 + 1>(buf, tb, qf, Pt, lane);
+  if constexpr (WV == 2) score_tile<W, CT, InT, R, 2>(buf, tb, qf, Pt, lane);
+  if constexpr (WV == 0) {
+    score_rows<W, InT, 0>(qbuf, qf, lane);
     score_tile<W, CT, InT, 0, 0>(buf, tb, qf, Pt, lane);
   }
 }
@@ -266,7 +272,7 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
       Op<NP> kf;
 #pragma unroll
       for (int i = 0; i < NP; ++i)
-        kf.t[i] = frag_chan<W>(buf + Sh::OFF_K + i * Sh::QK, PART * Sp::U + (t >> 1), t & 1, u, lane);
+        kf.t[i] = frag_chan<W>(buf + i * Sh::QK, PART * Sp::U + (t >> 1), t & 1, u, lane);
       mma(st[t], kf.t, vt[u]);
     }
   }
@@ -341,15 +347,66 @@ __device__ __forceinline__ void scaled_store(const Piece<T>& x, float f, unsigne
   for (int e = 0; e < 3; ++e) *reinterpret_cast<bf16x8*>(at + e * plane) = t.t[e];
 }
 
+// The filling waves of a chunk step: P of the chunk in its first half; in its second half the next chunk's data from
+// registers to LDS, and the loads of the one after it. Their latency and that of P's short chains then
+// pass beside the state's work instead of in line with it.
 template <int W, int CT, typename InT, bool OUT>
-__global__ __launch_bounds__(64 * MAIN_WAVES) void decay_main_kernel(const DecayParams p) {
+struct Filler {
+  using Sh = MainShape<W, CT, InT>;
+  Stage<W, InT> sq, sk;
+  Stage<16 * CT, InT, DCH, false> sv;
+  const InT *q, *k, *v;
+  const float* al;
+  int64_t a_ts, q_ts, k_ts, v_ts;
+  int len, nc, d, tid, lane, wave;
+  float a_next;  // decays of chunk 4 g + wave
+  __device__ __forceinline__ void fetch(int c) {
+    const int64_t c0 = (int64_t)(c < nc ? c : nc - 1) * DCH;  // (past the end the last chunk again: no branch, see below)
+    const int rows = len - (int)c0;
+    if constexpr (OUT) sq.load(q + c0 * q_ts, q_ts, rows);
+    sk.load(k + c0 * k_ts, k_ts, rows);
+    sv.load(v + c0 * v_ts, v_ts, rows);
+  }
+  // Decays lie H apart: each of the four waves takes one chunk of every four.
+  __device__ __forceinline__ void fetch_decays(int g) {
+    const int64_t t = (int64_t)(4 * g + wave) * DCH + lane;
+    a_next = al[(t < len ? t : len - 1) * a_ts];
+  }
+  __device__ __forceinline__ void put_decays(int g, float (&ring)[2][4][DCH]) const { ring[g & 1][wave][lane] = a_next; }
+  __device__ __forceinline__ void put(int c, unsigned char* qbuf, unsigned char* buf, DecayTab& tab, const float (&ring)[2][4][DCH]) {
+    const int rows = len - c * DCH;
+    const float* ac = ring[(c >> 2) & 1][c & 3];
+    const float a = lane < rows ? ac[lane] : 1.f;
+    const int t16 = 16 * wave + (lane & 15);
+    const float a16 = t16 < rows ? ac[t16] : 1.f;
+    if constexpr (OUT) sq.store(qbuf, Sh::QK, rows, d, tid);
+    sk.store(buf, Sh::QK, rows, d, tid);
+    sv.mask(rows, 16 * CT, tid);
+    float all;
+    const float wt = chunk_weight<false>(a, lane, all);
+#pragma unroll
+    for (int i = 0; i < sv.NPC; ++i) {
+      const float f = __shfl(wt, sv.row + i * sv.STEP);
+      if (sv.mine(i, tid)) {
+        if constexpr (OUT) sv.x[i].store(buf + Sh::OFF_V + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+        scaled_store(sv.x[i], f, buf + Sh::OFF_T + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+      }
+    }
+    decay_table(tab, wave, a16, lane);
+  }
+};
+
+template <int W, int CT, typename InT, bool OUT>
+__global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_kernel(const DecayParams p) {
   using Sh = MainShape<W, CT, InT>;
   using Sp = Split<W, CT>;
-  constexpr int NB = Sh::NB, NT = 2 * Sp::U, NTH = 64 * MAIN_WAVES;
+  constexpr int NB = Sh::NB, NT = 2 * Sp::U, NTH = 64 * (MAIN_WAVES + FILL_WAVES);
+  __shared__ __align__(16) unsigned char qbuf[OUT ? Sh::QB : 16];
   __shared__ __align__(16) unsigned char smem[NB * Sh::BUF];
   __shared__ __align__(16) unsigned char Pt[OUT ? 3 * Sh::PB : 16];
   __shared__ __align__(16) unsigned char xch[OUT && Sh::XCH ? Sh::XCH : 16];
   __shared__ __align__(16) DecayTab tabs[NB];
+  __shared__ float ring[2][4][DCH];
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   if (id >= p.grid) return;
   const int cb = id % p.ncb, sh = id / p.ncb;
@@ -358,17 +415,77 @@ __global__ __launch_bounds__(64 * MAIN_WAVES) void decay_main_kernel(const Decay
   if (sp.n < 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ct = wave % CT, m = wave / CT, part = m % Sp::IS;
-  const int hk = h / (p.H / p.Hk);
-  const InT* q = static_cast<const InT*>(p.q) + sp.b * p.q_bs + sp.row0 * p.q_ts + (int64_t)hk * p.DK;
-  const InT* k = static_cast<const InT*>(p.k) + sp.b * p.k_bs + sp.row0 * p.k_ts + (int64_t)hk * p.DK;
-  const InT* v = static_cast<const InT*>(p.v) + sp.b * p.v_bs + sp.row0 * p.v_ts + (int64_t)h * p.DV + cb * 16 * CT;
   const int64_t trow = sp.b * p.T + sp.row0;  // row in the dense per-token arrays
-  const float* al = p.alpha + (p.a_tok ? trow * p.H : 0) + h;
-  const int64_t a_ts = p.a_tok ? p.H : 0;
+  const int nc = (sp.len + DCH - 1) / DCH;
+  if constexpr (OUT) {
+    // the two tiles of P above the diagonal that the 32-token products meet
+    for (int i = tid; i < 3 * 2 * 16 * 2; i += NTH) {
+      const int e = i / 64, w = i % 64, R = (w / 32) * 2, r = (w % 32) / 2, hf = w & 1;
+      *reinterpret_cast<u32x4*>(Pt + e * Sh::PB + ((16 * R + r) * Sh::PP + 16 * (R + 1)) * 2 + 16 * hf) = u32x4{0, 0, 0, 0};
+    }
+  }
+  // (both kinds of wave meet the same barriers: one in the prologue, then two or three a chunk)
+  if (wave >= MAIN_WAVES) {
+    const int hk = h / (p.H / p.Hk);
+    Filler<W, CT, InT, OUT> f;
+    f.q = static_cast<const InT*>(p.q) + sp.b * p.q_bs + sp.row0 * p.q_ts + (int64_t)hk * p.DK;
+    f.k = static_cast<const InT*>(p.k) + sp.b * p.k_bs + sp.row0 * p.k_ts + (int64_t)hk * p.DK;
+    f.v = static_cast<const InT*>(p.v) + sp.b * p.v_bs + sp.row0 * p.v_ts + (int64_t)h * p.DV + cb * 16 * CT;
+    f.al = p.alpha + (p.a_tok ? trow * p.H : 0) + h;
+    f.a_ts = p.a_tok ? p.H : 0;
+    f.q_ts = p.q_ts;
+    f.k_ts = p.k_ts;
+    f.v_ts = p.v_ts;
+    f.len = sp.len;
+    f.nc = nc;
+    f.d = p.DK;
+    f.tid = tid - 64 * MAIN_WAVES;
+    f.lane = lane;
+    f.wave = wave - MAIN_WAVES;
+    if constexpr (OUT) f.sq.init(p.q_ts, p.DK, f.tid);
+    f.sk.init(p.k_ts, p.DK, f.tid);
+    f.sv.init(p.v_ts, 16 * CT, f.tid);
+    if (nc > 0) {
+      f.fetch(0);
+      f.fetch_decays(0);
+      f.put_decays(0, ring);
+      f.fetch_decays(1);
+    }
+    __syncthreads();
+    if (nc > 0) {
+      f.put(0, qbuf, smem, tabs[0], ring);
+      f.fetch(1);
+    }
+    for (int c = 0; c < nc; ++c) {
+      const int nb = (c + 1) % NB;
+      __syncthreads();
+      if constexpr (OUT) {
+        const unsigned char* buf = smem + (c % NB) * Sh::BUF;
+        const DecayTab& tb = tabs[c % NB];
+        if (f.wave == 0)
+          scores<W, CT, InT, 0>(qbuf, buf, tb, Pt, lane);
+        else if (f.wave == 1)
+          scores<W, CT, InT, 1>(qbuf, buf, tb, Pt, lane);
+        else if (f.wave == 2)
+          scores<W, CT, InT, 2>(qbuf, buf, tb, Pt, lane);
+        else
+          scores<W, CT, InT, 3>(qbuf, buf, tb, Pt, lane);
+      }
+      __syncthreads();
+      if constexpr (NB == 1) __syncthreads();
+      if (c + 1 < nc) f.put(c + 1, qbuf, smem + nb * Sh::BUF, tabs[nb], ring);
+      f.fetch(c + 2);
+      if ((c & 3) == 0) {  // the next four chunks' decays; those two groups back are done with
+        f.put_decays((c >> 2) + 1, ring);
+        f.fetch_decays((c >> 2) + 2);
+      }
+    }
+    return;
+  }
+
+  const int ct = wave % CT, m = wave / CT, part = m % Sp::IS;
   const int64_t o_ts = (int64_t)p.H * p.DV;
   float* o = OUT ? p.o + trow * o_ts + (int64_t)h * p.DV + cb * 16 * CT : nullptr;
-
   // the state at the segment's start: lane's column l % 16, channels 32 u + 8 (l / 16) + 4 e + i of the wave's slices
   const int col = cb * 16 * CT + 16 * ct + (lane & 15), tile0 = part * NT;
   const int64_t hsz = (int64_t)p.DK * p.DV;
@@ -381,90 +498,34 @@ __global__ __launch_bounds__(64 * MAIN_WAVES) void decay_main_kernel(const Decay
                             : (p.S0 && srow >= 0 ? p.S0 + (srow * p.H + h) * hsz : nullptr);
   f32x4 st[NT];
   state_load<W>(st, src, tile0, p.DK, p.DV, col, lane);
-
-  Stage<W, InT, DCH, true, NTH> sq, sk;
-  Stage<16 * CT, InT, DCH, false, 256> sv;  // the first four waves; the others fill the decays' table
-  if constexpr (OUT) sq.init(p.q_ts, p.DK, tid);
-  sk.init(p.k_ts, p.DK, tid);
-  sv.init(p.v_ts, 16 * CT, tid & 255);
-  float a_next = 1.f;
-  const int nc = (sp.len + DCH - 1) / DCH;
-  auto fetch = [&](int c) {
-    const int64_t c0 = (int64_t)c * DCH;
-    const int rows = sp.len - (int)c0;
-    if constexpr (OUT) sq.load(q + c0 * p.q_ts, p.q_ts, rows);
-    sk.load(k + c0 * p.k_ts, p.k_ts, rows);
-    sv.load(v + c0 * p.v_ts, p.v_ts, rows);
-    a_next = al[(c0 + (lane < rows ? lane : rows - 1)) * a_ts];
-  };
-  auto put = [&](int c) {
-    const int rows = sp.len - c * DCH;
-    unsigned char* buf = smem + (c % NB) * Sh::BUF;
-    if constexpr (OUT) sq.store(buf, Sh::QK, rows, p.DK, tid);
-    sk.store(buf + Sh::OFF_K, Sh::QK, rows, p.DK, tid);
-    if (lane >= rows) a_next = 1.f;
-    if (wave < 4) {
-      sv.mask(rows, 16 * CT, tid);
-      float all;
-      const float wt = chunk_weight<false>(a_next, lane, all);
-#pragma unroll
-      for (int i = 0; i < sv.NPC; ++i) {
-        const float f = __shfl(wt, sv.row + i * sv.STEP);
-        if (sv.mine(i, tid)) {
-          if constexpr (OUT) sv.x[i].store(buf + Sh::OFF_V + sv.at + i * sv.STEP * CT * 32, Sh::VB);
-          scaled_store(sv.x[i], f, buf + Sh::OFF_T + sv.at + i * sv.STEP * CT * 32, Sh::VB);
-        }
-      }
-    } else {
-      decay_table(tabs[c % NB], wave - 4, __shfl(a_next, 16 * (wave - 4) + (lane & 15)), lane);
-    }
-  };
-  if constexpr (OUT) {
-    // the two tiles of P above the diagonal that the 32-token products meet
-    for (int i = tid; i < 3 * 2 * 16 * 2; i += NTH) {
-      const int e = i / 64, w = i % 64, R = (w / 32) * 2, r = (w % 32) / 2, hf = w & 1;
-      *reinterpret_cast<u32x4*>(Pt + e * Sh::PB + ((16 * R + r) * Sh::PP + 16 * (R + 1)) * 2 + 16 * hf) = u32x4{0, 0, 0, 0};
-    }
-  }
-  // Loads run two chunks ahead: a chunk's data goes from registers to LDS while the chunk before it is worked
-  // on, and the registers then wait for the chunk after it. (Past the end the last chunk is fetched again: a
-  // branch would make the loads' results merge with the old ones, and that copy waits for them.)
-  if (nc > 0) {
-    fetch(0);
-    put(0);
-    fetch(nc > 1 ? 1 : 0);
-  }
   const int first_chunk = sp.t0 / DCH;
+  __syncthreads();
   for (int c = 0; c < nc; ++c) {
     __syncthreads();
     const unsigned char* buf = smem + (c % NB) * Sh::BUF;
     const DecayTab& tb = tabs[c % NB];
     const int rows = sp.len - c * DCH;
-    if constexpr (NB == 2) {
-      if (c + 1 < nc) put(c + 1);
-      fetch(c + 2 < nc ? c + 2 : nc - 1);
-    }
     f32x4 oa[Sp::RO];
     float* oc = OUT ? o + (int64_t)c * DCH * o_ts : nullptr;
     if constexpr (OUT) {
       if (wave == 0)
-        chunk_first<W, CT, InT, 0>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 0>(qbuf, st, oa, xch, lane);
       else if (wave == 1)
-        chunk_first<W, CT, InT, 1>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 1>(qbuf, st, oa, xch, lane);
       else if (wave == 2)
-        chunk_first<W, CT, InT, 2>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 2>(qbuf, st, oa, xch, lane);
       else if (wave == 3)
-        chunk_first<W, CT, InT, 3>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 3>(qbuf, st, oa, xch, lane);
       else if (wave == 4)
-        chunk_first<W, CT, InT, 4>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 4>(qbuf, st, oa, xch, lane);
       else if (wave == 5)
-        chunk_first<W, CT, InT, 5>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 5>(qbuf, st, oa, xch, lane);
       else if (wave == 6)
-        chunk_first<W, CT, InT, 6>(buf, tb, st, oa, Pt, xch, lane);
+        chunk_first<W, CT, InT, 6>(qbuf, st, oa, xch, lane);
       else
-        chunk_first<W, CT, InT, 7>(buf, tb, st, oa, Pt, xch, lane);
-      __syncthreads();
+        chunk_first<W, CT, InT, 7>(qbuf, st, oa, xch, lane);
     }
+    __syncthreads();
     if (wave == 0)
       chunk_second<W, CT, InT, OUT, 0>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
     else if (wave == 1)
@@ -486,11 +547,7 @@ __global__ __launch_bounds__(64 * MAIN_WAVES) void decay_main_kernel(const Decay
       const int64_t row = (p.cu ? p.snap_first[sp.n] : sp.n * per) + (first_chunk + c + 1) / p.snap_chunks - 1;
       state_store<W>(st, p.snap + (row * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
     }
-    if constexpr (NB == 1) {
-      __syncthreads();
-      if (c + 1 < nc) put(c + 1);
-      fetch(c + 2 < nc ? c + 2 : nc - 1);
-    }
+    if constexpr (NB == 1) __syncthreads();
   }
   if (p.S && m < Sp::IS && srow >= 0 && sp.t0 + sp.len >= sp.total)
     state_store<W>(st, p.S + (srow * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
@@ -505,9 +562,9 @@ static hipError_t launch_main_t(DecayParams p, hipStream_t s) {
   p.grid = (int32_t)grid;
   const dim3 blocks((unsigned)((grid + 7) / 8 * 8));
   if (p.o)
-    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(64 * MAIN_WAVES), 0, s, p);
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p);
   else
-    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(64 * MAIN_WAVES), 0, s, p);
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p);
   return hipGetLastError();
 }
 template <int W, typename InT>
