@@ -119,11 +119,29 @@ struct MainShape {
   static constexpr int QK = DCH * W * 2;      // bytes of one plane
   static constexpr int VB = DCH * CT * 32;
   // Q has one buffer: it is read in the first half of a chunk and filled in the second
-  static constexpr int QB = NP * QK, OFF_V = NP * QK, OFF_T = OFF_V + NP * VB, BUF = OFF_T + 3 * VB;
+  // Up to two column tiles share each of the scaled rows of V among four waves or more: scaled and cut into terms
+  // once, through LDS. With more tiles a row has one or two readers, which form their terms in registers.
+  static constexpr bool VT = CT <= 2;
+  static constexpr int QB = NP * QK, OFF_V = NP * QK, OFF_T = OFF_V + NP * VB, BUF = OFF_T + (VT ? 3 * VB : 0);
   static constexpr int PP = DCH + 8, PB = DCH * PP * 2;  // P: row pitch free of bank conflicts, bytes of one plane
   using Sp = Split<W, CT>;
   static constexpr int XCH = Sp::IS > 1 ? CT * 4 * (Sp::IS - 1) * 1024 : 0;  // parts of Q S0 on their way
 };
+
+// Column tile n of V, tokens along the product (see frag_cols). Rows of 16 or 32 columns lie in order; wider ones are
+// swizzled as K is, for which the column tiles are taken in frag_chan's order (col_of).
+template <int CT>
+__device__ __forceinline__ bf16x8 frag_v(const unsigned char* tile, int n, int u, int lane) {
+  if constexpr (CT <= 2)
+    return frag_cols<16 * CT>(tile, 16 * n, u, lane);
+  else
+    return frag_chan<16 * CT>(tile, n >> 1, n & 1, u, lane);
+}
+// The column of lane index r (0 .. 15) of column tile n
+template <int CT>
+__device__ __forceinline__ int col_of(int n, int r) {
+  return CT <= 2 ? 16 * n + r : 32 * (n >> 1) + 8 * (r >> 2) + 4 * (n & 1) + (r & 3);
+}
 
 // P = (Q K^T) . ratio of tile (R, S) as bf16 terms into LDS, rows r
 template <int W, int CT, typename InT, int R, int S>
@@ -170,30 +188,31 @@ __device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x
   using Sh = MainShape<W, CT, InT>;
   using Sp = Split<W, CT>;
   constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
-  Tri sf[Sp::U];
   if constexpr (REP < Sp::D) {
+    f32x4 acc[Sp::RT];
 #pragma unroll
-  for (int u = 0; u < Sp::U; ++u) {
-    const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
-                        st[2 * u + 1][0], st[2 * u + 1][1], st[2 * u + 1][2], st[2 * u + 1][3]};
-    sf[u] = split3(x);
-  }
-#pragma unroll
-  for (int i = 0; i < Sp::RT; ++i) {
-    const int R = Sp::tile(REP, i), owner = i / Sp::RO;
-    f32x4 acc = {0, 0, 0, 0};
+    for (int i = 0; i < Sp::RT; ++i) acc[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < Sp::U; ++u) {
-      Op<NP> qf;
+      const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
+                          st[2 * u + 1][0], st[2 * u + 1][1], st[2 * u + 1][2], st[2 * u + 1][3]};
+      const Tri sf = split3(x);
 #pragma unroll
-      for (int e = 0; e < NP; ++e) qf.t[e] = frag_rows<W>(buf + e * Sh::QK, 16 * R, PART * Sp::U + u, lane);
-      mma(acc, sf[u].t, qf.t);
+      for (int i = 0; i < Sp::RT; ++i) {
+        Op<NP> qf;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) qf.t[e] = frag_rows<W>(buf + e * Sh::QK, 16 * Sp::tile(REP, i), PART * Sp::U + u, lane);
+        mma(acc[i], sf.t, qf.t);
+      }
     }
-    if (owner == PART)
-      oa[i % Sp::RO] = acc;
-    else  // slot of this part among the owner's IS - 1 others
-      *reinterpret_cast<f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + (PART < owner ? PART : PART - 1)) * 64 + lane) * 16) = acc;
-  }
+#pragma unroll
+    for (int i = 0; i < Sp::RT; ++i) {
+      const int R = Sp::tile(REP, i), owner = i / Sp::RO;
+      if (owner == PART)
+        oa[i % Sp::RO] = acc[i];
+      else  // slot of this part among the owner's IS - 1 others
+        *reinterpret_cast<f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + (PART < owner ? PART : PART - 1)) * 64 + lane) * 16) = acc[i];
+    }
   }
 }
 
@@ -223,20 +242,17 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
   using Sp = Split<W, CT>;
   constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
   const int g = lane >> 4, r16 = lane & 15;
-  bf16x8 vt[2][3];
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int e = 0; e < 3; ++e) vt[u][e] = frag_cols<16 * CT>(buf + Sh::OFF_T + e * Sh::VB, 16 * CTI, u, lane);
   const float G = tb.tile[0] * tb.tile[1] * tb.tile[2] * tb.tile[3];
-  if constexpr (OUT && REP < Sp::D && PART * Sp::RO < Sp::RT) {
-    // rows past the end fall outside the descriptor and are dropped
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
-    Op<NP> vf[2];
+  Op<NP> vf[2];
+  if constexpr (OUT || !Sh::VT) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_cols<16 * CT>(buf + Sh::OFF_V + i * Sh::VB, 16 * CTI, u, lane);
+      for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_v<CT>(buf + Sh::OFF_V + i * Sh::VB, CTI, u, lane);
+  }
+  if constexpr (OUT && REP < Sp::D && PART * Sp::RO < Sp::RT) {
+    // rows past the end fall outside the descriptor and are dropped
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
 #pragma unroll
     for (int j = 0; j < Sp::RO; ++j) {
       const int R = Sp::tile(REP, PART * Sp::RO + j);
@@ -260,7 +276,34 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
         mma(acc, vf[u].t, pf);
       }
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), rsrc,
-                                             ((16 * R + r16) * o_ts + 16 * CTI + 4 * g) * 4, 0, 0);
+                                             ((16 * R + r16) * o_ts + col_of<CT>(CTI, 4 * g)) * 4, 0, 0);
+    }
+  }
+  bf16x8 vt[2][3];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if constexpr (Sh::VT) {
+#pragma unroll
+      for (int e = 0; e < 3; ++e) vt[u][e] = frag_v<CT>(buf + Sh::OFF_T + e * Sh::VB, CTI, u, lane);
+    } else {
+      float x[8];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float f = 1.f;
+#pragma unroll
+        for (int j = 2 * u + a + 1; j < 4; ++j) f *= tb.tile[j];
+        const f32x4 suf = *reinterpret_cast<const f32x4*>(&tb.suf[16 * (2 * u + a) + 4 * g]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y = 0.f;
+#pragma unroll
+          for (int e = NP - 1; e >= 0; --e) y += (float)vf[u].t[e][4 * a + i];
+          x[4 * a + i] = y * (suf[i] * f);
+        }
+      }
+      const Tri tr = split3(x);
+#pragma unroll
+      for (int e = 0; e < 3; ++e) vt[u][e] = tr.t[e];
     }
   }
 #pragma unroll
@@ -354,7 +397,7 @@ template <int W, int CT, typename InT, bool OUT>
 struct Filler {
   using Sh = MainShape<W, CT, InT>;
   Stage<W, InT> sq, sk;
-  Stage<16 * CT, InT, DCH, false> sv;
+  Stage<16 * CT, InT, DCH, (CT > 2)> sv;
   const InT *q, *k, *v;
   const float* al;
   int64_t a_ts, q_ts, k_ts, v_ts;
@@ -376,20 +419,23 @@ struct Filler {
   __device__ __forceinline__ void put(int c, unsigned char* qbuf, unsigned char* buf, DecayTab& tab, const float (&ring)[2][4][DCH]) {
     const int rows = len - c * DCH;
     const float* ac = ring[(c >> 2) & 1][c & 3];
-    const float a = lane < rows ? ac[lane] : 1.f;
     const int t16 = 16 * wave + (lane & 15);
     const float a16 = t16 < rows ? ac[t16] : 1.f;
     if constexpr (OUT) sq.store(qbuf, Sh::QK, rows, d, tid);
     sk.store(buf, Sh::QK, rows, d, tid);
-    sv.mask(rows, 16 * CT, tid);
-    float all;
-    const float wt = chunk_weight<false>(a, lane, all);
+    if constexpr (!Sh::VT) {
+      sv.store(buf + Sh::OFF_V, Sh::VB, rows, 16 * CT, tid);
+    } else {
+      sv.mask(rows, 16 * CT, tid);
+      float all;
+      const float wt = chunk_weight<false>(lane < rows ? ac[lane] : 1.f, lane, all);
 #pragma unroll
-    for (int i = 0; i < sv.NPC; ++i) {
-      const float f = __shfl(wt, sv.row + i * sv.STEP);
-      if (sv.mine(i, tid)) {
-        if constexpr (OUT) sv.x[i].store(buf + Sh::OFF_V + sv.at + i * sv.STEP * CT * 32, Sh::VB);
-        scaled_store(sv.x[i], f, buf + Sh::OFF_T + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+      for (int i = 0; i < sv.NPC; ++i) {
+        const float f = __shfl(wt, sv.row + i * sv.STEP);
+        if (sv.mine(i, tid)) {
+          if constexpr (OUT) sv.x[i].store(buf + Sh::OFF_V + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+          scaled_store(sv.x[i], f, buf + Sh::OFF_T + sv.at + i * sv.STEP * CT * 32, Sh::VB);
+        }
       }
     }
     decay_table(tab, wave, a16, lane);
@@ -397,7 +443,7 @@ struct Filler {
 };
 
 template <int W, int CT, typename InT, bool OUT>
-__global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_kernel(const DecayParams p) {
+__global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_kernel(const DecayParams p, int local) {
   using Sh = MainShape<W, CT, InT>;
   using Sp = Split<W, CT>;
   constexpr int NB = Sh::NB, NT = 2 * Sp::U, NTH = 64 * (MAIN_WAVES + FILL_WAVES);
@@ -413,6 +459,8 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
   const int h = sh % p.H, slot = sh / p.H;
   const Span sp = slot_span(p, slot);
   if (sp.n < 0) return;
+  // local: a segment's own contribution; nothing comes behind a sequence's last segment
+  if (local && sp.t0 + sp.len >= sp.total) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t trow = sp.b * p.T + sp.row0;  // row in the dense per-token arrays
@@ -487,18 +535,20 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
   const int64_t o_ts = (int64_t)p.H * p.DV;
   float* o = OUT ? p.o + trow * o_ts + (int64_t)h * p.DV + cb * 16 * CT : nullptr;
   // the state at the segment's start: lane's column l % 16, channels 32 u + 8 (l / 16) + 4 e + i of the wave's slices
-  const int col = cb * 16 * CT + 16 * ct + (lane & 15), tile0 = part * NT;
+  const int col = cb * 16 * CT + col_of<CT>(ct, lane & 15), tile0 = part * NT;
   const int64_t hsz = (int64_t)p.DK * p.DV;
   int64_t srow = sp.n;  // row of the state buffers
   if (p.sidx) {
     srow = p.sidx[sp.n];
     if (srow < 0 || srow >= p.nslots) srow = -1;
   }
-  const float* src = p.part ? p.part + ((int64_t)slot * p.H + h) * hsz
-                            : (p.S0 && srow >= 0 ? p.S0 + (srow * p.H + h) * hsz : nullptr);
+  const float* src = nullptr;
+  if (!local) src = p.part ? p.part + ((int64_t)slot * p.H + h) * hsz
+                           : (p.S0 && srow >= 0 ? p.S0 + (srow * p.H + h) * hsz : nullptr);
   f32x4 st[NT];
   state_load<W>(st, src, tile0, p.DK, p.DV, col, lane);
   const int first_chunk = sp.t0 / DCH;
+  float gall = 1.f;
   __syncthreads();
   for (int c = 0; c < nc; ++c) {
     __syncthreads();
@@ -542,45 +592,49 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
       chunk_second<W, CT, InT, OUT, 6>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
     else
       chunk_second<W, CT, InT, OUT, 7>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    if (p.snap && m < Sp::IS && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
+    if (local) gall *= tb.tile[0] * tb.tile[1] * tb.tile[2] * tb.tile[3];
+    if (!local && p.snap && m < Sp::IS && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
       const int64_t per = p.T / DCH / p.snap_chunks;  // fixed length: snapshots per sequence
       const int64_t row = (p.cu ? p.snap_first[sp.n] : sp.n * per) + (first_chunk + c + 1) / p.snap_chunks - 1;
       state_store<W>(st, p.snap + (row * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
     }
     if constexpr (NB == 1) __syncthreads();
   }
-  if (p.S && m < Sp::IS && srow >= 0 && sp.t0 + sp.len >= sp.total)
+  if (local) {
+    if (m < Sp::IS) state_store<W>(st, p.part + ((int64_t)slot * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
+    if (tid == 0 && cb == 0) p.gpart[(int64_t)slot * p.H + h] = gall;
+  } else if (p.S && m < Sp::IS && srow >= 0 && sp.t0 + sp.len >= sp.total)
     state_store<W>(st, p.S + (srow * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
 }
 
 template <int W, int CT, typename InT>
-static hipError_t launch_main_t(DecayParams p, hipStream_t s) {
+static hipError_t launch_main_t(DecayParams p, int local, hipStream_t s) {
   p.ncb = p.DV / (16 * CT);
   const int64_t grid = (int64_t)p.slots * p.H * p.ncb;
   if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX - 8) return hipErrorInvalidValue;
   p.grid = (int32_t)grid;
   const dim3 blocks((unsigned)((grid + 7) / 8 * 8));
-  if (p.o)
-    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p);
+  if (p.o && !local)
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p, local);
   else
-    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p);
+    hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, false>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p, local);
   return hipGetLastError();
 }
 template <int W, typename InT>
-static hipError_t launch_main_w(const DecayParams& p, const DecayPlan& pl, hipStream_t s) {
-  return pl.ct == 2 ? launch_main_t<W, 2, InT>(p, s) : launch_main_t<W, 1, InT>(p, s);
+static hipError_t launch_main_w(const DecayParams& p, const DecayPlan& pl, int local, hipStream_t s) {
+  switch (pl.ct) {
+    case 8: if constexpr (sizeof(InT) == 2) return launch_main_t<W, 8, InT>(p, local, s);
+    case 4: if constexpr (sizeof(InT) == 2) return launch_main_t<W, 4, InT>(p, local, s);
+    case 2: if constexpr (sizeof(InT) == 2 || W < 128) return launch_main_t<W, 2, InT>(p, local, s);
+    default: return launch_main_t<W, 1, InT>(p, local, s);
+  }
 }
 template <typename InT>
-static hipError_t launch_main(const DecayParams& p, const DecayPlan& pl, hipStream_t s) {
-  if (p.DK == 128) {
-    if constexpr (sizeof(InT) == 4)  // (two column tiles of three-term data do not fit the LDS)
-      return launch_main_t<128, 1, InT>(p, s);
-    else
-      return launch_main_w<128, InT>(p, pl, s);
-  }
-  if (p.DK == 64) return launch_main_w<64, InT>(p, pl, s);
-  return launch_main_w<32, InT>(p, pl, s);
+static hipError_t launch_main(const DecayParams& p, const DecayPlan& pl, int local, hipStream_t s) {
+  if (p.DK == 128) return launch_main_w<128, InT>(p, pl, local, s);
+  if (p.DK == 64) return launch_main_w<64, InT>(p, pl, local, s);
+  return launch_main_w<32, InT>(p, pl, local, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -814,13 +868,13 @@ hipError_t launch_decay_fwd(DecayParams p, const DecayPlan& pl, bool bf16, hipSt
     p.cu = p.cu_ok;
   }
   if (pl.nseg > 1) {
-    e = launch_decay_states(p, bf16, false, 1, s);
+    e = bf16 ? launch_main<__bf16>(p, pl, 1, s) : launch_main<float>(p, pl, 1, s);
     if (e == hipSuccess) e = launch_decay_join(p, 0, s);
     if (e != hipSuccess) return e;
   } else {
     p.part = nullptr;
   }
-  return bf16 ? launch_main<__bf16>(p, pl, s) : launch_main<float>(p, pl, s);
+  return bf16 ? launch_main<__bf16>(p, pl, 0, s) : launch_main<float>(p, pl, 0, s);
 }
 
 }  // namespace dr

@@ -131,9 +131,11 @@ int64_t env_int(const char* name) {
 dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   dr::DecayPlan pl{};
   const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads;
-  pl.ct = tiles >= 2 ? 2 : 1;
+  const bool bf16 = d->in_dtype == DR_BF16;
+  // all columns in one workgroup (fp32 data, three times as large, in one or two tiles)
+  pl.ct = bf16 ? (int)tiles : tiles >= 2 && d->head_dim_k < 128 ? 2 : 1;
   if (const int64_t c = env_int("DR_DECAY_CT"))
-    if ((c == 1 || c == 2) && c <= tiles) pl.ct = (int)c;
+    if ((c == 1 || c == 2 || c == 4 || c == 8) && c <= pl.ct) pl.ct = (int)c;
   const int64_t wide = tiles / pl.ct;  // workgroups per segment and head
   // enough segments for 512 workgroups, none shorter than 512 tokens
   int64_t seg;
