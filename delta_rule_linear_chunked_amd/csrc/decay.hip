@@ -12,6 +12,8 @@
 // index orders of the 32-deep products, see decay.hpp), so O^T comes out with 4 consecutive columns per
 // lane and the state never leaves the registers. With fewer column tiles than waves, 4 / CT waves
 // hold the same state columns and share the chunk's 16-token row tiles.
+#include <type_traits>
+
 #include "decay.hpp"
 #include "launch.hpp"
 
@@ -128,19 +130,16 @@ struct MainShape {
   static constexpr int XCH = Sp::IS > 1 ? CT * 4 * (Sp::IS - 1) * 1024 : 0;  // parts of Q S0 on their way
 };
 
-// Column tile n of V, tokens along the product (see frag_cols). Rows of 16 or 32 columns lie in order; wider ones are
-// swizzled as K is, for which the column tiles are taken in frag_chan's order (col_of).
+// Column tile n of V, tokens along the product (see frag_cols). Rows of 16 or 32 columns lie in order, wider ones are
+// swizzled as K is (four rows' 32 bytes of a tile are then in different banks as well).
 template <int CT>
 __device__ __forceinline__ bf16x8 frag_v(const unsigned char* tile, int n, int u, int lane) {
-  if constexpr (CT <= 2)
-    return frag_cols<16 * CT>(tile, 16 * n, u, lane);
-  else
-    return frag_chan<16 * CT>(tile, n >> 1, n & 1, u, lane);
-}
-// The column of lane index r (0 .. 15) of column tile n
-template <int CT>
-__device__ __forceinline__ int col_of(int n, int r) {
-  return CT <= 2 ? 16 * n + r : 32 * (n >> 1) + 8 * (r >> 2) + 4 * (n & 1) + (r & 3);
+  if constexpr (CT <= 2) return frag_cols<16 * CT>(tile, 16 * n, u, lane);
+  const int at = (16 * swz<16 * CT>(4 * (lane >> 4) + ((lane >> 2) & 3), (lane >> 1) & 1)) ^ (32 * n);
+  const unsigned char* p = tile + at + 8 * (lane & 1) + 32 * u * CT * 32;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * CT * 32));
+  return join(a, b);
 }
 
 // P = (Q K^T) . ratio of tile (R, S) as bf16 terms into LDS, rows r
@@ -181,29 +180,58 @@ __device__ __forceinline__ void score_rows(const unsigned char* buf, Op<Terms<In
     for (int i = 0; i < NP; ++i) qf[u].t[i] = frag_rows<W>(buf + i * DCH * W * 2, 16 * R, u, lane);
 }
 
-// First half of a chunk, wave WV: its part of Q S0, kept for the row tiles that it finishes, handed on for the others.
-template <int W, int CT, typename InT, int WV>
+// acc[i] += A B[i] for several i, the terms outermost: an accumulator's next MFMA then follows the others' instead
+// of waiting for its own result (32 cycles, twice an MFMA's issue time).
+template <int N, int NP>
+__device__ __forceinline__ void mma_rows(f32x4 (&acc)[N], const Tri& a, const Op<NP> (&b)[N]) {
+#pragma unroll
+  for (int sum = NP + 1 < 2 ? NP + 1 : 2; sum >= 0; --sum)
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+        if (p + q == sum) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.t[p], b[i].t[q], acc[i], 0, 0, 0);
+        }
+}
+
+// First half of a chunk, wave M of column tile ct: its part of Q S0, kept for the row tiles that it finishes, handed on for the others.
+template <int W, int CT, typename InT, int M>
 __device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x4* st, f32x4 (&oa)[Split<W, CT>::RO],
-                                            unsigned char* xch, int lane) {
+                                            unsigned char* xch, int ct, int lane) {
   using Sh = MainShape<W, CT, InT>;
   using Sp = Split<W, CT>;
-  constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
+  constexpr int NP = Sh::NP, IS = Sp::IS, PART = M % IS, REP = M / IS;
   if constexpr (REP < Sp::D) {
     f32x4 acc[Sp::RT];
+    Op<NP> qf[2][Sp::RT];
+    Tri sf[2];
+    auto load = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < Sp::RT; ++i)
+#pragma unroll
+        for (int e = 0; e < NP; ++e)
+          qf[u & 1][i].t[e] = frag_rows<W>(buf + e * Sh::QK, 16 * Sp::tile(REP, i), PART * Sp::U + u, lane);
+    };
+    auto split = [&](int u) {
+      const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
+                          st[2 * u + 1][0], st[2 * u + 1][1], st[2 * u + 1][2], st[2 * u + 1][3]};
+      sf[u & 1] = split3(x);
+    };
+    load(0);
+    fence();
+    split(0);
 #pragma unroll
     for (int i = 0; i < Sp::RT; ++i) acc[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < Sp::U; ++u) {
-      const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
-                          st[2 * u + 1][0], st[2 * u + 1][1], st[2 * u + 1][2], st[2 * u + 1][3]};
-      const Tri sf = split3(x);
-#pragma unroll
-      for (int i = 0; i < Sp::RT; ++i) {
-        Op<NP> qf;
-#pragma unroll
-        for (int e = 0; e < NP; ++e) qf.t[e] = frag_rows<W>(buf + e * Sh::QK, 16 * Sp::tile(REP, i), PART * Sp::U + u, lane);
-        mma(acc[i], sf.t, qf.t);
-      }
+      if (u + 1 < Sp::U) load(u + 1);
+      fence();
+      if (u + 1 < Sp::U) split(u + 1);
+      mma_rows<Sp::RT>(acc, sf[u & 1], qf[u & 1]);
+      fence();
     }
 #pragma unroll
     for (int i = 0; i < Sp::RT; ++i) {
@@ -211,7 +239,7 @@ __device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x
       if (owner == PART)
         oa[i % Sp::RO] = acc[i];
       else  // slot of this part among the owner's IS - 1 others
-        *reinterpret_cast<f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + (PART < owner ? PART : PART - 1)) * 64 + lane) * 16) = acc[i];
+        *reinterpret_cast<f32x4*>(xch + (((ct * 4 + R) * (IS - 1) + (PART < owner ? PART : PART - 1)) * 64 + lane) * 16) = acc[i];
     }
   }
 }
@@ -232,92 +260,185 @@ __device__ __forceinline__ void scores(const unsigned char* qbuf, const unsigned
   }
 }
 
-// Second half: the row tiles that wave WV finishes, and its channels of the state:
+// The row tile of index j among those that a part finishes (-1: none)
+template <int W, int CT>
+constexpr int own_row(int rep, int part, int j) {
+  using Sp = Split<W, CT>;
+  return j < Sp::RO && part * Sp::RO + j < Sp::RT ? Sp::tile(rep, part * Sp::RO + j) : -1;
+}
+// Steps of P V: two row tiles j, j + 1 and one half of the tokens each, as 2 j + half
+template <int W, int CT>
+constexpr int pv_step(int rep, int part, int s, bool count) {
+  int n = 0;
+  for (int j = 0; j < 4; j += 2)
+    for (int u = 0; u < 2; ++u)
+      if (own_row<W, CT>(rep, part, j) >= 2 * u || own_row<W, CT>(rep, part, j + 1) >= 2 * u) {
+        if (!count && n == s) return 2 * j + u;
+        ++n;
+      }
+  return count ? n : 0;
+}
+
+// Second half: the row tiles that wave M of column tile ct finishes, and its channels of the state:
 // S <- Gamma_C S + K^T (tail . V).
-template <int W, int CT, typename InT, bool OUT, int WV>
+template <int W, int CT, typename InT, bool OUT, int M>
 __device__ __forceinline__ void chunk_second(const unsigned char* buf, const DecayTab& tb, f32x4 (&st)[2 * Split<W, CT>::U],
                                              f32x4 (&oa)[Split<W, CT>::RO], const unsigned char* Pt,
-                                             const unsigned char* xch, float* o, int o_ts, int rows, int lane) {
+                                             const unsigned char* xch, float* o, int o_ts, int rows, int ct, int lane) {
   using Sh = MainShape<W, CT, InT>;
   using Sp = Split<W, CT>;
-  constexpr int NP = Sh::NP, CTI = WV % CT, M = WV / CT, IS = Sp::IS, PART = M % IS, REP = M / IS;
+  constexpr int NP = Sh::NP, IS = Sp::IS, PART = M % IS, REP = M / IS;
   const int g = lane >> 4, r16 = lane & 15;
-  const float G = tb.tile[0] * tb.tile[1] * tb.tile[2] * tb.tile[3];
-  Op<NP> vf[2];
-  if constexpr (OUT || !Sh::VT) {
+  constexpr bool OWN = OUT && REP < Sp::D && PART * Sp::RO < Sp::RT;  // the wave finishes row tiles
+  constexpr int NPV = OWN ? pv_step<W, CT>(REP, PART, 0, true) : 0, STEPS = NPV + Sp::U;
+  // Steps: of P V (12 reads each), then the state's tiles in pairs (8 reads each); a step's reads are issued
+  // before the products of the step before it.
+  bf16x8 fr[2][4 * NP > 6 ? 4 * NP : 6];  // P: [row tile][term]; K: [tile][half][term]
+  auto load = [&](int s) {
+    if (s < NPV) {
+      const int ju = pv_step<W, CT>(REP, PART, s, false), u = ju & 1;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_v<CT>(buf + Sh::OFF_V + i * Sh::VB, CTI, u, lane);
-  }
-  if constexpr (OUT && REP < Sp::D && PART * Sp::RO < Sp::RT) {
-    // rows past the end fall outside the descriptor and are dropped
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
-#pragma unroll
-    for (int j = 0; j < Sp::RO; ++j) {
-      const int R = Sp::tile(REP, PART * Sp::RO + j);
-      f32x4 acc = oa[j];
-#pragma unroll
-      for (int e = 0; e < IS - 1; ++e)
-        acc += *reinterpret_cast<const f32x4*>(xch + (((CTI * 4 + R) * (IS - 1) + e) * 64 + lane) * 16);
-      float gam = tb.pre[16 * R + r16];
-#pragma unroll
-      for (int t = 0; t < R; ++t) gam *= tb.tile[t];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] *= gam;
-#pragma unroll
-      for (int u = 0; u < R / 2 + 1; ++u) {
-        bf16x8 pf[3];
+      for (int i = 0; i < 2; ++i) {
+        const int R = own_row<W, CT>(REP, PART, (ju >> 1) + i);
+        if (R < 2 * u) continue;
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
           const unsigned char* at = Pt + e * Sh::PB + ((16 * R + r16) * Sh::PP + 32 * u + 4 * g) * 2;
-          pf[e] = join(*reinterpret_cast<const s16x4*>(at), *reinterpret_cast<const s16x4*>(at + 32));
+          fr[s & 1][3 * i + e] = join(*reinterpret_cast<const s16x4*>(at), *reinterpret_cast<const s16x4*>(at + 32));
         }
-        mma(acc, vf[u].t, pf);
       }
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), rsrc,
-                                             ((16 * R + r16) * o_ts + col_of<CT>(CTI, 4 * g)) * 4, 0, 0);
+    } else if (s < STEPS) {
+      const int w = s - NPV;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < NP; ++e)
+            fr[s & 1][(2 * i + u) * NP + e] = frag_chan<W>(buf + e * Sh::QK, PART * Sp::U + w, i, u, lane);
+    }
+  };
+  // reads that the first steps need
+  Op<NP> vf[2];
+  bf16x8 vt[2][3];
+  f32x4 suf[4], part[Sp::RO][IS > 1 ? IS - 1 : 1];
+  float pre[Sp::RO], P[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) P[j] = tb.tile[j];
+  if constexpr (OWN || !Sh::VT) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) vf[u].t[i] = frag_v<CT>(buf + Sh::OFF_V + i * Sh::VB, ct, u, lane);
+  }
+  if constexpr (OWN) {
+#pragma unroll
+    for (int j = 0; j < Sp::RO; ++j) {
+      const int R = Sp::tile(REP, PART * Sp::RO + j);
+      pre[j] = tb.pre[16 * R + r16];
+#pragma unroll
+      for (int e = 0; e < IS - 1; ++e)
+        part[j][e] = *reinterpret_cast<const f32x4*>(xch + (((ct * 4 + R) * (IS - 1) + e) * 64 + lane) * 16);
     }
   }
-  bf16x8 vt[2][3];
+  load(0);
+  if constexpr (Sh::VT) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    if constexpr (Sh::VT) {
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int e = 0; e < 3; ++e) vt[u][e] = frag_v<CT>(buf + Sh::OFF_T + e * Sh::VB, CTI, u, lane);
-    } else {
+      for (int e = 0; e < 3; ++e) vt[u][e] = frag_v<CT>(buf + Sh::OFF_T + e * Sh::VB, ct, u, lane);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) suf[j] = *reinterpret_cast<const f32x4*>(&tb.suf[16 * j + 4 * g]);
+  }
+  fence();
+  // Gamma . (Q S0)
+  if constexpr (OWN) {
+#pragma unroll
+    for (int j = 0; j < Sp::RO; ++j) {
+      float gam = pre[j];
+#pragma unroll
+      for (int t = 0; t < Sp::tile(REP, PART * Sp::RO + j); ++t) gam *= P[t];
+#pragma unroll
+      for (int e = 0; e < IS - 1; ++e) oa[j] += part[j][e];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) oa[j][i] *= gam;
+    }
+  }
+  auto scale = [&](int u) {  // the scaled rows of V, in registers
+    if constexpr (!Sh::VT) {
       float x[8];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         float f = 1.f;
 #pragma unroll
-        for (int j = 2 * u + a + 1; j < 4; ++j) f *= tb.tile[j];
-        const f32x4 suf = *reinterpret_cast<const f32x4*>(&tb.suf[16 * (2 * u + a) + 4 * g]);
+        for (int j = 2 * u + a + 1; j < 4; ++j) f *= P[j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float y = 0.f;
 #pragma unroll
           for (int e = NP - 1; e >= 0; --e) y += (float)vf[u].t[e][4 * a + i];
-          x[4 * a + i] = y * (suf[i] * f);
+          x[4 * a + i] = y * (suf[2 * u + a][i] * f);
         }
       }
       const Tri tr = split3(x);
 #pragma unroll
       for (int e = 0; e < 3; ++e) vt[u][e] = tr.t[e];
     }
+  };
+  const float G = P[0] * P[1] * P[2] * P[3];
+  // rows past the end fall outside the descriptor and are dropped
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
+  if constexpr (NPV == 0) {
+    scale(0);
+    scale(1);
   }
 #pragma unroll
-  for (int t = 0; t < 2 * Sp::U; ++t) {
+  for (int s = 0; s < STEPS; ++s) {
+    load(s + 1);
+    fence();
+    if (s < NPV) {
+      const int ju = pv_step<W, CT>(REP, PART, s, false), j = ju >> 1, u = ju & 1;
+      const int R0 = own_row<W, CT>(REP, PART, j), R1 = own_row<W, CT>(REP, PART, j + 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) st[t][i] *= G;
+      for (int sum = NP + 1 < 2 ? NP + 1 : 2; sum >= 0; --sum)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      Op<NP> kf;
+        for (int q = 0; q < NP; ++q) {
+          if (sum - q < 0 || sum - q > 2) continue;
+          if (R0 >= 2 * u)
+            oa[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[u].t[q], fr[s & 1][sum - q], oa[j], 0, 0, 0);
+          if (R1 >= 2 * u)
+            oa[j + 1 < Sp::RO ? j + 1 : 0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                vf[u].t[q], fr[s & 1][3 + sum - q], oa[j + 1 < Sp::RO ? j + 1 : 0], 0, 0, 0);
+        }
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
-        kf.t[i] = frag_chan<W>(buf + i * Sh::QK, PART * Sp::U + (t >> 1), t & 1, u, lane);
-      mma(st[t], kf.t, vt[u]);
+      for (int i = 0; i < 2; ++i) {
+        const int R = i ? R1 : R0;
+        if (R >= 0 && u == R / 2)  // the row tile is complete
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, oa[j + i < Sp::RO ? j + i : 0]), rsrc,
+                                                 ((16 * R + r16) * o_ts + 16 * ct + 4 * g) * 4, 0, 0);
+      }
+      if (s == 0) scale(0);
+      if (s == (NPV > 1 ? 1 : 0)) scale(1);
+    } else {
+      const int w = s - NPV;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[2 * w + i][e] *= G;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int sum = NP + 1 < 2 ? NP + 1 : 2; sum >= 0; --sum)
+#pragma unroll
+          for (int q = 0; q < NP; ++q) {
+            if (sum - q < 0 || sum - q > 2) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              st[2 * w + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[s & 1][(2 * i + u) * NP + q], vt[u][sum - q], st[2 * w + i], 0, 0, 0);
+          }
     }
+    fence();
   }
 }
 
@@ -388,6 +509,19 @@ __device__ __forceinline__ void scaled_store(const Piece<T>& x, float f, unsigne
   const Tri t = split3(z);
 #pragma unroll
   for (int e = 0; e < 3; ++e) *reinterpret_cast<bf16x8*>(at + e * plane) = t.t[e];
+}
+
+// f with the (uniform) index m < N as a compile-time constant: what a wave does is then straight code
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void by_wave(int m, const F& f) {
+  if constexpr (I == N - 1) {
+    f(std::integral_constant<int, I>{});
+  } else {
+    if (m == I)
+      f(std::integral_constant<int, I>{});
+    else
+      by_wave<N, F, I + 1>(m, f);
+  }
 }
 
 // The filling waves of a chunk step: P of the chunk in its first half; in its second half the next chunk's data from
@@ -510,14 +644,7 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
       if constexpr (OUT) {
         const unsigned char* buf = smem + (c % NB) * Sh::BUF;
         const DecayTab& tb = tabs[c % NB];
-        if (f.wave == 0)
-          scores<W, CT, InT, 0>(qbuf, buf, tb, Pt, lane);
-        else if (f.wave == 1)
-          scores<W, CT, InT, 1>(qbuf, buf, tb, Pt, lane);
-        else if (f.wave == 2)
-          scores<W, CT, InT, 2>(qbuf, buf, tb, Pt, lane);
-        else
-          scores<W, CT, InT, 3>(qbuf, buf, tb, Pt, lane);
+        by_wave<4>(f.wave, [&](auto M) { scores<W, CT, InT, M.value>(qbuf, buf, tb, Pt, lane); });
       }
       __syncthreads();
       if constexpr (NB == 1) __syncthreads();
@@ -535,7 +662,7 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
   const int64_t o_ts = (int64_t)p.H * p.DV;
   float* o = OUT ? p.o + trow * o_ts + (int64_t)h * p.DV + cb * 16 * CT : nullptr;
   // the state at the segment's start: lane's column l % 16, channels 32 u + 8 (l / 16) + 4 e + i of the wave's slices
-  const int col = cb * 16 * CT + col_of<CT>(ct, lane & 15), tile0 = part * NT;
+  const int col = cb * 16 * CT + 16 * ct + (lane & 15), tile0 = part * NT;
   const int64_t hsz = (int64_t)p.DK * p.DV;
   int64_t srow = sp.n;  // row of the state buffers
   if (p.sidx) {
@@ -557,41 +684,17 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
     const int rows = sp.len - c * DCH;
     f32x4 oa[Sp::RO];
     float* oc = OUT ? o + (int64_t)c * DCH * o_ts : nullptr;
+    // (addresses are formed anew in every chunk: kept over the loop, those of all eight waves' code would not fit
+    // the registers)
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
     if constexpr (OUT) {
-      if (wave == 0)
-        chunk_first<W, CT, InT, 0>(qbuf, st, oa, xch, lane);
-      else if (wave == 1)
-        chunk_first<W, CT, InT, 1>(qbuf, st, oa, xch, lane);
-      else if (wave == 2)
-        chunk_first<W, CT, InT, 2>(qbuf, st, oa, xch, lane);
-      else if (wave == 3)
-        chunk_first<W, CT, InT, 3>(qbuf, st, oa, xch, lane);
-      else if (wave == 4)
-        chunk_first<W, CT, InT, 4>(qbuf, st, oa, xch, lane);
-      else if (wave == 5)
-        chunk_first<W, CT, InT, 5>(qbuf, st, oa, xch, lane);
-      else if (wave == 6)
-        chunk_first<W, CT, InT, 6>(qbuf, st, oa, xch, lane);
-      else
-        chunk_first<W, CT, InT, 7>(qbuf, st, oa, xch, lane);
+      by_wave<Sp::G>(m, [&](auto M) { chunk_first<W, CT, InT, M.value>(qbuf, st, oa, xch, ct, ln); });
     }
     __syncthreads();
-    if (wave == 0)
-      chunk_second<W, CT, InT, OUT, 0>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else if (wave == 1)
-      chunk_second<W, CT, InT, OUT, 1>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else if (wave == 2)
-      chunk_second<W, CT, InT, OUT, 2>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else if (wave == 3)
-      chunk_second<W, CT, InT, OUT, 3>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else if (wave == 4)
-      chunk_second<W, CT, InT, OUT, 4>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else if (wave == 5)
-      chunk_second<W, CT, InT, OUT, 5>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else if (wave == 6)
-      chunk_second<W, CT, InT, OUT, 6>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
-    else
-      chunk_second<W, CT, InT, OUT, 7>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, lane);
+    by_wave<Sp::G>(m, [&](auto M) {
+      chunk_second<W, CT, InT, OUT, M.value>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, ct, ln);
+    });
     if (local) gall *= tb.tile[0] * tb.tile[1] * tb.tile[2] * tb.tile[3];
     if (!local && p.snap && m < Sp::IS && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
       const int64_t per = p.T / DCH / p.snap_chunks;  // fixed length: snapshots per sequence

@@ -140,6 +140,9 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
         if (p + q == sum) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], b[q], acc, 0, 0, 0);
 }
 
+// Nothing moves across (the scheduler otherwise sinks every LDS read to its use, and each then waits in full)
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // The wait between an MFMA and the first use of its result behind a branch, which the compiler does not always
 // leave (seen in its output: 3 or 7 instead of 8 cycles where the two stand in different blocks).
 __device__ __forceinline__ void settle(f32x4& acc) { asm volatile("s_nop 7" : "+v"(acc)); }
@@ -158,10 +161,13 @@ __device__ __forceinline__ int swz(int row, int piece) {
   return row * 4 + (piece ^ h);
 }
 
-// Fragment with token rows on the lanes: row row0 + l % 16, channels 32 u + 8 (l / 16) .. + 7.
+// Fragment with token rows on the lanes: row row0 + l % 16 (row0 a multiple of 16), channels 32 u + 8 (l / 16) .. + 7.
+// (The address is one lane term, an exclusive or with 64 u and constants: spelled out because the compiler
+// otherwise keeps an address register for every fragment of a loop, and spills.)
 template <int W>
 __device__ __forceinline__ bf16x8 frag_rows(const unsigned char* tile, int row0, int u, int lane) {
-  return *reinterpret_cast<const bf16x8*>(tile + 16 * swz<W>(row0 + (lane & 15), 4 * u + (lane >> 4)));
+  const int at = (16 * swz<W>(lane & 15, lane >> 4)) ^ (64 * u);
+  return *reinterpret_cast<const bf16x8*>(tile + at + row0 * W * 2);
 }
 __device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
   union {
@@ -180,10 +186,10 @@ __device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
 // eight consecutive channels of a fragment along the channels.
 template <int W>
 __device__ __forceinline__ bf16x8 frag_chan(const unsigned char* tile, int w, int e, int u, int lane) {
-  const int g = lane >> 4, p = lane & 15;
-  const int r = 32 * u + 4 * g + (p >> 2), piece = 4 * w + (p & 3);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + 16 * swz<W>(r, piece) + 8 * e));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + 16 * swz<W>(r + 16, piece) + 8 * e));
+  const int at = (16 * swz<W>(4 * (lane >> 4) + ((lane >> 2) & 3), lane & 3)) ^ (64 * w);
+  const unsigned char* p = tile + at + 32 * u * W * 2 + 8 * e;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * W * 2));
   return join(a, b);
 }
 // The same for a tile with rows of CW elements in order, no swizzle: lane l's column is n0 + l % 16.
