@@ -587,10 +587,8 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
   __shared__ __align__(16) unsigned char xch[OUT && Sh::XCH ? Sh::XCH : 16];
   __shared__ __align__(16) DecayTab tabs[NB];
   __shared__ float ring[2][4][DCH];
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  if (id >= p.grid) return;
-  const int cb = id % p.ncb, sh = id / p.ncb;
-  const int h = sh % p.H, slot = sh / p.H;
+  int cb, h, slot;
+  if (!work_of(p, cb, h, slot)) return;
   const Span sp = slot_span(p, slot);
   if (sp.n < 0) return;
   // local: a segment's own contribution; nothing comes behind a sequence's last segment
@@ -713,11 +711,10 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
 template <int W, int CT, typename InT>
 static hipError_t launch_main_t(DecayParams p, int local, hipStream_t s) {
   p.ncb = p.DV / (16 * CT);
-  const int64_t grid = (int64_t)p.slots * p.H * p.ncb;
+  const int64_t grid = work_grid(p);
   if (grid == 0) return hipSuccess;
-  if (grid > INT32_MAX - 8) return hipErrorInvalidValue;
-  p.grid = (int32_t)grid;
-  const dim3 blocks((unsigned)((grid + 7) / 8 * 8));
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 blocks((unsigned)grid);
   if (p.o && !local)
     hipLaunchKernelGGL((decay_main_kernel<W, CT, InT, true>), blocks, dim3(64 * (MAIN_WAVES + FILL_WAVES)), 0, s, p, local);
   else
@@ -757,10 +754,8 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
   constexpr int NB = NPX == 1 ? 2 : 1;
   __shared__ __align__(16) unsigned char smem[NB * BUF];
   __shared__ float s_gam[NB];
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  if (id >= p.grid) return;
-  const int cb = id % p.ncb, sh = id / p.ncb;
-  const int h = sh % p.H, slot = sh / p.H;
+  int cb, h, slot;
+  if (!work_of(p, cb, h, slot)) return;
   const Span sp = slot_span(p, slot);
   if (sp.n < 0) return;
   // nothing comes behind the last segment (before the first, in reverse)
@@ -925,12 +920,10 @@ __global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p, in
 template <int W, int CT, int DC, typename XT, typename YT, bool REV>
 static hipError_t launch_state_t(DecayParams p, int local, hipStream_t s) {
   p.ncb = p.DV / (16 * CT);
-  const int64_t grid = (int64_t)p.slots * p.H * p.ncb;
+  const int64_t grid = work_grid(p);
   if (grid == 0) return hipSuccess;
-  if (grid > INT32_MAX - 8) return hipErrorInvalidValue;
-  p.grid = (int32_t)grid;
-  hipLaunchKernelGGL((decay_state_kernel<W, CT, DC, XT, YT, REV>), dim3((unsigned)((grid + 7) / 8 * 8)), dim3(256), 0, s, p,
-                     local);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((decay_state_kernel<W, CT, DC, XT, YT, REV>), dim3((unsigned)grid), dim3(256), 0, s, p, local);
   return hipGetLastError();
 }
 template <int W, int DC, typename XT, typename YT, bool REV>

@@ -247,6 +247,21 @@ __device__ __forceinline__ void decay_table(DecayTab& t, int w, float a, int lan
   }
 }
 
+// Workgroups of a launch over slots, heads and column blocks. Those of one (slot, query/key head) read the same keys and
+// queries: they take consecutive places on one XCD (workgroups go round-robin over the eight), and the
+// (slot, query/key head) pairs are dealt over the XCDs in turn, so that unused slots, the last ones, leave none idle.
+__host__ __device__ __forceinline__ int64_t work_grid(const DecayParams& p) {
+  return ((int64_t)p.slots * p.Hk + 7) / 8 * 8 * (p.H / p.Hk * p.ncb);
+}
+__device__ __forceinline__ bool work_of(const DecayParams& p, int& cb, int& h, int& slot) {
+  const int per = p.H / p.Hk * p.ncb, b = blockIdx.x / 8;
+  const int unit = b / per * 8 + blockIdx.x % 8, in = b % per;
+  slot = unit / p.Hk;
+  cb = in % p.ncb;
+  h = (unit - slot * p.Hk) * (p.H / p.Hk) + in / p.ncb;
+  return slot < p.slots;
+}
+
 // One slot's sequence and token span.
 struct Span {
   int n;         // sequence (-1: unused slot)

@@ -127,33 +127,45 @@ int64_t env_int(const char* name) {
   return e ? atoll(e) : 0;
 }
 
-// Segments and column blocks (the same for the forward and for the backward's state passes).
-dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
+// Segments and column blocks. A workgroup of the main pass fills a CU and carries one segment of one head; a
+// segment's own state, needed when a sequence has more than one, costs it 0.42 of the main pass again (40 and 95 us on
+// 4 x 4096 tokens, 16 heads, d = 128 in segments of 1024). Of the segment lengths from 512 tokens up the one with
+// the least (rounds of 256 workgroups) x (tokens of a segment + 192) x (1 or 1.42) is taken: for that problem 1024 tokens,
+// 131 us (512: 152, 2048: 212, whole sequences 268).
+dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed) {
   dr::DecayPlan pl{};
-  const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads;
+  const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads, T = d->seqlen;
   const bool bf16 = d->in_dtype == DR_BF16;
   // all columns in one workgroup (fp32 data, three times as large, in one or two tiles)
-  pl.ct = bf16 ? (int)tiles : tiles >= 2 && d->head_dim_k < 128 ? 2 : 1;
-  if (const int64_t c = env_int("DR_DECAY_CT"))
-    if ((c == 1 || c == 2 || c == 4 || c == 8) && c <= pl.ct) pl.ct = (int)c;
-  const int64_t wide = tiles / pl.ct;  // workgroups per segment and head
-  // enough segments for 512 workgroups, none shorter than 512 tokens
-  int64_t seg;
-  if (packed) {
-    seg = d->seqlen * d->num_heads * wide / 512;
-  } else {
-    const int64_t have = pairs * wide;
-    const int64_t want = have >= 256 || have == 0 ? 1 : (512 + have - 1) / have;
-    seg = (d->seqlen + want - 1) / want;
+  const int most = bf16 ? (int)tiles : tiles >= 2 && d->head_dim_k < 128 ? 2 : 1;
+  const int64_t blocks = tiles / most;
+  int64_t seg = (T + 63) / 64 * 64;
+  double best = 0;
+  for (int64_t n = 1; n == 1 || n * 512 <= T; ++n) {
+    const int64_t s = ((T + n - 1) / n + 63) / 64 * 64, nseg = s > 0 ? (T + s - 1) / s : 1;
+    // (packed lengths are not known here: half a segment per sequence for their ragged ends)
+    const double wgs = (packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg) * d->num_heads * blocks;
+    // (uneven segments fill a last round's gaps; 192 tokens' time for a workgroup's start and end)
+    const double rounds = wgs <= 256 ? 1 : packed || wgs > 8192 ? wgs / 256 + 0.5 : (double)(int64_t)((wgs + 255) / 256);
+    const double cost = rounds * (s + 192) * (nseg > 1 ? 1.42 : 1.0);
+    if (best == 0 || cost < best) {
+      best = cost;
+      seg = s;
+    }
   }
-  if (seg < 512) seg = 512;
   if (const int64_t s = env_int("DR_DECAY_SEG"))
-    if (s > 0) seg = s;
-  seg = (seg + 63) / 64 * 64;
-  pl.nseg = (d->seqlen + seg - 1) / seg;
-  if (pl.nseg < 1) pl.nseg = 1;
+    if (s > 0) seg = (s + 63) / 64 * 64;
+  if (seg < 64) seg = 64;
   pl.seg = seg;
-  pl.slots = packed ? d->seqlen / seg + d->num_seqs : d->num_seqs * pl.nseg;
+  pl.nseg = (T + seg - 1) / seg;
+  if (pl.nseg < 1) pl.nseg = 1;
+  pl.slots = packed ? T / seg + d->num_seqs : d->num_seqs * pl.nseg;
+  // fewer columns per workgroup while that still finds idle CUs (a chunk of 16, 32 or 128 columns takes 1.9, 2.6 and 4.2 us)
+  pl.ct = most;
+  const int64_t heads = packed ? (T / seg + 1) * d->num_heads : pairs * pl.nseg;
+  while (pl.ct > 1 && heads * (tiles / pl.ct) < 256 && heads * (tiles / pl.ct) * 2 <= 256) pl.ct /= 2;
+  if (const int64_t c = env_int("DR_DECAY_CT"))
+    if ((c == 1 || c == 2 || c == 4 || c == 8) && c <= most) pl.ct = (int)c;
   return pl;
 }
 
@@ -189,7 +201,7 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
   if (st) return st;
   if (dims->num_seqs == 0) return DR_OK;
   const bool packed = cu_seqlens != nullptr;
-  const dr::DecayPlan pl = plan_decay(dims, packed, false);
+  const dr::DecayPlan pl = plan_decay(dims, packed);
   dr::DecayParams p{};
   set_dims(p, dims);
   p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.cu = cu_seqlens; p.o = o; p.S = S_T;
@@ -283,7 +295,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   if (st) return st;
   const bool packed = cu_seqlens != nullptr, bf16 = dims->in_dtype == DR_BF16;
   if (N == 0 && !per_head) return DR_OK;
-  const dr::DecayPlan pl = plan_decay(dims, packed, true);
+  const dr::DecayPlan pl = plan_decay(dims, packed);
   const int64_t chunk = dr::decay_bwd_chunk(bf16);
   const int64_t cslots = packed ? dims->seqlen / chunk + N : N * ((dims->seqlen + chunk - 1) / chunk);
   if (pl.slots * H * (dims->head_dim_v / 16) > INT32_MAX - 8 || cslots * H > INT32_MAX - 8 || pl.seg > INT32_MAX ||
