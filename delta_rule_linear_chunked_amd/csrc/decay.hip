@@ -180,23 +180,6 @@ __device__ __forceinline__ void score_rows(const unsigned char* buf, Op<Terms<In
     for (int i = 0; i < NP; ++i) qf[u].t[i] = frag_rows<W>(buf + i * DCH * W * 2, 16 * R, u, lane);
 }
 
-// acc[i] += A B[i] for several i, the terms outermost: an accumulator's next MFMA then follows the others' instead
-// of waiting for its own result (32 cycles, twice an MFMA's issue time).
-template <int N, int NP>
-__device__ __forceinline__ void mma_rows(f32x4 (&acc)[N], const Tri& a, const Op<NP> (&b)[N]) {
-#pragma unroll
-  for (int sum = NP + 1 < 2 ? NP + 1 : 2; sum >= 0; --sum)
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-#pragma unroll
-      for (int q = 0; q < NP; ++q)
-        if (p + q == sum) {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.t[p], b[i].t[q], acc[i], 0, 0, 0);
-        }
-}
-
 // First half of a chunk, wave M of column tile ct: its part of Q S0, kept for the row tiles that it finishes, handed on for the others.
 template <int W, int CT, typename InT, int M>
 __device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x4* st, f32x4 (&oa)[Split<W, CT>::RO],
@@ -206,14 +189,14 @@ __device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x
   constexpr int NP = Sh::NP, IS = Sp::IS, PART = M % IS, REP = M / IS;
   if constexpr (REP < Sp::D) {
     f32x4 acc[Sp::RT];
-    Op<NP> qf[2][Sp::RT];
+    bf16x8 qf[2][Sp::RT][NP];
     Tri sf[2];
     auto load = [&](int u) {
 #pragma unroll
       for (int i = 0; i < Sp::RT; ++i)
 #pragma unroll
         for (int e = 0; e < NP; ++e)
-          qf[u & 1][i].t[e] = frag_rows<W>(buf + e * Sh::QK, 16 * Sp::tile(REP, i), PART * Sp::U + u, lane);
+          qf[u & 1][i][e] = frag_rows<W>(buf + e * Sh::QK, 16 * Sp::tile(REP, i), PART * Sp::U + u, lane);
     };
     auto split = [&](int u) {
       const float x[8] = {st[2 * u][0],     st[2 * u][1],     st[2 * u][2],     st[2 * u][3],
@@ -230,7 +213,7 @@ __device__ __forceinline__ void chunk_first(const unsigned char* buf, const f32x
       if (u + 1 < Sp::U) load(u + 1);
       fence();
       if (u + 1 < Sp::U) split(u + 1);
-      mma_rows<Sp::RT>(acc, sf[u & 1], qf[u & 1]);
+      mma_rows(acc, sf[u & 1].t, qf[u & 1]);
       fence();
     }
 #pragma unroll

@@ -140,6 +140,22 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
         if (p + q == sum) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], b[q], acc, 0, 0, 0);
 }
 
+// acc[i] += A B[i] for several i, the terms outermost: an accumulator's next MFMA then follows the others' instead
+// of waiting for its own result (32 cycles, twice an MFMA's issue time).
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma_rows(f32x4 (&acc)[N], const bf16x8 (&a)[NA], const bf16x8 (&b)[N][NB]) {
+#pragma unroll
+  for (int sum = NA + NB - 2 < 2 ? NA + NB - 2 : 2; sum >= 0; --sum)
+#pragma unroll
+    for (int p = 0; p < NA; ++p)
+#pragma unroll
+      for (int q = 0; q < NB; ++q)
+        if (p + q == sum) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], b[i][q], acc[i], 0, 0, 0);
+        }
+}
+
 // Nothing moves across (the scheduler otherwise sinks every LDS read to its use, and each then waits in full)
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 

@@ -147,9 +147,10 @@ __device__ __forceinline__ void grad_rows(unsigned char* sm, const DecayTab& tb,
 }
 
 template <int W, int V, typename InT, int DC>
-__global__ __launch_bounds__(256) void decay_grad_kernel(const DecayParams p) {
+__global__ __launch_bounds__(512) void decay_grad_kernel(const DecayParams p) {
   using Sh = GradShape<W, V, InT, DC>;
-  constexpr int NP = Sh::NP, NT = DC / 16, NU = DC / 32, UW = W / 32, UV = V / 32;
+  constexpr int NP = Sh::NP, NT = DC / 16, NU = DC / 32, UW = W / 32, UV = V / 32, NTH = 512;
+  constexpr int NIT = W / 16, TI = NIT >= 4 ? NIT / 4 : 1, NVT = V / 16, TV = NVT >= 4 ? NVT / 4 : 1;
   __shared__ __align__(16) unsigned char sm[Sh::BYTES];
   __shared__ __align__(16) DecayTab tb;
   __shared__ float s_x[4][DC], s_y[4][DC], s_da[4][DC], s_z[4];
@@ -184,22 +185,59 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(const DecayParams p) {
   const float* S = p.cs + ((int64_t)cslot * p.H + h) * hsz;
   const float* G = p.ds + ((int64_t)cslot * p.H + h) * hsz;
   const int64_t o_ts = (int64_t)p.H * p.DV;
+  const bool second = wave >= 4;  // waves 0-3: P, E and the path sums, then dV; waves 4-7: dQ and dK
+  const int rw = wave & 3;
+
+  // rows of S and G as operands along the value columns (dQ, dK): channel as frag_chan has it
+  auto load_sg = [&](int ti, int u, float (&sx)[8], float (&gx)[8]) {
+    const int it = rw * TI + ti, ch = 32 * (it >> 1) + 8 * (r16 >> 2) + 4 * (it & 1) + (r16 & 3), nn = 32 * u + 8 * g;
+    const bool ok = (W > 32 || ch < p.DK) && (V > 32 || nn < p.DV);
+    const int at = ok ? ch * p.DV + nn : 0;
+    load8(S + at, sx);
+    load8(G + at, gx);
+    if (W == 32 || V == 32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sx[j] = ok ? sx[j] : 0.f;
+        gx[j] = ok ? gx[j] : 0.f;
+      }
+    }
+  };
+  // columns of G as operands along the channels (dV)
+  auto load_g = [&](int tv, int u, float (&gx)[8]) {
+    const int vt = rw * TV + tv, col = 32 * (vt >> 1) + 8 * (r16 >> 2) + 4 * (vt & 1) + (r16 & 3);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int ch = 32 * u + 8 * g + j;
+      const bool ok = (W > 32 || ch < p.DK) && (V > 32 || col < p.DV);
+      gx[j] = G[ok ? ch * p.DV + col : 0];
+      if (W == 32 || V == 32) gx[j] = ok ? gx[j] : 0.f;
+    }
+  };
+  // the first tile's rows of S and G are on their way while the inputs go to LDS
+  float sx[UV][8], gx[UV][8];
   {
-    Stage<W, InT, DC> sq, sk;
-    Stage<V, InT, DC> sv;
-    Stage<V, float, DC> so;
+    Stage<W, InT, DC, true, NTH> sq, sk;
+    Stage<V, InT, DC, true, NTH> sv;
+    Stage<V, float, DC, true, NTH> so;
     sq.init(p.q_ts, p.DK, tid);
     sk.init(p.k_ts, p.DK, tid);
     sv.init(p.v_ts, p.DV, tid);
     so.init(o_ts, p.DV, tid);
+    const int t = 16 * rw + r16;
+    float a = p.alpha[(p.a_tok ? (trow + (t < len ? t : len - 1)) * p.H : 0) + h];
     sq.load(static_cast<const InT*>(p.q) + b * p.q_bs + row0 * p.q_ts + (int64_t)hk * p.DK, p.q_ts, len);
     sk.load(static_cast<const InT*>(p.k) + b * p.k_bs + row0 * p.k_ts + (int64_t)hk * p.DK, p.k_ts, len);
     sv.load(static_cast<const InT*>(p.v) + b * p.v_bs + row0 * p.v_ts + (int64_t)h * p.DV, p.v_ts, len);
     so.load(p.dO + trow * o_ts + (int64_t)h * p.DV, o_ts, len);
-    const int t = 16 * wave + r16;
-    float a = p.alpha[(p.a_tok ? (trow + (t < len ? t : len - 1)) * p.H : 0) + h];
+    fence();
+    if (second && rw * TI < NIT) {
+#pragma unroll
+      for (int u = 0; u < UV; ++u) load_sg(0, u, sx[u], gx[u]);
+    }
+    fence();
     if (t >= len) a = 1.f;
-    decay_table(tb, wave, a, lane);
+    if (!second) decay_table(tb, rw, a, lane);
     sq.store(sm, Sh::QK, len, p.DK, tid);
     sk.store(sm + Sh::OFF_K, Sh::QK, len, p.DK, tid);
     sv.store(sm + Sh::OFF_V, Sh::VO, len, p.DV, tid);
@@ -217,203 +255,211 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(const DecayParams p) {
   for (int i = 0; i < 4; ++i) PT[i] = tb.tile[i];
   const unsigned char *Qt = sm, *Kt = sm + Sh::OFF_K, *Vt = sm + Sh::OFF_V, *Ot = sm + Sh::OFF_O;
 
-  // ---- A: wave w, rows of tile w: P and E into LDS, the path sums of the decay's gradient
-  if (wave == 0)
-    grad_rows<W, V, InT, DC, 0>(sm, tb, PT, s_da[0], lane);
-  else if (wave == 1)
-    grad_rows<W, V, InT, DC, 1>(sm, tb, PT, s_da[1], lane);
-  if constexpr (NT == 4) {
-    if (wave == 2)
-      grad_rows<W, V, InT, DC, 2>(sm, tb, PT, s_da[2], lane);
-    else if (wave == 3)
-      grad_rows<W, V, InT, DC, 3>(sm, tb, PT, s_da[3], lane);
-  }
-  __syncthreads();
-
-  // ---- B: wave w, its channel tiles of dQ and dK
-  constexpr int NIT = W / 16, TI = NIT >= 4 ? NIT / 4 : 1;
-  float xs[NT], ys[NT], z = 0.f;
+  if (!second) {
+    // ---- P and E into LDS, the path sums of the decay's gradient: wave w, rows of tile w
+    if (wave == 0)
+      grad_rows<W, V, InT, DC, 0>(sm, tb, PT, s_da[0], lane);
+    else if (wave == 1)
+      grad_rows<W, V, InT, DC, 1>(sm, tb, PT, s_da[1], lane);
+    if constexpr (NT == 4) {
+      if (wave == 2)
+        grad_rows<W, V, InT, DC, 2>(sm, tb, PT, s_da[2], lane);
+      else if (wave == 3)
+        grad_rows<W, V, InT, DC, 3>(sm, tb, PT, s_da[3], lane);
+    }
+    // ---- dV, the wave's value-column tiles: tail . (K G), then P^T dO
+    f32x4 av[TV][NT];
+    if (rw * TV < NVT) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xs[i] = ys[i] = 0.f;
-  if (wave * TI < NIT) {
+      for (int tv = 0; tv < TV; ++tv) {
 #pragma unroll
-    for (int ti = 0; ti < TI; ++ti) {
-      const int it = wave * TI + ti, w2 = it >> 1, e2 = it & 1;
-      // lane's operand row r16: channel as frag_chan has it
-      const int ch = 32 * w2 + 8 * (r16 >> 2) + 4 * e2 + (r16 & 3);
-      f32x4 aq[NT], ak[NT];
+        for (int r = 0; r < NT; ++r) av[tv][r] = f32x4{0, 0, 0, 0};
+        float gc[UW][8];
 #pragma unroll
-      for (int r = 0; r < NT; ++r) aq[r] = ak[r] = f32x4{0, 0, 0, 0};
+        for (int u = 0; u < UW; ++u) load_g(tv, u, gc[u]);
+        fence();
 #pragma unroll
-      for (int u = 0; u < UV; ++u) {
-        float sx[8], gx[8];
-        const int nn = 32 * u + 8 * g;
-        const bool ok = (W > 32 || ch < p.DK) && (V > 32 || nn < p.DV);
-        const int64_t at = ok ? (int64_t)ch * p.DV + nn : 0;
-        load8(S + at, sx);
-        load8(G + at, gx);
-        if (!ok) {
+        for (int u = 0; u < UW; ++u) {
+          const Tri gf = split3(gc[u]);
+          bf16x8 kf[NT][NP];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sx[j] = gx[j] = 0.f;
+          for (int r = 0; r < NT; ++r)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) kf[r][i] = frag_rows<W>(Kt + i * Sh::QK, 16 * r, u, lane);
+          mma_rows(av[tv], gf.t, kf);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z = fmaf(sx[j], gx[j], z);
-        const Tri sf = split3(sx), gf = split3(gx);
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
-          bf16x8 of[3];
-          Op<NP> vf;
+          float tail = tb.suf[16 * r + r16];
 #pragma unroll
-          for (int i = 0; i < 3; ++i) of[i] = frag_rows<V>(Ot + i * Sh::VO, 16 * r, u, lane);
+          for (int j = r + 1; j < NT; ++j) tail *= PT[j];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) vf.t[i] = frag_rows<V>(Vt + i * Sh::VO, 16 * r, u, lane);
-          mma(aq[r], sf.t, of);
-          mma(ak[r], gf.t, vf.t);
+          for (int i = 0; i < 4; ++i) av[tv][r][i] *= tail;
         }
       }
-      // X_r, Y_s from these channels, then the chunk's ends
-      const int oc = 32 * w2 + 8 * g + 4 * e2;  // the lane's 4 output channels
+    }
+    __syncthreads();
+    if (rw * TV < NVT) {
 #pragma unroll
-      for (int r = 0; r < NT; ++r) {
-        const int row = 16 * r + r16, at = 16 * swz<W>(row, oc >> 3) + 2 * (oc & 7);
-        float gam = tb.pre[row], tail = tb.suf[row];
+      for (int tv = 0; tv < TV; ++tv) {
+        const int vt = rw * TV + tv, w2 = vt >> 1, e2 = vt & 1;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j < r) gam *= PT[j];
-          if (j > r) tail *= PT[j];
+        for (int u = 0; u < NU; ++u) {
+          bf16x8 of[3];
+#pragma unroll
+          for (int e = 0; e < 3; ++e) of[e] = frag_chan<V>(Ot + e * Sh::VO, w2, e2, u, lane);
+#pragma unroll
+          for (int r = 0; r < NT; ++r) {
+            if (r <= 2 * u + 1) {
+              bf16x8 pf[3];
+#pragma unroll
+              for (int e = 0; e < 3; ++e) pf[e] = frag_cols<Sh::EP>(sm + Sh::OFF_P + e * Sh::EB, 16 * r, u, lane);
+              mma(av[tv][r], of, pf);
+            }
+          }
+        }
+        const int oc = 32 * w2 + 8 * g + 4 * e2;
+#pragma unroll
+        for (int r = 0; r < NT; ++r) settle(av[tv][r]);
+        if (V > 32 || oc < p.DV) {
+#pragma unroll
+          for (int r = 0; r < NT; ++r) {
+            const int row = 16 * r + r16;
+            if (row < len) *reinterpret_cast<f32x4*>(p.dv + (trow + row) * o_ts + (int64_t)h * p.DV + oc) = av[tv][r];
+          }
+        }
+      }
+    }
+  } else {
+    // ---- dQ and dK, the wave's channel tiles: Gamma . (dO S^T) and tail . (V G^T), then E K and E^T Q
+    float xs[NT], ys[NT], z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) xs[i] = ys[i] = 0.f;
+    f32x4 aq[TI][NT], ak[TI][NT];
+    if (rw * TI < NIT) {
+#pragma unroll
+      for (int ti = 0; ti < TI; ++ti) {
+        const int it = rw * TI + ti, w2 = it >> 1, e2 = it & 1;
+        if (ti > 0) {
+#pragma unroll
+          for (int u = 0; u < UV; ++u) load_sg(ti, u, sx[u], gx[u]);
+          fence();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float qv = 0.f, kv = 0.f;
+        for (int r = 0; r < NT; ++r) aq[ti][r] = ak[ti][r] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < UV; ++u) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z = fmaf(sx[u][j], gx[u][j], z);
+          const Tri sf = split3(sx[u]), gf = split3(gx[u]);
+          bf16x8 of[NT][3], vf[NT][NP];
+#pragma unroll
+          for (int r = 0; r < NT; ++r) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) of[r][i] = frag_rows<V>(Ot + i * Sh::VO, 16 * r, u, lane);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) vf[r][i] = frag_rows<V>(Vt + i * Sh::VO, 16 * r, u, lane);
+          }
+          mma_rows(aq[ti], sf.t, of);
+          mma_rows(ak[ti], gf.t, vf);
+        }
+        // X_r, Y_s from these channels, then the chunk's ends
+        const int oc = 32 * w2 + 8 * g + 4 * e2;  // the lane's 4 output channels
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+          const int row = 16 * r + r16, at = 16 * swz<W>(row, oc >> 3) + 2 * (oc & 7);
+          float gam = tb.pre[row], tail = tb.suf[row];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (j < r) gam *= PT[j];
+            if (j > r) tail *= PT[j];
+          }
+          float qv[4] = {0.f, 0.f, 0.f, 0.f}, kv[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int e = NP - 1; e >= 0; --e) {
-            qv += (float)*reinterpret_cast<const __bf16*>(Qt + e * Sh::QK + at + 2 * i);
-            kv += (float)*reinterpret_cast<const __bf16*>(Kt + e * Sh::QK + at + 2 * i);
-          }
-          xs[r] = fmaf(qv, aq[r][i], xs[r]);
-          ys[r] = fmaf(kv, ak[r][i], ys[r]);
-          aq[r][i] *= gam;
-          ak[r][i] *= tail;
-        }
-      }
-      // E K and E^T Q
+            const bf16x4 q4 = *reinterpret_cast<const bf16x4*>(Qt + e * Sh::QK + at);
+            const bf16x4 k4 = *reinterpret_cast<const bf16x4*>(Kt + e * Sh::QK + at);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        Op<NP> kf, qf;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          kf.t[i] = frag_chan<W>(Kt + i * Sh::QK, w2, e2, u, lane);
-          qf.t[i] = frag_chan<W>(Qt + i * Sh::QK, w2, e2, u, lane);
-        }
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          if (r >= 2 * u) {  // tokens s of half u reach row tile r
-            bf16x8 ef[3];
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-              const unsigned char* at = sm + Sh::OFF_E + e * Sh::EB + ((16 * r + r16) * Sh::EP + 32 * u + 4 * g) * 2;
-              ef[e] = join(*reinterpret_cast<const s16x4*>(at), *reinterpret_cast<const s16x4*>(at + 32));
+            for (int i = 0; i < 4; ++i) {
+              qv[i] += (float)q4[i];
+              kv[i] += (float)k4[i];
             }
-            mma(aq[r], kf.t, ef);
           }
-          if (r <= 2 * u + 1) {  // rows r' of half u reach token tile r
-            bf16x8 ef[3];
 #pragma unroll
-            for (int e = 0; e < 3; ++e) ef[e] = frag_cols<Sh::EP>(sm + Sh::OFF_E + e * Sh::EB, 16 * r, u, lane);
-            mma(ak[r], qf.t, ef);
-          }
-        }
-      }
-      const int heads = p.dq_heads;  // heads of the buffers: Hk, or H for the partial sums of shared heads
-      const int hq = heads == p.H ? h : hk;
-      if (W > 32 || oc < p.DK) {
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          const int row = 16 * r + r16;
-          if (row < len) {
-            const int64_t at = ((trow + row) * heads + hq) * p.DK + oc;
-            *reinterpret_cast<f32x4*>(p.dq + at) = aq[r];
-            *reinterpret_cast<f32x4*>(p.dk + at) = ak[r];
+          for (int i = 0; i < 4; ++i) {
+            xs[r] = fmaf(qv[i], aq[ti][r][i], xs[r]);
+            ys[r] = fmaf(kv[i], ak[ti][r][i], ys[r]);
+            aq[ti][r][i] *= gam;
+            ak[ti][r][i] *= tail;
           }
         }
       }
     }
+    __syncthreads();
+    if (rw * TI < NIT) {
 #pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      xs[r] += __shfl_xor(xs[r], 16);
-      xs[r] += __shfl_xor(xs[r], 32);
-      ys[r] += __shfl_xor(ys[r], 16);
-      ys[r] += __shfl_xor(ys[r], 32);
-      if (g == 0) {
-        s_x[wave][16 * r + r16] = xs[r];
-        s_y[wave][16 * r + r16] = ys[r];
-      }
-    }
+      for (int ti = 0; ti < TI; ++ti) {
+        const int it = rw * TI + ti, w2 = it >> 1, e2 = it & 1, oc = 32 * w2 + 8 * g + 4 * e2;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) z += __shfl_xor(z, d);
-    if (lane == 0) s_z[wave] = z;
-  }
-
-  // ---- C: wave w, its value-column tiles of dV
-  constexpr int NVT = V / 16, TV = NVT >= 4 ? NVT / 4 : 1;
-  if (wave * TV < NVT) {
+        for (int u = 0; u < NU; ++u) {
+          Op<NP> kf, qf;
 #pragma unroll
-    for (int tv = 0; tv < TV; ++tv) {
-      const int vt = wave * TV + tv, w2 = vt >> 1, e2 = vt & 1;
-      const int col = 32 * w2 + 8 * (r16 >> 2) + 4 * e2 + (r16 & 3);
-      f32x4 av[NT];
+          for (int i = 0; i < NP; ++i) {
+            kf.t[i] = frag_chan<W>(Kt + i * Sh::QK, w2, e2, u, lane);
+            qf.t[i] = frag_chan<W>(Qt + i * Sh::QK, w2, e2, u, lane);
+          }
 #pragma unroll
-      for (int r = 0; r < NT; ++r) av[r] = f32x4{0, 0, 0, 0};
+          for (int r = 0; r < NT; ++r) {
+            if (r >= 2 * u) {  // tokens s of half u reach row tile r
+              bf16x8 ef[3];
 #pragma unroll
-      for (int u = 0; u < UW; ++u) {
-        float gx[8];
+              for (int e = 0; e < 3; ++e) {
+                const unsigned char* at = sm + Sh::OFF_E + e * Sh::EB + ((16 * r + r16) * Sh::EP + 32 * u + 4 * g) * 2;
+                ef[e] = join(*reinterpret_cast<const s16x4*>(at), *reinterpret_cast<const s16x4*>(at + 32));
+              }
+              mma(aq[ti][r], kf.t, ef);
+            }
+            if (r <= 2 * u + 1) {  // rows r' of half u reach token tile r
+              bf16x8 ef[3];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int ch = 32 * u + 8 * g + j;
-          const bool ok = (W > 32 || ch < p.DK) && (V > 32 || col < p.DV);
-          gx[j] = G[ok ? (int64_t)ch * p.DV + col : 0];
-          if (!ok) gx[j] = 0.f;
+              for (int e = 0; e < 3; ++e) ef[e] = frag_cols<Sh::EP>(sm + Sh::OFF_E + e * Sh::EB, 16 * r, u, lane);
+              mma(ak[ti][r], qf.t, ef);
+            }
+          }
         }
-        const Tri gf = split3(gx);
+        const int heads = p.dq_heads;  // heads of the buffers: Hk, or H for the partial sums of shared heads
+        const int hq = heads == p.H ? h : hk;
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
-          Op<NP> kf;
+          settle(aq[ti][r]);
+          settle(ak[ti][r]);
+        }
+        if (W > 32 || oc < p.DK) {
 #pragma unroll
-          for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(Kt + i * Sh::QK, 16 * r, u, lane);
-          mma(av[r], gf.t, kf.t);
+          for (int r = 0; r < NT; ++r) {
+            const int row = 16 * r + r16;
+            if (row < len) {
+              const int64_t at = ((trow + row) * heads + hq) * p.DK + oc;
+              *reinterpret_cast<f32x4*>(p.dq + at) = aq[ti][r];
+              *reinterpret_cast<f32x4*>(p.dk + at) = ak[ti][r];
+            }
+          }
         }
       }
 #pragma unroll
       for (int r = 0; r < NT; ++r) {
-        float tail = tb.suf[16 * r + r16];
-#pragma unroll
-        for (int j = r + 1; j < NT; ++j) tail *= PT[j];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) av[r][i] *= tail;
-      }
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        bf16x8 of[3];
-#pragma unroll
-        for (int e = 0; e < 3; ++e) of[e] = frag_chan<V>(Ot + e * Sh::VO, w2, e2, u, lane);
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          if (r <= 2 * u + 1) {
-            bf16x8 pf[3];
-#pragma unroll
-            for (int e = 0; e < 3; ++e) pf[e] = frag_cols<Sh::EP>(sm + Sh::OFF_P + e * Sh::EB, 16 * r, u, lane);
-            mma(av[r], of, pf);
-          }
+        xs[r] += __shfl_xor(xs[r], 16);
+        xs[r] += __shfl_xor(xs[r], 32);
+        ys[r] += __shfl_xor(ys[r], 16);
+        ys[r] += __shfl_xor(ys[r], 32);
+        if (g == 0) {
+          s_x[rw][16 * r + r16] = xs[r];
+          s_y[rw][16 * r + r16] = ys[r];
         }
       }
-      const int oc = 32 * w2 + 8 * g + 4 * e2;
-      if (V > 32 || oc < p.DV) {
 #pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          const int row = 16 * r + r16;
-          if (row < len) *reinterpret_cast<f32x4*>(p.dv + (trow + row) * o_ts + (int64_t)h * p.DV + oc) = av[r];
-        }
-      }
+      for (int d = 1; d < 64; d <<= 1) z += __shfl_xor(z, d);
+      if (lane == 0) s_z[rw] = z;
     }
   }
   __syncthreads();
@@ -514,7 +560,7 @@ __global__ __launch_bounds__(256) void decay_head_kernel(const DecayParams p, co
 template <int W, int V, typename InT>
 static hipError_t launch_grad_t(const DecayParams& p, hipStream_t s) {
   constexpr int DC = decay_bwd_chunk(sizeof(InT) == 2);
-  hipLaunchKernelGGL((decay_grad_kernel<W, V, InT, DC>), dim3((unsigned)(((int64_t)p.grid + 7) / 8 * 8)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((decay_grad_kernel<W, V, InT, DC>), dim3((unsigned)(((int64_t)p.grid + 7) / 8 * 8)), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 template <int W, typename InT>
