@@ -729,14 +729,16 @@ static hipError_t launch_main(const DecayParams& p, const DecayPlan& pl, int loc
 //   CHUNKS: the state at each chunk's start (reverse: the gradient at its end) into cs / ds, from the
 //           segment's start state
 // ---------------------------------------------------------------------------
+template <int W, int CT, int DC, typename XT>
+constexpr int state_buf() {
+  return Terms<XT>::N * DC * W * 2 + 3 * DC * CT * 32;
+}
 template <int W, int CT, int DC, typename XT, typename YT, bool REV>
-__global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, int local) {
+__device__ __forceinline__ void state_body(const DecayParams& p, int local, unsigned char* smem, float* s_gam) {
   constexpr int NPX = Terms<XT>::N;
   constexpr int IW = W / 16 < 4 ? W / 16 : 4, TI = W / 16 / IW, CW = 4 / IW, TC = CT / CW > 0 ? CT / CW : 1;
   constexpr int XB = DC * W * 2, YB = DC * CT * 32, BUF = NPX * XB + 3 * YB;
   constexpr int NB = NPX == 1 ? 2 : 1;
-  __shared__ __align__(16) unsigned char smem[NB * BUF];
-  __shared__ float s_gam[NB];
   int cb, h, slot;
   if (!work_of(p, cb, h, slot)) return;
   const Span sp = slot_span(p, slot);
@@ -854,15 +856,28 @@ __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, i
   }
   if (local) {
     save(part + ((int64_t)slot * p.H + h) * hsz);
-    if (tid == 0 && cb == 0) p.gpart[(int64_t)slot * p.H + h] = gall;
+    if (tid == 0 && cb == 0) (REV ? p.rgpart : p.gpart)[(int64_t)slot * p.H + h] = gall;
   } else if (REV && p.dS0 && sp.t0 == 0) {
     save(p.dS0 + ((int64_t)sp.n * p.H + h) * hsz);
   }
 }
 
+// Both directions in one launch (blockIdx.y): each alone leaves half of the CUs' places empty.
+template <int W, int CT, int DC, typename XT>
+__global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, int local) {
+  constexpr int NB = Terms<XT>::N == 1 ? 2 : 1;
+  __shared__ __align__(16) unsigned char smem[NB * state_buf<W, CT, DC, XT>()];
+  __shared__ float s_gam[NB];
+  if (blockIdx.y == 0)
+    state_body<W, CT, DC, XT, XT, false>(p, local, smem, s_gam);
+  else
+    state_body<W, CT, DC, XT, float, true>(p, local, smem, s_gam);
+}
+
 // Segments joined: the state at each segment's start (reverse: the gradient at its end) from the
 // segments' own contributions, in their place. One thread per 4 elements walks the sequence's segments.
-__global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p, int rev) {
+__global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p) {
+  const int rev = blockIdx.y;
   const int64_t hsz = (int64_t)p.DK * p.DV;
   const int per = (int)((hsz / 4 + 255) / 256);  // workgroups per (sequence, head)
   const int nh = blockIdx.x / per, n = nh / p.H, h = nh - n * p.H;
@@ -890,7 +905,7 @@ __global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p, in
     f32x4* at = reinterpret_cast<f32x4*>(part + sl * hsz + e);
     if (j + 1 < ns) {
       const f32x4 own = *at;
-      const float G = p.gpart[sl];
+      const float G = (rev ? p.rgpart : p.gpart)[sl];
       *at = x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = fmaf(G, x[i], own[i]);
@@ -900,38 +915,35 @@ __global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p, in
   }
 }
 
-template <int W, int CT, int DC, typename XT, typename YT, bool REV>
+template <int W, int CT, int DC, typename XT>
 static hipError_t launch_state_t(DecayParams p, int local, hipStream_t s) {
   p.ncb = p.DV / (16 * CT);
   const int64_t grid = work_grid(p);
   if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((decay_state_kernel<W, CT, DC, XT, YT, REV>), dim3((unsigned)grid), dim3(256), 0, s, p, local);
+  hipLaunchKernelGGL((decay_state_kernel<W, CT, DC, XT>), dim3((unsigned)grid, 2), dim3(256), 0, s, p, local);
   return hipGetLastError();
 }
-template <int W, int DC, typename XT, typename YT, bool REV>
+template <int W, int DC, typename XT>
 static hipError_t launch_state_w(const DecayParams& p, int local, hipStream_t s) {
-  return p.DV >= 32 ? launch_state_t<W, 2, DC, XT, YT, REV>(p, local, s) : launch_state_t<W, 1, DC, XT, YT, REV>(p, local, s);
+  return p.DV >= 32 ? launch_state_t<W, 2, DC, XT>(p, local, s) : launch_state_t<W, 1, DC, XT>(p, local, s);
 }
-template <int DC, typename XT, typename YT, bool REV>
+template <int DC, typename XT>
 static hipError_t launch_state(const DecayParams& p, int local, hipStream_t s) {
-  if (p.DK == 128) return launch_state_w<128, DC, XT, YT, REV>(p, local, s);
-  if (p.DK == 64) return launch_state_w<64, DC, XT, YT, REV>(p, local, s);
-  return launch_state_w<32, DC, XT, YT, REV>(p, local, s);
+  if (p.DK == 128) return launch_state_w<128, DC, XT>(p, local, s);
+  if (p.DK == 64) return launch_state_w<64, DC, XT>(p, local, s);
+  return launch_state_w<32, DC, XT>(p, local, s);
 }
-
-// (the contribution of whole segments does not depend on the chunk length)
-hipError_t launch_decay_states(const DecayParams& p, bool bf16, bool rev, int local, hipStream_t s) {
-  constexpr int CB = decay_bwd_chunk(true), CF = decay_bwd_chunk(false);
-  if (rev) return bf16 ? launch_state<CB, __bf16, float, true>(p, local, s) : launch_state<CF, float, float, true>(p, local, s);
-  return bf16 ? launch_state<CB, __bf16, __bf16, false>(p, local, s) : launch_state<CF, float, float, false>(p, local, s);
+hipError_t launch_decay_states(const DecayParams& p, bool bf16, int local, hipStream_t s) {
+  return bf16 ? launch_state<decay_bwd_chunk(true), __bf16>(p, local, s)
+              : launch_state<decay_bwd_chunk(false), float>(p, local, s);
 }
-hipError_t launch_decay_join(const DecayParams& p, int rev, hipStream_t s) {
+hipError_t launch_decay_join(const DecayParams& p, bool both, hipStream_t s) {
   const int64_t hsz = (int64_t)p.DK * p.DV;
   const int64_t grid = (int64_t)p.nseq * p.H * ((hsz / 4 + 255) / 256);
   if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)grid), dim3(256), 0, s, p, rev);
+  hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)grid, both ? 2 : 1), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 hipError_t launch_decay_plan(const DecayParams& p, hipStream_t s) {
@@ -948,7 +960,7 @@ hipError_t launch_decay_fwd(DecayParams p, const DecayPlan& pl, bool bf16, hipSt
   }
   if (pl.nseg > 1) {
     e = bf16 ? launch_main<__bf16>(p, pl, 1, s) : launch_main<float>(p, pl, 1, s);
-    if (e == hipSuccess) e = launch_decay_join(p, 0, s);
+    if (e == hipSuccess) e = launch_decay_join(p, false, s);
     if (e != hipSuccess) return e;
   } else {
     p.part = nullptr;

@@ -51,6 +51,7 @@ struct DecayParams {
   float* cs;             // [chunk slots, H, d_k, d_v] state at each chunk's start
   float* ds;             // [chunk slots, H, d_k, d_v] state gradient at each chunk's end
   float* rpart;          // segments of the reverse pass, as part / gpart
+  float* rgpart;
   int32_t* chunk_seq;    // packed: [cslots] sequence of the chunk slot (-1: unused)
   int32_t* chunk_first;  // packed: [nseq + 1]
   int32_t cslots;
@@ -399,7 +400,8 @@ hipError_t launch_decay_step(const DecayParams& p, bool bf16, hipStream_t s);
 hipError_t launch_decay_bwd(DecayParams p, const DecayPlan& pl, bool bf16, hipStream_t s);
 // Tokens per chunk of the backward: its chunk holds q, k, v and dO in LDS, fp32 data three times as large.
 constexpr int decay_bwd_chunk(bool bf16) { return bf16 ? 64 : 32; }
-hipError_t launch_decay_states(const DecayParams& p, bool bf16, bool rev, int local, hipStream_t s);
-hipError_t launch_decay_join(const DecayParams& p, int rev, hipStream_t s);
+// The backward's state passes, forward and reverse together, and the joining of segments (forward alone, or both).
+hipError_t launch_decay_states(const DecayParams& p, bool bf16, int local, hipStream_t s);
+hipError_t launch_decay_join(const DecayParams& p, bool both, hipStream_t s);
 
 }  // namespace dr

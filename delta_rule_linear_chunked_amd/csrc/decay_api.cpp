@@ -132,13 +132,15 @@ int64_t env_int(const char* name) {
 // 4 x 4096 tokens, 16 heads, d = 128 in segments of 1024). Of the segment lengths from 512 tokens up the one with
 // the least (rounds of 256 workgroups) x (tokens of a segment + 192) x (1 or 1.42) is taken: for that problem 1024 tokens,
 // 131 us (512: 152, 2048: 212, whole sequences 268).
-dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed) {
+// The backward's state passes take 32 columns per workgroup, two of which share a CU with one for each direction.
+dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   dr::DecayPlan pl{};
   const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads, T = d->seqlen;
   const bool bf16 = d->in_dtype == DR_BF16;
   // all columns in one workgroup (fp32 data, three times as large, in one or two tiles)
   const int most = bf16 ? (int)tiles : tiles >= 2 && d->head_dim_k < 128 ? 2 : 1;
-  const int64_t blocks = tiles / most;
+  const int64_t blocks = backward ? (tiles + 1) / 2 : tiles / most;
+  const double again = backward ? 1.7 : 1.42;
   int64_t seg = (T + 63) / 64 * 64;
   double best = 0;
   for (int64_t n = 1; n == 1 || n * 512 <= T; ++n) {
@@ -147,7 +149,7 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed) {
     const double wgs = (packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg) * d->num_heads * blocks;
     // (uneven segments fill a last round's gaps; 192 tokens' time for a workgroup's start and end)
     const double rounds = wgs <= 256 ? 1 : packed || wgs > 8192 ? wgs / 256 + 0.5 : (double)(int64_t)((wgs + 255) / 256);
-    const double cost = rounds * (s + 192) * (nseg > 1 ? 1.42 : 1.0);
+    const double cost = rounds * (s + 192) * (nseg > 1 ? again : 1.0);
     if (best == 0 || cost < best) {
       best = cost;
       seg = s;
@@ -201,7 +203,7 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
   if (st) return st;
   if (dims->num_seqs == 0) return DR_OK;
   const bool packed = cu_seqlens != nullptr;
-  const dr::DecayPlan pl = plan_decay(dims, packed);
+  const dr::DecayPlan pl = plan_decay(dims, packed, false);
   dr::DecayParams p{};
   set_dims(p, dims);
   p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.cu = cu_seqlens; p.o = o; p.S = S_T;
@@ -295,7 +297,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   if (st) return st;
   const bool packed = cu_seqlens != nullptr, bf16 = dims->in_dtype == DR_BF16;
   if (N == 0 && !per_head) return DR_OK;
-  const dr::DecayPlan pl = plan_decay(dims, packed);
+  const dr::DecayPlan pl = plan_decay(dims, packed, true);
   const int64_t chunk = dr::decay_bwd_chunk(bf16);
   const int64_t cslots = packed ? dims->seqlen / chunk + N : N * ((dims->seqlen + chunk - 1) / chunk);
   if (pl.slots * H * (dims->head_dim_v / 16) > INT32_MAX - 8 || cslots * H > INT32_MAX - 8 || pl.seg > INT32_MAX ||
@@ -316,6 +318,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   const bool segs = pl.nseg > 1, shared = dims->num_k_heads != H;
   const int64_t off_cs = lay.take(cslots * H * hsz * 4), off_ds = lay.take(cslots * H * hsz * 4);
   const int64_t off_part = segs ? lay.take(pl.slots * H * hsz * 4) : 0, off_g = segs ? lay.take(pl.slots * H * 4) : 0;
+  const int64_t off_rpart = segs ? lay.take(pl.slots * H * hsz * 4) : 0, off_rg = segs ? lay.take(pl.slots * H * 4) : 0;
   const int64_t off_pq = shared ? lay.take(tokens * H * dims->head_dim_k * 4) : 0;
   const int64_t off_pk = shared ? lay.take(tokens * H * dims->head_dim_k * 4) : 0;
   const int64_t off_da = per_head ? lay.take(tokens * H * 4) : 0;
@@ -330,8 +333,10 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   p.cs = f(off_cs);
   p.ds = f(off_ds);
   if (segs) {
-    p.part = p.rpart = f(off_part);  // (the reverse passes run after the forward ones)
+    p.part = f(off_part);
     p.gpart = f(off_g);
+    p.rpart = f(off_rpart);
+    p.rgpart = f(off_rg);
   }
   if (shared) {
     p.pq = f(off_pq);

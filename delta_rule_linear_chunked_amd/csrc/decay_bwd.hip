@@ -583,13 +583,11 @@ hipError_t launch_decay_bwd(DecayParams p, const DecayPlan& pl, bool bf16, hipSt
     if (e != hipSuccess) return e;
     p.cu = p.cu_ok;
   }
-  for (int rev = 0; rev < 2 && e == hipSuccess; ++rev) {
-    if (pl.nseg > 1) {
-      e = launch_decay_states(p, bf16, rev != 0, 1, s);
-      if (e == hipSuccess) e = launch_decay_join(p, rev, s);
-    }
-    if (e == hipSuccess) e = launch_decay_states(p, bf16, rev != 0, 0, s);
+  if (pl.nseg > 1) {
+    e = launch_decay_states(p, bf16, 1, s);
+    if (e == hipSuccess) e = launch_decay_join(p, true, s);
   }
+  if (e == hipSuccess) e = launch_decay_states(p, bf16, 0, s);
   if (e != hipSuccess || p.cslots == 0) {
     if (e == hipSuccess && p.head_da) {
       hipLaunchKernelGGL(decay_head_kernel, dim3((unsigned)p.H), dim3(256), 0, s, p, p.dalpha, p.head_da);
