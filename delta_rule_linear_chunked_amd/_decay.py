@@ -12,8 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import (_DT, _Opts, _capturing, _check, _need, _need_rows, _opts, _ptr, _stream, check_offsets, load_library,
-               snapshot_count)
+from . import _DT, _Opts, _capturing, _check, _need, _need_rows, check_offsets, load_library, snapshot_count
 
 # code types of the state cache (dr_cache_format)
 CACHE_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
@@ -39,37 +38,91 @@ def declare(lib):
     """Signatures of this part of the library."""
     vp, ip = ctypes.c_void_p, ctypes.c_int
     dp, op, cp = ctypes.POINTER(_DecayDims), ctypes.POINTER(_Opts), ctypes.POINTER(_CacheDims)
-    lib.dr_decay_fwd.argtypes = [vp] * 8 + [dp, op, vp]
+    lib.dr_decay_workspace.argtypes = [dp, ip, ip, ctypes.POINTER(ctypes.c_int64)]
+    lib.dr_decay_fwd.argtypes = [vp] * 8 + [dp, op, vp, ctypes.c_int64, vp]
     lib.dr_decay_step.argtypes = [vp] * 6 + [dp, op, vp]
     lib.dr_state_pack.argtypes = [vp] * 5 + [cp, vp]
     lib.dr_state_unpack.argtypes = [vp] * 5 + [cp, vp]
-    lib.dr_decay_bwd.argtypes = [vp] * 13 + [dp, vp]
-    for f in (lib.dr_decay_fwd, lib.dr_decay_step, lib.dr_decay_bwd, lib.dr_state_pack, lib.dr_state_unpack):
+    lib.dr_decay_bwd.argtypes = [vp] * 13 + [dp, vp, ctypes.c_int64, vp]
+    for f in (lib.dr_decay_workspace, lib.dr_decay_fwd, lib.dr_decay_step, lib.dr_decay_bwd, lib.dr_state_pack, lib.dr_state_unpack):
         f.restype = ip
+
+
+# These calls are made once per token and layer with little GPU work behind them: what the checks cost on the host
+# counts. The common case (dense tensors of the right kind on the current device) takes the short ways below;
+# anything else goes to the checks that say what is wrong.
+def _is(t, shape, dtype, device) -> bool:
+    return t is not None and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()
+
+
+def _require(t, name, shape, dtype, device):
+    if not _is(t, shape, dtype, device):
+        _need(t, name, shape, dtype, device)
+
+
+def _call(lib, entry, device, *args):
+    """Calls an entry point with the device's current stream, on that device."""
+    index = device.index
+    if device.type != "cuda":  # the library has nothing to launch on
+        raise ValueError(f"{entry}: tensors must be on a GPU, got {device}")
+    fn = getattr(lib, entry)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):  # the library launches on the current device
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        _check(lib, st, entry)
+
+
+def _workspace(lib, d, dev, packed, backward):
+    """A call's workspace from torch's allocator: a captured call's then belongs to its graph."""
+    n = ctypes.c_int64()
+    _check(lib, lib.dr_decay_workspace(ctypes.byref(d), packed, backward, ctypes.byref(n)), "dr_decay_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _options(state_idx, rows, snapshots=None, every=0):
+    if state_idx is None and snapshots is None:
+        return None
+    return ctypes.byref(_Opts(_addr(state_idx), rows, _addr(snapshots), int(every or 0)))
+
+
+def _ranks(q, v, alpha, lead):
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} dimensions, got {q.dim()} and {v.dim()}")
+    if alpha is None:
+        raise ValueError("alpha is required")
 
 
 def _inputs(q, k, v, alpha, lead):
     """Checks q, k, v, alpha with ``lead`` leading dimensions (2: batch and token, 1: sequence) and returns the sizes
-    block without num_seqs."""
-    if q.dim() != lead + 2 or v.dim() != lead + 2:
-        raise ValueError(f"q and v must have {lead + 2} dimensions, got {q.dim()} and {v.dim()}")
-    dev, first = q.device, tuple(q.shape[:lead])
-    Hk, dk = q.shape[lead:]
-    H, dv = v.shape[lead:]
-    if q.dtype not in _DT:
-        raise ValueError(f"q dtype {q.dtype} is not float32 or bfloat16")
+    block, num_seqs that of unpacked inputs."""
+    _ranks(q, v, alpha, lead)
+    dev, dtype, qs, vs = q.device, q.dtype, q.shape, v.shape
+    first = tuple(qs[:lead])
+    Hk, dk = qs[lead:]
+    H, dv = vs[lead:]
+    if dtype not in _DT:
+        raise ValueError(f"q dtype {dtype} is not float32 or bfloat16")
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"{H} value heads are not a multiple of {Hk} query/key heads")
-    sq = _need_rows(q, "q", first + (Hk, dk), lead, q.dtype, dev)
-    sk = _need_rows(k, "k", first + (Hk, dk), lead, q.dtype, dev)
-    sv = _need_rows(v, "v", first + (H, dv), lead, q.dtype, dev)
-    per_head = alpha is not None and alpha.dim() == 1
-    _need(alpha, "alpha", (H,) if per_head else first + (H,), torch.float32, dev)
-    d = _DecayDims(first[0], first[1] if lead == 2 else 1, H, Hk, dk, dv, first[0], _DT[q.dtype], int(per_head), 0, 0)
-    if not all(x.is_contiguous() for x in (q, k, v)):
+    strides = None
+    if not (q.is_contiguous() and _is(k, qs, dtype, dev) and _is(v, first + (H, dv), dtype, dev)):
+        strides = (_need_rows(q, "q", first + (Hk, dk), lead, dtype, dev),
+                   _need_rows(k, "k", first + (Hk, dk), lead, dtype, dev),
+                   _need_rows(v, "v", first + (H, dv), lead, dtype, dev))
+    per_head = alpha.dim() == 1
+    _require(alpha, "alpha", (H,) if per_head else first + (H,), torch.float32, dev)
+    d = _DecayDims(first[0], first[1] if lead == 2 else 1, H, Hk, dk, dv, first[0], _DT[dtype], int(per_head), 0, 0)
+    if strides is not None:
         d.strided = 1
         (d.q_token_stride, d.q_batch_stride), (d.k_token_stride, d.k_batch_stride), \
-            (d.v_token_stride, d.v_batch_stride) = [((s[1], s[0]) if lead == 2 else (0, s[0])) for s in (sq, sk, sv)]
+            (d.v_token_stride, d.v_batch_stride) = [((s[1], s[0]) if lead == 2 else (0, s[0])) for s in strides]
     return d
 
 
@@ -77,7 +130,7 @@ def _offsets(cu_seqlens, d, dev):
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens must be a vector of num_seqs + 1 offsets")
-        _need(cu_seqlens, "cu_seqlens", (cu_seqlens.shape[0],), torch.int32, dev)
+        _require(cu_seqlens, "cu_seqlens", (cu_seqlens.shape[0],), torch.int32, dev)
         d.num_seqs = cu_seqlens.shape[0] - 1
 
 
@@ -93,12 +146,12 @@ def dr_decay_fwd(q, k, v, alpha, S0, cu_seqlens, o, S_T, state_idx=None, snapsho
     _offsets(cu_seqlens, d, dev)
     rows = d.num_seqs
     if state_idx is not None:
-        _need(state_idx, "state_idx", (d.num_seqs,), torch.int32, dev)
+        _require(state_idx, "state_idx", (d.num_seqs,), torch.int32, dev)
         pools = [t for t in (S0, S_T) if t is not None]
         rows = pools[0].shape[0] if pools else 0
     for t, name in ((S0, "S0"), (S_T, "S_T")):
         if t is not None:
-            _need(t, name, (rows, H, dk, dv), torch.float32, dev)
+            _require(t, name, (rows, H, dk, dv), torch.float32, dev)
     if snapshots is not None:
         if not snapshot_every or snapshot_every <= 0:
             raise ValueError("snapshots need a positive snapshot_every")
@@ -108,14 +161,13 @@ def dr_decay_fwd(q, k, v, alpha, S0, cu_seqlens, o, S_T, state_idx=None, snapsho
             rows_s = snapshot_count(check_offsets(cu_seqlens, T), snapshot_every)
         else:
             rows_s = snapshots.shape[0]
-        _need(snapshots, "snapshots", (rows_s, H, dk, dv), torch.float32, dev)
+        _require(snapshots, "snapshots", (rows_s, H, dk, dv), torch.float32, dev)
     if o is not None:
-        _need(o, "o", (B, T, H, dv), torch.float32, dev)
-    opts = _opts(state_idx, rows, snapshots, snapshot_every)
-    with torch.cuda.device(dev):  # the library launches on the current device
-        st = lib.dr_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(cu_seqlens), _ptr(o), _ptr(S_T),
-                              ctypes.byref(d), ctypes.byref(opts), _stream(dev))
-    _check(lib, st, "dr_decay_fwd")
+        _require(o, "o", (B, T, H, dv), torch.float32, dev)
+    ws = _workspace(lib, d, dev, cu_seqlens is not None, False)
+    _call(lib, "dr_decay_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), _addr(S0),
+          _addr(cu_seqlens), _addr(o), _addr(S_T), ctypes.byref(d), _options(state_idx, rows, snapshots, snapshot_every),
+          _addr(ws), 0 if ws is None else ws.numel())
 
 
 def decay_fwd(q, k, v, alpha, S0=None, cu_seqlens=None, output_final_state: bool = True, state_idx=None,
@@ -123,6 +175,7 @@ def decay_fwd(q, k, v, alpha, S0=None, cu_seqlens=None, output_final_state: bool
     """Allocates ``o`` (and ``S_T``) and runs ``dr_decay_fwd``. Returns (o, S_T or None), plus the snapshots when
     ``snapshot_every`` is given. With ``state_idx``, S0 is a pool that is updated in place and returned as S_T.
     Rows of ``o`` past the last packed sequence are not written."""
+    _ranks(q, v, alpha, 2)
     B, T, _, dk = q.shape
     H, dv = v.shape[-2:]
     N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
@@ -152,15 +205,12 @@ def dr_decay_step(q, k, v, alpha, S, o, state_idx=None) -> None:
     dev, N, H, dk, dv = q.device, d.batch, d.num_heads, d.head_dim_k, d.head_dim_v
     rows = N
     if state_idx is not None:
-        _need(state_idx, "state_idx", (N,), torch.int32, dev)
+        _require(state_idx, "state_idx", (N,), torch.int32, dev)
         rows = S.shape[0]
-    _need(S, "S", (rows, H, dk, dv), torch.float32, dev)
-    _need(o, "o", (N, H, dv), torch.float32, dev)
-    opts = _opts(state_idx, rows)
-    with torch.cuda.device(dev):
-        st = lib.dr_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S), _ptr(o), ctypes.byref(d),
-                               ctypes.byref(opts), _stream(dev))
-    _check(lib, st, "dr_decay_step")
+    _require(S, "S", (rows, H, dk, dv), torch.float32, dev)
+    _require(o, "o", (N, H, dv), torch.float32, dev)
+    _call(lib, "dr_decay_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), S.data_ptr(),
+          o.data_ptr(), ctypes.byref(d), _options(state_idx, rows))
 
 
 def decay_step(q, k, v, alpha, S, state_idx=None):
@@ -179,19 +229,19 @@ def dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dalpha, d
     _offsets(cu_seqlens, d, dev)
     for t, name in ((S0, "S0"), (dS_T, "dS_T"), (dS0, "dS0")):
         if t is not None:
-            _need(t, name, (d.num_seqs, H, dk_, dv_), torch.float32, dev)
+            _require(t, name, (d.num_seqs, H, dk_, dv_), torch.float32, dev)
     for t, name, shape in ((dO, "dO", (B, T, H, dv_)), (dq, "dq", tuple(q.shape)), (dk, "dk", tuple(q.shape)),
                            (dv, "dv", (B, T, H, dv_)), (dalpha, "dalpha", tuple(alpha.shape))):
-        _need(t, name, shape, torch.float32, dev)
-    with torch.cuda.device(dev):
-        st = lib.dr_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0), _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T),
-                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dalpha), _ptr(dS0), ctypes.byref(d), _stream(dev))
-    _check(lib, st, "dr_decay_bwd")
+        _require(t, name, shape, torch.float32, dev)
+    ws = _workspace(lib, d, dev, cu_seqlens is not None, True)
+    _call(lib, "dr_decay_bwd", dev, *map(_addr, (q, k, v, alpha, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dalpha, dS0)),
+          ctypes.byref(d), _addr(ws), 0 if ws is None else ws.numel())
 
 
 def decay_bwd(q, k, v, alpha, S0=None, cu_seqlens=None, dO=None, dS_T=None, need_dS0: bool = True):
     """Allocates the gradients and runs ``dr_decay_bwd``. Returns a dict with dq, dk, dv, dalpha and dS0 (None unless
     ``need_dS0``). Rows past the last packed sequence are not written."""
+    _ranks(q, v, alpha, 2)
     new = lambda s: torch.empty(tuple(s), dtype=torch.float32, device=q.device)  # noqa: E731
     N = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
     g = dict(dq=new(q.shape), dk=new(k.shape), dv=new(v.shape), dalpha=new(alpha.shape),
@@ -229,7 +279,8 @@ class _DecayAttention(torch.autograd.Function):
 
 def decay_attention(q, k, v, alpha, S0=None, cu_seqlens=None):
     """The prefill with gradients through torch autograd: returns (o, S_T) as ``decay_fwd``; ``backward()`` fills the
-    ``.grad`` of q, k, v, alpha and S0 (gradients of bf16 inputs are computed in fp32 and returned in bf16)."""
+    ``.grad`` of q, k, v, alpha and S0 (gradients of bf16 inputs are computed in fp32 and returned in bf16). In a graph capture take forward and backward
+    together, on leaves that no eager graph holds (torch would accumulate into those on the other stream)."""
     return _DecayAttention.apply(q, k, v, alpha, S0, cu_seqlens)
 
 
@@ -239,22 +290,22 @@ def _cache_dims(S, codes, scales, state_idx, slot_idx):
     dev = S.device
     rows, H, dk, dv = S.shape
     slots = codes.shape[0]
-    fmt = [f for f, t in CACHE_FORMATS.values() if t == codes.dtype]
-    if not fmt:
+    fmt = 0 if codes.dtype is torch.int8 else 1 if codes.dtype is torch.float8_e4m3fn else None
+    if fmt is None:
         raise ValueError(f"codes have dtype {codes.dtype}, expected int8 or float8_e4m3fn")
-    _need(S, "S", (rows, H, dk, dv), torch.float32, dev)
-    _need(codes, "codes", (slots, H, dk, dv), codes.dtype, dev)
-    _need(scales, "scales", (slots, H, dk), torch.float32, dev)
+    _require(S, "S", (rows, H, dk, dv), torch.float32, dev)
+    _require(codes, "codes", (slots, H, dk, dv), codes.dtype, dev)
+    _require(scales, "scales", (slots, H, dk), torch.float32, dev)
     count = None
     for t, name in ((state_idx, "state_idx"), (slot_idx, "slot_idx")):
         if t is not None:
             if t.dim() != 1:
                 raise ValueError(f"{name} must be a vector")
-            _need(t, name, (t.shape[0] if count is None else count,), torch.int32, dev)
+            _require(t, name, (t.shape[0] if count is None else count,), torch.int32, dev)
             count = t.shape[0]
     if count is None and rows != slots:
         raise ValueError(f"{rows} states and {slots} slots: give state_idx or slot_idx")
-    return _CacheDims(rows if count is None else count, rows, slots, H, dk, dv, fmt[0], 0)
+    return _CacheDims(rows if count is None else count, rows, slots, H, dk, dv, fmt, 0)
 
 
 def dr_state_pack(S, codes, scales, slot_idx=None, state_idx=None) -> None:
@@ -263,11 +314,8 @@ def dr_state_pack(S, codes, scales, slot_idx=None, state_idx=None) -> None:
     slot outside the cache is skipped; other slots are left as they are."""
     lib = load_library()
     d = _cache_dims(S, codes, scales, state_idx, slot_idx)
-    dev = S.device
-    with torch.cuda.device(dev):
-        st = lib.dr_state_pack(_ptr(S), _ptr(state_idx), _ptr(codes), _ptr(scales), _ptr(slot_idx), ctypes.byref(d),
-                               _stream(dev))
-    _check(lib, st, "dr_state_pack")
+    _call(lib, "dr_state_pack", S.device, S.data_ptr(), _addr(state_idx), codes.data_ptr(), scales.data_ptr(),
+          _addr(slot_idx), ctypes.byref(d))
 
 
 def dr_state_unpack(codes, scales, S, slot_idx=None, state_idx=None) -> None:
@@ -275,11 +323,8 @@ def dr_state_unpack(codes, scales, S, slot_idx=None, state_idx=None) -> None:
     ``dr_state_pack``. A slot outside the cache gives the zero state, a state row outside S is skipped."""
     lib = load_library()
     d = _cache_dims(S, codes, scales, state_idx, slot_idx)
-    dev = S.device
-    with torch.cuda.device(dev):
-        st = lib.dr_state_unpack(_ptr(codes), _ptr(scales), _ptr(slot_idx), _ptr(S), _ptr(state_idx), ctypes.byref(d),
-                                 _stream(dev))
-    _check(lib, st, "dr_state_unpack")
+    _call(lib, "dr_state_unpack", S.device, codes.data_ptr(), scales.data_ptr(), _addr(slot_idx), S.data_ptr(),
+          _addr(state_idx), ctypes.byref(d))
 
 
 def state_pack(S, fmt: str = "int8"):

@@ -70,12 +70,10 @@ struct DecayParams {
 
 // What the host decides for a call.
 struct DecayPlan {
-  int ct;              // column tiles of 16 per workgroup of the main pass (1, 2 or 4)
+  int ct;              // column tiles of 16 per workgroup of the main pass (1, 2, 4 or 8)
   int64_t seg;         // tokens per segment
   int64_t nseg;        // fixed length: segments per sequence; packed: more than 1 if any may have more
   int64_t slots;
-  int64_t workspace;   // bytes
-  int64_t off_part, off_gpart, off_tab;
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));

@@ -171,23 +171,105 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   return pl;
 }
 
-// Lays out a workspace: offsets of 256-byte aligned pieces.
-struct Layout {
+// A call's workspace: 256-byte aligned pieces one behind the other.
+struct Space {
   int64_t size = 0;
   int64_t take(int64_t bytes) {
     const int64_t at = size;
     size += round256(bytes);
     return at;
   }
+  // segments: their own states and decays (r: of the reverse pass); packed: tables; backward: states and state
+  // gradients at chunk boundaries, shared heads' partial sums, tokens' gradients of a decay per head
+  int64_t part, g, rpart, rg, tab, cs, ds, pq, pk, da;
 };
+
+Space fwd_space(const dr_decay_dims* d, const dr::DecayPlan& pl, bool packed) {
+  Space s{};
+  const int64_t nh = pl.slots * d->num_heads;
+  if (pl.nseg > 1) {
+    s.part = s.take(nh * d->head_dim_k * d->head_dim_v * 4);
+    s.g = s.take(nh * 4);
+  }
+  if (packed) s.tab = s.take((pl.slots + 3 * d->num_seqs + 2) * 4);
+  return s;
+}
+
+int64_t bwd_slots(const dr_decay_dims* d, bool packed) {
+  const int64_t chunk = dr::decay_bwd_chunk(d->in_dtype == DR_BF16);
+  return packed ? d->seqlen / chunk + d->num_seqs : d->num_seqs * ((d->seqlen + chunk - 1) / chunk);
+}
+
+Space bwd_space(const dr_decay_dims* d, const dr::DecayPlan& pl, bool packed) {
+  Space s{};
+  const int64_t H = d->num_heads, hsz = d->head_dim_k * d->head_dim_v, tokens = d->batch * d->seqlen;
+  const int64_t cslots = bwd_slots(d, packed);
+  s.cs = s.take(cslots * H * hsz * 4);
+  s.ds = s.take(cslots * H * hsz * 4);
+  if (pl.nseg > 1) {
+    s.part = s.take(pl.slots * H * hsz * 4);
+    s.g = s.take(pl.slots * H * 4);
+    s.rpart = s.take(pl.slots * H * hsz * 4);
+    s.rg = s.take(pl.slots * H * 4);
+  }
+  if (d->num_k_heads != H) {
+    s.pq = s.take(tokens * H * d->head_dim_k * 4);
+    s.pk = s.take(tokens * H * d->head_dim_k * 4);
+  }
+  if (d->decay_layout == DR_DECAY_HEAD) s.da = s.take(tokens * H * 4);
+  if (packed) s.tab = s.take((pl.slots + cslots + 4 * d->num_seqs + 3) * 4);
+  return s;
+}
+
+// The call's workspace: the caller's, or one from the library's pool (`owned`, given back stream-ordered). The pool
+// is refused while the stream is being captured: a graph would hold it as memory nodes, and a replay of one of two
+// such graphs has run its kernels on addresses that were not mapped.
+int get_space(const char* what, int64_t need, void* given, int64_t given_bytes, hipStream_t stream, unsigned char** ws,
+              bool* owned) {
+  *ws = nullptr;
+  *owned = false;
+  if (given != nullptr) {
+    if (!aligned16(given)) return host_fail(DR_ERR_LAYOUT, "`workspace` is not 16-byte aligned");
+    if (given_bytes < need)
+      return host_fail(DR_ERR_SHAPE, "`workspace` has %lld bytes, the call needs %lld", (long long)given_bytes,
+                       (long long)need);
+    *ws = static_cast<unsigned char*>(given);
+    return DR_OK;
+  }
+  if (need == 0) return DR_OK;
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  hipError_t e = hipStreamIsCapturing(stream, &cap);
+  if (e == hipSuccess && cap != hipStreamCaptureStatusNone)
+    return host_fail(DR_ERR_UNSUPPORTED, "the %s needs a workspace of %lld bytes: a captured call takes the caller's", what,
+                     (long long)need);
+  void* mem = nullptr;
+  if (e == hipSuccess) e = dr::host_workspace((size_t)need, stream, &mem);
+  if (e != hipSuccess)
+    return host_fail(DR_ERR_HIP, "%s workspace (%lld bytes) allocation failed: %s", what, (long long)need,
+                     hipGetErrorString(e));
+  *ws = static_cast<unsigned char*>(mem);
+  *owned = true;
+  return DR_OK;
+}
 
 }  // namespace
 
 extern "C" {
 
+int dr_decay_workspace(const dr_decay_dims* dims, int packed, int backward, int64_t* bytes) {
+  dr::host_clear_error();
+  const int32_t some = 0;  // (only whether there are offsets counts)
+  const int st = check_dims(dims, packed ? &some : nullptr, false);
+  if (st) return st;
+  if (bytes == nullptr) return host_fail(DR_ERR_NULL, "`bytes` is NULL");
+  const dr::DecayPlan pl = plan_decay(dims, packed != 0, backward != 0);
+  *bytes = backward ? bwd_space(dims, pl, packed != 0).size : fwd_space(dims, pl, packed != 0).size;
+  return DR_OK;
+}
+
 int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
                  const int32_t* cu_seqlens, float* o, float* S_T, const dr_decay_dims* dims, const dr_opts* opts,
-                 hipStream_t stream) {
+                 void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   dr::host_clear_error();
   int st = check_dims(dims, cu_seqlens, false);
   if (st) return st;
@@ -218,34 +300,23 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
   p.seg = (int32_t)pl.seg;
   p.nseg = (int32_t)pl.nseg;
   p.slots = (int32_t)pl.slots;
-  const int64_t nh = pl.slots * dims->num_heads;
-  Layout lay;
-  const bool segs = pl.nseg > 1;
-  const int64_t off_part = segs ? lay.take(nh * dims->head_dim_k * dims->head_dim_v * 4) : 0;
-  const int64_t off_g = segs ? lay.take(nh * 4) : 0;
-  const int64_t off_tab = packed ? lay.take((pl.slots + 3 * dims->num_seqs + 2) * 4) : 0;
+  const Space sp = fwd_space(dims, pl, packed);
   unsigned char* ws = nullptr;
-  hipError_t e = hipSuccess;
-  if (lay.size > 0) {
-    void* mem = nullptr;
-    e = dr::host_workspace((size_t)lay.size, stream, &mem);
-    if (e != hipSuccess)
-      return host_fail(DR_ERR_HIP, "decay prefill workspace (%lld bytes) allocation failed: %s", (long long)lay.size,
-                       hipGetErrorString(e));
-    ws = static_cast<unsigned char*>(mem);
-  }
-  if (segs) {
-    p.part = reinterpret_cast<float*>(ws + off_part);
-    p.gpart = reinterpret_cast<float*>(ws + off_g);
+  bool owned = false;
+  st = get_space("decay prefill", sp.size, workspace, workspace_bytes, stream, &ws, &owned);
+  if (st) return st;
+  if (pl.nseg > 1) {
+    p.part = reinterpret_cast<float*>(ws + sp.part);
+    p.gpart = reinterpret_cast<float*>(ws + sp.g);
   }
   if (packed) {
-    p.slot_seq = reinterpret_cast<int32_t*>(ws + off_tab);
+    p.slot_seq = reinterpret_cast<int32_t*>(ws + sp.tab);
     p.slot_first = p.slot_seq + pl.slots;
     p.cu_ok = p.slot_first + dims->num_seqs + 1;
     p.snap_first = p.cu_ok + dims->num_seqs + 1;
   }
-  e = dr::launch_decay_fwd(p, pl, dims->in_dtype == DR_BF16, stream);
-  const hipError_t ef = ws ? hipFreeAsync(ws, stream) : hipSuccess;
+  const hipError_t e = dr::launch_decay_fwd(p, pl, dims->in_dtype == DR_BF16, stream);
+  const hipError_t ef = owned ? hipFreeAsync(ws, stream) : hipSuccess;
   if (e != hipSuccess) return host_fail(DR_ERR_HIP, "decay prefill launch failed: %s", hipGetErrorString(e));
   if (ef != hipSuccess) return host_fail(DR_ERR_HIP, "decay prefill workspace release failed: %s", hipGetErrorString(ef));
   return DR_OK;
@@ -277,7 +348,8 @@ int dr_decay_step(const void* q, const void* k, const void* v, const float* alph
 
 int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
                  const int32_t* cu_seqlens, const float* dO, const float* dS_T, float* dq, float* dk, float* dv,
-                 float* dalpha, float* dS0, const dr_decay_dims* dims, hipStream_t stream) {
+                 float* dalpha, float* dS0, const dr_decay_dims* dims, void* workspace, int64_t workspace_bytes,
+                 hipStream_t stream) {
   dr::host_clear_error();
   int st = check_dims(dims, cu_seqlens, false);
   if (st) return st;
@@ -299,7 +371,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   if (N == 0 && !per_head) return DR_OK;
   const dr::DecayPlan pl = plan_decay(dims, packed, true);
   const int64_t chunk = dr::decay_bwd_chunk(bf16);
-  const int64_t cslots = packed ? dims->seqlen / chunk + N : N * ((dims->seqlen + chunk - 1) / chunk);
+  const int64_t cslots = bwd_slots(dims, packed);
   if (pl.slots * H * (dims->head_dim_v / 16) > INT32_MAX - 8 || cslots * H > INT32_MAX - 8 || pl.seg > INT32_MAX ||
       tokens * dims->num_k_heads * (dims->head_dim_k / 4) / 256 >= INT32_MAX)
     return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
@@ -313,48 +385,37 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   p.cslots = (int32_t)cslots;
   p.bwd_chunk = (int32_t)chunk;
   p.nbatch = (int32_t)dims->batch;
-  const int64_t hsz = dims->head_dim_k * dims->head_dim_v;
-  Layout lay;
-  const bool segs = pl.nseg > 1, shared = dims->num_k_heads != H;
-  const int64_t off_cs = lay.take(cslots * H * hsz * 4), off_ds = lay.take(cslots * H * hsz * 4);
-  const int64_t off_part = segs ? lay.take(pl.slots * H * hsz * 4) : 0, off_g = segs ? lay.take(pl.slots * H * 4) : 0;
-  const int64_t off_rpart = segs ? lay.take(pl.slots * H * hsz * 4) : 0, off_rg = segs ? lay.take(pl.slots * H * 4) : 0;
-  const int64_t off_pq = shared ? lay.take(tokens * H * dims->head_dim_k * 4) : 0;
-  const int64_t off_pk = shared ? lay.take(tokens * H * dims->head_dim_k * 4) : 0;
-  const int64_t off_da = per_head ? lay.take(tokens * H * 4) : 0;
-  const int64_t off_tab = packed ? lay.take((pl.slots + cslots + 4 * N + 3) * 4) : 0;
-  void* mem = nullptr;
-  hipError_t e = dr::host_workspace((size_t)(lay.size > 0 ? lay.size : 256), stream, &mem);
-  if (e != hipSuccess)
-    return host_fail(DR_ERR_HIP, "decay backward workspace (%lld bytes) allocation failed: %s", (long long)lay.size,
-                     hipGetErrorString(e));
-  unsigned char* ws = static_cast<unsigned char*>(mem);
+  const Space sp = bwd_space(dims, pl, packed);
+  unsigned char* ws = nullptr;
+  bool owned = false;
+  st = get_space("decay backward", sp.size, workspace, workspace_bytes, stream, &ws, &owned);
+  if (st) return st;
   auto f = [&](int64_t off) { return reinterpret_cast<float*>(ws + off); };
-  p.cs = f(off_cs);
-  p.ds = f(off_ds);
-  if (segs) {
-    p.part = f(off_part);
-    p.gpart = f(off_g);
-    p.rpart = f(off_rpart);
-    p.rgpart = f(off_rg);
+  p.cs = f(sp.cs);
+  p.ds = f(sp.ds);
+  if (pl.nseg > 1) {
+    p.part = f(sp.part);
+    p.gpart = f(sp.g);
+    p.rpart = f(sp.rpart);
+    p.rgpart = f(sp.rg);
   }
-  if (shared) {
-    p.pq = f(off_pq);
-    p.pk = f(off_pk);
+  if (dims->num_k_heads != H) {
+    p.pq = f(sp.pq);
+    p.pk = f(sp.pk);
   }
   if (per_head) {
     p.head_da = dalpha;
-    p.dalpha = f(off_da);
+    p.dalpha = f(sp.da);
   }
   if (packed) {
-    p.slot_seq = reinterpret_cast<int32_t*>(ws + off_tab);
+    p.slot_seq = reinterpret_cast<int32_t*>(ws + sp.tab);
     p.slot_first = p.slot_seq + pl.slots;
     p.cu_ok = p.slot_first + N + 1;
     p.chunk_first = p.cu_ok + N + 1;
     p.chunk_seq = p.chunk_first + N + 1;
   }
-  e = dr::launch_decay_bwd(p, pl, bf16, stream);
-  const hipError_t ef = hipFreeAsync(mem, stream);
+  const hipError_t e = dr::launch_decay_bwd(p, pl, bf16, stream);
+  const hipError_t ef = owned ? hipFreeAsync(ws, stream) : hipSuccess;
   if (e != hipSuccess) return host_fail(DR_ERR_HIP, "decay backward launch failed: %s", hipGetErrorString(e));
   if (ef != hipSuccess) return host_fail(DR_ERR_HIP, "decay backward workspace release failed: %s", hipGetErrorString(ef));
   return DR_OK;

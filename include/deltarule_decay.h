@@ -59,6 +59,15 @@ typedef struct dr_decay_dims {
 } dr_decay_dims;
 
 /*
+ * Bytes of workspace that a call of dr_decay_fwd (backward == 0) or dr_decay_bwd (backward != 0) with these dims takes;
+ * packed: whether it has cu_seqlens. May be 0. Nothing in a workspace is kept from one call for the next.
+ * Both calls take it as `workspace`, `workspace_bytes` (device memory, 16-byte aligned, not in use by another call
+ * until this one is over on the stream). With NULL it comes from the library's pool, stream-ordered; while the
+ * stream is being captured a call that needs any is then refused (DR_ERR_UNSUPPORTED).
+ */
+int dr_decay_workspace(const dr_decay_dims* dims, int packed, int backward, int64_t* bytes);
+
+/*
  * Prefill.
  *   q, k       [B, T, Hk, d_k]  in_dtype;   v [B, T, H, d_v] in_dtype
  *   alpha      float32, [B, T, H] or [H]
@@ -66,12 +75,12 @@ typedef struct dr_decay_dims {
  *   opts       NULL, or state_idx / num_slots and snapshots / snapshot_every (a positive multiple of 64)
  *              as in dr_chunk_fwd_ex; the input preparation fields must be zero
  * Sequences that are too few to fill the GPU are cut into segments whose own states are formed
- * first; the workspace for them (one state per segment and head) comes from the library's pool. A
- * call that needs no segments takes none (packed sequences: a few integers per sequence).
+ * first; the workspace holds one state per segment and head. A call that needs no segments takes none (packed
+ * sequences: a few integers per sequence).
  */
 int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
                  const int32_t* cu_seqlens, float* o, float* S_T, const dr_decay_dims* dims, const dr_opts* opts,
-                 hipStream_t stream);
+                 void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * One token for each of N sequences x H heads, the states updated in place.
@@ -87,14 +96,15 @@ int dr_decay_step(const void* q, const void* k, const void* v, const float* alph
  * and dense, in the shapes of the inputs:
  *   dq, dk [B, T, Hk, d_k] (summed over the value heads of a query/key head), dv [B, T, H, d_v],
  *   dalpha [B, T, H], or [H] summed over all tokens,  dS0 [N, H, d_k, d_v] or NULL
- * The call forms the states and the state gradients at every 64th token itself; they and the partial sums
- * come from the library's pool: 8 d_k d_v bytes per 64 tokens and head, and with shared heads 8 d_k bytes per
- * token and head. No atomics: the same call gives the same bits. Rows of tokens past
+ * The call forms the states and the state gradients at every 64th token (float32 inputs: every 32nd) itself; they and
+ * the partial sums are its workspace: 8 d_k d_v bytes per 64 (32) tokens and head, and with shared heads 8 d_k
+ * bytes per token and head. No atomics: the same call gives the same bits. Rows of tokens past
  * cu_seqlens[N] are not written.
  */
 int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha, const float* S0,
                  const int32_t* cu_seqlens, const float* dO, const float* dS_T, float* dq, float* dk, float* dv,
-                 float* dalpha, float* dS0, const dr_decay_dims* dims, hipStream_t stream);
+                 float* dalpha, float* dS0, const dr_decay_dims* dims, void* workspace, int64_t workspace_bytes,
+                 hipStream_t stream);
 
 /*
  * 8-bit state cache: fp32 states (of any recurrence of this library: a decode pool, a prefill's final states
