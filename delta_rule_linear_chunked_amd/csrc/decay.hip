@@ -308,6 +308,9 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
   float pre[Sp::RO], P[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) P[j] = tb.tile[j];
+  double W4[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) W4[j] = tb.whole[j];
   if constexpr (OWN || !Sh::VT) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -369,7 +372,7 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
       for (int e = 0; e < 3; ++e) vt[u][e] = tr.t[e];
     }
   };
-  const float G = P[0] * P[1] * P[2] * P[3];
+  const Factor G(W4[0] * W4[1] * W4[2] * W4[3]);
   // rows past the end fall outside the descriptor and are dropped
   const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
   if constexpr (NPV == 0) {
@@ -406,9 +409,7 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
     } else {
       const int w = s - NPV;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st[2 * w + i][e] *= G;
+      for (int i = 0; i < 2; ++i) G.scale(st[2 * w + i]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -465,17 +466,21 @@ __device__ __forceinline__ void state_store(const f32x4 (&st)[NT], float* dst, i
 // A chunk's token weights from its decays a (lane t: token t): the product of the decays behind the token (or, REV,
 // from the chunk's start through it) and of the whole chunk.
 template <bool REV>
-__device__ __forceinline__ float chunk_weight(float a, int lane, float& all) {
-  const float pre = row_prefix_prod(a), suf = row_suffix_prod_excl(a);
-  float P[4];
+__device__ __forceinline__ float chunk_weight(double a, int lane, double& all) {
+  const double pre = row_prefix(a);
+  double P[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    P[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, pre), 16 * j + 15));
-  float wt = REV ? pre : suf;
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, pre);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 16 * j + 15);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 16 * j + 15);
+    P[j] = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  }
+  double wt = REV ? pre : row_suffix_excl(a);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) wt *= (REV ? j < (lane >> 4) : j > (lane >> 4)) ? P[j] : 1.f;
+  for (int j = 0; j < 4; ++j) wt *= (REV ? j < (lane >> 4) : j > (lane >> 4)) ? P[j] : 1.;
   all = P[0] * P[1] * P[2] * P[3];
-  return wt;
+  return (float)wt;
 }
 // One piece of V or dO, its row scaled by f, as three bf16 terms into LDS
 template <typename T>
@@ -544,7 +549,7 @@ struct Filler {
       sv.store(buf + Sh::OFF_V, Sh::VB, rows, 16 * CT, tid);
     } else {
       sv.mask(rows, 16 * CT, tid);
-      float all;
+      double all;
       const float wt = chunk_weight<false>(lane < rows ? ac[lane] : 1.f, lane, all);
 #pragma unroll
       for (int i = 0; i < sv.NPC; ++i) {
@@ -656,7 +661,7 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
   f32x4 st[NT];
   state_load<W>(st, src, tile0, p.DK, p.DV, col, lane);
   const int first_chunk = sp.t0 / DCH;
-  float gall = 1.f;
+  double gall = 1.;
   __syncthreads();
   for (int c = 0; c < nc; ++c) {
     __syncthreads();
@@ -676,7 +681,7 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
     by_wave<Sp::G>(m, [&](auto M) {
       chunk_second<W, CT, InT, OUT, M.value>(buf, tb, st, oa, Pt, xch, oc, (int)o_ts, rows, ct, ln);
     });
-    if (local) gall *= tb.tile[0] * tb.tile[1] * tb.tile[2] * tb.tile[3];
+    if (local) gall *= tb.whole[0] * tb.whole[1] * tb.whole[2] * tb.whole[3];
     if (!local && p.snap && m < Sp::IS && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
       const int64_t per = p.T / DCH / p.snap_chunks;  // fixed length: snapshots per sequence
       const int64_t row = (p.cu ? p.snap_first[sp.n] : sp.n * per) + (first_chunk + c + 1) / p.snap_chunks - 1;
@@ -734,7 +739,7 @@ constexpr int state_buf() {
   return Terms<XT>::N * DC * W * 2 + 3 * DC * CT * 32;
 }
 template <int W, int CT, int DC, typename XT, typename YT, bool REV>
-__device__ __forceinline__ void state_body(const DecayParams& p, int local, unsigned char* smem, float* s_gam) {
+__device__ __forceinline__ void state_body(const DecayParams& p, int local, unsigned char* smem, double* s_gam) {
   constexpr int NPX = Terms<XT>::N;
   constexpr int IW = W / 16 < 4 ? W / 16 : 4, TI = W / 16 / IW, CW = 4 / IW, TC = CT / CW > 0 ? CT / CW : 1;
   constexpr int XB = DC * W * 2, YB = DC * CT * 32, BUF = NPX * XB + 3 * YB;
@@ -796,7 +801,7 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
     sx.store(buf, XB, rows, p.DK, tid);
     sy.mask(rows, 16 * CT, tid);
     if (lane >= DC || lane >= rows) a_next = 1.f;
-    float all;
+    double all;
     const float wt = chunk_weight<REV>(a_next, lane, all);
     if (tid == 0) s_gam[i % NB] = all;
 #pragma unroll
@@ -811,7 +816,7 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
     fetch(nc > 1 ? 1 : 0);
   }
   const int64_t cslot0 = (p.cu ? (local ? 0 : p.chunk_first[sp.n]) : (int64_t)sp.n * ((p.T + DC - 1) / DC)) + sp.t0 / DC;
-  float gall = 1.f;
+  double gall = 1.;
   for (int i = 0; i < nc; ++i) {
     __syncthreads();
     if constexpr (NB == 2) {
@@ -820,8 +825,9 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
     }
     if (!local) save((REV ? p.ds : p.cs) + ((cslot0 + chunk_of(i)) * p.H + h) * hsz);
     const unsigned char* buf = smem + (i % NB) * BUF;
-    const float G = s_gam[i % NB];
-    gall *= G;
+    const double all = s_gam[i % NB];
+    const Factor G(all);
+    gall *= all;
     if (active) {
       bf16x8 yf[TC][DC / 32][3];
 #pragma unroll
@@ -835,9 +841,7 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
       for (int ti = 0; ti < TI; ++ti) {
         const int t = wi * TI + ti;
 #pragma unroll
-        for (int tc = 0; tc < TC; ++tc)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st[tc][ti][e] *= G;
+        for (int tc = 0; tc < TC; ++tc) G.scale(st[tc][ti]);
 #pragma unroll
         for (int u = 0; u < DC / 32; ++u) {
           bf16x8 xf[NPX];
@@ -867,7 +871,7 @@ template <int W, int CT, int DC, typename XT>
 __global__ __launch_bounds__(256) void decay_state_kernel(const DecayParams p, int local) {
   constexpr int NB = Terms<XT>::N == 1 ? 2 : 1;
   __shared__ __align__(16) unsigned char smem[NB * state_buf<W, CT, DC, XT>()];
-  __shared__ float s_gam[NB];
+  __shared__ double s_gam[NB];
   if (blockIdx.y == 0)
     state_body<W, CT, DC, XT, XT, false>(p, local, smem, s_gam);
   else
@@ -905,10 +909,10 @@ __global__ __launch_bounds__(256) void decay_join_kernel(const DecayParams p) {
     f32x4* at = reinterpret_cast<f32x4*>(part + sl * hsz + e);
     if (j + 1 < ns) {
       const f32x4 own = *at;
-      const float G = (rev ? p.rgpart : p.gpart)[sl];
+      const double G = (rev ? p.rgpart : p.gpart)[sl];
       *at = x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = fmaf(G, x[i], own[i]);
+      for (int i = 0; i < 4; ++i) x[i] = (float)__builtin_fma(G, (double)x[i], (double)own[i]);
     } else {
       *at = x;
     }

@@ -189,7 +189,7 @@ Space fwd_space(const dr_decay_dims* d, const dr::DecayPlan& pl, bool packed) {
   const int64_t nh = pl.slots * d->num_heads;
   if (pl.nseg > 1) {
     s.part = s.take(nh * d->head_dim_k * d->head_dim_v * 4);
-    s.g = s.take(nh * 4);
+    s.g = s.take(nh * 8);
   }
   if (packed) s.tab = s.take((pl.slots + 3 * d->num_seqs + 2) * 4);
   return s;
@@ -208,9 +208,9 @@ Space bwd_space(const dr_decay_dims* d, const dr::DecayPlan& pl, bool packed) {
   s.ds = s.take(cslots * H * hsz * 4);
   if (pl.nseg > 1) {
     s.part = s.take(pl.slots * H * hsz * 4);
-    s.g = s.take(pl.slots * H * 4);
+    s.g = s.take(pl.slots * H * 8);
     s.rpart = s.take(pl.slots * H * hsz * 4);
-    s.rg = s.take(pl.slots * H * 4);
+    s.rg = s.take(pl.slots * H * 8);
   }
   if (d->num_k_heads != H) {
     s.pq = s.take(tokens * H * d->head_dim_k * 4);
@@ -307,7 +307,7 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
   if (st) return st;
   if (pl.nseg > 1) {
     p.part = reinterpret_cast<float*>(ws + sp.part);
-    p.gpart = reinterpret_cast<float*>(ws + sp.g);
+    p.gpart = reinterpret_cast<double*>(ws + sp.g);
   }
   if (packed) {
     p.slot_seq = reinterpret_cast<int32_t*>(ws + sp.tab);
@@ -395,9 +395,9 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   p.ds = f(sp.ds);
   if (pl.nseg > 1) {
     p.part = f(sp.part);
-    p.gpart = f(sp.g);
+    p.gpart = reinterpret_cast<double*>(ws + sp.g);
     p.rpart = f(sp.rpart);
-    p.rgpart = f(sp.rg);
+    p.rgpart = reinterpret_cast<double*>(ws + sp.rg);
   }
   if (dims->num_k_heads != H) {
     p.pq = f(sp.pq);

@@ -80,7 +80,9 @@ __global__ __launch_bounds__(256) void state_pack_kernel(const CacheParams p) {
         code = (uint32_t)w;
       }
     } else {
-      scale = fmaxf(amax / 127.f, 0x1p-126f);
+      // amax times the fp32 number next to 1/127 (within 1.5 roundings of amax / 127): the value that torch's division
+      // of a tensor by 127 gives on the GPU, so that caches written by such a program hold the same codes
+      scale = fmaxf(amax * (1.f / 127.f), 0x1p-126f);
       const float inv = __builtin_amdgcn_rcpf(scale);
       if (!bad)
 #pragma unroll

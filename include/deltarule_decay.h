@@ -110,7 +110,8 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
  * 8-bit state cache: fp32 states (of any recurrence of this library: a decode pool, a prefill's final states
  * or snapshots) written at a quarter of their size, and read back. A row is the d_v values of one key channel of
  * one head; it is held as d_v codes and one float32 scale, and stands for code * scale.
- *   DR_CACHE_INT8   scale = max(amax / 127, 2^-126), code = the integer nearest to x / scale (the exact quotient,
+ *   DR_CACHE_INT8   scale = max(amax * r, 2^-126) with r the float32 number next to 1/127, the product rounded to
+ *                   float32; code = the integer nearest to x / scale (the exact quotient,
  *                   ties to even)
  *   DR_CACHE_E4M3   scale = the least power of two, 2^-126 at the least, with amax <= 448 scale; code = x / scale
  *                   rounded to OCP e4m3 (nearest, ties to even)

@@ -105,7 +105,8 @@ def pack(S, fmt):
     top = np.where(bad, 0.0, top)
     x = np.where(bad[..., None], 0.0, S)
     if fmt == "int8":
-        scale = np.maximum((top / 127).astype(np.float32).astype(np.float64), 2.0 ** -126)
+        r = np.float64(np.float32(1) / np.float32(127))
+        scale = np.maximum((top * r).astype(np.float32).astype(np.float64), 2.0 ** -126)
         held = np.rint(x / scale[..., None])
     else:
         m, e = np.frexp(top)
