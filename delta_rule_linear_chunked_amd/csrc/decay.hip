@@ -5,13 +5,18 @@
 //
 //   O = Gamma . (Q S0) + ((Q K^T) . ratio) V,     S <- Gamma_C S0 + K^T (ratio(C, .) . V)
 //
-// One workgroup of 8 waves, with 4 more to fill the LDS, carries 16 CT value columns of one head through one segment of a sequence; the
-// waves of a column tile hold its d_k x 16 state in their accumulators for the whole segment. The
-// layouts are chosen so that nothing but the inputs goes through LDS: the accumulators of K^T V are, lane
+// One workgroup of 8 waves, with 4 more to fill the LDS, carries 16 CT value columns of one head through one
+// segment of a sequence; the waves of a column tile hold its d_k x 16 state in their accumulators for the whole
+// segment. The layouts are chosen so that nothing but the inputs goes through LDS: the accumulators of K^T V are, lane
 // for lane, the S^T operand of Q S0, and the accumulators of K Q^T are the P^T operand of P V (common
 // index orders of the 32-deep products, see decay.hpp), so O^T comes out with 4 consecutive columns per
-// lane and the state never leaves the registers. With fewer column tiles than waves, 4 / CT waves
-// hold the same state columns and share the chunk's 16-token row tiles.
+// lane and the state never leaves the registers. With fewer column tiles than waves, 8 / CT waves share a
+// tile: they split the state's channels, then the chunk's 16-token row tiles.
+//
+// What bounds it: a chunk's two phases (Q S0 and the scores; P V and the state) follow one another through
+// barriers, with LDS reads and the cutting of the state and of scaled V into bf16 terms beside the MFMA. 4 x 4096
+// tokens, 16 heads, d = 128, bf16: main pass 92 us, states of the segments of 1024 tokens 36, join 7; all told 139,
+// where the inputs and outputs alone take 66 at the copy rate.
 #include <type_traits>
 
 #include "decay.hpp"
