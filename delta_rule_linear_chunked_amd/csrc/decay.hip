@@ -739,6 +739,18 @@ static hipError_t launch_main(const DecayParams& p, const DecayPlan& pl, int loc
 //   CHUNKS: the state at each chunk's start (reverse: the gradient at its end) into cs / ds, from the
 //           segment's start state
 // ---------------------------------------------------------------------------
+// The state pass's accumulators hold the state's transpose (columns 4 (l / 16) + i of a column tile, channel by frag_chan
+// in lane l % 16), so that a lane loads and stores 16 bytes of a row.
+template <int W, bool STORE, class P>
+__device__ __forceinline__ void state_rows(f32x4& st, P* at, int t, int DK, int DV, int col0, int lane) {
+  const int r16 = lane & 15, ch = 32 * (t >> 1) + 8 * (r16 >> 2) + 4 * (t & 1) + (r16 & 3);
+  if (W == 32 && ch >= DK) return;
+  if constexpr (STORE)
+    *reinterpret_cast<f32x4*>(at + ch * DV + col0 + 4 * (lane >> 4)) = st;
+  else
+    st = *reinterpret_cast<const f32x4*>(at + ch * DV + col0 + 4 * (lane >> 4));
+}
+
 template <int W, int CT, int DC, typename XT>
 constexpr int state_buf() {
   return Terms<XT>::N * DC * W * 2 + 3 * DC * CT * 32;
@@ -777,13 +789,20 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
       src = (REV ? p.dST : p.S0) + ((int64_t)sp.n * p.H + h) * hsz;
   }
   f32x4 st[TC][TI];
-  const int t0 = wi * TI, col0 = cb * 16 * CT + 16 * wc * TC + (lane & 15);
+  const int t0 = wi * TI, col0 = cb * 16 * CT + 16 * wc * TC;
 #pragma unroll
-  for (int tc = 0; tc < TC; ++tc) state_load<W>(st[tc], active ? src : nullptr, t0, p.DK, p.DV, col0 + 16 * tc, lane);
+  for (int tc = 0; tc < TC; ++tc)
+#pragma unroll
+    for (int ti = 0; ti < TI; ++ti) {
+      st[tc][ti] = f32x4{0, 0, 0, 0};
+      if (active && src) state_rows<W, false>(st[tc][ti], src, t0 + ti, p.DK, p.DV, col0 + 16 * tc, lane);
+    }
   auto save = [&](float* dst) {
     if (!active) return;
 #pragma unroll
-    for (int tc = 0; tc < TC; ++tc) state_store<W>(st[tc], dst, t0, p.DK, p.DV, col0 + 16 * tc, lane);
+    for (int tc = 0; tc < TC; ++tc)
+#pragma unroll
+      for (int ti = 0; ti < TI; ++ti) state_rows<W, true>(st[tc][ti], dst, t0 + ti, p.DK, p.DV, col0 + 16 * tc, lane);
   };
 
   Stage<W, XT, DC> sx;
@@ -853,7 +872,7 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
 #pragma unroll
           for (int e = 0; e < NPX; ++e) xf[e] = frag_chan<W>(buf + e * XB, t >> 1, t & 1, u, lane);
 #pragma unroll
-          for (int tc = 0; tc < TC; ++tc) mma(st[tc][ti], xf, yf[tc][u]);
+          for (int tc = 0; tc < TC; ++tc) mma(st[tc][ti], yf[tc][u], xf);
         }
       }
     }
