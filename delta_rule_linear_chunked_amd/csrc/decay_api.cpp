@@ -128,11 +128,16 @@ int64_t env_int(const char* name) {
 }
 
 // Segments and column blocks. A workgroup of the main pass fills a CU and carries one segment of one head; a
-// segment's own state, needed when a sequence has more than one, costs it 0.42 of the main pass again (40 and 95 us on
-// 4 x 4096 tokens, 16 heads, d = 128 in segments of 1024). Of the segment lengths from 512 tokens up the one with
-// the least (rounds of 256 workgroups) x (tokens of a segment + 192) x (1 or 1.42) is taken: for that problem 1024 tokens,
-// 131 us (512: 152, 2048: 212, whole sequences 268).
-// The backward's state passes take 32 columns per workgroup, two of which share a CU with one for each direction.
+// segment's own state, needed when a sequence has more than one, costs it 0.42 of the main pass again. In units of a
+// token's time (0.034 us in bf16) the call takes about
+//   (rounds of 256 workgroups) x (tokens of a segment + 256) x (1 or 1.42) + (0 or 250 + 8 x segments)
+// with the launches and the joining walk last; the segment length with the least is taken. Measured, us (all inputs
+// bf16, d = 128, but the third): 4 x 4096 tokens, 16 heads: 1024 tokens 135, 512 154, 2048 169, whole sequences
+// 184; 1000 tokens, 4 heads: 128 tokens 23, 256 30, whole 43; 3 x 1333 tokens, 6 heads, fp32, d = 64 / 32: 128 tokens 30, 64 39,
+// 256 38, whole 84; 512 tokens, 16 heads: whole 24, 128 tokens 25.
+// The backward's state passes take 32 columns per workgroup, two of which share a CU with one for each direction; a
+// token takes them 0.012 us in bf16, 0.04 in fp32, which scales the launches' share. 4000 tokens, 4 heads, d = 64,
+// bf16: 256 tokens 42, 128 49, 1024 59, whole 81; 4 x 4096, 16 heads, d = 128: whole 593, 2048 664.
 dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   dr::DecayPlan pl{};
   const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads, T = d->seqlen;
@@ -140,16 +145,18 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   // all columns in one workgroup (fp32 data, three times as large, in one or two tiles)
   const int most = bf16 ? (int)tiles : tiles >= 2 && d->head_dim_k < 128 ? 2 : 1;
   const int64_t blocks = backward ? (tiles + 1) / 2 : tiles / most;
-  const double again = backward ? 1.7 : 1.42;
+  const double start = backward ? 128 : 256, again = !backward ? 1.42 : bf16 ? 2 : 1.65;
+  const double launches = backward && bf16 ? 800 : 250, step = backward && bf16 ? 25 : 8;
   int64_t seg = (T + 63) / 64 * 64;
   double best = 0;
-  for (int64_t n = 1; n == 1 || n * 512 <= T; ++n) {
+  for (int64_t n = 1; n == 1 || (n * 128 < T + 128 && n * pairs * blocks <= 8192); ++n) {
     const int64_t s = ((T + n - 1) / n + 63) / 64 * 64, nseg = s > 0 ? (T + s - 1) / s : 1;
     // (packed lengths are not known here: half a segment per sequence for their ragged ends)
     const double wgs = (packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg) * d->num_heads * blocks;
-    // (uneven segments fill a last round's gaps; 192 tokens' time for a workgroup's start and end)
-    const double rounds = wgs <= 256 ? 1 : packed || wgs > 8192 ? wgs / 256 + 0.5 : (double)(int64_t)((wgs + 255) / 256);
-    const double cost = rounds * (s + 192) * (nseg > 1 ? again : 1.0);
+    // (packed: half a round more than the expected number, which is all that is known)
+    double rounds = packed || wgs > 8192 ? wgs / 256 + 0.5 : (double)(int64_t)((wgs + 255) / 256);
+    if (rounds < 1) rounds = 1;
+    const double cost = rounds * (s + start) * (nseg > 1 ? again : 1.0) + (nseg > 1 ? launches + step * nseg : 0.0);
     if (best == 0 || cost < best) {
       best = cost;
       seg = s;
