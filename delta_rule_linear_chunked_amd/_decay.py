@@ -11,6 +11,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _DT, _Opts, _capturing, _check, _need, _need_rows, check_offsets, load_library, snapshot_count
 
@@ -266,6 +267,7 @@ class _DecayAttention(torch.autograd.Function):
         return o, S_T
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dO, dS_T):
         q, k, v, alpha, S0, cu_seqlens = ctx.saved_tensors
         new = torch.empty if cu_seqlens is None else torch.zeros

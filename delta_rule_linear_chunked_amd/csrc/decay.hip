@@ -379,7 +379,8 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
   };
   const Factor G(W4[0] * W4[1] * W4[2] * W4[3]);
   // rows past the end fall outside the descriptor and are dropped
-  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (rows < DCH ? rows : DCH) * o_ts * 4, 0x00020000);
+  // (32-bit offsets: at most 64 rows of 2^16 heads of 128 columns of 4 bytes, 2^31)
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o, 0, (int)((uint32_t)(rows < DCH ? rows : DCH) * (uint32_t)o_ts * 4u), 0x00020000);
   if constexpr (NPV == 0) {
     scale(0);
     scale(1);
@@ -407,7 +408,7 @@ __device__ __forceinline__ void chunk_second(const unsigned char* buf, const Dec
         const int R = i ? R1 : R0;
         if (R >= 0 && u == R / 2)  // the row tile is complete
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, oa[j + i < Sp::RO ? j + i : 0]), rsrc,
-                                                 ((16 * R + r16) * o_ts + 16 * ct + 4 * g) * 4, 0, 0);
+                                                 (int)(((uint32_t)(16 * R + r16) * (uint32_t)o_ts + 16 * ct + 4 * g) * 4u), 0, 0);
       }
       if (s == 0) scale(0);
       if (s == (NPV > 1 ? 1 : 0)) scale(1);

@@ -85,7 +85,8 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
 /*
  * One token for each of N sequences x H heads, the states updated in place.
  *   q, k [N, Hk, d_k], v [N, H, d_v] in_dtype;  alpha float32 [N, H] or [H];  S [N, H, d_k, d_v] (or the pool,
- *   with opts->state_idx: a slot outside it gives o = 0 and touches no state);  o [N, H, d_v] float32
+ *   with opts->state_idx: a slot outside it gives o = 0 and touches no state, two
+ *   sequences naming the same slot race);  o [N, H, d_v] float32
  * dims: batch = num_seqs = N, seqlen = 1. Uses no other device memory.
  */
 int dr_decay_step(const void* q, const void* k, const void* v, const float* alpha, float* S, float* o,

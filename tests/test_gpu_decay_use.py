@@ -293,3 +293,60 @@ def test_captured_gradients():
         again = [a.detach().requires_grad_() for a in leaves]  # eager work between the replays
         eager = torch.autograd.grad(drl.decay_attention(*again), again, (w, wS))
         assert all(torch.equal(a, b) for a, b in zip(eager, want)), f"eager {r}"
+
+
+def test_second_derivatives_are_refused():
+    x = make(67, 1, 20, 2, 2, 16, 16, "f32", "token")
+    leaves = [a.requires_grad_() for a in tensors(x, "f32").values()]
+    o, _ = drl.decay_attention(*leaves)
+    g, = torch.autograd.grad(o.square().sum(), leaves[:1], create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
+def test_offsets_past_32_bits(monkeypatch):
+    # 2^31 elements of v, of the outputs and of the pool lie before what is checked: the last tokens of a long row that
+    # is zero up to them, and the last slots of a pool
+    H, Hk, d, tail = 128, 2, 128, 150
+    T = 64 * 2049 + tail
+    x = make(70, 1, tail, H, Hk, d, d, "bf16", "token", s0=False)
+    t = tensors(x, "bf16")
+    big = {n: torch.zeros((1, T) + tuple(t[n].shape[2:]), dtype=t[n].dtype, device="cuda") for n in NAMES}
+    for n in NAMES:
+        big[n][:, T - tail:] = t[n]
+    assert big["v"].numel() - tail * H * d > 2 ** 31
+    heads = [0, 1, H - 1]
+    pick = lambda a, hk: a[:, :, [h // (H // Hk) for h in heads]] if hk else a[:, :, heads]  # noqa: E731
+    small = [pick(x["q"], True), pick(x["k"], True), pick(x["v"], False), pick(x["alpha"], False)]
+    zero = np.zeros((1, len(heads), d, d), np.float32)
+    o, S = drl.decay_fwd(*[big[n] for n in NAMES])
+    want, wS = oracle.forward(*small, zero)
+    mo, mS = oracle.forward(*small, zero, magnitudes=True)
+    close(o[:, T - tail:, heads], want, mo, tail, "o")
+    close(S[:, heads], wS, mS, tail, "S")
+    del o
+    dO = torch.zeros(1, T, H, d, device="cuda")
+    dO[:, T - tail:] = torch.randn(1, tail, H, d, device="cuda")
+    monkeypatch.setenv("DR_DECAY_SEG", str(1 << 20))  # one segment: the tail's chunks are then the same work in both
+    g = drl.decay_bwd(*[big[n] for n in NAMES], dO=dO)
+    part = drl.decay_bwd(*[t[n] for n in NAMES], S0=torch.zeros(1, H, d, d, device="cuda"), dO=dO[:, T - tail:].contiguous())
+    for n in ("dv", "dq", "dk", "dalpha"):
+        assert torch.equal(g[n][:, T - tail:], part[n]), n
+        assert (g[n][:, :T - tail] == 0).all(), n
+    del g, dO, big
+    slots = 4 + 2 ** 31 // (32 * d * d)
+    pool = torch.zeros(slots, 32, d, d, device="cuda")
+    idx = i32([slots - 1, 0, slots - 2])
+    y = make(71, 1, 3, 32, 32, d, d, "bf16", "token", n=3)
+    u = tensors(y, "bf16")
+    pool[idx.long()] = u["S0"]
+    one = [u[n][0] for n in NAMES]
+    S1 = u["S0"].clone()
+    assert torch.equal(drl.decay_step(*one, pool, state_idx=idx), drl.decay_step(*one, S1))
+    assert torch.equal(pool[idx.long()], S1)
+    codes = torch.zeros(slots, 32, d, d, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(slots, 32, d, device="cuda")
+    drl.dr_state_pack(pool, codes, scales, slot_idx=idx, state_idx=idx)
+    back = torch.zeros(3, 32, d, d, device="cuda")
+    drl.dr_state_unpack(codes, scales, back, slot_idx=idx, state_idx=i32([0, 1, 2]))
+    assert torch.equal(back, drl.state_unpack(*drl.state_pack(S1)))
