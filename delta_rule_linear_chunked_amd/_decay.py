@@ -67,7 +67,7 @@ def _call(lib, entry, device, *args):
     if device.type != "cuda":  # the library has nothing to launch on
         raise ValueError(f"{entry}: tensors must be on a GPU, got {device}")
     fn = getattr(lib, entry)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):  # the library launches on the current device
@@ -81,6 +81,11 @@ def _workspace(lib, d, dev, packed, backward):
     n = ctypes.c_int64()
     _check(lib, lib.dr_decay_workspace(ctypes.byref(d), packed, backward, ctypes.byref(n)), "dr_decay_workspace")
     return torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+
+
+def _like(t, dtype=torch.float32):
+    """An uninitialised dense tensor of t's shape (a third of the time of ``torch.empty``)."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _addr(t):
@@ -105,21 +110,28 @@ def _inputs(q, k, v, alpha, lead):
     block, num_seqs that of unpacked inputs."""
     _ranks(q, v, alpha, lead)
     dev, dtype, qs, vs = q.device, q.dtype, q.shape, v.shape
-    first = tuple(qs[:lead])
-    Hk, dk = qs[lead:]
-    H, dv = vs[lead:]
+    if lead == 2:
+        B, T, Hk, dk = qs
+        vB, vT, H, dv = vs
+        first = (B, T)
+    else:
+        B, Hk, dk = qs
+        vB, H, dv = vs
+        T = vT = 1
+        first = (B,)
     if dtype not in _DT:
         raise ValueError(f"q dtype {dtype} is not float32 or bfloat16")
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"{H} value heads are not a multiple of {Hk} query/key heads")
     strides = None
-    if not (q.is_contiguous() and _is(k, qs, dtype, dev) and _is(v, first + (H, dv), dtype, dev)):
+    if not (vB == B and vT == T and q.is_contiguous() and v.is_contiguous() and v.dtype is dtype and v.device == dev
+            and _is(k, qs, dtype, dev)):
         strides = (_need_rows(q, "q", first + (Hk, dk), lead, dtype, dev),
                    _need_rows(k, "k", first + (Hk, dk), lead, dtype, dev),
                    _need_rows(v, "v", first + (H, dv), lead, dtype, dev))
     per_head = alpha.dim() == 1
     _require(alpha, "alpha", (H,) if per_head else first + (H,), torch.float32, dev)
-    d = _DecayDims(first[0], first[1] if lead == 2 else 1, H, Hk, dk, dv, first[0], _DT[dtype], int(per_head), 0, 0)
+    d = _DecayDims(B, T, H, Hk, dk, dv, B, _DT[dtype], int(per_head), 0, 0)
     if strides is not None:
         d.strided = 1
         (d.q_token_stride, d.q_batch_stride), (d.k_token_stride, d.k_batch_stride), \
@@ -180,10 +192,13 @@ def decay_fwd(q, k, v, alpha, S0=None, cu_seqlens=None, output_final_state: bool
     B, T, _, dk = q.shape
     H, dv = v.shape[-2:]
     N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    new = lambda *s: torch.empty(s, dtype=torch.float32, device=q.device)  # noqa: E731
     if state_idx is not None and S0 is None:
         raise ValueError("state_idx needs the pool of states as S0")
-    S_T = S0 if state_idx is not None else (new(N, H, dk, dv) if output_final_state else None)
+    S_T = None
+    if state_idx is not None:
+        S_T = S0
+    elif output_final_state:
+        S_T = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device) if S0 is None else _like(S0)
     snaps = None
     if snapshot_every is not None:
         if cu_seqlens is None:
@@ -192,8 +207,8 @@ def decay_fwd(q, k, v, alpha, S0=None, cu_seqlens=None, output_final_state: bool
             raise ValueError("snapshots of packed sequences need cu_seqlens on the host: not inside a graph capture")
         else:
             lens = check_offsets(cu_seqlens, T)
-        snaps = new(snapshot_count(lens, snapshot_every), H, dk, dv)
-    o = new(B, T, H, dv) if output else None
+        snaps = torch.empty((snapshot_count(lens, snapshot_every), H, dk, dv), dtype=torch.float32, device=q.device)
+    o = _like(v) if output else None
     dr_decay_fwd(q, k, v, alpha, S0, cu_seqlens, o, S_T, state_idx, snaps, snapshot_every or 0)
     return (o, S_T) if snapshot_every is None else (o, S_T, snaps)
 
@@ -216,7 +231,7 @@ def dr_decay_step(q, k, v, alpha, S, o, state_idx=None) -> None:
 
 def decay_step(q, k, v, alpha, S, state_idx=None):
     """Allocates ``o`` and runs ``dr_decay_step`` (S, or its rows ``state_idx``, updated in place). Returns o."""
-    o = torch.empty(tuple(v.shape), dtype=torch.float32, device=q.device)
+    o = _like(v)
     dr_decay_step(q, k, v, alpha, S, o, state_idx)
     return o
 
@@ -243,10 +258,13 @@ def decay_bwd(q, k, v, alpha, S0=None, cu_seqlens=None, dO=None, dS_T=None, need
     """Allocates the gradients and runs ``dr_decay_bwd``. Returns a dict with dq, dk, dv, dalpha and dS0 (None unless
     ``need_dS0``). Rows past the last packed sequence are not written."""
     _ranks(q, v, alpha, 2)
-    new = lambda s: torch.empty(tuple(s), dtype=torch.float32, device=q.device)  # noqa: E731
-    N = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    g = dict(dq=new(q.shape), dk=new(k.shape), dv=new(v.shape), dalpha=new(alpha.shape),
-             dS0=new((N, v.shape[2], q.shape[3], v.shape[3])) if need_dS0 else None)
+    dS0 = None
+    if need_dS0 and S0 is not None:
+        dS0 = _like(S0)
+    elif need_dS0:
+        N = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+        dS0 = torch.empty((N, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=q.device)
+    g = dict(dq=_like(q), dk=_like(k), dv=_like(v), dalpha=_like(alpha), dS0=dS0)
     dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, dS_T, g["dq"], g["dk"], g["dv"], g["dalpha"], g["dS0"])
     return g
 
@@ -333,7 +351,7 @@ def state_pack(S, fmt: str = "int8"):
     """``S`` [N,H,dk,dv] in 8 bits: (codes, scales), a cache of N slots."""
     if fmt not in CACHE_FORMATS:
         raise ValueError(f"unknown cache format {fmt!r}")
-    codes = torch.empty(tuple(S.shape), dtype=CACHE_FORMATS[fmt][1], device=S.device)
+    codes = _like(S, CACHE_FORMATS[fmt][1])
     scales = torch.empty(tuple(S.shape[:-1]), dtype=torch.float32, device=S.device)
     dr_state_pack(S, codes, scales)
     return codes, scales
