@@ -691,7 +691,9 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
     if (!local && p.snap && m < Sp::IS && rows >= DCH && (first_chunk + c + 1) % p.snap_chunks == 0) {
       const int64_t per = p.T / DCH / p.snap_chunks;  // fixed length: snapshots per sequence
       const int64_t row = (p.cu ? p.snap_first[sp.n] : sp.n * per) + (first_chunk + c + 1) / p.snap_chunks - 1;
-      state_store<W>(st, p.snap + (row * p.H + h) * hsz, tile0, p.DK, p.DV, col, lane);
+      int cl = col, dv = p.DV;  // (formed here, not kept over the loop: see above)
+      asm volatile("" : "+v"(cl), "+s"(dv));
+      state_store<W>(st, p.snap + (row * p.H + h) * hsz, tile0, p.DK, dv, cl, ln);
     }
     if constexpr (NB == 1) __syncthreads();
   }

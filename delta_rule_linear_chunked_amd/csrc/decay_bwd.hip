@@ -356,16 +356,19 @@ __global__ __launch_bounds__(512) void decay_grad_kernel(const DecayParams p) {
         for (int u = 0; u < UV; ++u) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) z = fmaf(sx[u][j], gx[u][j], z);
-          const Tri sf = split3(sx[u]), gf = split3(gx[u]);
+          const Tri sf = split3(sx[u]);
           bf16x8 of[NT][3], vf[NT][NP];
 #pragma unroll
-          for (int r = 0; r < NT; ++r) {
+          for (int r = 0; r < NT; ++r)
 #pragma unroll
             for (int i = 0; i < 3; ++i) of[r][i] = frag_rows<V>(Ot + i * Sh::VO, 16 * r, u, lane);
+          mma_rows(aq[ti], sf.t, of);
+          fence();  // (both products' operands at once do not fit the registers)
+          const Tri gf = split3(gx[u]);
+#pragma unroll
+          for (int r = 0; r < NT; ++r)
 #pragma unroll
             for (int i = 0; i < NP; ++i) vf[r][i] = frag_rows<V>(Vt + i * Sh::VO, 16 * r, u, lane);
-          }
-          mma_rows(aq[ti], sf.t, of);
           mma_rows(ak[ti], gf.t, vf);
         }
         // X_r, Y_s from these channels, then the chunk's ends
