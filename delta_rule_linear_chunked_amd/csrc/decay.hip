@@ -147,9 +147,15 @@ __device__ __forceinline__ bf16x8 frag_v(const unsigned char* tile, int n, int u
   return join(a, b);
 }
 
-// P = (Q K^T) . ratio of tile (R, S) as bf16 terms into LDS, rows r
+// P = (Q K^T) . ratio of tile (R, S) as bf16 terms into LDS, rows r. Q's rows are kept for the tiles of a row, but
+// for the widest fp32 heads, whose three terms do not fit the registers beside the loads on their way: there
+// every tile reads them again.
+template <int W, typename InT>
+constexpr bool keep_rows() {
+  return Terms<InT>::N * W <= 256;
+}
 template <int W, int CT, typename InT, int R, int S>
-__device__ __forceinline__ void score_tile(const unsigned char* buf, const DecayTab& tb, const Op<Terms<InT>::N> (&qf)[W / 32],
+__device__ __forceinline__ void score_tile(const unsigned char* qbuf, const unsigned char* buf, const DecayTab& tb, const Op<Terms<InT>::N> (&qf)[W / 32],
                                            unsigned char* Pt, int lane) {
   using Sh = MainShape<W, CT, InT>;
   constexpr int NP = Sh::NP;
@@ -160,7 +166,15 @@ __device__ __forceinline__ void score_tile(const unsigned char* buf, const Decay
     Op<NP> kf;
 #pragma unroll
     for (int i = 0; i < NP; ++i) kf.t[i] = frag_rows<W>(buf + i * Sh::QK, 16 * S, u, lane);
-    mma(sc, kf.t, qf[u].t);
+    if constexpr (keep_rows<W, InT>()) {
+      mma(sc, kf.t, qf[u].t);
+    } else {
+      Op<NP> qr;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) qr.t[i] = frag_rows<W>(qbuf + i * Sh::QK, 16 * R, u, lane);
+      mma(sc, kf.t, qr.t);
+      fence();
+    }
   }
   if constexpr (S == R) {
     const f32x4 in = *reinterpret_cast<const f32x4*>(&tb.in[S][r16 * LDP + 4 * g]);
@@ -179,6 +193,7 @@ __device__ __forceinline__ void score_tile(const unsigned char* buf, const Decay
 template <int W, typename InT, int R>
 __device__ __forceinline__ void score_rows(const unsigned char* buf, Op<Terms<InT>::N> (&qf)[W / 32], int lane) {
   constexpr int NP = Terms<InT>::N;
+  if constexpr (!keep_rows<W, InT>()) return;
 #pragma unroll
   for (int u = 0; u < W / 32; ++u)
 #pragma unroll
@@ -239,12 +254,12 @@ __device__ __forceinline__ void scores(const unsigned char* qbuf, const unsigned
   Op<Terms<InT>::N> qf[W / 32];
   constexpr int R = WV < 2 ? 3 : WV == 2 ? 2 : 1, S0 = WV == 1 ? 2 : 0;
   score_rows<W, InT, R>(qbuf, qf, lane);
-  score_tile<W, CT, InT, R, S0>(buf, tb, qf, Pt, lane);
-  score_tile<W, CT, InT, R, S0 + 1>(buf, tb, qf, Pt, lane);
-  if constexpr (WV == 2) score_tile<W, CT, InT, R, 2>(buf, tb, qf, Pt, lane);
+  score_tile<W, CT, InT, R, S0>(qbuf, buf, tb, qf, Pt, lane);
+  score_tile<W, CT, InT, R, S0 + 1>(qbuf, buf, tb, qf, Pt, lane);
+  if constexpr (WV == 2) score_tile<W, CT, InT, R, 2>(qbuf, buf, tb, qf, Pt, lane);
   if constexpr (WV == 0) {
     score_rows<W, InT, 0>(qbuf, qf, lane);
-    score_tile<W, CT, InT, 0, 0>(buf, tb, qf, Pt, lane);
+    score_tile<W, CT, InT, 0, 0>(qbuf, buf, tb, qf, Pt, lane);
   }
 }
 
