@@ -15,8 +15,8 @@
 //
 // What bounds it: a chunk's two phases (Q S0 and the scores; P V and the state) follow one another through
 // barriers, with LDS reads and the cutting of the state and of scaled V into bf16 terms beside the MFMA. 4 x 4096
-// tokens, 16 heads, d = 128, bf16: main pass 92 us, states of the segments of 1024 tokens 36, join 7; all told 139,
-// where the inputs and outputs alone take 66 at the copy rate.
+// tokens, 16 heads, d = 128, bf16: main pass 89 us (4.2 TB/s; MFMA busy a third of the time), states of the segments of
+// 1024 tokens 37, join 7; all told 132 to 139, where the inputs and outputs alone take 66 at the copy rate.
 #include <type_traits>
 
 #include "decay.hpp"

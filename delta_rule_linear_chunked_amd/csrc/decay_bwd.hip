@@ -17,9 +17,9 @@
 // All products are fp32-grade: fp32 operands are cut into three bf16 terms (decay.hpp).
 //
 // What bounds it: S and G in fp32 for every chunk, read once each (131 KB a chunk of 64 tokens at d = 128, beside
-// 114 KB of inputs and gradients), and one workgroup a CU (162 KB of LDS), whose loads and products do not
-// overlap those of another. 4 x 4096 tokens, 16 heads, d = 128, bf16: 374 us (the bytes alone take 240 at the copy
-// rate; four waves that took the two halves of the work in turn: 489), after 217 us of the state passes.
+// 180 KB of inputs and gradients), and one workgroup a CU (162 KB of LDS), whose loads and products do not
+// overlap those of another. 4 x 4096 tokens, 16 heads, d = 128, bf16: 350 us, 3.8 TB/s (a copy 5.2; four waves that took
+// the two halves of the work in turn 489, with 13 registers spilled 376), after 217 us of the state passes (4.2 TB/s).
 #include "decay.hpp"
 #include "launch.hpp"
 
