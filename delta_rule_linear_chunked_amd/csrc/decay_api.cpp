@@ -163,7 +163,7 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
     }
   }
   if (const int64_t s = env_int("DR_DECAY_SEG"))
-    if (s > 0) seg = (s + 63) / 64 * 64;
+    if (s > 0 && s <= INT32_MAX - 63) seg = (s + 63) / 64 * 64;
   if (seg < 64) seg = 64;
   pl.seg = seg;
   pl.nseg = (T + seg - 1) / seg;
