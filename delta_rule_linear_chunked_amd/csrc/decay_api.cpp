@@ -149,7 +149,9 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   const double launches = backward && bf16 ? 800 : 250, step = backward && bf16 ? 25 : 8;
   int64_t seg = (T + 63) / 64 * 64;
   double best = 0;
-  for (int64_t n = 1; n == 1 || (n * 128 < T + 128 && n * pairs * blocks <= 8192); ++n) {
+  // (the limit keeps the segments' states within 1 GiB or the final states' size; from 16 on every value of n is not tried)
+  const auto many = [&](int64_t n) { return (packed ? (n + d->num_seqs) * d->num_heads : n * pairs) * blocks > 16384; };
+  for (int64_t n = 1; n == 1 || (n * 128 < T + 128 && !many(n)); n += 1 + n / 16) {
     const int64_t s = ((T + n - 1) / n + 63) / 64 * 64, nseg = s > 0 ? (T + s - 1) / s : 1;
     // (packed lengths are not known here: half a segment per sequence for their ragged ends)
     const double wgs = (packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg) * d->num_heads * blocks;
