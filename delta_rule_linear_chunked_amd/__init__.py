@@ -128,6 +128,12 @@ def load_library(path: Optional[str] = None):
     lib.dr_chunk_bwd_ex.argtypes = [vp, vp, vp, fp, fp, fp, ip, fp, vp, fp, fp, fp, fp, fp, fp, fp, fp, fp, fp,
                                     ctypes.POINTER(_Dims), vp]
     lib.dr_chunk_bwd_ex.restype = ip
+    lib.dr_chunk_workspace.argtypes = [ctypes.POINTER(_Dims), ip, ip, ip, ctypes.POINTER(ctypes.c_int64)]
+    lib.dr_chunk_workspace.restype = ip
+    for ex, ws in (("dr_chunk_fwd_ex", "dr_chunk_fwd_ws"), ("dr_chunk_bwd_ex", "dr_chunk_bwd_ws")):
+        fn = getattr(lib, ws)
+        fn.argtypes = getattr(lib, ex).argtypes[:-1] + [vp, ctypes.c_int64, vp]
+        fn.restype = ip
     lib.dr_status_string.argtypes = [ip]
     lib.dr_status_string.restype = ctypes.c_char_p
     lib.dr_last_error.argtypes = []
@@ -271,6 +277,19 @@ def _capturing() -> bool:
     return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
 
 
+def _captured_workspace(lib, d, variant: str, packed: bool, backward: int, device):
+    """For a call that is being captured: its workspace from torch's allocator, which then belongs to the graph, as
+    the arguments of the ``_ws`` entry points (the library's pool is refused in a capture). None otherwise.
+    ``backward`` as for dr_chunk_workspace; called with ``device`` current."""
+    if not _capturing():
+        return None
+    n = ctypes.c_int64()
+    _check(lib, lib.dr_chunk_workspace(_dims_arg(d), VARIANTS[variant], int(packed), backward, ctypes.byref(n)),
+           "dr_chunk_workspace")
+    buf = torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
+    return buf, (_ptr(buf), n.value)
+
+
 def dr_chunk_fwd(q, k, v, alpha, erase, write, variant: str, S0, cu_seqlens, o, S_T) -> None:
     """Chunkwise prefill into caller-provided ``o`` (and ``S_T``). Shapes as in
     include/deltarule.h: q,k [B,T,H,dk]; v [B,T,H,dv]; alpha [B,T,H,dk] fp32; gates per
@@ -352,9 +371,13 @@ def _chunk_fwd_call(entry, q, k, v, alpha, erase, write, variant, S0, cu_seqlens
     d = _dims_for(B, T, H, dk, dv, N, q.dtype, strides)
     opts = _opts(state_idx, rows, snapshots, snapshot_every, prep, alpha)
     with torch.cuda.device(dev):  # the library launches on the current device
-        st = getattr(lib, entry)(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write),
-                                 VARIANTS[variant], _ptr(S0), _ptr(cu_seqlens), _ptr(o), _ptr(S_T),
-                                 _dims_arg(d), ctypes.byref(opts), _stream(dev))
+        space = None
+        if entry == "dr_chunk_fwd_ex":
+            space = _captured_workspace(lib, d, variant, cu_seqlens is not None, 0, dev)
+        fn = getattr(lib, entry) if space is None else lib.dr_chunk_fwd_ws
+        st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant], _ptr(S0),
+                _ptr(cu_seqlens), _ptr(o), _ptr(S_T), _dims_arg(d), ctypes.byref(opts),
+                *(() if space is None else space[1]), _stream(dev))
     _check(lib, st, entry)
 
 
@@ -494,10 +517,12 @@ def dr_chunk_bwd(q, k, v, alpha, erase, write, variant: str, S0, cu_seqlens, dO,
         _need(checkpoints, "checkpoints", (rows, H, dk_, dv_), torch.float32, dev)
     d = _dims_for(B, T, H, dk_, dv_, N, q.dtype, strides)
     with torch.cuda.device(dev):
-        st = lib.dr_chunk_bwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant],
-                                 _ptr(S0), _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv),
-                                 _ptr(dalpha), _ptr(derase), _ptr(dwrite), _ptr(dS0), _ptr(checkpoints),
-                                 _dims_arg(d), _stream(dev))
+        space = _captured_workspace(lib, d, variant, cu_seqlens is not None, 1 if checkpoints is None else 2, dev)
+        fn = lib.dr_chunk_bwd_ex if space is None else lib.dr_chunk_bwd_ws
+        st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant],
+                _ptr(S0), _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv),
+                _ptr(dalpha), _ptr(derase), _ptr(dwrite), _ptr(dS0), _ptr(checkpoints),
+                _dims_arg(d), *(() if space is None else space[1]), _stream(dev))
     _check(lib, st, "dr_chunk_bwd")
 
 

@@ -128,8 +128,9 @@ int check_ptrs(std::initializer_list<std::pair<const void*, const char*>> req,
   return DR_OK;
 }
 
-// Workspace pool of the prefill (per device): stream-ordered allocations that stay cached in
-// the pool between calls, so steady-state calls do not reach the device allocator.
+// Workspace pool of the library (per device): stream-ordered allocations that stay cached in
+// the pool between calls, so steady-state calls do not reach the device allocator. Taken through
+// dr::host_space alone, which keeps it out of captures.
 hipError_t workspace_alloc(size_t bytes, hipStream_t stream, void** ptr) {
   static std::mutex mu;
   static hipMemPool_t pools[256] = {};
@@ -205,7 +206,33 @@ int host_fail(int status, const char* fmt, ...) {
   return status;
 }
 
-hipError_t host_workspace(size_t bytes, hipStream_t stream, void** ptr) { return workspace_alloc(bytes, stream, ptr); }
+int host_space(const char* what, int64_t need, void* given, int64_t given_bytes, uintptr_t align, hipStream_t stream,
+               unsigned char** ws, bool* owned) {
+  *ws = nullptr;
+  *owned = false;
+  if (given != nullptr) {
+    if (reinterpret_cast<uintptr_t>(given) % align != 0)
+      return fail(DR_ERR_LAYOUT, "`workspace` is not %d-byte aligned", (int)align);
+    if (given_bytes < need)
+      return fail(DR_ERR_SHAPE, "`workspace` has %lld bytes, the call needs %lld", (long long)given_bytes, (long long)need);
+    *ws = static_cast<unsigned char*>(given);
+    return DR_OK;
+  }
+  if (need <= 0) return DR_OK;
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  const hipError_t known = hipStreamIsCapturing(stream, &cap);
+  if (known == hipSuccess && cap != hipStreamCaptureStatusNone)
+    return fail(DR_ERR_UNSUPPORTED, "the %s needs a workspace of %lld bytes: a captured call takes the caller's", what,
+                (long long)need);
+  if (known != hipSuccess) (void)hipGetLastError();  // (the allocation reports what is wrong)
+  void* mem = nullptr;
+  const hipError_t e = workspace_alloc((size_t)need, stream, &mem);
+  if (e != hipSuccess)
+    return fail(DR_ERR_HIP, "%s workspace (%lld bytes) allocation failed: %s", what, (long long)need, hipGetErrorString(e));
+  *ws = static_cast<unsigned char*>(mem);
+  *owned = true;
+  return DR_OK;
+}
 
 int host_check_offsets(const int32_t* cu, int64_t nseq, int64_t tokens, hipStream_t stream) {
   return cu != nullptr && debug_validate() ? check_offsets(cu, nseq, tokens, stream) : DR_OK;
@@ -233,15 +260,14 @@ const char* dr_last_error(void) { return g_last_error.c_str(); }
 
 int dr_version(void) { return 200; }
 
-static int prefill_checks(const dr_dims* dims, int variant, const float* erase, const float* write,
-                          const int32_t* cu_seqlens, bool* vec) {
-  int st = check_dims_common(dims);
-  if (st) return st;
+// Sizes of a prefill or backward beyond what every call has.
+static int check_tokens(const dr_dims* dims, int variant) {
   if (variant == DR_PRODUCT2 && dims->batch * dims->seqlen >= ((int64_t)1 << 30))
     return fail(DR_ERR_SHAPE, "problem too large: two transitions per token need 2 * tokens < 2^31 steps");
-  st = check_variant(variant, erase, write, dims->batch * dims->seqlen > 0, vec);
-  if (st) return st;
-  if (cu_seqlens != nullptr) {
+  return DR_OK;
+}
+static int check_sequences(const dr_dims* dims, bool packed) {
+  if (packed) {
     if (dims->batch != 1)
       return fail(DR_ERR_SHAPE, "packed sequences (cu_seqlens) need batch == 1, got %lld",
                   (long long)dims->batch);
@@ -250,6 +276,17 @@ static int prefill_checks(const dr_dims* dims, int variant, const float* erase, 
                 (long long)dims->num_seqs, (long long)dims->batch);
   }
   return DR_OK;
+}
+
+static int prefill_checks(const dr_dims* dims, int variant, const float* erase, const float* write,
+                          const int32_t* cu_seqlens, bool* vec) {
+  int st = check_dims_common(dims);
+  if (st) return st;
+  st = check_tokens(dims, variant);
+  if (st) return st;
+  st = check_variant(variant, erase, write, dims->batch * dims->seqlen > 0, vec);
+  if (st) return st;
+  return check_sequences(dims, cu_seqlens != nullptr);
 }
 
 int dr_chunk_fwd_plan(const dr_dims* dims, int variant, int32_t* chunk, int32_t* dv_block,
@@ -349,13 +386,20 @@ int dr_chunk_fwd(const void* q, const void* k, const void* v, const float* alpha
   return dr_chunk_fwd_ex(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, o, S_T, dims, nullptr, stream);
 }
 
-// The prefill behind dr_chunk_fwd_ex (workspace from the pool) and dr_chunk_fwd_noalloc (workspace
-// in the static scratch array).
+// Where a prefill's workspace comes from: the caller or, without one, the library's pool; the static scratch array.
+struct SpaceFrom {
+  void* given;
+  int64_t bytes;
+  bool scratch;
+};
+
+// The prefill behind dr_chunk_fwd_ex, dr_chunk_fwd_ws and dr_chunk_fwd_noalloc.
 static int chunk_fwd_impl(const void* q, const void* k, const void* v, const void* alpha,
                           const float* erase, const float* write, int variant,
                           const float* S0, const int32_t* cu_seqlens,
                           float* o, float* S_T, const dr_dims* dims, const dr_opts* opts,
-                          hipStream_t stream, bool noalloc) {
+                          hipStream_t stream, const SpaceFrom& from) {
+  const bool noalloc = from.scratch;
   g_last_error.clear();
   bool vec = false;
   int st = prefill_checks(dims, variant, erase, write, cu_seqlens, &vec);
@@ -406,6 +450,7 @@ static int chunk_fwd_impl(const void* q, const void* k, const void* v, const voi
   }
   set_prep(p, opts);
   void* ws = nullptr;
+  bool owned = false;
   hipError_t e = hipSuccess;
   if (noalloc) {
     if ((uint64_t)pl.workspace > DR_NOALLOC_SCRATCH_BYTES)
@@ -416,14 +461,14 @@ static int chunk_fwd_impl(const void* q, const void* k, const void* v, const voi
       e = dr::scratch_buffer(&ws);
       if (e != hipSuccess) return fail(DR_ERR_HIP, "static scratch lookup failed: %s", hipGetErrorString(e));
     }
-  } else if (pl.workspace > 0) {
-    e = workspace_alloc((size_t)pl.workspace, stream, &ws);
-    if (e != hipSuccess)
-      return fail(DR_ERR_HIP, "prefill workspace (%lld bytes) allocation failed: %s", (long long)pl.workspace,
-                  hipGetErrorString(e));
+  } else {
+    unsigned char* mem = nullptr;
+    st = dr::host_space("prefill", pl.workspace, from.given, from.bytes, 256, stream, &mem, &owned);
+    if (st) return st;
+    ws = mem;
   }
   e = dr::launch_prefill(p, pl, ws, (int)dims->head_dim_k, dims->in_dtype == DR_BF16, vec, stream);
-  hipError_t ef = (ws && !noalloc) ? hipFreeAsync(ws, stream) : hipSuccess;
+  hipError_t ef = owned ? hipFreeAsync(ws, stream) : hipSuccess;
   if (e != hipSuccess) return fail(DR_ERR_HIP, "prefill launch failed: %s", hipGetErrorString(e));
   if (ef != hipSuccess) return fail(DR_ERR_HIP, "prefill workspace release failed: %s", hipGetErrorString(ef));
   return DR_OK;
@@ -434,7 +479,17 @@ int dr_chunk_fwd_ex(const void* q, const void* k, const void* v, const void* alp
                     const float* S0, const int32_t* cu_seqlens,
                     float* o, float* S_T, const dr_dims* dims, const dr_opts* opts,
                     hipStream_t stream) {
-  return chunk_fwd_impl(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, o, S_T, dims, opts, stream, false);
+  return chunk_fwd_impl(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, o, S_T, dims, opts, stream,
+                        {nullptr, 0, false});
+}
+
+int dr_chunk_fwd_ws(const void* q, const void* k, const void* v, const void* alpha,
+                    const float* erase, const float* write, int variant,
+                    const float* S0, const int32_t* cu_seqlens,
+                    float* o, float* S_T, const dr_dims* dims, const dr_opts* opts,
+                    void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  return chunk_fwd_impl(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, o, S_T, dims, opts, stream,
+                        {workspace, workspace_bytes, false});
 }
 
 int dr_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const void* alpha,
@@ -442,10 +497,68 @@ int dr_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const void
                          const float* S0, const int32_t* cu_seqlens,
                          float* o, float* S_T, const dr_dims* dims, const dr_opts* opts,
                          hipStream_t stream) {
-  return chunk_fwd_impl(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, o, S_T, dims, opts, stream, true);
+  return chunk_fwd_impl(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, o, S_T, dims, opts, stream,
+                        {nullptr, 0, true});
 }
 
 static int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
+// The backward's plan and where the parts of its workspace lie. checkpoints: the caller has the states, so of the
+// prefill's workspace only the packed plan's tables are needed, not the records. The chunked MFMA path (one or two
+// transitions per token, d_k 64 or 128, d_v a multiple of 32 up to 128) keeps its records and chunk-end gradients in
+// the walk's partial-sum buffers: the walk's kernels write them only if it flagged a chunk whose gates it does not
+// take, and then after the chunked passes are done with them. The flag sits apart.
+struct BwdSpace {
+  dr::PrefillPlan pl, plw;  // of the forward pass; with what the backward keeps of its workspace
+  int64_t nsnap, TH, ncpb, cslots, crec;
+  int ndvb;
+  bool chunked;
+  int64_t off_snap, off_part, off_parts, off_flag, total;
+};
+static BwdSpace bwd_space(const dr_dims* dims, int lg, bool packed, bool checkpoints) {
+  BwdSpace s{};
+  const int dkh = (int)dims->head_dim_k, dvh = (int)dims->head_dim_v;
+  const int64_t H = dims->num_heads, steps = (dims->batch * dims->seqlen) << lg;
+  s.pl = dr::plan_prefill(dims->num_seqs * H, dims->num_seqs, dims->batch, dims->seqlen << lg, H, dkh, dvh, packed);
+  // at most floor(steps / 64) checkpoints in all (sum of floor(len_n / 64) over the sequences)
+  s.nsnap = packed ? steps / 64 : dims->batch * ((dims->seqlen << lg) / 64);
+  s.ndvb = dvh / dr::bwd_dv_block(dvh);
+  s.TH = steps * H;
+  s.plw = s.pl;
+  if (checkpoints) {
+    s.plw.workspace -= s.pl.slots * H * s.pl.rec_size;
+    s.plw.rec_size = 0;
+  }
+  s.chunked = (dkh == 64 || dkh == 128) && dvh % 32 == 0 && dvh <= 128 && dims->seqlen > 0 && !walk_forced();
+  s.ncpb = ((dims->seqlen << lg) + 63) / 64;  // 64-step chunks per sequence
+  // chunk slots x heads: fixed length B x chunks per sequence, packed the plan's upper bound
+  s.cslots = (packed ? s.pl.slots : dims->batch * s.ncpb) * H;
+  s.crec = s.chunked ? dr::cbwd_record_bytes(dkh, dvh) : 0;
+  const int64_t chunk_bytes = s.chunked ? round256(s.cslots * s.crec) + round256(s.cslots * dkh * dvh * 4) : 0;
+  s.off_snap = round256(s.plw.workspace);
+  s.off_part = s.off_snap + (checkpoints ? 0 : round256(s.nsnap * H * dkh * dvh * 4));
+  s.off_parts = s.off_part + round256((int64_t)s.ndvb * s.TH * 4 * dkh * 4);
+  const int64_t walk_end = s.off_parts + round256((int64_t)s.ndvb * s.TH * 4);
+  s.off_flag = walk_end > s.off_part + chunk_bytes ? walk_end : s.off_part + chunk_bytes;
+  s.total = s.off_flag + 256;
+  return s;
+}
+
+int dr_chunk_workspace(const dr_dims* dims, int variant, int packed, int backward, int64_t* bytes) {
+  g_last_error.clear();
+  int st = check_dims_common(dims);
+  if (st) return st;
+  if (variant < DR_KDA || variant > DR_PRODUCT2) return fail(DR_ERR_VARIANT, "unknown variant %d", variant);
+  st = check_tokens(dims, variant);
+  if (!st) st = check_sequences(dims, packed != 0);
+  if (st) return st;
+  if (backward < 0 || backward > 2) return fail(DR_ERR_SHAPE, "backward must be 0, 1 or 2, got %d", backward);
+  if (bytes == nullptr) return fail(DR_ERR_NULL, "`bytes` is NULL");
+  const int lg = variant == DR_PRODUCT2 ? 1 : 0;
+  *bytes = backward ? bwd_space(dims, lg, packed != 0, backward == 2).total
+                    : make_plan(dims, lg, packed != 0, false).workspace;
+  return DR_OK;
+}
 
 int dr_chunk_bwd(const void* q, const void* k, const void* v, const float* alpha,
                  const float* erase, const float* write, int variant,
@@ -463,6 +576,17 @@ int dr_chunk_bwd_ex(const void* q, const void* k, const void* v, const float* al
                     const float* dO, const float* dS_T,
                     float* dq, float* dk, float* dv, float* dalpha, float* derase, float* dwrite,
                     float* dS0, const float* checkpoints, const dr_dims* dims, hipStream_t stream) {
+  return dr_chunk_bwd_ws(q, k, v, alpha, erase, write, variant, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dalpha,
+                         derase, dwrite, dS0, checkpoints, dims, nullptr, 0, stream);
+}
+
+int dr_chunk_bwd_ws(const void* q, const void* k, const void* v, const float* alpha,
+                    const float* erase, const float* write, int variant,
+                    const float* S0, const int32_t* cu_seqlens,
+                    const float* dO, const float* dS_T,
+                    float* dq, float* dk, float* dv, float* dalpha, float* derase, float* dwrite,
+                    float* dS0, const float* checkpoints, const dr_dims* dims,
+                    void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   g_last_error.clear();
   bool vec = false;
   int st = prefill_checks(dims, variant, erase, write, cu_seqlens, &vec);
@@ -502,52 +626,25 @@ int dr_chunk_bwd_ex(const void* q, const void* k, const void* v, const float* al
   p.T = dims->seqlen << lg;
   p.H = (int32_t)H;
   p.DV = (int32_t)dvh;
-  const dr::PrefillPlan pl = dr::plan_prefill(pairs, dims->num_seqs, dims->batch, dims->seqlen << lg, H, dkh, dvh,
-                                              cu_seqlens != nullptr);
-  if (pl.workgroups > INT32_MAX || pl.slots * H > INT32_MAX || pairs * (dvh / dr::bwd_dv_block(dvh)) > INT32_MAX)
+  const BwdSpace sp = bwd_space(dims, lg, cu_seqlens != nullptr, checkpoints != nullptr);
+  const dr::PrefillPlan &pl = sp.pl, &plw = sp.plw;
+  if (pl.workgroups > INT32_MAX || pl.slots * H > INT32_MAX || pairs * sp.ndvb > INT32_MAX ||
+      (sp.chunked && sp.cslots > INT32_MAX))
     return fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
   p.num_pairs = (int32_t)pairs;
   p.ndvb = pl.ndvb;
   p.grid_logical = (int32_t)(pairs * pl.ndvb);
   p.nseq = (int32_t)dims->num_seqs;
   p.snap_chunks = 1;
-  // at most floor(steps / 64) checkpoints in all (sum of floor(len_n / 64) over the sequences)
-  const int64_t steps = tokens << lg;
-  const int64_t nsnap = cu_seqlens ? steps / 64 : dims->batch * ((dims->seqlen << lg) / 64);
-  const int ndvb = dvh / dr::bwd_dv_block(dvh);
-  const int64_t TH = steps * H;
-  // with the caller's checkpoints only the packed plan's tables are needed, not the records
-  dr::PrefillPlan plw = pl;
-  if (checkpoints) {
-    plw.workspace -= pl.slots * H * pl.rec_size;
-    plw.rec_size = 0;
-  }
-  // The chunked MFMA path (one or two transitions per token, d_k 64 or 128, d_v a multiple of 32
-  // up to 128) runs first; the walk's kernels then run only if it flagged a chunk whose gates
-  // it does not take. Its records and chunk-end gradients share the walk's partial-sum buffers
-  // (the walk writes them only when it runs, after the chunked passes are done with them); the
-  // flag sits apart.
-  const bool chunked = (dkh == 64 || dkh == 128) && dvh % 32 == 0 && dvh <= 128 && dims->seqlen > 0 &&
-                       !walk_forced();
-  const int64_t ncpb = ((dims->seqlen << lg) + 63) / 64;  // 64-step chunks per sequence
-  // chunk slots x heads: fixed length B x chunks per sequence, packed the plan's upper bound
-  const int64_t cslots = (cu_seqlens ? pl.slots : dims->batch * ncpb) * H;
-  const int64_t crec = chunked ? dr::cbwd_record_bytes(dkh, dvh) : 0;
-  const int64_t chunk_bytes = chunked ? round256(cslots * crec) + round256(cslots * dkh * dvh * 4) : 0;
-  if (chunked && cslots > INT32_MAX)
-    return fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
-  const int64_t off_snap = round256(plw.workspace);
-  const int64_t off_part = off_snap + (checkpoints ? 0 : round256(nsnap * H * dkh * dvh * 4));
-  const int64_t off_parts = off_part + round256((int64_t)ndvb * TH * 4 * dkh * 4);
-  const int64_t walk_end = off_parts + round256((int64_t)ndvb * TH * 4);
-  const int64_t off_flag = walk_end > off_part + chunk_bytes ? walk_end : off_part + chunk_bytes;
-  const int64_t total = off_flag + 256;
-  void* ws = nullptr;
-  hipError_t e = workspace_alloc((size_t)total, stream, &ws);
-  if (e != hipSuccess)
-    return fail(DR_ERR_HIP, "backward workspace (%lld bytes) allocation failed: %s", (long long)total,
-                hipGetErrorString(e));
-  unsigned char* wsb = static_cast<unsigned char*>(ws);
+  const int64_t nsnap = sp.nsnap, off_snap = sp.off_snap, off_part = sp.off_part, off_parts = sp.off_parts;
+  // the chunked MFMA path runs first; the walk's kernels then run only if it flagged a chunk whose gates it does not take
+  const bool chunked = sp.chunked;
+  unsigned char* wsb = nullptr;
+  bool owned = false;
+  st = dr::host_space("backward", sp.total, workspace, workspace_bytes, 256, stream, &wsb, &owned);
+  if (st) return st;
+  void* ws = wsb;
+  hipError_t e = hipSuccess;
   if (checkpoints) {
     // read only here: the plan pass uses the pointer's presence to lay out the rows
     p.snap = nsnap > 0 ? const_cast<float*>(checkpoints) : nullptr;
@@ -572,7 +669,7 @@ int dr_chunk_bwd_ex(const void* q, const void* k, const void* v, const float* al
     b.part = reinterpret_cast<float*>(wsb + off_part);
     b.parts = reinterpret_cast<float*>(wsb + off_parts);
     b.T = dims->seqlen << lg;
-    b.TH = TH;
+    b.TH = sp.TH;
     b.lgnh = lg;
     b.H = (int32_t)H;
     b.DV = dvh;
@@ -597,16 +694,16 @@ int dr_chunk_bwd_ex(const void* q, const void* k, const void* v, const float* al
       cb.dq = dq; cb.dk = dk; cb.dv = dv; cb.dalpha = dalpha; cb.derase = derase; cb.dwrite = dwrite;
       cb.dS0 = dS0;
       cb.rec = wsb + off_part;
-      cb.rec_size = crec;
-      cb.dsc = reinterpret_cast<float*>(wsb + off_part + round256(cslots * crec));
-      cb.flag = reinterpret_cast<int32_t*>(wsb + off_flag);
+      cb.rec_size = sp.crec;
+      cb.dsc = reinterpret_cast<float*>(wsb + off_part + round256(sp.cslots * sp.crec));
+      cb.flag = reinterpret_cast<int32_t*>(wsb + sp.off_flag);
       cb.T = dims->seqlen << lg;
       cb.H = (int32_t)H;
       cb.DV = dvh;
       cb.B = (int32_t)dims->batch;
-      cb.nc = (int32_t)ncpb;
+      cb.nc = (int32_t)sp.ncpb;
       cb.nseq = (int32_t)dims->num_seqs;
-      cb.slots = (int32_t)(cslots / H);
+      cb.slots = (int32_t)(sp.cslots / H);
       if (cu_seqlens) {  // the plan pass's tables (written by the forward or by launch_plan_only above)
         int32_t* tab = dr::prefill_chunk_tables(ws, plw, H);
         cb.cu = b.cu;
@@ -624,7 +721,7 @@ int dr_chunk_bwd_ex(const void* q, const void* k, const void* v, const float* al
     }
     if (e == hipSuccess) e = dr::launch_backward(b, pairs, dkh, dvh, dims->in_dtype == DR_BF16, vec, stream);
   }
-  hipError_t ef = hipFreeAsync(ws, stream);
+  hipError_t ef = owned ? hipFreeAsync(ws, stream) : hipSuccess;
   if (e != hipSuccess) return fail(DR_ERR_HIP, "backward launch failed: %s", hipGetErrorString(e));
   if (ef != hipSuccess) return fail(DR_ERR_HIP, "backward workspace release failed: %s", hipGetErrorString(ef));
   return DR_OK;

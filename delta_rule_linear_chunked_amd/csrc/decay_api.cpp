@@ -230,37 +230,6 @@ Space bwd_space(const dr_decay_dims* d, const dr::DecayPlan& pl, bool packed) {
   return s;
 }
 
-// The call's workspace: the caller's, or one from the library's pool (`owned`, given back stream-ordered). The pool
-// is refused while the stream is being captured: a graph would hold it as memory nodes, and a replay of one of two
-// such graphs has run its kernels on addresses that were not mapped.
-int get_space(const char* what, int64_t need, void* given, int64_t given_bytes, hipStream_t stream, unsigned char** ws,
-              bool* owned) {
-  *ws = nullptr;
-  *owned = false;
-  if (given != nullptr) {
-    if (!aligned16(given)) return host_fail(DR_ERR_LAYOUT, "`workspace` is not 16-byte aligned");
-    if (given_bytes < need)
-      return host_fail(DR_ERR_SHAPE, "`workspace` has %lld bytes, the call needs %lld", (long long)given_bytes,
-                       (long long)need);
-    *ws = static_cast<unsigned char*>(given);
-    return DR_OK;
-  }
-  if (need == 0) return DR_OK;
-  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-  hipError_t e = hipStreamIsCapturing(stream, &cap);
-  if (e == hipSuccess && cap != hipStreamCaptureStatusNone)
-    return host_fail(DR_ERR_UNSUPPORTED, "the %s needs a workspace of %lld bytes: a captured call takes the caller's", what,
-                     (long long)need);
-  void* mem = nullptr;
-  if (e == hipSuccess) e = dr::host_workspace((size_t)need, stream, &mem);
-  if (e != hipSuccess)
-    return host_fail(DR_ERR_HIP, "%s workspace (%lld bytes) allocation failed: %s", what, (long long)need,
-                     hipGetErrorString(e));
-  *ws = static_cast<unsigned char*>(mem);
-  *owned = true;
-  return DR_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -312,7 +281,7 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
   const Space sp = fwd_space(dims, pl, packed);
   unsigned char* ws = nullptr;
   bool owned = false;
-  st = get_space("decay prefill", sp.size, workspace, workspace_bytes, stream, &ws, &owned);
+  st = dr::host_space("decay prefill", sp.size, workspace, workspace_bytes, 16, stream, &ws, &owned);
   if (st) return st;
   if (pl.nseg > 1) {
     p.part = reinterpret_cast<float*>(ws + sp.part);
@@ -397,7 +366,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   const Space sp = bwd_space(dims, pl, packed);
   unsigned char* ws = nullptr;
   bool owned = false;
-  st = get_space("decay backward", sp.size, workspace, workspace_bytes, stream, &ws, &owned);
+  st = dr::host_space("decay backward", sp.size, workspace, workspace_bytes, 16, stream, &ws, &owned);
   if (st) return st;
   auto f = [&](int64_t off) { return reinterpret_cast<float*>(ws + off); };
   p.cs = f(sp.cs);

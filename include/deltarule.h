@@ -45,7 +45,9 @@
  * takes it stream-ordered on `stream`
  * from a per-device memory pool owned by the library, which keeps what it has
  * reserved for later calls (a larger problem grows it once). Apart from that
- * pool the library holds only a thread-local error message. Work is enqueued
+ * pool the library holds only a thread-local error message. While `stream` is
+ * being captured the pool is refused (DR_ERR_UNSUPPORTED, see
+ * dr_chunk_workspace). Work is enqueued
  * on `stream` and runs asynchronously; outputs are valid once the stream
  * reaches that point.
  *
@@ -339,6 +341,31 @@ int dr_chunk_bwd_ex(const void* q, const void* k, const void* v, const float* al
                     const float* dO, const float* dS_T,
                     float* dq, float* dk, float* dv, float* dalpha, float* derase, float* dwrite,
                     float* dS0, const float* checkpoints, const dr_dims* dims, hipStream_t stream);
+
+/*
+ * The prefill and the backward with the caller's workspace. dr_chunk_workspace gives the bytes that a call with these
+ * dims takes (may be 0): of dr_chunk_fwd_ws (backward = 0) or of dr_chunk_bwd_ws without (1) or with (2) checkpoints;
+ * packed: whether the call has cu_seqlens. `workspace`, `workspace_bytes`: device memory, 256-byte aligned, not in use
+ * by another call until this one is over on the stream; nothing in it is kept from one call for the next. With NULL
+ * it comes from the library's pool, and the calls are dr_chunk_fwd_ex and dr_chunk_bwd_ex.
+ *
+ * A call on a stream that is being captured needs its workspace from here (or dr_chunk_fwd_noalloc, one call at a
+ * time): the pool's memory would become memory nodes of the graph, and replays of two such graphs in turn have read
+ * addresses that were not mapped. dr_chunk_fwd(_ex) and dr_chunk_bwd(_ex) therefore return DR_ERR_UNSUPPORTED there.
+ */
+int dr_chunk_workspace(const dr_dims* dims, int variant, int packed, int backward, int64_t* bytes);
+int dr_chunk_fwd_ws(const void* q, const void* k, const void* v, const void* alpha,
+                    const float* erase, const float* write, int variant,
+                    const float* S0, const int32_t* cu_seqlens,
+                    float* o, float* S_T, const dr_dims* dims, const dr_opts* opts,
+                    void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int dr_chunk_bwd_ws(const void* q, const void* k, const void* v, const float* alpha,
+                    const float* erase, const float* write, int variant,
+                    const float* S0, const int32_t* cu_seqlens,
+                    const float* dO, const float* dS_T,
+                    float* dq, float* dk, float* dv, float* dalpha, float* derase, float* dwrite,
+                    float* dS0, const float* checkpoints, const dr_dims* dims,
+                    void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /* Static description of a status code. Never NULL. */
 const char* dr_status_string(int status);
