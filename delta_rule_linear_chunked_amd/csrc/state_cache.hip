@@ -20,13 +20,14 @@ __device__ __forceinline__ int64_t cache_row(const int32_t* idx, int64_t rows, i
 
 // The integer nearest to the exact quotient x / s (ties to even), |x / s| < 128: a candidate from the
 // hardware reciprocal, at most one off next to a tie, set right by its remainder, which an fma gives exactly
-// (x and q s are multiples of the smaller one's last place and differ by less than 2 s).
+// (x and q s are multiples of the smaller one's last place and differ by less than 2 s). Twice the remainder is
+// compared with s: half of s is no float32 number when s lies below 2^-125.
 __device__ __forceinline__ int code_int8(float x, float s, float inv) {
   float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x), h = 0.5f * s;
+  const float r = fmaf(-q, s, x), r2 = r + r;
   const bool odd = ((int)q & 1) != 0;
-  if (r > h || (r == h && odd)) q += 1.f;
-  if (r < -h || (r == -h && odd)) q -= 1.f;
+  if (r2 > s || (r2 == s && odd)) q += 1.f;
+  if (r2 < -s || (r2 == -s && odd)) q -= 1.f;
   return (int)q;
 }
 
