@@ -544,6 +544,15 @@ def chunk_bwd(q, k, v, alpha, erase, write=None, variant: str = "kda", S0=None, 
     return g
 
 
+def _dense(t):
+    """``t`` as the library takes it: dense and 16-byte aligned. (A gradient that autograd hands over may be a part of
+    a larger tensor, dense but starting anywhere in it.)"""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _DeltaRule(torch.autograd.Function):
     """``chunk_fwd`` as an autograd node. The forward stores the states after every 64 tokens (32
     for product2) as the backward's checkpoints, so the backward runs only its reverse walk
@@ -567,8 +576,7 @@ class _DeltaRule(torch.autograd.Function):
         q, k, v, alpha, erase, write, S0, cu_seqlens, ck = ctx.saved_tensors
         if dO is None:
             dO = torch.zeros(q.shape[:3] + (v.shape[-1],), dtype=torch.float32, device=q.device)
-        g = chunk_bwd(q, k, v, alpha, erase, write, ctx.variant, S0, cu_seqlens, dO=dO.contiguous(),
-                      dS_T=None if dS_T is None else dS_T.contiguous(),
+        g = chunk_bwd(q, k, v, alpha, erase, write, ctx.variant, S0, cu_seqlens, dO=_dense(dO), dS_T=_dense(dS_T),
                       need_dS0=S0 is not None and ctx.needs_input_grad[6], checkpoints=ck)
         cast = lambda grad, x: None if grad is None else grad.to(x.dtype)
         return (cast(g["dq"], q), cast(g["dk"], k), cast(g["dv"], v), g["dalpha"], g["derase"], g["dwrite"],

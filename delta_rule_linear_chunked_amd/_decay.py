@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _DT, _Opts, _capturing, _check, _need, _need_rows, check_offsets, load_library, snapshot_count
+from . import _DT, _Opts, _capturing, _check, _dense, _need, _need_rows, check_offsets, load_library, snapshot_count
 
 # code types of the state cache (dr_cache_format)
 CACHE_FORMATS = {"int8": (0, torch.int8), "e4m3": (1, torch.float8_e4m3fn)}
@@ -290,10 +290,10 @@ class _DecayAttention(torch.autograd.Function):
         q, k, v, alpha, S0, cu_seqlens = ctx.saved_tensors
         new = torch.empty if cu_seqlens is None else torch.zeros
         like = lambda x: new(tuple(x.shape), dtype=torch.float32, device=x.device)  # noqa: E731
-        dO = torch.zeros(tuple(v.shape), dtype=torch.float32, device=q.device) if dO is None else dO.contiguous()
+        dO = torch.zeros(tuple(v.shape), dtype=torch.float32, device=q.device) if dO is None else _dense(dO)
         dq, dk, dv, da = like(q), like(k), like(v), like(alpha)
         dS0 = torch.empty_like(S0) if S0 is not None and ctx.needs_input_grad[4] else None
-        dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, None if dS_T is None else dS_T.contiguous(), dq, dk, dv, da, dS0)
+        dr_decay_bwd(q, k, v, alpha, S0, cu_seqlens, dO, _dense(dS_T), dq, dk, dv, da, dS0)
         return dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), da, dS0, None
 
 
