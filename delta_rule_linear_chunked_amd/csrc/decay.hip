@@ -34,7 +34,7 @@ __device__ __forceinline__ void scan_table(int nseq, int* s_scan, int* s_carry, 
     int c = 0;
     if (n < nseq) {
       const int len = cu[n + 1] - cu[n];
-      c = ceil_one ? max((len + unit - 1) / unit, 1) : len / unit;
+      c = ceil_one ? max(pieces(len, unit), 1) : len / unit;
     }
     s_scan[tid] = c;
     __syncthreads();
@@ -605,7 +605,7 @@ __global__ __launch_bounds__(64 * (MAIN_WAVES + FILL_WAVES)) void decay_main_ker
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t trow = sp.b * p.T + sp.row0;  // row in the dense per-token arrays
-  const int nc = (sp.len + DCH - 1) / DCH;
+  const int nc = pieces(sp.len, DCH);
   if constexpr (OUT) {
     // the two tiles of P above the diagonal that the 32-token products meet
     for (int i = tid; i < 3 * 2 * 16 * 2; i += NTH) {
@@ -833,7 +833,7 @@ __device__ __forceinline__ void state_body(const DecayParams& p, int local, unsi
     sy[e].init(y_ts, 16 * CT, tid);
   }
   float a_next[2] = {1.f, 1.f};
-  const int nc = (sp.len + DC - 1) / DC;
+  const int nc = pieces(sp.len, DC);
   auto chunk_of = [&](int i) { return REV ? nc - 1 - i : i; };
   auto fetch = [&](int i, auto E) {  // chunk i (past the end the last one: no branch, see the main pass)
     constexpr int e = E.value;

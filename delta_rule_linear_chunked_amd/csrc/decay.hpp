@@ -11,6 +11,11 @@ namespace dr {
 
 constexpr int DCH = 64;  // tokens per chunk
 
+// Pieces of `unit` tokens that n tokens take, n + unit past 32 bits included.
+__host__ __device__ constexpr int pieces(int n, int unit) { return n > 0 ? (n - 1) / unit + 1 : 0; }
+static_assert(pieces(INT32_MAX, 1 << 21) == 1024 && pieces(INT32_MAX, INT32_MAX) == 1 && pieces(64, 64) == 1 &&
+              pieces(65, 64) == 2 && pieces(0, 64) == 0, "whole and ragged lengths");
+
 // Sequences are cut into segments of `seg` tokens (a multiple of 64; one segment when that fills the
 // chip): a slot is one segment of one sequence. Fixed length: slot n * nseg + j. Packed: the plan pass
 // writes the table.
