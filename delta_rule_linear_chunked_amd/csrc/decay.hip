@@ -105,7 +105,6 @@ __global__ __launch_bounds__(256) void decay_plan_kernel(DecayParams p) {
 // IS parts (whole 32-channel slices) and repeat them D times: a wave forms its channels' part of Q S0 for the row
 // tiles of its repeat, hands the parts of row tiles that it does not finish to their owner, and updates its channels
 // of the state.
-constexpr int MAIN_WAVES = 8, FILL_WAVES = 4;
 template <int W, int CT>
 struct Split {
   static constexpr int G = MAIN_WAVES / CT, IS = G < W / 32 ? G : W / 32, D = G / IS < 4 ? G / IS : 4;
@@ -994,7 +993,7 @@ static hipError_t launch_state_t(DecayParams p, int local, hipStream_t s) {
 }
 template <int W, int DC, typename XT>
 static hipError_t launch_state_w(const DecayParams& p, int local, hipStream_t s) {
-  return p.DV >= 32 ? launch_state_t<W, 2, DC, XT>(p, local, s) : launch_state_t<W, 1, DC, XT>(p, local, s);
+  return state_tiles(p.DV) == 2 ? launch_state_t<W, 2, DC, XT>(p, local, s) : launch_state_t<W, 1, DC, XT>(p, local, s);
 }
 template <int DC, typename XT>
 static hipError_t launch_state(const DecayParams& p, int local, hipStream_t s) {
@@ -1007,8 +1006,7 @@ hipError_t launch_decay_states(const DecayParams& p, bool bf16, int local, hipSt
               : launch_state<decay_bwd_chunk(false), float>(p, local, s);
 }
 hipError_t launch_decay_join(const DecayParams& p, bool both, hipStream_t s) {
-  const int64_t hsz = (int64_t)p.DK * p.DV;
-  const int64_t grid = (int64_t)p.nseq * p.H * ((hsz / 4 + 255) / 256);
+  const int64_t grid = join_grid(p);
   if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)grid, both ? 2 : 1), dim3(256), 0, s, p);

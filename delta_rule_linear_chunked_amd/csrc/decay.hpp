@@ -439,6 +439,37 @@ struct Stage {
   }
 };
 
+// Sizes of the launches, checked before the first of a call: the work items along an axis are a 32-bit number.
+inline bool launch_fits(int64_t blocks, int threads) { return blocks <= INT32_MAX && blocks * threads <= (int64_t)UINT32_MAX; }
+constexpr int MAIN_WAVES = 8, FILL_WAVES = 4;  // of the main pass (see decay.hip)
+inline int64_t join_grid(const DecayParams& p) { return (int64_t)p.nseq * p.H * (((int64_t)p.DK * p.DV / 4 + 255) / 256); }
+inline int64_t grad_grid(const DecayParams& p) { return ((int64_t)p.cslots * p.H + 7) / 8 * 8; }
+inline int64_t shared_grid(const DecayParams& p) { return ((int64_t)p.nbatch * p.T * p.Hk * p.DK / 4 + 255) / 256; }
+constexpr int state_tiles(int dv) { return dv >= 32 ? 2 : 1; }  // column tiles per workgroup of the state passes
+inline bool decay_fwd_fits(DecayParams p, const DecayPlan& pl) {
+  p.ncb = p.DV / (16 * pl.ct);
+  return launch_fits(work_grid(p), 64 * (MAIN_WAVES + FILL_WAVES)) && (pl.nseg <= 1 || launch_fits(join_grid(p), 256));
+}
+inline bool decay_bwd_fits(DecayParams p, const DecayPlan& pl) {
+  p.ncb = p.DV / (16 * state_tiles(p.DV));
+  return launch_fits(work_grid(p), 256) && (pl.nseg <= 1 || launch_fits(join_grid(p), 256)) &&
+         launch_fits(grad_grid(p), 512) && (p.H == p.Hk || launch_fits(shared_grid(p), 256));
+}
+// Value columns per workgroup of the step: whole rows once the heads alone give every CU a few workgroups, slices of 32
+// columns for fewer (d = 128, us: 64 heads 3.9 in slices and 4.3 whole, 256 heads 6.4 and 7.5, 1024 heads 26.0 and
+// 23.5; slices of 16 columns, 64 heads, 6.1).
+inline int step_columns(const DecayParams& p) {
+  int dvs = p.DV;
+  const int64_t heads = (int64_t)p.nseq * p.H;
+  while (dvs > 32 && heads * (p.DV / dvs) < 1024) dvs /= 2;
+  return dvs;
+}
+constexpr int step_threads(int dk, int dvs) { return dk * (dvs / 4) < 256 ? dk * (dvs / 4) : 256; }
+inline bool decay_step_fits(const DecayParams& p) {
+  const int dvs = step_columns(p);
+  return launch_fits((int64_t)p.nseq * p.H * (p.DV / dvs), step_threads(p.DK, dvs));
+}
+
 hipError_t launch_decay_plan(const DecayParams& p, hipStream_t s);
 hipError_t launch_decay_fwd(DecayParams p, const DecayPlan& pl, bool bf16, hipStream_t s);
 hipError_t launch_decay_step(const DecayParams& p, bool bf16, hipStream_t s);

@@ -17,6 +17,7 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool head_dim_ok(int64_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+const char* const kTooLarge = "problem too large: more than 2^31 - 1 workgroups or 2^32 - 1 work items per kernel";
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 using Named = std::pair<const void*, const char*>;
@@ -274,10 +275,11 @@ int dr_decay_fwd(const void* q, const void* k, const void* v, const float* alpha
     p.snap_chunks = opts->snapshots ? (int32_t)(opts->snapshot_every / 64) : 0;
   }
   if (pl.slots * dims->num_heads * (dims->head_dim_v / 16) > INT32_MAX - 8 || pl.seg > INT32_MAX)
-    return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
+    return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   p.seg = (int32_t)pl.seg;
   p.nseg = (int32_t)pl.nseg;
   p.slots = (int32_t)pl.slots;
+  if (!dr::decay_fwd_fits(p, pl)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   const Space sp = fwd_space(dims, pl, packed);
   unsigned char* ws = nullptr;
   bool owned = false;
@@ -318,7 +320,8 @@ int dr_decay_step(const void* q, const void* k, const void* v, const float* alph
     p.nslots = opts->num_slots;
   }
   if (dims->num_seqs * dims->num_heads * (dims->head_dim_v / 16) > INT32_MAX)
-    return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
+    return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
+  if (!dr::decay_step_fits(p)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   const hipError_t e = dr::launch_decay_step(p, dims->in_dtype == DR_BF16, stream);
   if (e != hipSuccess) return host_fail(DR_ERR_HIP, "decay step launch failed: %s", hipGetErrorString(e));
   return DR_OK;
@@ -352,7 +355,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   const int64_t cslots = bwd_slots(dims, packed);
   if (pl.slots * H * (dims->head_dim_v / 16) > INT32_MAX - 8 || cslots * H > INT32_MAX - 8 || pl.seg > INT32_MAX ||
       tokens * dims->num_k_heads * (dims->head_dim_k / 4) / 256 >= INT32_MAX)
-    return host_fail(DR_ERR_UNSUPPORTED, "problem too large: more than 2^31 - 1 workgroups per kernel");
+    return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   dr::DecayParams p{};
   set_dims(p, dims);
   p.q = q; p.k = k; p.v = v; p.alpha = alpha; p.S0 = S0; p.cu = cu_seqlens;
@@ -363,6 +366,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
   p.cslots = (int32_t)cslots;
   p.bwd_chunk = (int32_t)chunk;
   p.nbatch = (int32_t)dims->batch;
+  if (!dr::decay_bwd_fits(p, pl)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   const Space sp = bwd_space(dims, pl, packed);
   unsigned char* ws = nullptr;
   bool owned = false;
@@ -412,8 +416,9 @@ static int cache_checks(const void* S, const int32_t* state_idx, const void* cod
     return host_fail(DR_ERR_UNSUPPORTED, "head sizes d_k=%lld d_v=%lld: each must be 16, 32, 64 or 128",
                      (long long)d->head_dim_k, (long long)d->head_dim_v);
   if (d->num_states > INT32_MAX || d->num_slots > INT32_MAX || d->num_heads > INT32_MAX || d->count > INT32_MAX ||
-      d->count * d->num_heads > INT32_MAX / 4)
-    return host_fail(DR_ERR_UNSUPPORTED, "too many states for one call");
+      d->count * d->num_heads > INT32_MAX / 4 || !dr::cache_fits(d->count * d->num_heads, (int)(d->head_dim_k * d->head_dim_v)))
+    return host_fail(DR_ERR_UNSUPPORTED, "%lld states of %lld heads: too many for one call", (long long)d->count,
+                     (long long)d->num_heads);
   if (state_idx == nullptr && d->num_states < d->count)
     return host_fail(DR_ERR_SHAPE, "%lld states for a count of %lld", (long long)d->num_states, (long long)d->count);
   if (slot_idx == nullptr && d->num_slots < d->count)

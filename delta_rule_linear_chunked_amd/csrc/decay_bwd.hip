@@ -568,7 +568,7 @@ __global__ __launch_bounds__(256) void decay_head_kernel(const DecayParams p, co
 template <int W, int V, typename InT>
 static hipError_t launch_grad_t(const DecayParams& p, hipStream_t s) {
   constexpr int DC = decay_bwd_chunk(sizeof(InT) == 2);
-  hipLaunchKernelGGL((decay_grad_kernel<W, V, InT, DC>), dim3((unsigned)(((int64_t)p.grid + 7) / 8 * 8)), dim3(512), 0, s, p);
+  hipLaunchKernelGGL((decay_grad_kernel<W, V, InT, DC>), dim3((unsigned)grad_grid(p)), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 template <int W, typename InT>
@@ -613,8 +613,7 @@ hipError_t launch_decay_bwd(DecayParams p, const DecayPlan& pl, bool bf16, hipSt
   g.grid = p.cslots * p.H;
   e = bf16 ? launch_grad<__bf16>(g, s) : launch_grad<float>(g, s);
   if (e == hipSuccess && p.H != p.Hk && p.T > 0) {
-    const int64_t n = ((int64_t)p.nbatch * p.T * p.Hk * p.DK / 4 + 255) / 256;
-    hipLaunchKernelGGL(decay_shared_kernel, dim3((unsigned)n), dim3(256), 0, s, p, p.pq, p.pk);
+    hipLaunchKernelGGL(decay_shared_kernel, dim3((unsigned)shared_grid(p)), dim3(256), 0, s, p, p.pq, p.pk);
     e = hipGetLastError();
   }
   if (e == hipSuccess && p.head_da) {

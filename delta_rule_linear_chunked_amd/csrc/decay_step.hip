@@ -11,7 +11,7 @@ namespace dr {
 template <int DK, int DVS>
 struct StepShape {
   static constexpr int COLS4 = DVS / 4;
-  static constexpr int NT = DK * COLS4 < 256 ? DK * COLS4 : 256;
+  static constexpr int NT = step_threads(DK, DVS);
   static constexpr int RG = NT / COLS4;       // row groups
   static constexpr int RPT = DK / RG;         // rows per thread
   static constexpr int NW = NT / 64;
@@ -114,11 +114,7 @@ static hipError_t launch_step_k(const DecayParams& p, int dvs, bool bf16, hipStr
   return launch_step_t<DK, 16>(p, bf16, s);
 }
 hipError_t launch_decay_step(const DecayParams& p, bool bf16, hipStream_t s) {
-  // whole rows once the heads alone give every CU a few workgroups, slices of 32 columns for fewer (d = 128, us: 64 heads
-  // 3.9 in slices and 4.3 whole, 256 heads 6.4 and 7.5, 1024 heads 26.0 and 23.5; slices of 16 columns, 64 heads, 6.1)
-  int dvs = p.DV;
-  const int64_t heads = (int64_t)p.nseq * p.H;
-  while (dvs > 32 && heads * (p.DV / dvs) < 1024) dvs /= 2;
+  const int dvs = step_columns(p);
   if (p.DK == 128) return launch_step_k<128>(p, dvs, bf16, s);
   if (p.DK == 64) return launch_step_k<64>(p, dvs, bf16, s);
   if (p.DK == 32) return launch_step_k<32>(p, dvs, bf16, s);

@@ -9,9 +9,6 @@
 
 namespace dr {
 
-constexpr int CACHE_VPT = 4;                       // float4 per thread
-constexpr int CACHE_BLOCK = 256 * CACHE_VPT;       // float4 per workgroup
-
 // Row of the state buffer and of the cache of item n; -1: outside.
 __device__ __forceinline__ int64_t cache_row(const int32_t* idx, int64_t rows, int64_t n) {
   const int64_t r = idx ? (int64_t)idx[n] : n;
@@ -143,8 +140,7 @@ __global__ __launch_bounds__(256) void state_unpack_kernel(const CacheParams p) 
 
 template <int DV>
 static hipError_t launch_cache(const CacheParams& p, bool e4m3, bool pack, hipStream_t s) {
-  const int64_t per = (p.DK * (DV / 4) + CACHE_BLOCK - 1) / CACHE_BLOCK;
-  const dim3 grid((unsigned)(p.count * p.H * per));
+  const dim3 grid((unsigned)(p.count * p.H * cache_parts(p.DK * DV)));
   if (pack && e4m3)
     hipLaunchKernelGGL((state_pack_kernel<DV, true>), grid, dim3(256), 0, s, p);
   else if (pack)

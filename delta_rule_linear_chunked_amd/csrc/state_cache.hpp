@@ -16,6 +16,12 @@ struct CacheParams {
   int32_t H, DK, DV;
 };
 
+constexpr int CACHE_VPT = 4;                  // float4 per thread
+constexpr int CACHE_BLOCK = 256 * CACHE_VPT;  // float4 per workgroup
+// Workgroups of one head's state, and whether a launch over `heads` states of one head fits (its work items are a 32-bit number).
+constexpr int64_t cache_parts(int hsz) { return (hsz / 4 + CACHE_BLOCK - 1) / CACHE_BLOCK; }
+constexpr bool cache_fits(int64_t heads, int hsz) { return heads * cache_parts(hsz) * 256 <= (int64_t)UINT32_MAX; }
+
 hipError_t launch_state_pack(const CacheParams& p, bool e4m3, hipStream_t s);
 hipError_t launch_state_unpack(const CacheParams& p, bool e4m3, hipStream_t s);
 

@@ -40,7 +40,9 @@ typedef enum dr_decay_layout {
  * num_heads must be a multiple of num_k_heads. strided = 0: q, k and v are dense; 1: the element strides
  * between consecutive tokens of a batch row and between batch rows (decode: between sequences) are given,
  * under the rules of dr_dims_v2 (heads and channels dense, non-negative, multiples of 16 bytes; token strides at
- * most 2^24 elements). At most 65536 heads. */
+ * most 2^24 elements). At most 65536 heads. A kernel has at most 2^32 - 1 work items, which bounds the
+ * (sequence, head) pairs of a call: about 5.5 million for the prefill (its workgroups have 768), 8.3 million chunks of
+ * heads for the gradients, 16.7 million heads for the step; larger ones are refused (DR_ERR_UNSUPPORTED). */
 typedef struct dr_decay_dims {
   int64_t batch;
   int64_t seqlen;
@@ -121,7 +123,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
 typedef enum dr_cache_format { DR_CACHE_INT8 = 0, DR_CACHE_E4M3 = 1 } dr_cache_format;
 
 /*
- * count      states moved by the call
+ * count      states moved by the call; at most 16.7 million workgroups of 16 KiB of one head (DR_ERR_UNSUPPORTED)
  * num_states rows of S [num_states, H, d_k, d_v]; num_slots rows of codes [num_slots, H, d_k, d_v] (1 byte each)
  *            and scales [num_slots, H, d_k]
  * state_idx  [count] int32 (device): row of S of each state, NULL: row n (num_states >= count)
