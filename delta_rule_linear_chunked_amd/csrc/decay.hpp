@@ -163,10 +163,6 @@ __device__ __forceinline__ void mma_rows(f32x4 (&acc)[N], const bf16x8 (&a)[NA],
 // Nothing moves across (the scheduler otherwise sinks every LDS read to its use, and each then waits in full)
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// The wait between an MFMA and the first use of its result behind a branch, which the compiler does not always
-// leave (seen in its output: 3 or 7 instead of 8 cycles where the two stand in different blocks).
-__device__ __forceinline__ void settle(f32x4& acc) { asm volatile("s_nop 7" : "+v"(acc)); }
-
 // LDS tile of token rows x W bf16 channels (W 32, 64 or 128), 16-byte pieces permuted within a row so that both
 // kinds of read are free of bank conflicts: a fragment along the channels (16 rows, one piece each; the
 // hardware serves rows 0-3 and 12-15 of one piece together with rows 4-11 of its neighbour) and a

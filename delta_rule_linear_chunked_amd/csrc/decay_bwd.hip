@@ -68,9 +68,8 @@ __device__ __forceinline__ f32x4 ratio_col(const DecayTab& tb, const float (&P)[
 }
 
 // Rows of tile R: P = (Q K^T) . ratio and E = (dO V^T) . ratio as bf16 terms into LDS, and their path sums
-// sum_r ratio(r, t) sum_{s<t} ratio(t-1, s) A[r, s] for the tile's rows r. R is a template argument so that no branch
-// stands between an MFMA and the first use of its result: where one did, the compiler left out the
-// wait that this needs (the last accumulator register was read 3 instead of 8 cycles after the MFMA).
+// sum_r ratio(r, t) sum_{s<t} ratio(t-1, s) A[r, s] for the tile's rows r. R is a template argument: the tiles
+// of A are then registers that no index selects at run time, and the loops over them straight code.
 template <int W, int V, typename InT, int DC, int R>
 __device__ __forceinline__ void grad_rows(unsigned char* sm, const DecayTab& tb, const float (&PT)[4], float* s_da, int lane) {
   using Sh = GradShape<W, V, InT, DC>;
@@ -324,8 +323,6 @@ __global__ __launch_bounds__(512) void decay_grad_kernel(const DecayParams p) {
           }
         }
         const int oc = 32 * w2 + 8 * g + 4 * e2;
-#pragma unroll
-        for (int r = 0; r < NT; ++r) settle(av[tv][r]);
         if (V > 32 || oc < p.DV) {
 #pragma unroll
           for (int r = 0; r < NT; ++r) {
@@ -437,11 +434,6 @@ __global__ __launch_bounds__(512) void decay_grad_kernel(const DecayParams p) {
         }
         const int heads = p.dq_heads;  // heads of the buffers: Hk, or H for the partial sums of shared heads
         const int hq = heads == p.H ? h : hk;
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          settle(aq[ti][r]);
-          settle(ak[ti][r]);
-        }
         if (W > 32 || oc < p.DK) {
 #pragma unroll
           for (int r = 0; r < NT; ++r) {
