@@ -15,7 +15,8 @@
  * on the current device, 16-byte aligned, work enqueued on `stream`, argument errors found on the host before
  * anything is launched, no pointer kept. Products and sums are held to fp32 (bf16 inputs enter exactly, fp32
  * values as three bf16 terms that hold all 24 bits): results agree with a float64 evaluation to about 1e-6
- * of the output's size. Zero and negative decays are exact: no quotient or logarithm of a decay is formed.
+ * of the output's size (2-norm; the gradient of one decay per head: of the sum of its tokens' magnitudes).
+ * Zero and negative decays are exact: no quotient or logarithm of a decay is formed.
  * Decays are not range-checked; the accuracy statement covers |a| <= 1. A NaN or an infinity in a token's
  * inputs makes the outputs of its 64-token chunk (earlier tokens of the chunk included) and of every later
  * chunk of that head unspecified; other heads and sequences are not affected, and neither are tokens that
