@@ -7,16 +7,16 @@
 //
 // One workgroup of 8 waves, with 4 more to fill the LDS, carries 16 CT value columns of one head through one
 // segment of a sequence; the waves of a column tile hold its d_k x 16 state in their accumulators for the whole
-// segment. The layouts are chosen so that nothing but the inputs goes through LDS: the accumulators of K^T V are, lane
-// for lane, the S^T operand of Q S0, and the accumulators of K Q^T are the P^T operand of P V (common
-// index orders of the 32-deep products, see decay.hpp), so O^T comes out with 4 consecutive columns per
-// lane and the state never leaves the registers. With fewer column tiles than waves, 8 / CT waves share a
-// tile: they split the state's channels, then the chunk's 16-token row tiles.
+// segment. The accumulators of K^T V are, lane for lane, the S^T operand of Q S0 (common index orders of the 32-deep
+// products, see decay.hpp), so the state never leaves the registers and O^T comes out with 4 consecutive columns per
+// lane. Through LDS go the inputs, with one or two column tiles V scaled for the state as well, P as three bf16 planes
+// (the filling waves form it once for all columns), and with fewer column tiles than waves the parts of Q S0: 8 / CT
+// waves then share a tile and split the state's channels, then the chunk's 16-token row tiles.
 //
 // What bounds it: a chunk's two phases (Q S0 and the scores; P V and the state) follow one another through
 // barriers, with LDS reads and the cutting of the state and of scaled V into bf16 terms beside the MFMA. 4 x 4096
 // tokens, 16 heads, d = 128, bf16: main pass 89 us (4.2 TB/s; MFMA busy a third of the time), states of the segments of
-// 1024 tokens 37, join 7; all told 132 to 139, where the inputs and outputs alone take 66 at the copy rate.
+// 1024 tokens 37, join 7; all told 132 to 141, where the inputs and outputs alone take 66 at the copy rate.
 #include <type_traits>
 
 #include "decay.hpp"

@@ -139,6 +139,10 @@ int64_t env_int(const char* name) {
 // The backward's state passes take 32 columns per workgroup, two of which share a CU with one for each direction; a
 // token takes them 0.012 us in bf16, 0.04 in fp32, which scales the launches' share. 4000 tokens, 4 heads, d = 64,
 // bf16: 256 tokens 42, 128 49, 1024 59, whole 81; 4 x 4096, 16 heads, d = 128: whole 593, 2048 664.
+// Packed calls are the least known: only the total length is on the host, and neither the join's traffic nor the
+// backward's second state pass is in the formula. 12 sequences in 32768 tokens, 16 / 4 heads, d = 128: 307 to 333 at the
+// planned 896 tokens, 295 at 1024; backward, 5 sequences in 7777 tokens, 12 / 3 heads, d = 64 / 128: 198 to 210 at the
+// planned 576, 173 with whole sequences.
 dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   dr::DecayPlan pl{};
   const int64_t tiles = d->head_dim_v / 16, pairs = d->num_seqs * d->num_heads, T = d->seqlen;
@@ -150,7 +154,8 @@ dr::DecayPlan plan_decay(const dr_decay_dims* d, bool packed, bool backward) {
   const double launches = backward && bf16 ? 800 : 250, step = backward && bf16 ? 25 : 8;
   int64_t seg = (T + 63) / 64 * 64;
   double best = 0;
-  // (the limit keeps the segments' states within 1 GiB or the final states' size; from 16 on every value of n is not tried)
+  // (the limit on the workgroups of a call that is cut keeps the segments' states within 1 GiB, at d = 128; smaller
+  // states and packed calls with many sequences end there far below it. From 16 on not every value of n is tried)
   const auto many = [&](int64_t n) { return (packed ? (n + d->num_seqs) * d->num_heads : n * pairs) * blocks > 16384; };
   for (int64_t n = 1; n == 1 || (n * 128 < T + 128 && !many(n)); n += 1 + n / 16) {
     const int64_t s = ((T + n - 1) / n + 63) / 64 * 64, nseg = s > 0 ? (T + s - 1) / s : 1;

@@ -120,6 +120,7 @@ int dr_decay_bwd(const void* q, const void* k, const void* v, const float* alpha
  *   DR_CACHE_E4M3   scale = the least power of two, 2^-126 at the least, with amax <= 448 scale; code = x / scale
  *                   rounded to OCP e4m3 (nearest, ties to even)
  * A row that holds a NaN or an infinity gets a NaN scale and zero codes: the whole row reads back as NaN.
+ * What is read back is code * scale rounded to float32: magnitudes from about 3.3e38 on may come back as infinities.
  */
 typedef enum dr_cache_format { DR_CACHE_INT8 = 0, DR_CACHE_E4M3 = 1 } dr_cache_format;
 
