@@ -32,6 +32,7 @@ _LIB_PATH = os.path.join(_PKG, "lib", "libdeltarule.so")
 # "product2": two KDA transitions per token (k [.., 2, d_k], v [.., 2, d_v], beta [.., 2])
 VARIANTS = {"kda": 0, "rda": 1, "gdn2": 2, "ckda": 3, "product2": 4}
 _DT = {torch.float32: 0, torch.bfloat16: 1}
+_UNSUPPORTED = -5  # DR_ERR_UNSUPPORTED
 _lib = None
 # bytes of the static device scratch behind dr_chunk_fwd_noalloc (DR_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 256 << 20
@@ -277,17 +278,21 @@ def _capturing() -> bool:
     return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
 
 
-def _captured_workspace(lib, d, variant: str, packed: bool, backward: int, device):
-    """For a call that is being captured: its workspace from torch's allocator, which then belongs to the graph, as
-    the arguments of the ``_ws`` entry points (the library's pool is refused in a capture). None otherwise.
-    ``backward`` as for dr_chunk_workspace; called with ``device`` current."""
-    if not _capturing():
-        return None
+def _pooled(lib, entry: str, with_space: str, args, d, variant: str, packed: bool, backward: int, dev) -> int:
+    """Calls ``entry`` with ``args`` and the current stream of ``dev`` (which is current). Its workspace comes from the
+    library's pool, which a stream that is being captured is refused: ``with_space`` then takes one from torch's
+    allocator, which belongs to the graph. ``backward`` as for dr_chunk_workspace. (Asked for in this order, the calls
+    outside a capture, which short prompts make often, do no more than before.)"""
+    stream = _stream(dev)
+    st = getattr(lib, entry)(*args, stream)
+    if st != _UNSUPPORTED or not torch.cuda.is_current_stream_capturing():
+        return st
     n = ctypes.c_int64()
-    _check(lib, lib.dr_chunk_workspace(_dims_arg(d), VARIANTS[variant], int(packed), backward, ctypes.byref(n)),
-           "dr_chunk_workspace")
-    buf = torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
-    return buf, (_ptr(buf), n.value)
+    st = lib.dr_chunk_workspace(_dims_arg(d), VARIANTS[variant], int(packed), backward, ctypes.byref(n))
+    if st != 0:
+        return st
+    buf = torch.empty(max(n.value, 1), dtype=torch.uint8, device=dev)
+    return getattr(lib, with_space)(*args, _ptr(buf), n.value, stream)
 
 
 def dr_chunk_fwd(q, k, v, alpha, erase, write, variant: str, S0, cu_seqlens, o, S_T) -> None:
@@ -371,13 +376,12 @@ def _chunk_fwd_call(entry, q, k, v, alpha, erase, write, variant, S0, cu_seqlens
     d = _dims_for(B, T, H, dk, dv, N, q.dtype, strides)
     opts = _opts(state_idx, rows, snapshots, snapshot_every, prep, alpha)
     with torch.cuda.device(dev):  # the library launches on the current device
-        space = None
+        args = (_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant], _ptr(S0),
+                _ptr(cu_seqlens), _ptr(o), _ptr(S_T), _dims_arg(d), ctypes.byref(opts))
         if entry == "dr_chunk_fwd_ex":
-            space = _captured_workspace(lib, d, variant, cu_seqlens is not None, 0, dev)
-        fn = getattr(lib, entry) if space is None else lib.dr_chunk_fwd_ws
-        st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant], _ptr(S0),
-                _ptr(cu_seqlens), _ptr(o), _ptr(S_T), _dims_arg(d), ctypes.byref(opts),
-                *(() if space is None else space[1]), _stream(dev))
+            st = _pooled(lib, entry, "dr_chunk_fwd_ws", args, d, variant, cu_seqlens is not None, 0, dev)
+        else:
+            st = getattr(lib, entry)(*args, _stream(dev))
     _check(lib, st, entry)
 
 
@@ -517,12 +521,11 @@ def dr_chunk_bwd(q, k, v, alpha, erase, write, variant: str, S0, cu_seqlens, dO,
         _need(checkpoints, "checkpoints", (rows, H, dk_, dv_), torch.float32, dev)
     d = _dims_for(B, T, H, dk_, dv_, N, q.dtype, strides)
     with torch.cuda.device(dev):
-        space = _captured_workspace(lib, d, variant, cu_seqlens is not None, 1 if checkpoints is None else 2, dev)
-        fn = lib.dr_chunk_bwd_ex if space is None else lib.dr_chunk_bwd_ws
-        st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant],
-                _ptr(S0), _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv),
-                _ptr(dalpha), _ptr(derase), _ptr(dwrite), _ptr(dS0), _ptr(checkpoints),
-                _dims_arg(d), *(() if space is None else space[1]), _stream(dev))
+        args = (_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(erase), _ptr(write), VARIANTS[variant], _ptr(S0),
+                _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dalpha), _ptr(derase),
+                _ptr(dwrite), _ptr(dS0), _ptr(checkpoints), _dims_arg(d))
+        st = _pooled(lib, "dr_chunk_bwd_ex", "dr_chunk_bwd_ws", args, d, variant, cu_seqlens is not None,
+                     1 if checkpoints is None else 2, dev)
     _check(lib, st, "dr_chunk_bwd")
 
 
