@@ -249,7 +249,7 @@ const char* dr_status_string(int status) {
     case DR_ERR_SHAPE: return "DR_ERR_SHAPE: negative or inconsistent sizes";
     case DR_ERR_DTYPE: return "DR_ERR_DTYPE: unsupported input dtype";
     case DR_ERR_LAYOUT: return "DR_ERR_LAYOUT: pointer not 16-byte aligned, or strides the call does not take";
-    case DR_ERR_UNSUPPORTED: return "DR_ERR_UNSUPPORTED: head size not in {16, 32, 64, 128}";
+    case DR_ERR_UNSUPPORTED: return "DR_ERR_UNSUPPORTED: a head size (16, 32, 64, 128), size or option that the call does not take";
     case DR_ERR_VARIANT: return "DR_ERR_VARIANT: unknown variant or gates that do not fit it";
     case DR_ERR_HIP: return "DR_ERR_HIP: HIP runtime or launch failure";
   }

@@ -90,7 +90,7 @@ typedef enum dr_status {
   DR_ERR_DTYPE = -3,       /* in_dtype is not DR_F32 / DR_BF16 */
   DR_ERR_LAYOUT = -4,      /* a pointer not 16-byte aligned, or strides the call does not take */
   DR_ERR_ALIGN = -4,       /* the same code under its earlier name */
-  DR_ERR_UNSUPPORTED = -5, /* head size outside {16, 32, 64, 128}, or a size beyond the limits */
+  DR_ERR_UNSUPPORTED = -5, /* head size outside {16, 32, 64, 128}, a size beyond the limits, or an option not taken */
   DR_ERR_VARIANT = -6,     /* unknown variant, or gate pointers that do not fit it */
   DR_ERR_HIP = -7          /* a HIP runtime call or kernel launch failed */
 } dr_status;
