@@ -42,8 +42,8 @@ typedef enum dr_decay_layout {
  * between consecutive tokens of a batch row and between batch rows (decode: between sequences) are given,
  * under the rules of dr_dims_v2 (heads and channels dense, non-negative, multiples of 16 bytes; token strides at
  * most 2^24 elements). At most 65536 heads. A kernel has at most 2^32 - 1 work items, which bounds the
- * (sequence, head) pairs of a call: about 5.5 million for the prefill (its workgroups have 768), 8.3 million chunks of
- * heads for the gradients, 16.7 million heads for the step; larger ones are refused (DR_ERR_UNSUPPORTED). */
+ * (sequence, head) pairs of a call: about 5.5 million for the prefill (its workgroups have 768; float32 inputs take
+ * d_v / 32 of them a head, d_v / 16 with d_k = 128), 8.3 million chunks of heads for the gradients, 16.7 million heads for the step; larger ones are refused (DR_ERR_UNSUPPORTED). */
 typedef struct dr_decay_dims {
   int64_t batch;
   int64_t seqlen;
