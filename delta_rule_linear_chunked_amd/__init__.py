@@ -25,7 +25,10 @@ __all__ = ["dr_chunk_fwd", "dr_decode_step", "dr_chunk_fwd_ex", "dr_chunk_fwd_no
            "library_path",
            "load_library", "VARIANTS", "DeltaRuleError",
            "dr_decay_fwd", "dr_decay_step", "dr_decay_bwd", "decay_fwd", "decay_step", "decay_bwd", "decay_attention",
-           "dr_state_pack", "dr_state_unpack", "state_pack", "state_unpack"]
+           "dr_state_pack", "dr_state_unpack", "state_pack", "state_unpack",
+           "dr_conv_fwd", "dr_conv_step", "dr_conv_bwd", "conv_fwd", "conv_step", "conv_bwd", "causal_conv",
+           "dr_scan_fwd", "dr_scan_step", "dr_scan_bwd", "scan_fwd", "scan_step", "scan_bwd", "selective_scan",
+           "dr_norm_fwd", "dr_norm_bwd", "norm_fwd", "norm_bwd", "rms_norm"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "lib", "libdeltarule.so")
@@ -147,6 +150,8 @@ def load_library(path: Optional[str] = None):
     lib.dr_chunk_fwd_plan_ex.restype = ip
     if hasattr(lib, "dr_decay_fwd"):  # (a host-only build of api.cpp has the entry points of deltarule.h alone)
         _decay.declare(lib)
+    if hasattr(lib, "dr_scan_fwd"):
+        _scan.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -599,3 +604,7 @@ def delta_rule(q, k, v, alpha, erase, write=None, variant: str = "kda", S0=None,
 from . import _decay  # noqa: E402  (its functions use the helpers above)
 from ._decay import (decay_attention, decay_bwd, decay_fwd, decay_step, dr_decay_bwd, dr_decay_fwd,  # noqa: E402,F401
                      dr_decay_step, dr_state_pack, dr_state_unpack, state_pack, state_unpack)
+from . import _scan  # noqa: E402
+from ._scan import (causal_conv, conv_bwd, conv_fwd, conv_step, dr_conv_bwd, dr_conv_fwd, dr_conv_step,  # noqa: E402,F401
+                    dr_norm_bwd, dr_norm_fwd, dr_scan_bwd, dr_scan_fwd, dr_scan_step, norm_bwd, norm_fwd, rms_norm,
+                    scan_bwd, scan_fwd, scan_step, selective_scan)

@@ -1,0 +1,438 @@
+// Short causal convolution over the tokens of every channel on gfx950, its single-token step and its gradients.
+//
+// A few operations per value: bound by memory. A lane has one 16-byte piece of the channels (or one channel where rows are
+// not aligned), a wave a run of consecutive tokens whose last inputs slide through registers, so an input is read once
+// (and the width - 1 in front of a run again). A run that holds the ends of packed sequences is walked in
+// pieces, one per sequence.
+#include "scan.hpp"
+
+namespace dr {
+
+// The part of a run that lies in one sequence: tokens a .. b of row `row`, of sequence n with tokens start .. end.
+struct RunPiece {
+  int n, a, b, start, end;
+};
+__device__ __forceinline__ RunPiece piece_at(const ConvParams& p, int row, int t, int t1) {
+  RunPiece q;
+  q.a = t;
+  if (p.cu) {
+    q.n = seq_of(p.cu, p.nseq, t);
+    // (offsets out of order or outside the row still give 0 <= start <= t < end <= T)
+    q.start = min(max(p.cu[q.n], 0), t);
+    q.end = p.cu[q.n + 1];
+    if (q.end <= t || p.cu[q.n] > t) {  // no sequence holds token t
+      q.n = -1;
+      q.end = t1;
+    }
+    q.end = min(q.end, (int)p.T);
+  } else {
+    q.n = row;
+    q.start = 0;
+    q.end = (int)p.T;
+  }
+  q.b = min(t1, q.end);
+  return q;
+}
+
+template <typename InT, int VEC, int W>
+struct Conv {
+  using V = typename Vec<InT, VEC>::type;
+  const ConvParams& p;
+  int c;
+  bool in;
+  float w[W][VEC], bias[VEC];
+  __device__ __forceinline__ Conv(const ConvParams& p_, int c_) : p(p_), c(c_), in(c_ < p_.C) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      bias[v] = in && p.bias ? p.bias[c + v] : 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][v] = in ? p.w[(int64_t)(c + v) * W + j] : 0.f;
+    }
+  }
+  // x of token t of batch row `row` (in range)
+  __device__ __forceinline__ V load(const InT* x, int64_t t) const {
+    V r = V{};
+    if (in) r = *reinterpret_cast<const V*>(x + t * p.x_ts);
+    return r;
+  }
+  // input number k (0: the oldest) of the state of sequence n
+  __device__ __forceinline__ V old(int64_t srow, int k) const {
+    V r = V{};
+    if (in && p.state && srow >= 0)
+      r = *reinterpret_cast<const V*>(static_cast<const InT*>(p.state) + (srow * (W - 1) + k) * p.C + c);
+    return r;
+  }
+  // the W - 1 inputs in front of token a of a sequence that starts at `start`
+  __device__ __forceinline__ void window(const InT* x, int a, int start, int64_t srow, float (&e)[W][VEC]) const {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int t = a - (W - 1) + j;
+      unpack<VEC, InT>(t >= start ? load(x, t) : old(srow, t - start + W - 1), e[j]);
+    }
+  }
+  __device__ __forceinline__ void dot(const float (&e)[W][VEC], float (&u)[VEC]) const {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      u[v] = bias[v];
+#pragma unroll
+      for (int j = 0; j < W; ++j) u[v] = fmaf(w[j][v], e[j][v], u[v]);
+    }
+  }
+  static __device__ __forceinline__ void slide(float (&e)[W][VEC]) {
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) e[j][v] = e[j + 1][v];
+  }
+};
+
+// The last W - 1 inputs of sequence n, into its state (every row read before the first is written: they may be the same).
+template <typename InT, int VEC, int W>
+__device__ __forceinline__ void conv_tail(const ConvParams& p, int n, int c) {
+  using V = typename Vec<InT, VEC>::type;
+  const Conv<InT, VEC, W> k(p, c);
+  int start = 0, end = (int)p.T;
+  int64_t row = n;
+  if (p.cu) {
+    start = min(max(p.cu[n], 0), (int)p.T);
+    end = min(max(p.cu[n + 1], start), (int)p.T);
+    row = 0;
+  }
+  const int64_t s = state_row(p.sidx, p.nslots, n);
+  const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
+  V v[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const int t = end - (W - 1) + j;
+    v[j] = t >= start ? k.load(x, t) : k.old(s, t - start + W - 1);
+  }
+  if (s < 0 || !k.in) return;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+    *reinterpret_cast<V*>(static_cast<InT*>(p.state_T) + (s * (W - 1) + j) * p.C + c) = v[j];
+}
+
+template <typename InT, int VEC, int W>
+__global__ __launch_bounds__(64 * CONV_WAVES) void conv_fwd_kernel(const ConvParams p) {
+  using V = typename Vec<InT, VEC>::type;
+  constexpr int AHEAD = 8;  // tokens whose loads are issued together
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int blk = p.block0 + blockIdx.x, cb = blk % p.cblocks;
+  const int c = (cb * 64 + lane) * VEC;
+  if (blk >= p.nmain) {
+    const int n = (blk - p.nmain) / p.cblocks * CONV_WAVES + wave;
+    if (n < p.nseq) conv_tail<InT, VEC, W>(p, n, c);
+    return;
+  }
+  const int rid = blk / p.cblocks * CONV_WAVES + wave;
+  const int row = rid / p.runs;
+  if (row >= p.nbatch) return;
+  const int t0 = (rid - row * p.runs) * p.run;
+  const int t1 = (int)(p.T - t0 < p.run ? p.T : t0 + p.run);
+  const Conv<InT, VEC, W> k(p, c);
+  const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
+  InT* y = static_cast<InT*>(p.y) + (int64_t)row * p.T * p.C + c;
+  for (int t = t0; t < t1;) {
+    const RunPiece q = piece_at(p, row, t, t1);
+    if (q.n >= 0) {
+      float e[W][VEC];
+      k.window(x, q.a, q.start, state_row(p.sidx, p.nslots, q.n), e);
+      for (int a = q.a; a < q.b; a += AHEAD) {
+        V raw[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) raw[i] = k.load(x, min(a + i, q.b - 1));
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          if (a + i < q.b) {
+            unpack<VEC, InT>(raw[i], e[W - 1]);
+            float u[VEC];
+            k.dot(e, u);
+            if (p.silu)
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
+            if (k.in) *reinterpret_cast<V*>(y + (int64_t)(a + i) * p.C) = pack<VEC, InT>(u);
+            k.slide(e);
+          }
+        }
+      }
+    }
+    t = q.b;
+  }
+}
+
+template <typename InT, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_step_kernel(const ConvParams p) {
+  using V = typename Vec<InT, VEC>::type;
+  const int cb = blockIdx.x % p.cblocks;
+  const int n = blockIdx.x / p.cblocks * CONV_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = (cb * 64 + (threadIdx.x & 63)) * VEC;
+  if (n >= p.nseq || c >= p.C) return;
+  const int64_t s = state_row(p.sidx, p.nslots, n);
+  V* y = reinterpret_cast<V*>(static_cast<InT*>(p.y) + (int64_t)n * p.C + c);
+  if (s < 0) {  // no stored state
+    *y = V{};
+    return;
+  }
+  V* st = reinterpret_cast<V*>(static_cast<InT*>(p.state_T) + s * (W - 1) * p.C + c);
+  V r[W];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) r[j] = *reinterpret_cast<const V*>(reinterpret_cast<const InT*>(st) + (int64_t)j * p.C);
+  r[W - 1] = *reinterpret_cast<const V*>(static_cast<const InT*>(p.x) + n * p.x_bs + c);
+  const Conv<InT, VEC, W> k(p, c);
+  float e[W][VEC], u[VEC];
+#pragma unroll
+  for (int j = 0; j < W; ++j) unpack<VEC, InT>(r[j], e[j]);
+  k.dot(e, u);
+  if (p.silu)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<V*>(reinterpret_cast<InT*>(st) + (int64_t)j * p.C) = r[j + 1];
+  *y = pack<VEC, InT>(u);
+}
+
+// Gradient of a token's sum before the activation: dy, with silu times sigmoid(u) (1 + u sigmoid(-u)).
+template <int VEC>
+__device__ __forceinline__ void conv_du(const float (&u)[VEC], const float (&dy)[VEC], int silu, float (&du)[VEC]) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const float sg = sigmoid_f(u[v]);
+    du[v] = silu ? dy[v] * (sg * fmaf(u[v], 1.f - sg, 1.f)) : dy[v];
+  }
+}
+
+// An input reaches the outputs of its own and the next W - 1 tokens of its sequence: the gradients du of W consecutive
+// tokens slide through registers behind the inputs, and token t completes the gradient of input t - W + 1. The
+// gradients of the weights stay in registers over the run; a workgroup adds its four runs'.
+template <typename InT, int VEC, int W>
+__global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvParams p) {
+  using V = typename Vec<InT, VEC>::type;
+  constexpr int AHEAD = 8;
+  __shared__ float s_part[CONV_WAVES - 1][W + 1][64 * VEC];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int blk = blockIdx.x, cb = blk % p.cblocks;
+  const int c = (cb * 64 + lane) * VEC;
+  if (blk >= p.nmain) {  // the gradient of sequence n's starting state
+    const int n = (blk - p.nmain) / p.cblocks * CONV_WAVES + wave;
+    if (n >= p.nseq) return;
+    const Conv<InT, VEC, W> k(p, c);
+    int start = 0, end = (int)p.T, row = n;
+    if (p.cu) {
+      start = min(max(p.cu[n], 0), (int)p.T);
+      end = min(max(p.cu[n + 1], start), (int)p.T);
+      row = 0;
+    }
+    const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
+    const InT* dy = static_cast<const InT*>(p.dy) + (int64_t)row * p.T * p.C + c;
+    float e[W][VEC], ds[W - 1][VEC];
+    k.window(x, start, start, n, e);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) ds[j][v] = 0.f;
+      const int L = end - start;
+      if (j >= L && p.dstate_T && k.in)
+        unpack<VEC, InT>(*reinterpret_cast<const V*>(static_cast<const InT*>(p.dstate_T) + ((int64_t)n * (W - 1) + j - L) * p.C + c), ds[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i)
+      if (start + i < end) {
+        float u[VEC], g[VEC], du[VEC];
+        unpack<VEC, InT>(k.load(x, start + i), e[W - 1]);
+        k.dot(e, u);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) g[v] = 0.f;
+        if (k.in) unpack<VEC, InT>(*reinterpret_cast<const V*>(dy + (int64_t)(start + i) * p.C), g);
+        conv_du<VEC>(u, g, p.silu, du);
+#pragma unroll
+        for (int j = i; j < W - 1; ++j)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) ds[j][v] = fmaf(k.w[j - i][v], du[v], ds[j][v]);
+        k.slide(e);
+      }
+    if (k.in)
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        *reinterpret_cast<V*>(static_cast<InT*>(p.dstate) + ((int64_t)n * (W - 1) + j) * p.C + c) = pack<VEC, InT>(ds[j]);
+    return;
+  }
+  const Conv<InT, VEC, W> k(p, c);
+  float dw[W + 1][VEC];
+#pragma unroll
+  for (int j = 0; j <= W; ++j)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) dw[j][v] = 0.f;
+  const int rb = blk / p.cblocks, rid = rb * CONV_WAVES + wave;
+  const int row = rid / p.runs;
+  if (row < p.nbatch) {
+    const int t0 = (rid - row * p.runs) * p.run;
+    const int t1 = (int)(p.T - t0 < p.run ? p.T : t0 + p.run);
+    const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
+    const int64_t at = (int64_t)row * p.T * p.C + c;
+    const InT* dy = static_cast<const InT*>(p.dy) + at;
+    InT* dx = static_cast<InT*>(p.dx) + at;
+    for (int t = t0; t < t1;) {
+      const RunPiece q = piece_at(p, row, t, t1);
+      if (q.n >= 0) {
+        float e[W][VEC], du[W][VEC];  // du[j]: of token t - W + 1 + j
+        k.window(x, q.a, q.start, q.n, e);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) du[j][v] = 0.f;
+        const int stop = q.b + W - 1;  // (tokens past the sequence's end have no gradient)
+        for (int a = q.a; a < stop; a += AHEAD) {
+          V xr[AHEAD], gr[AHEAD];
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int at_t = min(a + i, q.end - 1);
+            xr[i] = k.load(x, at_t);
+            gr[i] = V{};
+            if (k.in) gr[i] = *reinterpret_cast<const V*>(dy + (int64_t)at_t * p.C);
+          }
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int tt = a + i;
+            if (tt < stop) {
+              k.slide(du);
+              if (tt < q.end) {
+                float u[VEC], g[VEC];
+                unpack<VEC, InT>(xr[i], e[W - 1]);
+                unpack<VEC, InT>(gr[i], g);
+                k.dot(e, u);
+                conv_du<VEC>(u, g, p.silu, du[W - 1]);
+                if (tt < q.b)
+#pragma unroll
+                  for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][v] = fmaf(du[W - 1][v], e[j][v], dw[j][v]);
+                    dw[W][v] += du[W - 1][v];
+                  }
+                k.slide(e);
+              } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) du[W - 1][v] = 0.f;
+              }
+              const int i0 = tt - (W - 1);  // this input's gradient is complete
+              if (i0 >= q.a) {
+                float g[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) g[v] = 0.f;
+                if (i0 >= q.end - (W - 1) && p.dstate_T && k.in)
+                  unpack<VEC, InT>(*reinterpret_cast<const V*>(static_cast<const InT*>(p.dstate_T) +
+                                                               ((int64_t)q.n * (W - 1) + i0 - (q.end - (W - 1))) * p.C + c), g);
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                  for (int v = 0; v < VEC; ++v) g[v] = fmaf(k.w[W - 1 - j][v], du[j][v], g[v]);
+                if (k.in) *reinterpret_cast<V*>(dx + (int64_t)i0 * p.C) = pack<VEC, InT>(g);
+              }
+            }
+          }
+        }
+      }
+      t = q.b;
+    }
+  }
+  if (wave > 0)
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) s_part[wave - 1][j][v * 64 + lane] = dw[j][v];
+  __syncthreads();
+  if (wave > 0 || !k.in) return;
+#pragma unroll
+  for (int j = 0; j <= W; ++j)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      float a = dw[j][v];
+#pragma unroll
+      for (int g = 0; g < CONV_WAVES - 1; ++g) a += s_part[g][j][v * 64 + lane];
+      p.part[((int64_t)rb * (W + 1) + j) * p.C + c + v] = a;
+    }
+}
+
+// dw [C, W] and db [C] from the workgroups' sums: 64 columns x 16 groups of run blocks a workgroup.
+template <int W>
+__global__ __launch_bounds__(1024) void conv_dw_kernel(const ConvParams p, int parts) {
+  __shared__ float s[16][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+  const int n = (W + 1) * p.C;
+  float v = 0.f;
+  if (col < n)
+    for (int r = g; r < parts; r += 16) v += p.part[(int64_t)r * n + col];
+  s[g][threadIdx.x & 63] = v;
+  __syncthreads();
+  if (g == 0 && col < n) {
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) a += s[k][threadIdx.x];
+    const int j = col / p.C, c = col - j * p.C;
+    if (j < W)
+      p.dw[(int64_t)c * W + j] = a;
+    else if (p.db)
+      p.db[c] = a;
+  }
+}
+
+static int64_t run_blocks(const ConvParams& p) { return ((int64_t)p.nbatch * p.runs + CONV_WAVES - 1) / CONV_WAVES; }
+static int64_t seq_blocks(const ConvParams& p) { return ((int64_t)p.nseq + CONV_WAVES - 1) / CONV_WAVES; }
+
+template <typename InT, int VEC, int W>
+static hipError_t launch_fwd_t(ConvParams p, hipStream_t s) {
+  const int64_t main = run_blocks(p) * p.cblocks, tail = p.state_T ? seq_blocks(p) * p.cblocks : 0;
+  p.nmain = (int32_t)main;
+  p.block0 = 0;
+  // the states' own launch where the tokens' still read the states that it writes
+  const bool apart = tail > 0 && p.state == p.state_T;
+  const int64_t first = apart ? main : main + tail;
+  if (first > 0)
+    hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), dim3((unsigned)first), dim3(64 * CONV_WAVES), 0, s, p);
+  if (apart) {
+    p.block0 = p.nmain;
+    hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), dim3((unsigned)tail), dim3(64 * CONV_WAVES), 0, s, p);
+  }
+  return hipGetLastError();
+}
+template <typename InT, int VEC, int W>
+static hipError_t launch_step_t(const ConvParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((conv_step_kernel<InT, VEC, W>), dim3((unsigned)(seq_blocks(p) * p.cblocks)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+template <typename InT, int VEC, int W>
+static hipError_t launch_bwd_t(ConvParams p, hipStream_t s) {
+  const int64_t main = run_blocks(p) * p.cblocks, tail = p.dstate ? seq_blocks(p) * p.cblocks : 0;
+  p.nmain = (int32_t)main;
+  p.block0 = 0;
+  if (main + tail > 0)
+    hipLaunchKernelGGL((conv_bwd_kernel<InT, VEC, W>), dim3((unsigned)(main + tail)), dim3(64 * CONV_WAVES), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((conv_dw_kernel<W>), dim3((unsigned)(((W + 1) * (int64_t)p.C + 63) / 64)), dim3(1024), 0, s, p, (int)run_blocks(p));
+  return hipGetLastError();
+}
+
+#define DR_CONV_LAUNCH(FN)                                                                      \
+  template <typename InT, int VEC>                                                              \
+  static hipError_t FN##_w(const ConvParams& p, int width, hipStream_t s) {                     \
+    return width == 4 ? FN##_t<InT, VEC, 4>(p, s) : width == 3 ? FN##_t<InT, VEC, 3>(p, s) : FN##_t<InT, VEC, 2>(p, s); \
+  }
+DR_CONV_LAUNCH(launch_fwd)
+DR_CONV_LAUNCH(launch_step)
+DR_CONV_LAUNCH(launch_bwd)
+#undef DR_CONV_LAUNCH
+
+hipError_t launch_conv_fwd(ConvParams p, int width, bool bf16, bool vec, hipStream_t s) {
+  if (bf16) return vec ? launch_fwd_w<__bf16, 8>(p, width, s) : launch_fwd_w<__bf16, 1>(p, width, s);
+  return vec ? launch_fwd_w<float, 4>(p, width, s) : launch_fwd_w<float, 1>(p, width, s);
+}
+hipError_t launch_conv_step(const ConvParams& p, int width, bool bf16, bool vec, hipStream_t s) {
+  if (bf16) return vec ? launch_step_w<__bf16, 8>(p, width, s) : launch_step_w<__bf16, 1>(p, width, s);
+  return vec ? launch_step_w<float, 4>(p, width, s) : launch_step_w<float, 1>(p, width, s);
+}
+hipError_t launch_conv_bwd(ConvParams p, int width, bool bf16, bool vec, hipStream_t s) {
+  if (bf16) return vec ? launch_bwd_w<__bf16, 4>(p, width, s) : launch_bwd_w<__bf16, 1>(p, width, s);
+  return vec ? launch_bwd_w<float, 4>(p, width, s) : launch_bwd_w<float, 1>(p, width, s);
+}
+
+}  // namespace dr

@@ -1,0 +1,500 @@
+// Gradients of the selective scan on gfx950.
+//
+// With G_t the gradient that reaches h_t (from y_t, from h_{t+1} and from the final state) and a_t = exp(d_t A):
+//   G_t = dy'_t C_t + a_{t+1} G_{t+1},  dy' = dy silu(z)
+//   dB_t = sum_c G_t d_t x_t,  dC_t = sum_c dy'_t h_t,  u = sum_n G_t B_t,  e = sum_n G_t a_t h_{t-1} A
+//   dx = u d + D dy',  d(d) = u x + e,  dA = sum_t d_t G_t a_t h_{t-1},  dz = dy (C h + D x) silu'(z)
+// Three steps. scan_states_kernel walks every segment once (a lane has a channel, as in the forward pass) and leaves its
+// state from zero at every 8th token, behind it, and the gradient that its outputs send to the state in front of it.
+// scan_join2_kernel joins segments in both directions. scan_grad_kernel takes a segment's chunks of 8 tokens from the last to the first: states and
+// decays of the chunk again from its checkpoint, held in registers (8 tokens x 4 channels x 2 states a lane), then
+// the tokens in reverse. A lane's square of channels and states shares the two kinds of sums between lanes evenly: over states (dx,
+// dd, y) across the lanes' rows, over channels (dB, dC) within eight lanes.
+#include "scan.hpp"
+
+namespace dr {
+
+typedef const __attribute__((address_space(4))) uint32_t* const_u32;
+template <typename InT>
+__device__ __forceinline__ float row_elem(const uint32_t* w, int i) {
+  if constexpr (sizeof(InT) == 4)
+    return __builtin_bit_cast(float, w[i]);
+  else
+    return __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+
+// Local states at every 8th token and behind the segment, the sums of d there, and (BOTH) the reverse part.
+template <int NS, int NW, typename InT, bool BOTH>
+__global__ __launch_bounds__(64 * NW) void scan_states_kernel(const ScanParams p) {
+  constexpr int N = NS * NW, TT = SCAN_CHUNK, RW = NS * (int)sizeof(InT) / 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ntiles = p.G * p.tiles;
+  const int slot = blockIdx.x / ntiles, tile = blockIdx.x - slot * ntiles;
+  const SlotSpan sp = slot_span(p, slot);
+  if (sp.n < 0) return;
+  const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + lane;
+  const bool on = in_g < p.Cg;
+  const int c = g * p.Cg + min(in_g, p.Cg - 1);
+  float A[NS], h[NS], P[NS], R[NS];
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    A[j] = p.A[(int64_t)c * N + wave * NS + j] * LOG2E;
+    h[j] = R[j] = 0.f;
+    P[j] = 1.f;
+  }
+  const float bias = p.bias ? p.bias[c] : 0.f;
+  const int len = sp.len;
+  const InT* x = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
+  const InT* dt = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
+  const InT* z = BOTH && p.z ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : nullptr;
+  const InT* dy = BOTH ? static_cast<const InT*>(p.dy) + (sp.b * p.T + sp.t0) * (int64_t)p.C + c : nullptr;
+  const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N + wave * NS;
+  const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N + wave * NS;
+  const int cps = p.seg / TT;
+  float sumd = 0.f;
+  InT xn[TT], dn[TT], zn[TT], yn[TT];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int64_t r = min(t + i, len - 1);
+      xn[i] = x[r * p.x_ts];
+      dn[i] = dt[r * p.dt_ts];
+      if constexpr (BOTH) {
+        zn[i] = z ? z[r * p.z_ts] : InT(0);
+        yn[i] = dy[r * p.C];
+      }
+    }
+  };
+  if (len > 0) fetch(0);
+  for (int t = 0; t < len; t += TT) {
+    if (on) {
+      const int64_t k = (int64_t)slot * cps + t / TT;
+      if (t > 0) {  // (a segment begins at zero)
+        float* to = p.ck + (k * p.C + c) * N + wave * NS;
+#pragma unroll
+        for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
+      }
+      if (wave == 0) p.ckd[k * p.C + c] = sumd;
+    }
+    float xv[TT], dv[TT], gv[TT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      xv[i] = (float)xn[i];
+      const float raw = (float)dn[i] + bias;
+      dv[i] = p.softplus ? softplus_f(raw) : raw;
+      if constexpr (BOTH) {
+        const float zv = (float)zn[i];
+        gv[i] = (float)yn[i];
+        if (z) gv[i] *= zv * sigmoid_f(zv);
+      }
+    }
+    if (t + TT < len) fetch(t + TT);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      if (t + i < len) {
+        uint32_t Bt[RW], Ct[RW];
+        const const_u32 bq = (const_u32)(uintptr_t)(Bp + (t + i) * p.b_ts), cq = (const_u32)(uintptr_t)(Cp + (t + i) * p.c_ts);
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          Bt[j] = bq[j];
+          if constexpr (BOTH) Ct[j] = cq[j];
+        }
+        const float d = dv[i], dx = d * xv[i];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const float a = __builtin_amdgcn_exp2f(d * A[j]);
+          h[j] = fmaf(a, h[j], dx * row_elem<InT>(Bt, j));
+          if constexpr (BOTH) {
+            P[j] *= a;
+            R[j] = fmaf(P[j], gv[i] * row_elem<InT>(Ct, j), R[j]);
+          }
+        }
+        sumd += d;
+      }
+    }
+  }
+  if constexpr (BOTH) {
+    if (!on) return;
+    const int64_t at = ((int64_t)slot * p.C + c) * N + wave * NS;
+#pragma unroll
+    for (int j = 0; j < NS; j += 4) {
+      *reinterpret_cast<f32x4*>(p.part + at + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
+      *reinterpret_cast<f32x4*>(p.rpart + at + j) = f32x4{R[j], R[j + 1], R[j + 2], R[j + 3]};
+    }
+    if (wave == 0) p.sumd[(int64_t)slot * p.C + c] = sumd;
+  }
+}
+
+// Segments joined: forward (blockIdx.y 0) the state at each one's start in the place of its own, in reverse (1) the gradient that reaches
+// the state behind each one in the place of what it sends forward.
+template <int N>
+__global__ __launch_bounds__(256) void scan_join2_kernel(const ScanParams p) {
+  const int per = (p.C * (N / 4) + 255) / 256;
+  const int n = blockIdx.x / per, e = (blockIdx.x - n * per) * 256 + threadIdx.x;
+  if (e >= p.C * (N / 4)) return;
+  const int c = e / (N / 4), j = e - c * (N / 4);
+  const int first = p.cu ? p.slot_first[n] : n * p.nseg, past = p.cu ? p.slot_first[n + 1] : first + p.nseg;
+  const bool back = blockIdx.y == 1;
+  f32x4 A = *reinterpret_cast<const f32x4*>(p.A + (int64_t)c * N + 4 * j), v = {0, 0, 0, 0};
+  const float* from = back ? p.dST : p.S0;
+  float* part = back ? p.rpart : p.part;
+  if (from) v = *reinterpret_cast<const f32x4*>(from + ((int64_t)n * p.C + c) * N + 4 * j);
+  for (int k = first; k < past; ++k) {
+    const int64_t s = back ? past - 1 - (k - first) : k;
+    f32x4* at = reinterpret_cast<f32x4*>(part + (s * p.C + c) * N + 4 * j);
+    const f32x4 own = *at;
+    const float d = p.sumd[s * p.C + c] * LOG2E;
+    *at = v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(__builtin_amdgcn_exp2f(d * A[i]), v[i], own[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums across lanes
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// over 8 neighbouring lanes, in all of them: swapped in pairs, in quads' halves, mirrored in eight
+__device__ __forceinline__ float sum8(float v) { return dpp_add<0x141>(dpp_add<0x4e>(dpp_add<0xb1>(v))); }
+// a of lanes l and l ^ 32 (l ^ 16) in the lower lanes of the pair, b's sum in the upper ones
+__device__ __forceinline__ float pair32(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+__device__ __forceinline__ float pair16(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// A workgroup: 4 waves, each 32 channels x 16 states (SL waves share channels), one segment.
+template <int N>
+struct GradShape {
+  static constexpr int SL = N / 16;           // slices of states
+  static constexpr int CB = 4 / SL;           // channel blocks
+  static constexpr int CH = 32 * CB;          // channels
+  static constexpr int ROWS = 256 / CH;       // token rows that the threads cover at once
+  static constexpr int PP = SCAN_CHUNK / ROWS;  // (token, channel) pairs of a thread
+};
+template <int N, typename InT, bool GATE>
+__global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
+  using Sh = GradShape<N>;
+  constexpr int K = SCAN_CHUNK, CH = Sh::CH, SL = Sh::SL, PP = Sh::PP, ROWS = Sh::ROWS;
+  __shared__ __align__(16) float s_d[K][CH], s_dx[K][CH], s_dy[K][CH];
+  __shared__ __align__(16) float s_b[K][N], s_c[K][N];
+  __shared__ float s_u[SL][K][CH], s_e[SL][K][CH], s_y[GATE ? SL : 1][GATE ? K : 1][GATE ? CH : 1];
+  __shared__ __align__(16) float s_bc[4][K][32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int sl = wave % SL, cb = wave / SL;
+  const int per = p.G * p.cblocks;
+  const int slot = blockIdx.x / per, blk = blockIdx.x - slot * per;
+  const int g = blk / p.cblocks, in0 = (blk - g * p.cblocks) * CH;  // the group, the first channel within it
+  const SlotSpan sp = slot_span(p, slot);
+  if (sp.n < 0) return;
+  const int len = sp.len, cps = p.seg / K, C = p.C;
+  // as the lane of states and gradients: 4 channels, 2 states
+  const int ng = lane >> 3, cg = lane & 7;
+  const int l_ch = cb * 32 + cg * 4, n0 = sl * 16 + ng * 2;
+  int lc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) lc[i] = g * p.Cg + min(in0 + l_ch + i, p.Cg - 1);
+  float A[4][2], hs[4][2], carry[4][2], dA[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t at = (int64_t)lc[i] * N + n0 + j;
+      A[i][j] = p.A[at] * LOG2E;
+      dA[i][j] = 0.f;
+      const float* from = p.part ? p.part + (int64_t)slot * C * N : p.S0 ? p.S0 + (int64_t)sp.n * C * N : nullptr;
+      hs[i][j] = from ? from[at] : 0.f;
+      const float* back = p.part ? p.rpart + (int64_t)slot * C * N : p.dST ? p.dST + (int64_t)sp.n * C * N : nullptr;
+      carry[i][j] = back ? back[at] : 0.f;
+    }
+  // as the thread of (token, channel) pairs: one channel, PP tokens of a chunk
+  const int pc = tid % CH, prow = tid / CH;
+  const bool on = in0 + pc < p.Cg;
+  const int c = g * p.Cg + min(in0 + pc, p.Cg - 1);
+  const float bias = p.bias ? p.bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
+  const InT* x = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
+  const InT* dt = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
+  const InT* z = GATE ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : nullptr;
+  const int64_t row0 = sp.b * p.T + sp.t0;
+  const InT* dy = static_cast<const InT*>(p.dy) + row0 * C + c;
+  const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N;
+  const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N;
+  float accD = 0.f, accb = 0.f;
+  InT xn[PP], dn[PP], zn[PP], yn[PP];
+  float hn[4][2], dsum[4];
+  constexpr int BCN = (2 * K * N + 255) / 256;  // elements of B and C of a thread
+  InT bn[BCN];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int64_t r = min(t + prow + i * ROWS, len - 1);
+      xn[i] = x[r * p.x_ts];
+      dn[i] = dt[r * p.dt_ts];
+      if constexpr (GATE) zn[i] = z[r * p.z_ts];
+      yn[i] = dy[r * C];
+    }
+#pragma unroll
+    for (int i = 0; i < BCN; ++i) {
+      const int q = tid + i * 256, m = q / (K * N), e = q % (K * N);  // B first, then C
+      const int64_t r = t + e / N;
+      bn[i] = InT(0);
+      if (m < 2 && r < len) bn[i] = m ? Cp[r * p.c_ts + e % N] : Bp[r * p.b_ts + e % N];
+    }
+    const int64_t k = (int64_t)slot * cps + t / K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dsum[i] = 0.f;
+      hn[i][0] = hn[i][1] = 0.f;
+      if (t > 0) {
+        dsum[i] = p.ckd[k * C + lc[i]];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) hn[i][j] = p.ck[(k * C + lc[i]) * N + n0 + j];
+      }
+    }
+  };
+  const int last = (len - 1) / K * K;
+  if (len > 0) fetch(last);
+  for (int t = last; len > 0 && t >= 0; t -= K) {
+    float xv[PP], dv[PP], sg[PP], gv[PP], zv[PP], yv[PP];
+    __syncthreads();  // (the chunk before has been written out)
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int r = prow + i * ROWS;
+      const bool here = on && t + r < len;
+      xv[i] = (float)xn[i];
+      const float raw = (float)dn[i] + bias;
+      dv[i] = p.softplus ? softplus_f(raw) : raw;
+      sg[i] = p.softplus ? sigmoid_f(raw) : 1.f;
+      yv[i] = gv[i] = (float)yn[i];
+      zv[i] = 0.f;
+      if constexpr (GATE) {
+        zv[i] = (float)zn[i];
+        gv[i] *= zv[i] * sigmoid_f(zv[i]);
+      }
+      // tokens past the end and channels past the group's: a decay of one, nothing in or out
+      s_d[r][pc] = here ? dv[i] : 0.f;
+      s_dx[r][pc] = here ? dv[i] * xv[i] : 0.f;
+      s_dy[r][pc] = here ? gv[i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < BCN; ++i) {
+      const int q = tid + i * 256, m = q / (K * N), e = q % (K * N);
+      if (m < 2) (m ? &s_c[0][0] : &s_b[0][0])[e] = (float)bn[i];
+    }
+    // the state in front of the chunk
+    float a[K][4][2], h[K + 1][4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) h[0][i][j] = fmaf(__builtin_amdgcn_exp2f(dsum[i] * A[i][j]), hs[i][j], hn[i][j]);
+    if (t > 0) fetch(t - K);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[k][l_ch]), dx = *reinterpret_cast<const f32x4*>(&s_dx[k][l_ch]);
+      const f32x2 b = *reinterpret_cast<const f32x2*>(&s_b[k][n0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          a[k][i][j] = __builtin_amdgcn_exp2f(d[i] * A[i][j]);
+          h[k + 1][i][j] = fmaf(a[k][i][j], h[k][i][j], dx[i] * b[j]);
+        }
+    }
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[k][l_ch]), dx = *reinterpret_cast<const f32x4*>(&s_dx[k][l_ch]);
+      const f32x4 gy = *reinterpret_cast<const f32x4*>(&s_dy[k][l_ch]);
+      const f32x2 b = *reinterpret_cast<const f32x2*>(&s_b[k][n0]), cc = *reinterpret_cast<const f32x2*>(&s_c[k][n0]);
+      float u[4], e[4], yo[4], vb[2] = {0.f, 0.f}, vc[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u[i] = e[i] = yo[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          vc[j] = fmaf(gy[i], h[k + 1][i][j], vc[j]);
+          if constexpr (GATE) yo[i] = fmaf(cc[j], h[k + 1][i][j], yo[i]);
+          const float G = fmaf(gy[i], cc[j], carry[i][j]);
+          vb[j] = fmaf(G, dx[i], vb[j]);
+          u[i] = fmaf(G, b[j], u[i]);
+          const float aG = a[k][i][j] * G;
+          const float w = aG * h[k][i][j];
+          e[i] = fmaf(w, A[i][j], e[i]);
+          dA[i][j] = fmaf(w, d[i], dA[i][j]);
+          carry[i][j] = aG;
+        }
+      }
+      // sums over states: the lower 32 lanes end with u, the upper with e; of four channels, even rows of 16 lanes have
+      // 0 and 1, odd rows 2 and 3; the last step is the same in both halves of a row, each of which writes one channel
+      {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pair32(u[i], e[i]);
+        const float r0 = dpp_add<0x128>(pair16(v[0], v[2])), r1 = dpp_add<0x128>(pair16(v[1], v[3]));
+        const int ch = l_ch + 2 * ((lane >> 4) & 1) + ((lane >> 3) & 1);
+        float* to = lane < 32 ? &s_u[sl][k][ch] : &s_e[sl][k][ch];
+        *to = lane & 8 ? r1 : r0;
+      }
+      if constexpr (GATE) {  // (one channel a row of 16 lanes: 0, 1, 2, 3)
+        const float v = dpp_add<0x128>(pair16(pair32(yo[0], yo[2]), pair32(yo[1], yo[3])));
+        if (!(lane & 8)) s_y[sl][k][l_ch + 2 * (lane >> 5) + ((lane >> 4) & 1)] = v;
+      }
+      // sums over channels
+      const float b0 = sum8(vb[0]), b1 = sum8(vb[1]), c0 = sum8(vc[0]), c1 = sum8(vc[1]);
+      if (cg == 0) *reinterpret_cast<f32x4*>(&s_bc[wave][k][ng * 4]) = f32x4{b0, b1, c0, c1};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int r = prow + i * ROWS;
+      if (t + r >= len || !on) continue;
+      float u = 0.f, e = 0.f, yo = 0.f;
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        u += s_u[s][r][pc];
+        e += s_e[s][r][pc];
+        if constexpr (GATE) yo += s_y[s][r][pc];
+      }
+      const float draw = fmaf(u, xv[i], e * LN2) * sg[i];
+      const int64_t at = (row0 + t + r) * C + c;
+      static_cast<InT*>(p.ddt)[at] = (InT)draw;
+      static_cast<InT*>(p.dx)[at] = (InT)fmaf(u, dv[i], D * gv[i]);
+      if constexpr (GATE) {
+        const float sz = sigmoid_f(zv[i]);
+        static_cast<InT*>(p.dz)[at] = (InT)(yv[i] * fmaf(D, xv[i], yo) * (sz * fmaf(zv[i], 1.f - sz, 1.f)));
+      }
+      accD = fmaf(gv[i], xv[i], accD);
+      accb += draw;
+    }
+    // this workgroup's part of dB and dC: value q of a token is state q / 2 of B (even) or C (odd)
+    for (int q = tid; q < 2 * K * N; q += 256) {
+      const int r = q / (2 * N), m = q / N & 1, n = q % N;
+      if (t + r >= len) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < Sh::CB; ++w) v += s_bc[w * SL + n / 16][r][(n % 16) / 2 * 4 + 2 * m + (n & 1)];
+      p.pBC[(((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0 + t + r) * p.G + g) * (2 * N) + m * N + n] = v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (in0 + l_ch + i >= p.Cg) continue;
+      const int64_t at = (int64_t)lc[i] * N + n0 + j;
+      p.pA[(int64_t)slot * C * N + at] = dA[i][j];
+      if (sp.first && p.dS0) p.dS0[(int64_t)sp.n * C * N + at] = carry[i][j];
+    }
+  // D and the bias: the token rows of a channel
+  __syncthreads();
+  float* red = &s_u[0][0][0];
+  red[tid] = accD;
+  red[256 + tid] = accb;
+  __syncthreads();
+  if (prow == 0 && on) {
+    float vD = 0.f, vb = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      vD += red[r * CH + pc];
+      vb += red[256 + r * CH + pc];
+    }
+    p.pD[(int64_t)slot * 2 * C + c] = vD;
+    p.pD[(int64_t)slot * 2 * C + C + c] = vb;
+  }
+}
+
+// dA [C, N], dD and ddt_bias from the slots' parts (blocks below nA: dA), 64 columns x 16 groups of slots a workgroup.
+template <int N>
+__global__ __launch_bounds__(1024) void scan_dparam_kernel(const ScanParams p, int nA) {
+  __shared__ float s[16][64];
+  const bool isA = (int)blockIdx.x < nA;
+  const int cols = isA ? p.C * N : 2 * p.C, col = ((int)blockIdx.x - (isA ? 0 : nA)) * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+  const float* part = isA ? p.pA : p.pD;
+  const int slots = p.cu ? p.slot_first[p.nseq] : p.slots;
+  float v = 0.f;
+  if (col < cols)
+    for (int r = g; r < slots; r += 16) v += part[(int64_t)r * cols + col];
+  s[g][threadIdx.x & 63] = v;
+  __syncthreads();
+  if (g == 0 && col < cols) {
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) a += s[k][threadIdx.x];
+    if (isA)
+      p.dA[col] = a;
+    else if (col < p.C && p.dD)
+      p.dD[col] = a;
+    else if (col >= p.C && p.dbias)
+      p.dbias[col - p.C] = a;
+  }
+}
+
+// dB and dC from the channel blocks' parts, a value a thread.
+template <int N, typename InT>
+__global__ __launch_bounds__(256) void scan_dbc_kernel(const ScanParams p) {
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, per = (int64_t)p.nbatch * p.T * p.G * (2 * N);
+  if (q >= per) return;
+  const int64_t row = q / (2 * N), tok = row / p.G;
+  if (p.cu && (tok < p.cu[0] || tok >= p.cu[p.nseq])) return;  // no sequence holds it
+  const int m = (int)(q / N & 1), n = (int)(q % N);
+  float v = 0.f;
+  for (int k = 0; k < p.cblocks; ++k) v += p.pBC[k * per + q];
+  static_cast<InT*>(m ? p.dC : p.dB)[row * N + n] = (InT)v;
+}
+
+template <int NS, int NW, typename InT>
+static void launch_states(const ScanParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.slots * p.G * p.tiles)), block(64 * NW);
+  if (p.part)
+    hipLaunchKernelGGL((scan_states_kernel<NS, NW, InT, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((scan_states_kernel<NS, NW, InT, false>), grid, block, 0, s, p);
+}
+template <int N, typename InT>
+static hipError_t launch_bwd_t(const ScanParams& p, hipStream_t s) {
+  if (p.slots > 0 && p.nseq > 0) {
+    launch_states<16, N / 16, InT>(p, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (p.part) {
+      hipLaunchKernelGGL((scan_join2_kernel<N>), dim3((unsigned)((int64_t)p.nseq * ((p.C * (N / 4) + 255) / 256)), 2), dim3(256), 0, s, p);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    const dim3 grid((unsigned)((int64_t)p.slots * p.G * p.cblocks));
+    if (p.z)
+      hipLaunchKernelGGL((scan_grad_kernel<N, InT, true>), grid, dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((scan_grad_kernel<N, InT, false>), grid, dim3(256), 0, s, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int nA = (int)(((int64_t)p.C * N + 63) / 64);
+  hipLaunchKernelGGL((scan_dparam_kernel<N>), dim3(nA + (2 * p.C + 63) / 64), dim3(1024), 0, s, p, nA);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t vals = (int64_t)p.nbatch * p.T * p.G * (2 * N);
+  if (vals > 0 && p.nseq > 0)
+    hipLaunchKernelGGL((scan_dbc_kernel<N, InT>), dim3((unsigned)((vals + 255) / 256)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+template <typename InT>
+static hipError_t launch_bwd_n(const ScanParams& p, int n, hipStream_t s) {
+  return n == 16 ? launch_bwd_t<16, InT>(p, s) : n == 32 ? launch_bwd_t<32, InT>(p, s) : launch_bwd_t<64, InT>(p, s);
+}
+hipError_t launch_scan_bwd(ScanParams p, int n, bool bf16, hipStream_t s) {
+  if (p.cu) {
+    const hipError_t e = launch_scan_plan(p, s);
+    if (e != hipSuccess) return e;
+    p.cu = p.cu_ok;
+  }
+  return bf16 ? launch_bwd_n<__bf16>(p, n, s) : launch_bwd_n<float>(p, n, s);
+}
+
+}  // namespace dr

@@ -4,8 +4,8 @@
 // thread 4 x 16 bytes of it, all loads issued before the first use. A row of d_v values lies in d_v / 4
 // neighbouring lanes of one wave, so its largest magnitude is a butterfly over those lanes. 256 states of 32
 // heads, d = 128, written in int8 and read back: 255 us, 5300 GB/s (a large copy on the card: 5175).
-#include "common.hpp"
 #include "state_cache.hpp"
+#include "state_code.hpp"
 
 namespace dr {
 
@@ -13,19 +13,6 @@ namespace dr {
 __device__ __forceinline__ int64_t cache_row(const int32_t* idx, int64_t rows, int64_t n) {
   const int64_t r = idx ? (int64_t)idx[n] : n;
   return r >= 0 && r < rows ? r : -1;
-}
-
-// The integer nearest to the exact quotient x / s (ties to even), |x / s| < 128: a candidate from the
-// hardware reciprocal, at most one off next to a tie, set right by its remainder, which an fma gives exactly
-// (x and q s are multiples of the smaller one's last place and differ by less than 2 s). Twice the remainder is
-// compared with s: half of s is no float32 number when s lies below 2^-125.
-__device__ __forceinline__ int code_int8(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x), r2 = r + r;
-  const bool odd = ((int)q & 1) != 0;
-  if (r2 > s || (r2 == s && odd)) q += 1.f;
-  if (r2 < -s || (r2 == -s && odd)) q -= 1.f;
-  return (int)q;
 }
 
 template <int DV, bool E4M3>
@@ -62,31 +49,8 @@ __global__ __launch_bounds__(256) void state_pack_kernel(const CacheParams p) {
 #pragma unroll
     for (int d = 1; d < LPR; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
     const bool bad = top >= 0x7f800000u;
-    const float amax = __builtin_bit_cast(float, top);
-    float scale;
-    uint32_t code = 0;
-    if constexpr (E4M3) {
-      // amax = m 2^(E - 126), m in [1/2, 1): amax <= 448 2^j (448 = 7/8 2^9) for j = E - 135, or one more if
-      // m > 7/8; a subnormal amax (E = 0) takes the least scale
-      const int E = (int)(top >> 23);
-      int j = E - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-      j = max(j, -126);
-      scale = __builtin_bit_cast(float, (uint32_t)(j + 127) << 23);
-      const float inv = __builtin_bit_cast(float, (uint32_t)(127 - j) << 23);  // exact
-      if (!bad) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[i][0] * inv, x[i][1] * inv, 0, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(x[i][2] * inv, x[i][3] * inv, w, true);
-        code = (uint32_t)w;
-      }
-    } else {
-      // amax times the fp32 number next to 1/127 (within 1.5 roundings of amax / 127): the value that torch's division
-      // of a tensor by 127 gives on the GPU, so that caches written by such a program hold the same codes
-      scale = fmaxf(amax * (1.f / 127.f), 0x1p-126f);
-      const float inv = __builtin_amdgcn_rcpf(scale);
-      if (!bad)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code |= (uint32_t)(code_int8(x[i][j], scale, inv) & 0xff) << (8 * j);
-    }
+    float inv, scale = row_scale<E4M3>(top, &inv);
+    const uint32_t code = bad ? 0u : codes4<E4M3>(x[i][0], x[i][1], x[i][2], x[i][3], scale, inv);
     if (bad) scale = __builtin_nanf("");
     if (e < hsz4) {
       __builtin_nontemporal_store(code, out + e);
