@@ -6,30 +6,11 @@
 // more states than NS the waves of a workgroup share a channel tile and add their parts of y through LDS.
 // Sequences that are too few to fill the GPU are cut into segments: their own states from zero first (one more pass without
 // C and y), then each segment's start by a walk over the segments, whose decay is exp(A sum d).
+#include <type_traits>
+
 #include "scan.hpp"
 
 namespace dr {
-
-// ---------------------------------------------------------------------------
-// Scalar loads of NS elements of a token's B or C (uniform addresses, 4-byte aligned, nothing writes them meanwhile).
-// ---------------------------------------------------------------------------
-typedef const __attribute__((address_space(4))) uint32_t* const_u32;
-template <typename InT, int NS>
-struct Row {
-  static constexpr int NW = NS * (int)sizeof(InT) / 4;
-  uint32_t w[NW];
-  __device__ __forceinline__ void load(const InT* at) {
-    const const_u32 q = (const_u32)(uintptr_t)at;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = q[i];
-  }
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (sizeof(InT) == 4)
-      return __builtin_bit_cast(float, w[i]);
-    else
-      return __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-  }
-};
 
 // The main pass (LOCAL false: outputs and final states) or the segments' own states and sums of d.
 template <int NS, int NW, typename InT, bool LOCAL>
@@ -42,8 +23,8 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(const ScanParams p) {
   const SlotSpan sp = slot_span(p, slot);
   if (sp.n < 0 || (LOCAL && sp.last)) return;
   const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + lane;
-  const bool on = in_g < p.Cg;
-  const int c = g * p.Cg + min(in_g, p.Cg - 1);
+  if (in_g >= p.Cg) return;  // (the same lanes of every wave, and never all of a wave's: the barriers below still meet)
+  const int c = g * p.Cg + in_g;
   float A[NS], h[NS];
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
@@ -68,52 +49,95 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(const ScanParams p) {
       }
   }
   const int len = sp.len;
-  const InT* x = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
-  const InT* dt = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
-  const InT* z = !LOCAL && p.z ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : nullptr;
+  const bool soft = p.softplus != 0, gate = !LOCAL && p.z != nullptr;
+  const InT* xp = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
+  const InT* dp = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
+  const InT* zp = gate ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : xp;
   const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N + wave * NS;
   const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N + wave * NS;
   InT* y = LOCAL ? nullptr : static_cast<InT*>(p.y) + (sp.b * p.T + sp.t0) * (int64_t)p.C + c;
+  const int64_t x_ts = p.x_ts, dt_ts = p.dt_ts, z_ts = gate ? p.z_ts : p.x_ts, b_ts = p.b_ts, c_ts = p.c_ts, C = p.C;
   float sumd = 0.f;
+  // A tile's inputs come a tile ahead, a token's rows of B and C a token ahead; nothing past the last token is read.
   InT xn[TT], dn[TT], zn[TT];
-  auto fetch = [&](int t) {
+  auto fetch = [&](int n) {  // the next n tokens (TT of them but at the end)
+    if (n >= TT) {
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const int64_t r = min(t + i, len - 1);
-      xn[i] = x[r * p.x_ts];
-      dn[i] = dt[r * p.dt_ts];
-      zn[i] = z ? z[r * p.z_ts] : InT(0);
+      for (int i = 0; i < TT; ++i) {
+        xn[i] = *xp;
+        dn[i] = *dp;
+        xp += x_ts;
+        dp += dt_ts;
+        if constexpr (!LOCAL) {
+          zn[i] = *zp;
+          zp += z_ts;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        xn[i] = dn[i] = zn[i] = InT(0);
+        if (i < n) {
+          xn[i] = *xp;
+          dn[i] = *dp;
+          xp += x_ts;
+          dp += dt_ts;
+          if constexpr (!LOCAL) {
+            zn[i] = *zp;
+            zp += z_ts;
+          }
+        }
+      }
     }
   };
-  if (len > 0) fetch(0);
+  Row<InT, NS> Bt[2], Ct[2];
+  auto rows = [&](int to, bool more) {
+    Bt[to].load(Bp);
+    Bp += more ? b_ts : 0;
+    if constexpr (!LOCAL) {
+      Ct[to].load(Cp);
+      Cp += more ? c_ts : 0;
+    }
+  };
+  if (len > 0) {
+    fetch(len);
+    rows(0, len > 1);
+  }
   int buf = 0;
-  for (int t = 0; t < len; t += TT, buf ^= 1) {
+  auto run = [&](int t, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
     float xv[TT], dv[TT], zv[TT], yv[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       xv[i] = (float)xn[i];
-      const float raw = (float)dn[i] + bias;
-      dv[i] = p.softplus ? softplus_f(raw) : raw;
-      zv[i] = (float)zn[i];
+      const float raw = (float)dn[i] + bias, sf = softplus_f(raw);
+      dv[i] = soft ? sf : raw;
+      // (tokens past the end: a decay of one and nothing added)
+      if (!WHOLE && t + i >= len) dv[i] = 0.f;
+      if constexpr (!LOCAL) {
+        zv[i] = (float)zn[i];
+        const float sg = zv[i] * sigmoid_f(zv[i]);
+        zv[i] = gate ? sg : 1.f;
+      }
     }
-    if (t + TT < len) fetch(t + TT);
+    if (WHOLE && t + TT < len) fetch(len - t - TT);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      yv[i] = 0.f;
-      if (t + i < len) {
-        Row<InT, NS> Bt, Ct;
-        Bt.load(Bp + (t + i) * p.b_ts);
-        if constexpr (!LOCAL) Ct.load(Cp + (t + i) * p.c_ts);
-        const float d = dv[i], dx = d * xv[i];
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      rows((i + 1) & 1, t + i + 2 < len);
+      __builtin_amdgcn_sched_barrier(0);
+      const float d = dv[i], dx = d * xv[i];
+      float a[NS], acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          h[j] = fmaf(__builtin_amdgcn_exp2f(d * A[j]), h[j], dx * Bt[j]);
-          if constexpr (!LOCAL) acc[j & 3] = fmaf(Ct[j], h[j], acc[j & 3]);
-        }
-        yv[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        if constexpr (LOCAL) sumd += d;
+      for (int j = 0; j < NS; ++j) a[j] = __builtin_amdgcn_exp2f(d * A[j]);
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        h[j] = fmaf(a[j], h[j], dx * Bt[i & 1][j]);
+        if constexpr (!LOCAL) acc[j & 3] = fmaf(Ct[i & 1][j], h[j], acc[j & 3]);
       }
+      yv[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      if constexpr (LOCAL) sumd += d;
+      if constexpr (!LOCAL) asm volatile("" : "+v"(yv[i]));  // (here, not where it is stored: C's rows are held no longer)
+      __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!LOCAL) {
       if constexpr (NW > 1) {
@@ -123,27 +147,28 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(const ScanParams p) {
       }
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
-        if (t + i >= len || (NW > 1 && i % NW != wave)) continue;  // (uniform over the wave)
-        float v = yv[i];
-        if constexpr (NW > 1) {
-          v = 0.f;
+        if ((WHOLE || t + i < len) && (NW == 1 || i % NW == wave)) {  // (uniform over the wave)
+          float v = yv[i];
+          if constexpr (NW > 1) {
+            v = 0.f;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) v += s_y[buf][w][i][lane];
+            for (int w = 0; w < NW; ++w) v += s_y[buf][w][i][lane];
+          }
+          *y = (InT)(fmaf(D, xv[i], v) * zv[i]);
         }
-        v = fmaf(D, xv[i], v);
-        if (z) v *= zv[i] * sigmoid_f(zv[i]);
-        if (on) y[(int64_t)(t + i) * p.C] = (InT)v;
+        y += C;
       }
     }
-  }
+  };
+  int t = 0;
+  for (; t + TT <= len; t += TT, buf ^= 1) run(t, std::true_type{});
+  if (t < len) run(t, std::false_type{});
   if constexpr (LOCAL) {
-    if (on) {
-      float* to = p.part + ((int64_t)slot * p.C + c) * N + wave * NS;
+    float* to = p.part + ((int64_t)slot * p.C + c) * N + wave * NS;
 #pragma unroll
-      for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
-      if (wave == 0) p.sumd[(int64_t)slot * p.C + c] = sumd;
-    }
-  } else if (sp.last && p.S && on) {
+    for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
+    if (wave == 0) p.sumd[(int64_t)slot * p.C + c] = sumd;
+  } else if (sp.last && p.S) {
     const int64_t r = state_row(p.sidx, p.nslots, sp.n);
     if (r >= 0) {
       float* to = p.S + (r * p.C + c) * N + wave * NS;

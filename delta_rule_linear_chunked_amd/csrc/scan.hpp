@@ -83,6 +83,25 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int nseq, int t) {
   return lo;
 }
 
+// Scalar loads of NS elements of a token's B or C (uniform addresses, 4-byte aligned, nothing writes them meanwhile).
+typedef const __attribute__((address_space(4))) uint32_t* const_u32;
+template <typename InT, int NS>
+struct Row {
+  static constexpr int NW = NS * (int)sizeof(InT) / 4;
+  uint32_t w[NW];
+  __device__ __forceinline__ void load(const InT* at) {
+    const const_u32 q = (const_u32)(uintptr_t)at;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = q[i];
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(InT) == 4)
+      return __builtin_bit_cast(float, w[i]);
+    else
+      return __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Convolution
 // ---------------------------------------------------------------------------

@@ -176,23 +176,25 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
   return DR_OK;
 }
 
-// Segments. A wave walks a segment of 64 channels x 16 states; the GPU runs about 1024 of them at full speed. A sequence
-// that is cut costs the segments' own states, 0.85 of the main pass (backward: the reverse part of the first
-// pass), two launches and a walk over the segments: in units of a token's time
-//   (rounds of 1024 waves) x (tokens of a segment) x (1 or 1.85) + (0 or 35 + 2 x segments)
+// Segments. A wave walks a segment of 64 channels x 16 states. Alone on its SIMD it takes 0.46 us a token (every instruction
+// waits for the one before), two take 0.58 together and four 1.0: k waves max(1, 0.25 + 0.5 k) times the time of one. A sequence that is cut
+// costs the segments' own states, 0.75 of the main pass (backward: the reverse part of the first pass), two launches
+// and a walk over the segments: in units of a token's time
+//   max(1, 0.25 + 0.5 waves / 1024) x (tokens of a segment) x (1 or 1.75) + (0 or 20 + segments)
+// 4 x 4096 tokens, 2048 channels, 16 states, bf16: 128 tokens 256 us, 256 285, 512 429, 1024 837, whole 1873.
 dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
   dr::ScanPlan pl{};
   const int64_t T = d->seqlen, tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE);
   const int64_t waves = tiles * (d->state_dim / 16);
-  const double again = backward ? 1.15 : 1.85;
+  const double again = backward ? 1.15 : 1.75;
   double best = 0;
   int64_t seg = ceil_div(T, 8) * 8;
   for (int64_t n = 1; n == 1 || (n * 16 < T + 16 && n <= 4096); n += 1 + n / 8) {
     const int64_t s = ceil_div(ceil_div(T, n), 8) * 8, nseg = s > 0 ? ceil_div(T, s) : 1;
     const double wgs = (packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg) * waves;
-    double rounds = wgs / 1024;
-    if (rounds < 1) rounds = 1;
-    const double cost = rounds * s * (nseg > 1 ? again : 1.0) + (nseg > 1 ? 35 + 2.0 * nseg : 0.0);
+    double load = 0.25 + 0.5 * wgs / 1024;
+    if (load < 1) load = 1;
+    const double cost = load * s * (nseg > 1 ? again : 1.0) + (nseg > 1 ? 20.0 + nseg : 0.0);
     if (best == 0 || cost < best) {
       best = cost;
       seg = s;

@@ -14,27 +14,18 @@
 
 namespace dr {
 
-typedef const __attribute__((address_space(4))) uint32_t* const_u32;
-template <typename InT>
-__device__ __forceinline__ float row_elem(const uint32_t* w, int i) {
-  if constexpr (sizeof(InT) == 4)
-    return __builtin_bit_cast(float, w[i]);
-  else
-    return __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-}
-
 // Local states at every 8th token and behind the segment, the sums of d there, and (BOTH) the reverse part.
 template <int NS, int NW, typename InT, bool BOTH>
 __global__ __launch_bounds__(64 * NW) void scan_states_kernel(const ScanParams p) {
-  constexpr int N = NS * NW, TT = SCAN_CHUNK, RW = NS * (int)sizeof(InT) / 4;
+  constexpr int N = NS * NW, TT = SCAN_CHUNK;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ntiles = p.G * p.tiles;
   const int slot = blockIdx.x / ntiles, tile = blockIdx.x - slot * ntiles;
   const SlotSpan sp = slot_span(p, slot);
   if (sp.n < 0) return;
   const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + lane;
-  const bool on = in_g < p.Cg;
-  const int c = g * p.Cg + min(in_g, p.Cg - 1);
+  if (in_g >= p.Cg) return;
+  const int c = g * p.Cg + in_g;
   float A[NS], h[NS], P[NS], R[NS];
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
@@ -44,77 +35,91 @@ __global__ __launch_bounds__(64 * NW) void scan_states_kernel(const ScanParams p
   }
   const float bias = p.bias ? p.bias[c] : 0.f;
   const int len = sp.len;
-  const InT* x = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
-  const InT* dt = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
-  const InT* z = BOTH && p.z ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : nullptr;
-  const InT* dy = BOTH ? static_cast<const InT*>(p.dy) + (sp.b * p.T + sp.t0) * (int64_t)p.C + c : nullptr;
+  const bool soft = p.softplus != 0, gate = BOTH && p.z != nullptr;
+  const InT* xp = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
+  const InT* dp = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
+  const InT* zp = gate ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : xp;
+  const InT* yp = static_cast<const InT*>(p.dy) + (sp.b * p.T + sp.t0) * (int64_t)p.C + c;
   const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N + wave * NS;
   const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N + wave * NS;
-  const int cps = p.seg / TT;
+  const int64_t x_ts = p.x_ts, dt_ts = p.dt_ts, z_ts = gate ? p.z_ts : p.x_ts, b_ts = p.b_ts, c_ts = p.c_ts, C = p.C;
+  float* ck = p.ck + ((int64_t)slot * (p.seg / TT) * C + c) * N + wave * NS;
+  float* ckd = p.ckd + (int64_t)slot * (p.seg / TT) * C + c;
   float sumd = 0.f;
   InT xn[TT], dn[TT], zn[TT], yn[TT];
-  auto fetch = [&](int t) {
+  auto fetch = [&](int n) {  // the next n tokens (TT of them but at the end)
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      const int64_t r = min(t + i, len - 1);
-      xn[i] = x[r * p.x_ts];
-      dn[i] = dt[r * p.dt_ts];
-      if constexpr (BOTH) {
-        zn[i] = z ? z[r * p.z_ts] : InT(0);
-        yn[i] = dy[r * p.C];
+      xn[i] = dn[i] = zn[i] = yn[i] = InT(0);
+      if (n >= TT || i < n) {
+        xn[i] = *xp;
+        dn[i] = *dp;
+        xp += x_ts;
+        dp += dt_ts;
+        if constexpr (BOTH) {
+          zn[i] = *zp;
+          yn[i] = *yp;
+          zp += z_ts;
+          yp += C;
+        }
       }
     }
   };
-  if (len > 0) fetch(0);
-  for (int t = 0; t < len; t += TT) {
-    if (on) {
-      const int64_t k = (int64_t)slot * cps + t / TT;
-      if (t > 0) {  // (a segment begins at zero)
-        float* to = p.ck + (k * p.C + c) * N + wave * NS;
-#pragma unroll
-        for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
-      }
-      if (wave == 0) p.ckd[k * p.C + c] = sumd;
+  Row<InT, NS> Bt[2], Ct[2];
+  auto rows = [&](int to, bool more) {
+    Bt[to].load(Bp);
+    Bp += more ? b_ts : 0;
+    if constexpr (BOTH) {
+      Ct[to].load(Cp);
+      Cp += more ? c_ts : 0;
     }
+  };
+  if (len > 0) {
+    fetch(len);
+    rows(0, len > 1);
+  }
+  for (int t = 0; t < len; t += TT) {
+    if (t > 0) {  // (a segment begins at zero)
+#pragma unroll
+      for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(ck + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
+    }
+    if (wave == 0) *ckd = sumd;
+    ck += C * N;
+    ckd += C;
     float xv[TT], dv[TT], gv[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       xv[i] = (float)xn[i];
-      const float raw = (float)dn[i] + bias;
-      dv[i] = p.softplus ? softplus_f(raw) : raw;
+      const float raw = (float)dn[i] + bias, sf = softplus_f(raw);
+      dv[i] = soft ? sf : raw;
+      if (t + i >= len) dv[i] = 0.f;  // (past the end: a decay of one and nothing added; dy is zero there)
       if constexpr (BOTH) {
-        const float zv = (float)zn[i];
-        gv[i] = (float)yn[i];
-        if (z) gv[i] *= zv * sigmoid_f(zv);
+        const float zv = (float)zn[i], sg = zv * sigmoid_f(zv);
+        gv[i] = (float)yn[i] * (gate ? sg : 1.f);
       }
     }
-    if (t + TT < len) fetch(t + TT);
+    if (t + TT < len) fetch(len - t - TT);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      if (t + i < len) {
-        uint32_t Bt[RW], Ct[RW];
-        const const_u32 bq = (const_u32)(uintptr_t)(Bp + (t + i) * p.b_ts), cq = (const_u32)(uintptr_t)(Cp + (t + i) * p.c_ts);
+      rows((i + 1) & 1, t + i + 2 < len);
+      __builtin_amdgcn_sched_barrier(0);
+      const float d = dv[i], dx = d * xv[i];
+      float a[NS];
 #pragma unroll
-        for (int j = 0; j < RW; ++j) {
-          Bt[j] = bq[j];
-          if constexpr (BOTH) Ct[j] = cq[j];
-        }
-        const float d = dv[i], dx = d * xv[i];
+      for (int j = 0; j < NS; ++j) a[j] = __builtin_amdgcn_exp2f(d * A[j]);
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          const float a = __builtin_amdgcn_exp2f(d * A[j]);
-          h[j] = fmaf(a, h[j], dx * row_elem<InT>(Bt, j));
-          if constexpr (BOTH) {
-            P[j] *= a;
-            R[j] = fmaf(P[j], gv[i] * row_elem<InT>(Ct, j), R[j]);
-          }
+      for (int j = 0; j < NS; ++j) {
+        h[j] = fmaf(a[j], h[j], dx * Bt[i & 1][j]);
+        if constexpr (BOTH) {
+          P[j] *= a[j];
+          R[j] = fmaf(P[j], gv[i] * Ct[i & 1][j], R[j]);
         }
-        sumd += d;
       }
+      sumd += d;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if constexpr (BOTH) {
-    if (!on) return;
     const int64_t at = ((int64_t)slot * p.C + c) * N + wave * NS;
 #pragma unroll
     for (int j = 0; j < NS; j += 4) {
@@ -186,6 +191,8 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   __shared__ __align__(16) float s_b[K][N], s_c[K][N];
   __shared__ float s_u[SL][K][CH], s_e[SL][K][CH], s_y[GATE ? SL : 1][GATE ? K : 1][GATE ? CH : 1];
   __shared__ __align__(16) float s_bc[4][K][32];
+  // what a thread needs of its pairs again at the end of a chunk, and its starting state, wait here instead of in registers
+  __shared__ __align__(16) float s_own[GATE ? 4 : 2][PP][256], s_hs[2][256][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int sl = wave % SL, cb = wave / SL;
   const int per = p.G * p.cblocks;
@@ -200,7 +207,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   int lc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) lc[i] = g * p.Cg + min(in0 + l_ch + i, p.Cg - 1);
-  float A[4][2], hs[4][2], carry[4][2], dA[4][2];
+  float A[4][2], carry[4][2], dA[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -209,7 +216,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       A[i][j] = p.A[at] * LOG2E;
       dA[i][j] = 0.f;
       const float* from = p.part ? p.part + (int64_t)slot * C * N : p.S0 ? p.S0 + (int64_t)sp.n * C * N : nullptr;
-      hs[i][j] = from ? from[at] : 0.f;
+      s_hs[j][tid][i] = from ? from[at] : 0.f;
       const float* back = p.part ? p.rpart + (int64_t)slot * C * N : p.dST ? p.dST + (int64_t)sp.n * C * N : nullptr;
       carry[i][j] = back ? back[at] : 0.f;
     }
@@ -225,6 +232,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   const InT* dy = static_cast<const InT*>(p.dy) + row0 * C + c;
   const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N;
   const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N;
+  const bool soft = p.softplus != 0;
   float accD = 0.f, accb = 0.f;
   InT xn[PP], dn[PP], zn[PP], yn[PP];
   float hn[4][2], dsum[4];
@@ -254,33 +262,33 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       if (t > 0) {
         dsum[i] = p.ckd[k * C + lc[i]];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) hn[i][j] = p.ck[(k * C + lc[i]) * N + n0 + j];
+        for (int j = 0; j < 2; ++j) hn[i][j] = p.ck[(k * C + lc[i]) * N + n0 + j];  // (8 bytes)
       }
     }
   };
   const int last = (len - 1) / K * K;
   if (len > 0) fetch(last);
   for (int t = last; len > 0 && t >= 0; t -= K) {
-    float xv[PP], dv[PP], sg[PP], gv[PP], zv[PP], yv[PP];
     __syncthreads();  // (the chunk before has been written out)
 #pragma unroll
     for (int i = 0; i < PP; ++i) {
       const int r = prow + i * ROWS;
       const bool here = on && t + r < len;
-      xv[i] = (float)xn[i];
-      const float raw = (float)dn[i] + bias;
-      dv[i] = p.softplus ? softplus_f(raw) : raw;
-      sg[i] = p.softplus ? sigmoid_f(raw) : 1.f;
-      yv[i] = gv[i] = (float)yn[i];
-      zv[i] = 0.f;
+      const float xv = (float)xn[i], raw = (float)dn[i] + bias, sf = softplus_f(raw), sr = sigmoid_f(raw);
+      const float dv = soft ? sf : raw;
+      float gv = (float)yn[i];
+      s_own[0][i][tid] = xv;
+      s_own[1][i][tid] = soft ? sr : 1.f;
       if constexpr (GATE) {
-        zv[i] = (float)zn[i];
-        gv[i] *= zv[i] * sigmoid_f(zv[i]);
+        const float zv = (float)zn[i];
+        s_own[2][i][tid] = zv;
+        s_own[3][i][tid] = gv;
+        gv *= zv * sigmoid_f(zv);
       }
       // tokens past the end and channels past the group's: a decay of one, nothing in or out
-      s_d[r][pc] = here ? dv[i] : 0.f;
-      s_dx[r][pc] = here ? dv[i] * xv[i] : 0.f;
-      s_dy[r][pc] = here ? gv[i] : 0.f;
+      s_d[r][pc] = here ? dv : 0.f;
+      s_dx[r][pc] = here ? dv * xv : 0.f;
+      s_dy[r][pc] = here ? gv : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < BCN; ++i) {
@@ -290,13 +298,15 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
     // the state in front of the chunk
     float a[K][4][2], h[K + 1][4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 2; ++j) {
+      const f32x4 hs = *reinterpret_cast<const f32x4*>(&s_hs[j][tid][0]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) h[0][i][j] = fmaf(__builtin_amdgcn_exp2f(dsum[i] * A[i][j]), hs[i][j], hn[i][j]);
-    if (t > 0) fetch(t - K);
+      for (int i = 0; i < 4; ++i) h[0][i][j] = fmaf(__builtin_amdgcn_exp2f(dsum[i] * A[i][j]), hs[i], hn[i][j]);
+    }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if (k % 2 == 0) __builtin_amdgcn_sched_barrier(0);
       const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[k][l_ch]), dx = *reinterpret_cast<const f32x4*>(&s_dx[k][l_ch]);
       const f32x2 b = *reinterpret_cast<const f32x2*>(&s_b[k][n0]);
 #pragma unroll
@@ -309,6 +319,9 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
     }
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
+      // the next chunk's loads start where half of this one's states and decays are no longer held
+      if (k == K / 2 - 1 && t > 0) fetch(t - K);
+      __builtin_amdgcn_sched_barrier(0);
       const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[k][l_ch]), dx = *reinterpret_cast<const f32x4*>(&s_dx[k][l_ch]);
       const f32x4 gy = *reinterpret_cast<const f32x4*>(&s_dy[k][l_ch]);
       const f32x2 b = *reinterpret_cast<const f32x2*>(&s_b[k][n0]), cc = *reinterpret_cast<const f32x2*>(&s_c[k][n0]);
@@ -361,15 +374,16 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
         e += s_e[s][r][pc];
         if constexpr (GATE) yo += s_y[s][r][pc];
       }
-      const float draw = fmaf(u, xv[i], e * LN2) * sg[i];
+      const float xv = s_own[0][i][tid], gv = s_dy[r][pc];
+      const float draw = fmaf(u, xv, e * LN2) * s_own[1][i][tid];
       const int64_t at = (row0 + t + r) * C + c;
       static_cast<InT*>(p.ddt)[at] = (InT)draw;
-      static_cast<InT*>(p.dx)[at] = (InT)fmaf(u, dv[i], D * gv[i]);
+      static_cast<InT*>(p.dx)[at] = (InT)fmaf(u, s_d[r][pc], D * gv);
       if constexpr (GATE) {
-        const float sz = sigmoid_f(zv[i]);
-        static_cast<InT*>(p.dz)[at] = (InT)(yv[i] * fmaf(D, xv[i], yo) * (sz * fmaf(zv[i], 1.f - sz, 1.f)));
+        const float zv = s_own[2][i][tid], sz = sigmoid_f(zv);
+        static_cast<InT*>(p.dz)[at] = (InT)(s_own[3][i][tid] * fmaf(D, xv, yo) * (sz * fmaf(zv, 1.f - sz, 1.f)));
       }
-      accD = fmaf(gv[i], xv[i], accD);
+      accD = fmaf(gv, xv, accD);
       accb += draw;
     }
     // this workgroup's part of dB and dC: value q of a token is state q / 2 of B (even) or C (odd)
