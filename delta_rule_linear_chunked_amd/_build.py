@@ -22,7 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "plan.cpp", "scratch.hip", "decode.hip", "prefill.hip", "prefill_state.hip", "backward.hip",
            "backward_chunked.hip", "decay_api.cpp", "decay.hip", "decay_bwd.hip", "decay_step.hip", "state_cache.hip",
-           "scan_api.cpp", "scan.hip", "scan_bwd.hip", "scan_step.hip", "conv.hip", "norm.hip"]
+           "scan_api.cpp", "scan.hip", "scan_block.hip", "scan_bwd.hip", "scan_step.hip", "conv.hip", "norm.hip"]
 
 # Packed-fp32 instructions are disabled for every device compile; hipcc's host
 # pass does not know the feature and says so, which is harmless.

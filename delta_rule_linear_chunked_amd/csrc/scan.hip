@@ -253,6 +253,7 @@ hipError_t launch_scan_fwd(ScanParams p, const ScanPlan& pl, int n, bool bf16, h
   } else {
     p.part = nullptr;
   }
+  if (pl.block) return launch_scan_block(p, n, bf16, s);
   return bf16 ? launch_any<__bf16>(p, n, false, s) : launch_any<float>(p, n, false, s);
 }
 

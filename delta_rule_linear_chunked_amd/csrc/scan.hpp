@@ -190,7 +190,7 @@ struct ScanParams {
   int64_t T;
   int64_t x_ts, x_bs, dt_ts, dt_bs, b_ts, b_bs, c_ts, c_bs, z_ts, z_bs;
   int32_t C, G, Cg;        // channels, groups, channels of a group
-  int32_t tiles;           // channel tiles of a group
+  int32_t tiles, btiles;   // channel tiles of a group: of 64, of 32
   int32_t nseq, nbatch;
   int32_t softplus;
   int32_t seg;             // tokens of a segment
@@ -224,7 +224,7 @@ struct ScanParams {
   int32_t cblocks;         // channel blocks of a group in the gradient pass
 };
 struct ScanPlan {
-  int ns;          // states of a lane in the main pass
+  bool block;  // the main pass with a workgroup's waves along the tokens
   int64_t seg, nseg, slots;
 };
 // What a slot is: sequence n (-1: none) in batch row b, tokens t0 .. t0 + len, the first / last of its sequence.
@@ -254,6 +254,8 @@ __device__ __forceinline__ SlotSpan slot_span(const ScanParams& p, int slot) {
   return s;
 }
 constexpr int SCAN_TILE = 64;  // channels of a wave
+constexpr int SCAN_BLOCK_WAVES = 8, SCAN_BLOCK_CH = 32;  // waves and channels of a workgroup of scan_block.hip
+hipError_t launch_scan_block(const ScanParams& p, int n, bool bf16, hipStream_t s);
 constexpr int scan_step_channels(int n) { return 1024 / n; }  // channels of a workgroup of the step (4 states a lane)
 hipError_t launch_scan_plan(const ScanParams& p, hipStream_t s);
 hipError_t launch_scan_fwd(ScanParams p, const ScanPlan& pl, int n, bool bf16, hipStream_t s);

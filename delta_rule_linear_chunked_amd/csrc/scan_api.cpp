@@ -15,7 +15,7 @@ using dr::host_fail;
 namespace {
 
 const char* const kTooLarge = "problem too large: more than 2^31 - 1 workgroups or 2^32 - 1 work items per kernel";
-constexpr int64_t kTokens = ((int64_t)1 << 31) - 1024, kStride = (int64_t)1 << 40;
+constexpr int64_t kTokens = ((int64_t)1 << 31) - 1024, kStride = (int64_t)1 << 40, kTokenStride = (int64_t)1 << 24;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
@@ -62,10 +62,10 @@ int check_tokens(int64_t batch, int64_t seqlen, int64_t channels, int64_t seqs, 
   }
   return DR_OK;
 }
-int check_stride(int64_t s, int64_t unit, const char* name) {
+int check_stride(int64_t s, int64_t unit, const char* name, int64_t most = kStride) {
   if (s < 0) return host_fail(DR_ERR_SHAPE, "%s stride %lld is negative", name, (long long)s);
-  if (s > kStride || s % unit != 0)
-    return host_fail(DR_ERR_LAYOUT, "%s stride %lld is not a multiple of %lld elements (or is beyond 2^40)", name, (long long)s, (long long)unit);
+  if (s > most || s % unit != 0)
+    return host_fail(DR_ERR_LAYOUT, "%s stride %lld is not a multiple of %lld elements (or is beyond %lld)", name, (long long)s, (long long)unit, (long long)most);
   return DR_OK;
 }
 int check_opts(const dr_opts* o) {
@@ -108,7 +108,7 @@ int check_conv(const dr_conv_dims* d, const void* cu, bool step) {
     return host_fail(DR_ERR_UNSUPPORTED, "activation %d is neither DR_CONV_NONE nor DR_CONV_SILU", d->activation);
   if (d->width < 2 || d->width > 4) return host_fail(DR_ERR_UNSUPPORTED, "width %lld: 2, 3 or 4", (long long)d->width);
   st = check_tokens(d->batch, d->seqlen, d->channels, d->num_seqs, cu, step);
-  if (!st) st = check_stride(d->x_token_stride, 1, "x token");
+  if (!st) st = check_stride(d->x_token_stride, 1, "x token", kTokenStride);
   return st ? st : check_stride(d->x_batch_stride, 1, "x batch");
 }
 // Vectors of channels need aligned rows; below 32 of them most lanes of a wave would be idle, and single channels do better.
@@ -158,19 +158,22 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
   if (d->softplus != 0 && d->softplus != 1) return host_fail(DR_ERR_SHAPE, "softplus must be 0 or 1, got %d", d->softplus);
   if (d->state_dim != 16 && d->state_dim != 32 && d->state_dim != 64)
     return host_fail(DR_ERR_UNSUPPORTED, "state_dim %lld: 16, 32 or 64", (long long)d->state_dim);
+  if (d->groups > 65536) return host_fail(DR_ERR_UNSUPPORTED, "%lld groups: at most 65536", (long long)d->groups);
   if (d->groups < 1) return host_fail(DR_ERR_SHAPE, "groups (%lld) must be positive", (long long)d->groups);
   st = check_tokens(d->batch, d->seqlen, d->channels, d->num_seqs, cu, step);
   if (st) return st;
   if (d->channels % d->groups != 0)
     return host_fail(DR_ERR_SHAPE, "channels (%lld) are not a multiple of groups (%lld)", (long long)d->channels, (long long)d->groups);
   const int64_t row = 16 / esize(d->in_dtype);
-  const struct { int64_t s, unit; const char* name; } strides[] = {
-      {d->x_token_stride, 1, "x token"}, {d->x_batch_stride, 1, "x batch"}, {d->dt_token_stride, 1, "dt token"},
-      {d->dt_batch_stride, 1, "dt batch"}, {d->b_token_stride, row, "B token"}, {d->b_batch_stride, row, "B batch"},
-      {d->c_token_stride, row, "C token"}, {d->c_batch_stride, row, "C batch"}, {d->z_token_stride, 1, "z token"},
-      {d->z_batch_stride, 1, "z batch"}};
+  // (rows of a chunk are reached with 32-bit offsets from its first one)
+  const struct { int64_t s, unit, most; const char* name; } strides[] = {
+      {d->x_token_stride, 1, kTokenStride, "x token"}, {d->x_batch_stride, 1, kStride, "x batch"},
+      {d->dt_token_stride, 1, kTokenStride, "dt token"}, {d->dt_batch_stride, 1, kStride, "dt batch"},
+      {d->b_token_stride, row, kTokenStride, "B token"}, {d->b_batch_stride, row, kStride, "B batch"},
+      {d->c_token_stride, row, kTokenStride, "C token"}, {d->c_batch_stride, row, kStride, "C batch"},
+      {d->z_token_stride, 1, kTokenStride, "z token"}, {d->z_batch_stride, 1, kStride, "z batch"}};
   for (const auto& s : strides) {
-    st = check_stride(s.s, s.unit, s.name);
+    st = check_stride(s.s, s.unit, s.name, s.most);
     if (st) return st;
   }
   return DR_OK;
@@ -182,22 +185,31 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
 // and a walk over the segments: in units of a token's time
 //   max(1, 0.25 + 0.5 waves / 1024) x (tokens of a segment) x (1 or 1.75) + (0 or 20 + segments)
 // 4 x 4096 tokens, 2048 channels, 16 states, bf16: 128 tokens 256 us, 256 285, 512 429, 1024 837, whole 1873.
+// With a workgroup's waves along the tokens (forward only) the decays are formed once; a workgroup fills a CU and takes 5.5 us (12 units) for 128 tokens of
+// 32 channels x 16 states.
 dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
   dr::ScanPlan pl{};
-  const int64_t T = d->seqlen, tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE);
-  const int64_t waves = tiles * (d->state_dim / 16);
+  const int64_t T = d->seqlen, per = d->channels / d->groups;
+  const int64_t waves = d->groups * ceil_div(per, dr::SCAN_TILE) * (d->state_dim / 16), tiles = d->groups * ceil_div(per, dr::SCAN_BLOCK_CH);
   const double again = backward ? 1.15 : 1.75;
   double best = 0;
   int64_t seg = ceil_div(T, 8) * 8;
+  const int64_t force = env_int("DR_SCAN_BLOCK");  // for tuning and tests: 1 always, 2 never
   for (int64_t n = 1; n == 1 || (n * 16 < T + 16 && n <= 4096); n += 1 + n / 8) {
     const int64_t s = ceil_div(ceil_div(T, n), 8) * 8, nseg = s > 0 ? ceil_div(T, s) : 1;
-    const double wgs = (packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg) * waves;
-    double load = 0.25 + 0.5 * wgs / 1024;
+    const double slots = packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg;
+    double load = 0.25 + 0.5 * slots * waves / 1024;
     if (load < 1) load = 1;
-    const double cost = load * s * (nseg > 1 ? again : 1.0) + (nseg > 1 ? 20.0 + nseg : 0.0);
+    const double join = nseg > 1 ? 20.0 + nseg : 0.0;
+    const double plain = load * s * (nseg > 1 ? again : 1.0) + join;
+    double rounds = std::ceil(slots * tiles / 256);
+    const double block = rounds * std::ceil((double)s * (d->state_dim / 16) / 128) * 12 + (nseg > 1 ? load * s * 0.75 + join : 0.0);
+    const bool by_block = !backward && force != 2 && (block < plain || force == 1);
+    const double cost = by_block ? block : plain;
     if (best == 0 || cost < best) {
       best = cost;
       seg = s;
+      pl.block = by_block;
     }
   }
   if (const int64_t s = env_int("DR_SCAN_SEG"))
@@ -214,6 +226,7 @@ int64_t grad_blocks(const dr_scan_dims* d) { return ceil_div(d->channels / d->gr
 bool scan_fits(const dr_scan_dims* d, const dr::ScanPlan& pl, bool backward) {
   const int64_t tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE), N = d->state_dim;
   if (pl.slots > INT32_MAX || pl.seg > INT32_MAX) return false;
+  if (pl.block && !dr::launch_fits(pl.slots * d->groups * ceil_div(d->channels / d->groups, dr::SCAN_BLOCK_CH) + 8, 64 * dr::SCAN_BLOCK_WAVES)) return false;
   if (!dr::launch_fits(pl.slots * tiles, (int)(64 * (N / 16))) || !dr::launch_fits(d->num_seqs * ceil_div(d->channels * (N / 4), 256), 256))
     return false;
   return !backward || (dr::launch_fits(pl.slots * d->groups * grad_blocks(d), 256) &&
@@ -261,6 +274,7 @@ dr::ScanParams scan_params(const dr_scan_dims* d) {
   p.G = (int32_t)d->groups;
   p.Cg = p.C / p.G;
   p.tiles = (int32_t)ceil_div(p.Cg, dr::SCAN_TILE);
+  p.btiles = (int32_t)ceil_div(p.Cg, dr::SCAN_BLOCK_CH);
   p.cblocks = (int32_t)grad_blocks(d);
   p.nseq = (int32_t)d->num_seqs;
   p.nbatch = (int32_t)d->batch;

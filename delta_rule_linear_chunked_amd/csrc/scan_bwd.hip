@@ -204,9 +204,10 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   // as the lane of states and gradients: 4 channels, 2 states
   const int ng = lane >> 3, cg = lane & 7;
   const int l_ch = cb * 32 + cg * 4, n0 = sl * 16 + ng * 2;
-  int lc[4];
+  int lc[4];  // (channels past the group's count as its last)
 #pragma unroll
   for (int i = 0; i < 4; ++i) lc[i] = g * p.Cg + min(in0 + l_ch + i, p.Cg - 1);
+  const int lim = max(p.Cg - 1 - in0 - l_ch, 0);
   float A[4][2], carry[4][2], dA[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -225,48 +226,84 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   const bool on = in0 + pc < p.Cg;
   const int c = g * p.Cg + min(in0 + pc, p.Cg - 1);
   const float bias = p.bias ? p.bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
-  const InT* x = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
-  const InT* dt = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
-  const InT* z = GATE ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : nullptr;
-  const int64_t row0 = sp.b * p.T + sp.t0;
-  const InT* dy = static_cast<const InT*>(p.dy) + row0 * C + c;
-  const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N;
-  const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N;
+  // Addresses: a uniform pointer for the chunk, moved back by a chunk after each, and 32-bit offsets of the lane that stay
+  // (token strides are limited to 2^24 elements, groups to 2^16).
+  const int last = len > 0 ? (len - 1) / K * K : 0;
+  const int64_t row0 = sp.b * p.T + sp.t0, x_ts = p.x_ts, dt_ts = p.dt_ts, z_ts = p.z_ts;
+  const InT* xb = static_cast<const InT*>(p.x) + sp.b * p.x_bs + (sp.t0 + last) * x_ts;
+  const InT* db = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + (sp.t0 + last) * dt_ts;
+  const InT* zb = GATE ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + (sp.t0 + last) * z_ts : nullptr;
+  int64_t row = row0 + last, next = row;  // of the outputs, of dy
+  const uint32_t xo = (uint32_t)(prow * x_ts) + c, dto = (uint32_t)(prow * dt_ts) + c, zo = GATE ? (uint32_t)(prow * z_ts) + c : 0u;
+  const uint32_t oo = (uint32_t)(prow * C) + c, cko = (uint32_t)lc[0] * N + n0;
+  int64_t chunk = (int64_t)slot * cps + last / K;
+  constexpr int BCN = 2 * K * N / 256;  // elements of B and C of a thread: B's first, then C's (a wave has one of them)
+  static_assert(2 * K * N % 256 == 0 && K * N % 64 == 0, "whole waves");
+  uint32_t bco[BCN];
+#pragma unroll
+  for (int i = 0; i < BCN; ++i) {
+    const int e = (tid + i * 256) % (K * N);
+    const bool isC = (wave * 64 + i * 256) / (K * N) == 1;
+    bco[i] = (uint32_t)(e / N * (isC ? p.c_ts : p.b_ts)) + e % N;
+  }
   const bool soft = p.softplus != 0;
   float accD = 0.f, accb = 0.f;
   InT xn[PP], dn[PP], zn[PP], yn[PP];
   float hn[4][2], dsum[4];
-  constexpr int BCN = (2 * K * N + 255) / 256;  // elements of B and C of a thread
   InT bn[BCN];
-  auto fetch = [&](int t) {
+  auto fetch = [&](int t) {  // (rows past the end are read from the last one and not used; those of B and C are zeros)
+    const InT *xr = xb, *dr = db, *zr = zb, *yr = static_cast<const InT*>(p.dy) + next * C;
+    if (t + K <= len) {
 #pragma unroll
-    for (int i = 0; i < PP; ++i) {
-      const int64_t r = min(t + prow + i * ROWS, len - 1);
-      xn[i] = x[r * p.x_ts];
-      dn[i] = dt[r * p.dt_ts];
-      if constexpr (GATE) zn[i] = z[r * p.z_ts];
-      yn[i] = dy[r * C];
+      for (int i = 0; i < PP; ++i) {
+        xn[i] = xr[xo];
+        dn[i] = dr[dto];
+        if constexpr (GATE) zn[i] = zr[zo];
+        yn[i] = yr[oo];
+        xr += ROWS * x_ts;
+        dr += ROWS * dt_ts;
+        if constexpr (GATE) zr += ROWS * z_ts;
+        yr += ROWS * (int64_t)C;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PP; ++i) {
+        const int64_t r = min(prow + i * ROWS, len - 1 - t);
+        xn[i] = xr[r * x_ts + c];
+        dn[i] = dr[r * dt_ts + c];
+        if constexpr (GATE) zn[i] = zr[r * z_ts + c];
+        yn[i] = yr[r * C + c];
+      }
     }
+    xb -= K * x_ts;
+    db -= K * dt_ts;
+    if constexpr (GATE) zb -= K * z_ts;
+    next -= K;
 #pragma unroll
     for (int i = 0; i < BCN; ++i) {
-      const int q = tid + i * 256, m = q / (K * N), e = q % (K * N);  // B first, then C
-      const int64_t r = t + e / N;
+      const bool isC = (wave * 64 + i * 256) / (K * N) == 1;
+      const InT* from = isC ? static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + (sp.t0 + t) * p.c_ts : static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + t) * p.b_ts;
       bn[i] = InT(0);
-      if (m < 2 && r < len) bn[i] = m ? Cp[r * p.c_ts + e % N] : Bp[r * p.b_ts + e % N];
+      if (t + K <= len || t + (tid + i * 256) % (K * N) / N < len) bn[i] = from[g * N + (uint64_t)bco[i]];
     }
-    const int64_t k = (int64_t)slot * cps + t / K;
+    const float *ck = p.ck + chunk * C * N, *ckd = p.ckd + chunk * C;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       dsum[i] = 0.f;
       hn[i][0] = hn[i][1] = 0.f;
       if (t > 0) {
-        dsum[i] = p.ckd[k * C + lc[i]];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) hn[i][j] = p.ck[(k * C + lc[i]) * N + n0 + j];  // (8 bytes)
+        const uint32_t o = min(i, lim);
+        dsum[i] = ckd[(uint32_t)lc[0] + o];
+        const f32x2 v = *reinterpret_cast<const f32x2*>(ck + (cko + o * N));
+        hn[i][0] = v[0];
+        hn[i][1] = v[1];
       }
     }
+    --chunk;
   };
-  const int last = (len - 1) / K * K;
+  // this workgroup's part of dB and dC: 2 N values to a token
+  float* pbc = p.pBC + (((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0 + last) * p.G + g) * (2 * N);
+  const uint32_t pbo = (uint32_t)(tid / (2 * N)) * p.G * (2 * N) + tid % (2 * N);
   if (len > 0) fetch(last);
   for (int t = last; len > 0 && t >= 0; t -= K) {
     __syncthreads();  // (the chunk before has been written out)
@@ -292,8 +329,8 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
     }
 #pragma unroll
     for (int i = 0; i < BCN; ++i) {
-      const int q = tid + i * 256, m = q / (K * N), e = q % (K * N);
-      if (m < 2) (m ? &s_c[0][0] : &s_b[0][0])[e] = (float)bn[i];
+      const int q = tid + i * 256;
+      (q < K * N ? &s_b[0][0] : &s_c[0][0] - K * N)[q] = (float)bn[i];
     }
     // the state in front of the chunk
     float a[K][4][2], h[K + 1][4][2];
@@ -376,25 +413,26 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       }
       const float xv = s_own[0][i][tid], gv = s_dy[r][pc];
       const float draw = fmaf(u, xv, e * LN2) * s_own[1][i][tid];
-      const int64_t at = (row0 + t + r) * C + c;
-      static_cast<InT*>(p.ddt)[at] = (InT)draw;
-      static_cast<InT*>(p.dx)[at] = (InT)fmaf(u, s_d[r][pc], D * gv);
+      const int64_t base = (row + i * ROWS) * C;
+      (static_cast<InT*>(p.ddt) + base)[oo] = (InT)draw;
+      (static_cast<InT*>(p.dx) + base)[oo] = (InT)fmaf(u, s_d[r][pc], D * gv);
       if constexpr (GATE) {
         const float zv = s_own[2][i][tid], sz = sigmoid_f(zv);
-        static_cast<InT*>(p.dz)[at] = (InT)(s_own[3][i][tid] * fmaf(D, xv, yo) * (sz * fmaf(zv, 1.f - sz, 1.f)));
+        (static_cast<InT*>(p.dz) + base)[oo] = (InT)(s_own[3][i][tid] * fmaf(D, xv, yo) * (sz * fmaf(zv, 1.f - sz, 1.f)));
       }
       accD = fmaf(gv, xv, accD);
       accb += draw;
     }
-    // this workgroup's part of dB and dC: value q of a token is state q / 2 of B (even) or C (odd)
-    for (int q = tid; q < 2 * K * N; q += 256) {
-      const int r = q / (2 * N), m = q / N & 1, n = q % N;
-      if (t + r >= len) continue;
+#pragma unroll
+    for (int i = 0; i < BCN; ++i) {
+      const int q = tid + i * 256, r = q / (2 * N), m = q / N & 1, n = q % N;
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < Sh::CB; ++w) v += s_bc[w * SL + n / 16][r][(n % 16) / 2 * 4 + 2 * m + (n & 1)];
-      p.pBC[(((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0 + t + r) * p.G + g) * (2 * N) + m * N + n] = v;
+      if (t + r < len) (pbc + i * (256 / (2 * N)) * (int64_t)p.G * (2 * N))[pbo] = v;
     }
+    row -= K;
+    pbc -= K * (int64_t)p.G * (2 * N);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)

@@ -18,7 +18,8 @@
  * evaluation to about 1e-6 of the output's size (2-norm) before that rounding.
  * Pointers need the alignment of their elements; parameters, scan states, cu_seqlens, state_idx, workspaces, B and C
  * 16 bytes. A tensor with strides may be a view whose channels are dense: "token" and "batch" strides are counted in elements,
- * not negative, at most 2^40, and for B and C multiples of 16 bytes. All other tensors are dense.
+ * not negative, at most 2^24 (token) and 2^40 (batch, rows), and for B and C multiples of 16 bytes. All other tensors are
+ * dense.
  * The offsets of packed sequences are not read on the host; rows that no sequence holds are neither read nor written.
  * At most 2^31 - 1024 tokens and sequences per call, at most 2^20 channels (norm: 32768); a call whose launches would pass
  * 2^32 - 1 work items is refused (DR_ERR_UNSUPPORTED).
@@ -76,7 +77,7 @@ int dr_conv_bwd(const void* x, const float* weight, const float* bias, const voi
                 const dr_conv_dims* dims, void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------------------ selective scan */
-/* batch, seqlen, num_seqs, in_dtype as in dr_dims; channels a multiple of groups; channel c reads the B and C of group
+/* batch, seqlen, num_seqs, in_dtype as in dr_dims; channels a multiple of groups (at most 65536); channel c reads the B and C of group
  * c / (channels / groups); state_dim 16, 32 or 64. softplus 0: d = dt + dt_bias, 1: softplus of it. */
 typedef struct dr_scan_dims {
   int64_t batch;

@@ -26,8 +26,10 @@ def check(x, dtype, cu=None, soft=True, drop=(), got=None, t=None):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [16, 32, 64])
-@pytest.mark.parametrize("T,C,G", [(1, 1, 1), (7, 3, 3), (8, 64, 1), (9, 130, 2), (65, 65, 1), (130, 128, 2)])
-def test_rows(T, C, G, N, dtype):
+@pytest.mark.parametrize("block", ["1", "2"])  # waves along the tokens, or along the channels
+@pytest.mark.parametrize("T,C,G", [(1, 1, 1), (7, 3, 3), (8, 64, 1), (9, 130, 2), (65, 65, 1), (130, 128, 2), (300, 40, 1)])
+def test_rows(T, C, G, block, N, dtype, monkeypatch):
+    monkeypatch.setenv("DR_SCAN_BLOCK", block)
     check(make_scan(seed_of("scan", T, C, G, N, dtype), 2, T, C, G, N, dtype), dtype)
 
 
@@ -40,8 +42,10 @@ def test_optional_inputs(drop, soft):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("seg", [0, 8, 40])
 @pytest.mark.parametrize("N", [16, 64])
+@pytest.mark.parametrize("block", ["1", "2"])
 @pytest.mark.parametrize("cu", [[0, 0, 1, 3, 3, 40, 41, 90, 90], [0, 64, 72, 72, 75], [0], [0, 0]])
-def test_packed(cu, N, seg, dtype, monkeypatch):
+def test_packed(cu, block, N, seg, dtype, monkeypatch):
+    monkeypatch.setenv("DR_SCAN_BLOCK", block)
     if seg:
         monkeypatch.setenv("DR_SCAN_SEG", str(seg))
     x = make_scan(seed_of("packed", cu, N, dtype), 1, 97, 70, 2, N, dtype, n=len(cu) - 1)
@@ -54,8 +58,10 @@ def test_packed(cu, N, seg, dtype, monkeypatch):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("seg", [8, 16, 48])
+@pytest.mark.parametrize("block", ["1", "2"])
 @pytest.mark.parametrize("T", [8, 47, 48, 49, 200])
-def test_segments(T, seg, dtype, monkeypatch):
+def test_segments(T, block, seg, dtype, monkeypatch):
+    monkeypatch.setenv("DR_SCAN_BLOCK", block)
     monkeypatch.setenv("DR_SCAN_SEG", str(seg))
     check(make_scan(seed_of("seg", T, seg), 2, T, 70, 1, 16, dtype), dtype)
 
