@@ -47,7 +47,8 @@ def _hipcc() -> str:
 _ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 _MFMA_VGPR = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 FILE_FLAGS = {"prefill.hip": _MFMA_VGPR, "prefill_state.hip": _ILP + _MFMA_VGPR, "backward.hip": _ILP,
-              "decay.hip": _MFMA_VGPR, "decay_bwd.hip": _MFMA_VGPR}
+              "decay.hip": _MFMA_VGPR, "decay_bwd.hip": _MFMA_VGPR, "scan.hip": _MFMA_VGPR, "scan_block.hip": _MFMA_VGPR,
+              "scan_bwd.hip": _MFMA_VGPR}
 
 
 def _compile(src: str) -> str:

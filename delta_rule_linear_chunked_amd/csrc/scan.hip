@@ -1,180 +1,182 @@
 // Selective scan over the tokens of every channel on gfx950: h <- exp(d A) h + d x B, y = (C h + D x) silu(z).
 //
-// A decay of its own for every (token, channel, state) leaves nothing for a matrix product: per state one exponential and four more
-// operations on the vector units, which is what bounds the pass. A lane has one channel and NS of its states in registers, so B and C are
-// the same for a whole wave and come through the scalar unit; the sum over states needs no exchange between lanes. With
-// more states than NS the waves of a workgroup share a channel tile and add their parts of y through LDS.
+// A decay of its own for every (token, channel, state): per state one exponential (twice an ordinary operation), one product and
+// two sums on the vector units, which bound the pass; what is added to the state comes from the matrix units (scan_tile.hpp). A wave
+// walks the tokens of 32 channels x 16 states; with more states the waves of a workgroup share the channels and add their parts of y
+// through LDS.
 // Sequences that are too few to fill the GPU are cut into segments: their own states from zero first (one more pass without
-// C and y), then each segment's start by a walk over the segments, whose decay is exp(A sum d).
-#include <type_traits>
-
-#include "scan.hpp"
+// C and y), then each segment's start by a walk over the segments, whose decay is exp(A sum d); or a workgroup's waves
+// go along the tokens (scan_block.hip).
+#include "scan_tile.hpp"
 
 namespace dr {
 
 // The main pass (LOCAL false: outputs and final states) or the segments' own states and sums of d.
-template <int NS, int NW, typename InT, bool LOCAL>
-__global__ __launch_bounds__(64 * NW) void scan_kernel(const ScanParams p) {
-  constexpr int N = NS * NW, TT = 8;
-  __shared__ float s_y[NW > 1 ? 2 : 1][NW > 1 ? NW : 1][NW > 1 ? TT : 1][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <int SL, typename InT, bool LOCAL>
+__global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
+  constexpr int N = 16 * SL, K = TILE_TOK, O = TILE_OWN;
+  __shared__ __align__(16) float s_c[LOCAL ? 1 : SL][LOCAL ? 1 : K][16];          // a wave's own rows of C
+  __shared__ float s_y[SL > 1 && !LOCAL ? 2 : 1][SL > 1 && !LOCAL ? SL : 1][SL > 1 && !LOCAL ? O : 1][64];
+  const int lane = threadIdx.x & 63, sl = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int ntiles = p.G * p.tiles;
   const int slot = blockIdx.x / ntiles, tile = blockIdx.x - slot * ntiles;
   const SlotSpan sp = slot_span(p, slot);
   if (sp.n < 0 || (LOCAL && sp.last)) return;
-  const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + lane;
-  if (in_g >= p.Cg) return;  // (the same lanes of every wave, and never all of a wave's: the barriers below still meet)
-  const int c = g * p.Cg + in_g;
-  float A[NS], h[NS];
+  const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + (lane & 31);
+  const bool on = in_g < p.Cg;  // (channels past the group's count as its last and store nothing)
+  const int c = g * p.Cg + min(in_g, p.Cg - 1), n0 = sl * 16 + 4 * half;
+  float A[8], h[8];
+  load_states(p.A + (int64_t)c * N + n0, A);
 #pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    A[j] = p.A[(int64_t)c * N + wave * NS + j] * LOG2E;
+  for (int j = 0; j < 8; ++j) {
+    A[j] *= LOG2E;
     h[j] = 0.f;
   }
   const float bias = p.bias ? p.bias[c] : 0.f, D = !LOCAL && p.D ? p.D[c] : 0.f;
   if constexpr (!LOCAL) {
-    const float* from = nullptr;
     if (p.part) {
-      from = p.part + ((int64_t)slot * p.C + c) * N;
+      load_states(p.part + ((int64_t)slot * p.C + c) * N + n0, h);
     } else if (p.S0) {
       const int64_t r = state_row(p.sidx, p.nslots, sp.n);
-      if (r >= 0) from = p.S0 + (r * p.C + c) * N;
+      if (r >= 0) load_states(p.S0 + (r * p.C + c) * N + n0, h);
     }
-    if (from)
-#pragma unroll
-      for (int j = 0; j < NS; j += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(from + wave * NS + j);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[j + k] = v[k];
-      }
   }
   const int len = sp.len;
   const bool soft = p.softplus != 0, gate = !LOCAL && p.z != nullptr;
-  const InT* xp = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
-  const InT* dp = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
-  const InT* zp = gate ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : xp;
-  const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N + wave * NS;
-  const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N + wave * NS;
-  InT* y = LOCAL ? nullptr : static_cast<InT*>(p.y) + (sp.b * p.T + sp.t0) * (int64_t)p.C + c;
-  const int64_t x_ts = p.x_ts, dt_ts = p.dt_ts, z_ts = gate ? p.z_ts : p.x_ts, b_ts = p.b_ts, c_ts = p.c_ts, C = p.C;
+  Rows<InT> X, T, Z, B;
+  X.init(p.x, sp.b * p.x_bs + sp.t0 * p.x_ts, p.x_ts, half, c);
+  T.init(p.dt, sp.b * p.dt_bs + sp.t0 * p.dt_ts, p.dt_ts, half, c);
+  if (gate)
+    Z.init(p.z, sp.b * p.z_bs + sp.t0 * p.z_ts, p.z_ts, half, c);
+  else
+    Z = X;
+  B.init(p.B, sp.b * p.b_bs + sp.t0 * p.b_ts, p.b_ts, half, g * N + sl * 16 + (lane & 15));
+  // C: lane l brings states 4 (l % 4) .. + 3 of token l / 4
+  typedef typename Vec<InT, 4>::type V4;
+  const InT* Ca = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts;
+  const uint32_t c_off = (uint32_t)((lane >> 2) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)) * sizeof(InT);
+  InT* y = LOCAL ? nullptr : static_cast<InT*>(p.y) + (sp.b * p.T + sp.t0) * (int64_t)p.C;
+  const uint32_t y_off = (uint32_t)(half * p.C + c) * sizeof(InT);
   float sumd = 0.f;
-  // A tile's inputs come a tile ahead, a token's rows of B and C a token ahead; nothing past the last token is read.
-  InT xn[TT], dn[TT], zn[TT];
-  auto fetch = [&](int n) {  // the next n tokens (TT of them but at the end)
-    if (n >= TT) {
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        xn[i] = *xp;
-        dn[i] = *dp;
-        xp += x_ts;
-        dp += dt_ts;
-        if constexpr (!LOCAL) {
-          zn[i] = *zp;
-          zp += z_ts;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        xn[i] = dn[i] = zn[i] = InT(0);
-        if (i < n) {
-          xn[i] = *xp;
-          dn[i] = *dp;
-          xp += x_ts;
-          dp += dt_ts;
-          if constexpr (!LOCAL) {
-            zn[i] = *zp;
-            zp += z_ts;
-          }
-        }
-      }
-    }
-  };
-  Row<InT, NS> Bt[2], Ct[2];
-  auto rows = [&](int to, bool more) {
-    Bt[to].load(Bp);
-    Bp += more ? b_ts : 0;
-    if constexpr (!LOCAL) {
-      Ct[to].load(Cp);
-      Cp += more ? c_ts : 0;
-    }
-  };
-  if (len > 0) {
-    fetch(len);
-    rows(0, len > 1);
-  }
-  int buf = 0;
-  auto run = [&](int t, auto whole) {
-    constexpr bool WHOLE = decltype(whole)::value;
-    float xv[TT], dv[TT], zv[TT], yv[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      xv[i] = (float)xn[i];
-      const float raw = (float)dn[i] + bias, sf = softplus_f(raw);
-      dv[i] = soft ? sf : raw;
-      // (tokens past the end: a decay of one and nothing added)
-      if (!WHOLE && t + i >= len) dv[i] = 0.f;
+  uint32_t xn[O], dn[O], zn[O], bn[O];
+  V4 cn{};
+  auto fetch = [&](int left) {
+    if (left >= K) {
+      X.whole(xn);
+      T.whole(dn);
+      B.whole(bn);
       if constexpr (!LOCAL) {
-        zv[i] = (float)zn[i];
-        const float sg = zv[i] * sigmoid_f(zv[i]);
-        zv[i] = gate ? sg : 1.f;
+        Z.whole(zn);
+        cn = *reinterpret_cast<const V4*>(byte_at(Ca, c_off));
+      }
+      whole_tile();
+    } else {
+      X.part(xn, left);
+      T.part(dn, left);
+      B.part(bn, left);
+      if constexpr (!LOCAL) {
+        Z.part(zn, left);
+        cn = *reinterpret_cast<const V4*>(Ca + ((int64_t)min(lane >> 2, left - 1) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)));
       }
     }
-    if (WHOLE && t + TT < len) fetch(len - t - TT);
+    X.at += K * X.ts;
+    T.at += K * T.ts;
+    B.at += K * B.ts;
+    if constexpr (!LOCAL) {
+      Z.at += K * Z.ts;
+      Ca += K * p.c_ts;
+    }
+  };
+  if (len > 0) fetch(len);
+  int buf = 0;
+  for (int t = 0; t < len; t += K, buf ^= 1) {
+    float xv[O], dv[O], zv[O], dx[O], bo[O], v[O];
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      rows((i + 1) & 1, t + i + 2 < len);
-      __builtin_amdgcn_sched_barrier(0);
-      const float d = dv[i], dx = d * xv[i];
-      float a[NS], acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < NS; ++j) a[j] = __builtin_amdgcn_exp2f(d * A[j]);
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        h[j] = fmaf(a[j], h[j], dx * Bt[i & 1][j]);
-        if constexpr (!LOCAL) acc[j & 3] = fmaf(Ct[i & 1][j], h[j], acc[j & 3]);
-      }
-      yv[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-      if constexpr (LOCAL) sumd += d;
-      if constexpr (!LOCAL) asm volatile("" : "+v"(yv[i]));  // (here, not where it is stored: C's rows are held no longer)
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < O; ++i) {
+      xv[i] = raw_value<InT>(xn[i]);
+      const float raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw);
+      float own = soft ? sf : raw;
+      here(own);
+      // (tokens past the end: a decay of one and nothing added)
+      const bool inside = t + K <= len || t + 2 * i + half < len;
+      dv[i] = inside ? own : 0.f;
+      dx[i] = inside ? dv[i] * xv[i] : 0.f;
+      bo[i] = operand<InT>(bn[i], lane);
+      if constexpr (!LOCAL) zv[i] = raw_value<InT>(zn[i]);
+      if constexpr (LOCAL) sumd += dv[i];
     }
     if constexpr (!LOCAL) {
-      if constexpr (NW > 1) {
+      float f[4];
+      unpack<4, InT>(cn, f);
+      *reinterpret_cast<f32x4*>(&s_c[sl][lane >> 2][4 * (lane & 3)]) = f32x4{f[0], f[1], f[2], f[3]};
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (t + K < len) fetch(len - t - K);
+    f32x16 in = outer_pair(bo[0], dx[0]);
 #pragma unroll
-        for (int i = 0; i < TT; ++i) s_y[buf][wave][i][lane] = yv[i];
+    for (int i = 0; i < O; ++i) {
+      tile_step();
+      float d[2], s[2];
+      both_halves(dv[i], d[0], d[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        f32x4 c0{}, c1{};
+        if constexpr (!LOCAL) {
+          c0 = *reinterpret_cast<const f32x4*>(&s_c[sl][2 * i + k][4 * half]);
+          c1 = *reinterpret_cast<const f32x4*>(&s_c[sl][2 * i + k][8 + 4 * half]);
+        }
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(d[k] * A[j]), h[j], in[8 * k + j]);
+        if (k == 1 && i + 1 < O) in = outer_pair(bo[i + 1], dx[i + 1]);  // (the decays hide it; two at once would hold 16 more registers)
+        if constexpr (!LOCAL) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < 4)
+              s0 = fmaf(c0[j & 3], h[j], s0);
+            else
+              s1 = fmaf(c1[j & 3], h[j], s1);
+        }
+        s[k] = s0 + s1;
+      }
+      if constexpr (!LOCAL) {
+        v[i] = sum_halves(s[0], s[1]);
+        here(v[i]);  // (the states of all tokens would be held otherwise)
+      }
+    }
+    if constexpr (!LOCAL) {
+      __builtin_amdgcn_wave_barrier();
+      if constexpr (SL > 1) {
+#pragma unroll
+        for (int i = 0; i < O; ++i) s_y[buf][sl][i][lane] = v[i];
         __syncthreads();
       }
+      InT* row = y;
 #pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        if ((WHOLE || t + i < len) && (NW == 1 || i % NW == wave)) {  // (uniform over the wave)
-          float v = yv[i];
-          if constexpr (NW > 1) {
-            v = 0.f;
+      for (int i = 0; i < O; ++i, row += 2 * (int64_t)p.C) {
+        if (SL > 1 && i % SL != sl) continue;
+        float o = v[i];
+        if constexpr (SL > 1) {
+          o = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) v += s_y[buf][w][i][lane];
-          }
-          *y = (InT)(fmaf(D, xv[i], v) * zv[i]);
+          for (int w = 0; w < SL; ++w) o += s_y[buf][w][i][lane];
         }
-        y += C;
+        o = fmaf(D, xv[i], o);
+        const float sg = zv[i] * sigmoid_f(zv[i]);
+        if (on && (t + K <= len || t + 2 * i + half < len)) *byte_at(row, y_off) = (InT)(o * (gate ? sg : 1.f));
       }
+      y += K * (int64_t)p.C;
     }
-  };
-  int t = 0;
-  for (; t + TT <= len; t += TT, buf ^= 1) run(t, std::true_type{});
-  if (t < len) run(t, std::false_type{});
+  }
+  if (!on) return;
   if constexpr (LOCAL) {
-    float* to = p.part + ((int64_t)slot * p.C + c) * N + wave * NS;
-#pragma unroll
-    for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
-    if (wave == 0) p.sumd[(int64_t)slot * p.C + c] = sumd;
+    store_states(p.part + ((int64_t)slot * p.C + c) * N + n0, h);
+    float lo, hi;  // (the halves' tokens)
+    both_halves(sumd, lo, hi);
+    if (sl == 0 && half == 0) p.sumd[(int64_t)slot * p.C + c] = lo + hi;
   } else if (sp.last && p.S) {
     const int64_t r = state_row(p.sidx, p.nslots, sp.n);
-    if (r >= 0) {
-      float* to = p.S + (r * p.C + c) * N + wave * NS;
-#pragma unroll
-      for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
-    }
+    if (r >= 0) store_states(p.S + (r * p.C + c) * N + n0, h);
   }
 }
 
@@ -203,18 +205,18 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const ScanParams p) {
   }
 }
 
-template <int NS, int NW, typename InT>
+template <int SL, typename InT>
 static hipError_t launch_t(const ScanParams& p, bool local, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.slots * p.G * p.tiles)), block(64 * NW);
+  const dim3 grid((unsigned)((int64_t)p.slots * p.G * p.tiles)), block(64 * SL);
   if (local)
-    hipLaunchKernelGGL((scan_kernel<NS, NW, InT, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((scan_kernel<SL, InT, true>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((scan_kernel<NS, NW, InT, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((scan_kernel<SL, InT, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 template <typename InT>
 static hipError_t launch_any(const ScanParams& p, int n, bool local, hipStream_t s) {
-  return n == 16 ? launch_t<16, 1, InT>(p, local, s) : n == 32 ? launch_t<16, 2, InT>(p, local, s) : launch_t<16, 4, InT>(p, local, s);
+  return n == 16 ? launch_t<1, InT>(p, local, s) : n == 32 ? launch_t<2, InT>(p, local, s) : launch_t<4, InT>(p, local, s);
 }
 
 // Offsets and slot tables of packed sequences: the plan pass of the decayed linear attention makes the same ones.

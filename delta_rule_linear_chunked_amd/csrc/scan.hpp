@@ -39,31 +39,22 @@ __device__ __forceinline__ typename Vec<T, VEC>::type pack(const float (&f)[VEC]
   }
 }
 
-// e^v with the product's rounding put back: the hardware exponential (1 ulp) of v log2 e as two floats.
 constexpr float LN2 = 0.6931471805599453f;
-__device__ __forceinline__ float exp_acc(float v) {
-  const float hi = v * LOG2E;
-  const float lo = fmaf(v, LOG2E, -hi) + v * 1.925963033500467e-8f;  // log2 e - its float
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return v < -104.f ? 0.f : fmaf(e, lo * LN2, e);
-}
 __device__ __forceinline__ float sigmoid_f(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * LOG2E));
 }
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1], and its derivative 1 / (1 + exp(-v)).
-// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the odd series through s^13 (what follows is below 2e-8 of it):
-// a small step (1e-3 and less is usual) keeps its relative precision, which log of the rounded 1 + e would lose.
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1].
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: a small step (1e-3 and less is usual) keeps its relative precision, which log of
+// the rounded 1 + e would lose. 2 atanh(s) / s as a polynomial of s^2 in [0, 1/9], a Chebyshev fit of degree 4, off by 8e-9 of it.
 __device__ __forceinline__ float softplus_f(float v) {
-  const float e = exp_acc(-fabsf(v));
-  const float s = e * __builtin_amdgcn_rcpf(2.f + e), s2 = s * s;
-  float q = 2.f / 13.f;
-  q = fmaf(q, s2, 2.f / 11.f);
-  q = fmaf(q, s2, 2.f / 9.f);
-  q = fmaf(q, s2, 2.f / 7.f);
-  q = fmaf(q, s2, 2.f / 5.f);
-  q = fmaf(q, s2, 2.f / 3.f);
-  const float l = fmaf(q * s2, s, 2.f * s);
-  return v != v ? v : fmaxf(v, 0.f) + l;
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * LOG2E);
+  const float s = e * __builtin_amdgcn_rcpf(2.f + e), z = s * s;
+  float q = 0.28174657f;
+  q = fmaf(q, z, 0.27961419f);
+  q = fmaf(q, z, 0.40024854f);
+  q = fmaf(q, z, 0.66666316f);
+  q = fmaf(q, z, 2.00000001f);
+  return fmaf(s, q, fmaxf(v, 0.f));
 }
 
 // Row of a state pool that sequence n has; -1: none.
@@ -82,25 +73,6 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int nseq, int t) {
   }
   return lo;
 }
-
-// Scalar loads of NS elements of a token's B or C (uniform addresses, 4-byte aligned, nothing writes them meanwhile).
-typedef const __attribute__((address_space(4))) uint32_t* const_u32;
-template <typename InT, int NS>
-struct Row {
-  static constexpr int NW = NS * (int)sizeof(InT) / 4;
-  uint32_t w[NW];
-  __device__ __forceinline__ void load(const InT* at) {
-    const const_u32 q = (const_u32)(uintptr_t)at;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = q[i];
-  }
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (sizeof(InT) == 4)
-      return __builtin_bit_cast(float, w[i]);
-    else
-      return __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-  }
-};
 
 // ---------------------------------------------------------------------------
 // Convolution
@@ -190,7 +162,7 @@ struct ScanParams {
   int64_t T;
   int64_t x_ts, x_bs, dt_ts, dt_bs, b_ts, b_bs, c_ts, c_bs, z_ts, z_bs;
   int32_t C, G, Cg;        // channels, groups, channels of a group
-  int32_t tiles, btiles;   // channel tiles of a group: of 64, of 32
+  int32_t tiles;           // channel tiles of a group
   int32_t nseq, nbatch;
   int32_t softplus;
   int32_t seg;             // tokens of a segment
@@ -253,8 +225,8 @@ __device__ __forceinline__ SlotSpan slot_span(const ScanParams& p, int slot) {
   s.last = s.t0 + s.len >= end;
   return s;
 }
-constexpr int SCAN_TILE = 64;  // channels of a wave
-constexpr int SCAN_BLOCK_WAVES = 8, SCAN_BLOCK_CH = 32;  // waves and channels of a workgroup of scan_block.hip
+constexpr int SCAN_TILE = 32;        // channels of a wave
+constexpr int SCAN_BLOCK_WAVES = 8;  // waves of a workgroup of scan_block.hip
 hipError_t launch_scan_block(const ScanParams& p, int n, bool bf16, hipStream_t s);
 constexpr int scan_step_channels(int n) { return 1024 / n; }  // channels of a workgroup of the step (4 states a lane)
 hipError_t launch_scan_plan(const ScanParams& p, hipStream_t s);

@@ -190,7 +190,7 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
 dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
   dr::ScanPlan pl{};
   const int64_t T = d->seqlen, per = d->channels / d->groups;
-  const int64_t waves = d->groups * ceil_div(per, dr::SCAN_TILE) * (d->state_dim / 16), tiles = d->groups * ceil_div(per, dr::SCAN_BLOCK_CH);
+  const int64_t tiles = d->groups * ceil_div(per, dr::SCAN_TILE), waves = tiles * (d->state_dim / 16);
   const double again = backward ? 1.15 : 1.75;
   double best = 0;
   int64_t seg = ceil_div(T, 8) * 8;
@@ -226,7 +226,7 @@ int64_t grad_blocks(const dr_scan_dims* d) { return ceil_div(d->channels / d->gr
 bool scan_fits(const dr_scan_dims* d, const dr::ScanPlan& pl, bool backward) {
   const int64_t tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE), N = d->state_dim;
   if (pl.slots > INT32_MAX || pl.seg > INT32_MAX) return false;
-  if (pl.block && !dr::launch_fits(pl.slots * d->groups * ceil_div(d->channels / d->groups, dr::SCAN_BLOCK_CH) + 8, 64 * dr::SCAN_BLOCK_WAVES)) return false;
+  if (pl.block && !dr::launch_fits(pl.slots * d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE) + 8, 64 * dr::SCAN_BLOCK_WAVES)) return false;
   if (!dr::launch_fits(pl.slots * tiles, (int)(64 * (N / 16))) || !dr::launch_fits(d->num_seqs * ceil_div(d->channels * (N / 4), 256), 256))
     return false;
   return !backward || (dr::launch_fits(pl.slots * d->groups * grad_blocks(d), 256) &&
@@ -274,7 +274,6 @@ dr::ScanParams scan_params(const dr_scan_dims* d) {
   p.G = (int32_t)d->groups;
   p.Cg = p.C / p.G;
   p.tiles = (int32_t)ceil_div(p.Cg, dr::SCAN_TILE);
-  p.btiles = (int32_t)ceil_div(p.Cg, dr::SCAN_BLOCK_CH);
   p.cblocks = (int32_t)grad_blocks(d);
   p.nseq = (int32_t)d->num_seqs;
   p.nbatch = (int32_t)d->batch;

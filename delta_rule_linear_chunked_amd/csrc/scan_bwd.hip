@@ -10,123 +10,145 @@
 // decays of the chunk again from its checkpoint, held in registers (8 tokens x 4 channels x 2 states a lane), then
 // the tokens in reverse. A lane's square of channels and states shares the two kinds of sums between lanes evenly: over states (dx,
 // dd, y) across the lanes' rows, over channels (dB, dC) within eight lanes.
-#include "scan.hpp"
+#include "scan_tile.hpp"
 
 namespace dr {
 
-// Local states at every 8th token and behind the segment, the sums of d there, and (BOTH) the reverse part.
-template <int NS, int NW, typename InT, bool BOTH>
-__global__ __launch_bounds__(64 * NW) void scan_states_kernel(const ScanParams p) {
-  constexpr int N = NS * NW, TT = SCAN_CHUNK;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// Local states at every 8th token and behind the segment, the sums of d there, and (BOTH) the reverse part: tiles as in the
+// forward pass, dy C by the matrix units as d x B is.
+template <int SL, typename InT, bool BOTH>
+__global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p) {
+  constexpr int N = 16 * SL, K = TILE_TOK, O = TILE_OWN;
+  static_assert(K == 2 * SCAN_CHUNK, "two checkpoints to a tile");
+  const int lane = threadIdx.x & 63, sl = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int ntiles = p.G * p.tiles;
   const int slot = blockIdx.x / ntiles, tile = blockIdx.x - slot * ntiles;
   const SlotSpan sp = slot_span(p, slot);
   if (sp.n < 0) return;
-  const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + lane;
-  if (in_g >= p.Cg) return;
-  const int c = g * p.Cg + in_g;
-  float A[NS], h[NS], P[NS], R[NS];
+  const int g = tile / p.tiles, in_g = (tile - g * p.tiles) * SCAN_TILE + (lane & 31);
+  const bool on = in_g < p.Cg;
+  const int c = g * p.Cg + min(in_g, p.Cg - 1), n0 = sl * 16 + 4 * half;
+  float A[8], h[8], P[8], R[8];
+  load_states(p.A + (int64_t)c * N + n0, A);
 #pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    A[j] = p.A[(int64_t)c * N + wave * NS + j] * LOG2E;
+  for (int j = 0; j < 8; ++j) {
+    A[j] *= LOG2E;
     h[j] = R[j] = 0.f;
     P[j] = 1.f;
   }
   const float bias = p.bias ? p.bias[c] : 0.f;
   const int len = sp.len;
   const bool soft = p.softplus != 0, gate = BOTH && p.z != nullptr;
-  const InT* xp = static_cast<const InT*>(p.x) + sp.b * p.x_bs + sp.t0 * p.x_ts + c;
-  const InT* dp = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + sp.t0 * p.dt_ts + c;
-  const InT* zp = gate ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + sp.t0 * p.z_ts + c : xp;
-  const InT* yp = static_cast<const InT*>(p.dy) + (sp.b * p.T + sp.t0) * (int64_t)p.C + c;
-  const InT* Bp = static_cast<const InT*>(p.B) + sp.b * p.b_bs + sp.t0 * p.b_ts + g * N + wave * NS;
-  const InT* Cp = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts + g * N + wave * NS;
-  const int64_t x_ts = p.x_ts, dt_ts = p.dt_ts, z_ts = gate ? p.z_ts : p.x_ts, b_ts = p.b_ts, c_ts = p.c_ts, C = p.C;
-  float* ck = p.ck + ((int64_t)slot * (p.seg / TT) * C + c) * N + wave * NS;
-  float* ckd = p.ckd + (int64_t)slot * (p.seg / TT) * C + c;
-  float sumd = 0.f;
-  InT xn[TT], dn[TT], zn[TT], yn[TT];
-  auto fetch = [&](int n) {  // the next n tokens (TT of them but at the end)
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      xn[i] = dn[i] = zn[i] = yn[i] = InT(0);
-      if (n >= TT || i < n) {
-        xn[i] = *xp;
-        dn[i] = *dp;
-        xp += x_ts;
-        dp += dt_ts;
-        if constexpr (BOTH) {
-          zn[i] = *zp;
-          yn[i] = *yp;
-          zp += z_ts;
-          yp += C;
-        }
-      }
-    }
-  };
-  Row<InT, NS> Bt[2], Ct[2];
-  auto rows = [&](int to, bool more) {
-    Bt[to].load(Bp);
-    Bp += more ? b_ts : 0;
-    if constexpr (BOTH) {
-      Ct[to].load(Cp);
-      Cp += more ? c_ts : 0;
-    }
-  };
-  if (len > 0) {
-    fetch(len);
-    rows(0, len > 1);
+  Rows<InT> X, T, Z, B, Y, Cr;
+  X.init(p.x, sp.b * p.x_bs + sp.t0 * p.x_ts, p.x_ts, half, c);
+  T.init(p.dt, sp.b * p.dt_bs + sp.t0 * p.dt_ts, p.dt_ts, half, c);
+  B.init(p.B, sp.b * p.b_bs + sp.t0 * p.b_ts, p.b_ts, half, g * N + sl * 16 + (lane & 15));
+  if constexpr (BOTH) {
+    if (gate)
+      Z.init(p.z, sp.b * p.z_bs + sp.t0 * p.z_ts, p.z_ts, half, c);
+    else
+      Z = X;
+    Cr.init(p.Cm, sp.b * p.c_bs + sp.t0 * p.c_ts, p.c_ts, half, g * N + sl * 16 + (lane & 15));
+    Y.init(p.dy, (sp.b * p.T + sp.t0) * (int64_t)p.C, p.C, half, c);
   }
-  for (int t = 0; t < len; t += TT) {
-    if (t > 0) {  // (a segment begins at zero)
-#pragma unroll
-      for (int j = 0; j < NS; j += 4) *reinterpret_cast<f32x4*>(ck + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
-    }
-    if (wave == 0) *ckd = sumd;
-    ck += C * N;
-    ckd += C;
-    float xv[TT], dv[TT], gv[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      xv[i] = (float)xn[i];
-      const float raw = (float)dn[i] + bias, sf = softplus_f(raw);
-      dv[i] = soft ? sf : raw;
-      if (t + i >= len) dv[i] = 0.f;  // (past the end: a decay of one and nothing added; dy is zero there)
+  const int64_t cps = p.seg / SCAN_CHUNK;
+  float* ck = p.ck + ((int64_t)slot * cps * p.C + c) * N + n0;
+  float* ckd = p.ckd + (int64_t)slot * cps * p.C + c;
+  float sumd = 0.f;
+  uint32_t xn[O], dn[O], zn[O], yn[O], bn[O], cn[O];
+  auto fetch = [&](int left) {
+    if (left >= K) {
+      X.whole(xn);
+      T.whole(dn);
+      B.whole(bn);
       if constexpr (BOTH) {
-        const float zv = (float)zn[i], sg = zv * sigmoid_f(zv);
-        gv[i] = (float)yn[i] * (gate ? sg : 1.f);
+        Z.whole(zn);
+        Y.whole(yn);
+        Cr.whole(cn);
+      }
+      whole_tile();
+    } else {
+      X.part(xn, left);
+      T.part(dn, left);
+      B.part(bn, left);
+      if constexpr (BOTH) {
+        Z.part(zn, left);
+        Y.part(yn, left);
+        Cr.part(cn, left);
       }
     }
-    if (t + TT < len) fetch(len - t - TT);
+    X.at += K * X.ts;
+    T.at += K * T.ts;
+    B.at += K * B.ts;
+    if constexpr (BOTH) {
+      Z.at += K * Z.ts;
+      Y.at += K * Y.ts;
+      Cr.at += K * Cr.ts;
+    }
+  };
+  if (len > 0) fetch(len);
+  for (int t = 0; t < len; t += K) {
+    float dv[O], dx[O], gy[O], bo[O], co[O];
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      rows((i + 1) & 1, t + i + 2 < len);
-      __builtin_amdgcn_sched_barrier(0);
-      const float d = dv[i], dx = d * xv[i];
-      float a[NS];
-#pragma unroll
-      for (int j = 0; j < NS; ++j) a[j] = __builtin_amdgcn_exp2f(d * A[j]);
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        h[j] = fmaf(a[j], h[j], dx * Bt[i & 1][j]);
-        if constexpr (BOTH) {
-          P[j] *= a[j];
-          R[j] = fmaf(P[j], gv[i] * Ct[i & 1][j], R[j]);
-        }
+    for (int i = 0; i < O; ++i) {
+      const float raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw);
+      float own = soft ? sf : raw;
+      here(own);
+      // (tokens past the end: a decay of one, nothing in or out)
+      const bool inside = t + K <= len || t + 2 * i + half < len;
+      dv[i] = inside ? own : 0.f;
+      dx[i] = inside ? dv[i] * raw_value<InT>(xn[i]) : 0.f;
+      bo[i] = operand<InT>(bn[i], lane);
+      if constexpr (BOTH) {
+        const float zv = raw_value<InT>(zn[i]), sg = zv * sigmoid_f(zv);
+        float out = raw_value<InT>(yn[i]) * (gate ? sg : 1.f);
+        here(out);
+        gy[i] = inside ? out : 0.f;
+        co[i] = operand<InT>(cn[i], lane);
       }
-      sumd += d;
-      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (t + K < len) fetch(len - t - K);
+    f32x16 in = outer_pair(bo[0], dx[0]), out = BOTH ? outer_pair(co[0], gy[0]) : f32x16{};
+#pragma unroll
+    for (int i = 0; i < O; ++i) {
+      tile_step();
+      if (i % (O / 2) == 0 && (i == 0 || t + SCAN_CHUNK < len)) {
+        if (on && (t > 0 || i > 0)) store_states(ck, h);  // (a segment begins at zero)
+        float lo, hi;
+        both_halves(sumd, lo, hi);
+        if (on && sl == 0 && half == 0) *ckd = lo + hi;
+        ck += (int64_t)p.C * N;
+        ckd += p.C;
+      }
+      float d[2];
+      both_halves(dv[i], d[0], d[1]);
+      sumd += dv[i];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = __builtin_amdgcn_exp2f(d[k] * A[j]);
+          h[j] = fmaf(a, h[j], in[8 * k + j]);
+          if constexpr (BOTH) {
+            P[j] *= a;
+            R[j] = fmaf(P[j], out[8 * k + j], R[j]);
+          }
+        }
+      if (i + 1 < O) {
+        in = outer_pair(bo[i + 1], dx[i + 1]);
+        if constexpr (BOTH) out = outer_pair(co[i + 1], gy[i + 1]);
+      }
+      if constexpr (BOTH) here(R);
     }
   }
   if constexpr (BOTH) {
-    const int64_t at = ((int64_t)slot * p.C + c) * N + wave * NS;
-#pragma unroll
-    for (int j = 0; j < NS; j += 4) {
-      *reinterpret_cast<f32x4*>(p.part + at + j) = f32x4{h[j], h[j + 1], h[j + 2], h[j + 3]};
-      *reinterpret_cast<f32x4*>(p.rpart + at + j) = f32x4{R[j], R[j + 1], R[j + 2], R[j + 3]};
-    }
-    if (wave == 0) p.sumd[(int64_t)slot * p.C + c] = sumd;
+    float lo, hi;
+    both_halves(sumd, lo, hi);
+    if (!on) return;
+    const int64_t at = ((int64_t)slot * p.C + c) * N + n0;
+    store_states(p.part + at, h);
+    store_states(p.rpart + at, R);
+    if (sl == 0 && half == 0) p.sumd[(int64_t)slot * p.C + c] = lo + hi;
   }
 }
 
@@ -234,8 +256,9 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   const InT* db = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + (sp.t0 + last) * dt_ts;
   const InT* zb = GATE ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + (sp.t0 + last) * z_ts : nullptr;
   int64_t row = row0 + last, next = row;  // of the outputs, of dy
-  const uint32_t xo = (uint32_t)(prow * x_ts) + c, dto = (uint32_t)(prow * dt_ts) + c, zo = GATE ? (uint32_t)(prow * z_ts) + c : 0u;
-  const uint32_t oo = (uint32_t)(prow * C) + c, cko = (uint32_t)lc[0] * N + n0;
+  constexpr uint32_t E = sizeof(InT);
+  const uint32_t xo = (uint32_t)(prow * x_ts + c) * E, dto = (uint32_t)(prow * dt_ts + c) * E, zo = GATE ? (uint32_t)(prow * z_ts + c) * E : 0u;
+  const uint32_t oo = (uint32_t)(prow * C + c) * E, cko = ((uint32_t)lc[0] * N + n0) * 4;
   int64_t chunk = (int64_t)slot * cps + last / K;
   constexpr int BCN = 2 * K * N / 256;  // elements of B and C of a thread: B's first, then C's (a wave has one of them)
   static_assert(2 * K * N % 256 == 0 && K * N % 64 == 0, "whole waves");
@@ -244,7 +267,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   for (int i = 0; i < BCN; ++i) {
     const int e = (tid + i * 256) % (K * N);
     const bool isC = (wave * 64 + i * 256) / (K * N) == 1;
-    bco[i] = (uint32_t)(e / N * (isC ? p.c_ts : p.b_ts)) + e % N;
+    bco[i] = (uint32_t)(e / N * (isC ? p.c_ts : p.b_ts) + g * N + e % N) * E;
   }
   const bool soft = p.softplus != 0;
   float accD = 0.f, accb = 0.f;
@@ -256,15 +279,16 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
     if (t + K <= len) {
 #pragma unroll
       for (int i = 0; i < PP; ++i) {
-        xn[i] = xr[xo];
-        dn[i] = dr[dto];
-        if constexpr (GATE) zn[i] = zr[zo];
-        yn[i] = yr[oo];
+        xn[i] = *byte_at(xr, xo);
+        dn[i] = *byte_at(dr, dto);
+        if constexpr (GATE) zn[i] = *byte_at(zr, zo);
+        yn[i] = *byte_at(yr, oo);
         xr += ROWS * x_ts;
         dr += ROWS * dt_ts;
         if constexpr (GATE) zr += ROWS * z_ts;
         yr += ROWS * (int64_t)C;
       }
+      whole_tile();
     } else {
 #pragma unroll
       for (int i = 0; i < PP; ++i) {
@@ -284,7 +308,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       const bool isC = (wave * 64 + i * 256) / (K * N) == 1;
       const InT* from = isC ? static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + (sp.t0 + t) * p.c_ts : static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + t) * p.b_ts;
       bn[i] = InT(0);
-      if (t + K <= len || t + (tid + i * 256) % (K * N) / N < len) bn[i] = from[g * N + (uint64_t)bco[i]];
+      if (t + K <= len || t + (tid + i * 256) % (K * N) / N < len) bn[i] = *byte_at(from, bco[i]);
     }
     const float *ck = p.ck + chunk * C * N, *ckd = p.ckd + chunk * C;
 #pragma unroll
@@ -293,8 +317,8 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       hn[i][0] = hn[i][1] = 0.f;
       if (t > 0) {
         const uint32_t o = min(i, lim);
-        dsum[i] = ckd[(uint32_t)lc[0] + o];
-        const f32x2 v = *reinterpret_cast<const f32x2*>(ck + (cko + o * N));
+        dsum[i] = *byte_at(ckd, ((uint32_t)lc[0] + o) * 4);
+        const f32x2 v = *reinterpret_cast<const f32x2*>(byte_at(ck, cko + o * (4 * N)));
         hn[i][0] = v[0];
         hn[i][1] = v[1];
       }
@@ -303,7 +327,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   };
   // this workgroup's part of dB and dC: 2 N values to a token
   float* pbc = p.pBC + (((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0 + last) * p.G + g) * (2 * N);
-  const uint32_t pbo = (uint32_t)(tid / (2 * N)) * p.G * (2 * N) + tid % (2 * N);
+  const uint32_t pbo = ((uint32_t)(tid / (2 * N)) * p.G * (2 * N) + tid % (2 * N)) * 4;
   if (len > 0) fetch(last);
   for (int t = last; len > 0 && t >= 0; t -= K) {
     __syncthreads();  // (the chunk before has been written out)
@@ -414,11 +438,11 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       const float xv = s_own[0][i][tid], gv = s_dy[r][pc];
       const float draw = fmaf(u, xv, e * LN2) * s_own[1][i][tid];
       const int64_t base = (row + i * ROWS) * C;
-      (static_cast<InT*>(p.ddt) + base)[oo] = (InT)draw;
-      (static_cast<InT*>(p.dx) + base)[oo] = (InT)fmaf(u, s_d[r][pc], D * gv);
+      *byte_at(static_cast<InT*>(p.ddt) + base, oo) = (InT)draw;
+      *byte_at(static_cast<InT*>(p.dx) + base, oo) = (InT)fmaf(u, s_d[r][pc], D * gv);
       if constexpr (GATE) {
         const float zv = s_own[2][i][tid], sz = sigmoid_f(zv);
-        (static_cast<InT*>(p.dz) + base)[oo] = (InT)(s_own[3][i][tid] * fmaf(D, xv, yo) * (sz * fmaf(zv, 1.f - sz, 1.f)));
+        *byte_at(static_cast<InT*>(p.dz) + base, oo) = (InT)(s_own[3][i][tid] * fmaf(D, xv, yo) * (sz * fmaf(zv, 1.f - sz, 1.f)));
       }
       accD = fmaf(gv, xv, accD);
       accb += draw;
@@ -429,7 +453,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < Sh::CB; ++w) v += s_bc[w * SL + n / 16][r][(n % 16) / 2 * 4 + 2 * m + (n & 1)];
-      if (t + r < len) (pbc + i * (256 / (2 * N)) * (int64_t)p.G * (2 * N))[pbo] = v;
+      if (t + r < len) *byte_at(pbc + i * (256 / (2 * N)) * (int64_t)p.G * (2 * N), pbo) = v;
     }
     row -= K;
     pbc -= K * (int64_t)p.G * (2 * N);
@@ -500,18 +524,18 @@ __global__ __launch_bounds__(256) void scan_dbc_kernel(const ScanParams p) {
   static_cast<InT*>(m ? p.dC : p.dB)[row * N + n] = (InT)v;
 }
 
-template <int NS, int NW, typename InT>
+template <int SL, typename InT>
 static void launch_states(const ScanParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.slots * p.G * p.tiles)), block(64 * NW);
+  const dim3 grid((unsigned)((int64_t)p.slots * p.G * p.tiles)), block(64 * SL);
   if (p.part)
-    hipLaunchKernelGGL((scan_states_kernel<NS, NW, InT, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((scan_states_kernel<SL, InT, true>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((scan_states_kernel<NS, NW, InT, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((scan_states_kernel<SL, InT, false>), grid, block, 0, s, p);
 }
 template <int N, typename InT>
 static hipError_t launch_bwd_t(const ScanParams& p, hipStream_t s) {
   if (p.slots > 0 && p.nseq > 0) {
-    launch_states<16, N / 16, InT>(p, s);
+    launch_states<N / 16, InT>(p, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (p.part) {
