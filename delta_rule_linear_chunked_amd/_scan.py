@@ -13,7 +13,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _DT, _Opts, _check, _dense, _need_rows, load_library
-from ._decay import CACHE_FORMATS, _addr, _call, _is, _like, _require
+from ._decay import CACHE_FORMATS, _addr, _call, _like, _require
 
 CONV_ACTS = {None: 0, "none": 0, "silu": 1}  # dr_conv_act
 _NORM_OUT = {None: 0, "int8": 1, "e4m3": 2}  # dr_norm_out
@@ -59,15 +59,25 @@ def _space(lib, entry, dev, *args):
     return (torch.empty(n.value, dtype=torch.uint8, device=dev), n.value) if n.value else (None, 0)
 
 
-def _strides(t, name, shape, lead, dtype, dev):
-    """(token, batch) strides of an activation with ``lead`` leading dimensions (2: batch and token, 1: sequence)."""
-    if _is(t, shape, dtype, dev):
-        inner = 1
-        for n in shape[lead:]:
-            inner *= n
-        return (inner, inner * shape[1]) if lead == 2 else (0, inner)
-    s = _need_rows(t, name, shape, lead, dtype, dev)
-    return (s[1], s[0]) if lead == 2 else (0, s[0])
+# The short ways below are for the usual case, dense inner dimensions (these calls are made once per token and layer with little
+# GPU work behind them); anything else goes to the checks that say what is wrong.
+def _strides(t, name, shape, dtype, dev):
+    """(token, batch) strides of [B, T, C] or [B, T, G, n]."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == dev:
+        s = t.stride()
+        if s[-1] == 1 and (len(s) == 3 or s[2] == shape[3] or shape[2] == 1):
+            return (s[1] if shape[1] != 1 else 0), (s[0] if shape[0] != 1 else 0)
+    s = _need_rows(t, name, shape, 2, dtype, dev)
+    return s[1], s[0]
+
+
+def _strides1(t, name, shape, dtype, dev):
+    """(0, stride between sequences) of a step's [N, C] or [N, G, n]."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == dev:
+        s = t.stride()
+        if s[-1] == 1 and (len(s) == 2 or s[1] == shape[2] or shape[1] == 1):
+            return 0, (s[0] if shape[0] != 1 else 0)
+    return 0, _need_rows(t, name, shape, 1, dtype, dev)[0]
 
 
 def _type(x, name="x"):
@@ -77,7 +87,7 @@ def _type(x, name="x"):
 
 
 def _optional(t, name, shape, dtype, dev):
-    if t is not None:
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev):
         _require(t, name, shape, dtype, dev)
 
 
@@ -114,7 +124,7 @@ def _conv_inputs(x, weight, bias, activation, lead):
     dev, C, W = x.device, x.shape[-1], weight.shape[1]
     B, T = (x.shape[0], x.shape[1]) if lead == 2 else (x.shape[0], 1)
     d = _ConvDims(B, T, C, W, B, 0, 0, _type(x), CONV_ACTS[activation])
-    d.x_token_stride, d.x_batch_stride = _strides(x, "x", x.shape, lead, x.dtype, dev)
+    d.x_token_stride, d.x_batch_stride = (_strides if lead == 2 else _strides1)(x, "x", x.shape, x.dtype, dev)
     _require(weight, "weight", (C, W), torch.float32, dev)
     _optional(bias, "bias", (C,), torch.float32, dev)
     return d
@@ -251,10 +261,10 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead):
     bs, T = (shape[0], shape[1]) if lead == 2 else (shape[0], 1)
     if G == 0 or Ch % G != 0:
         raise ValueError(f"{Ch} channels are not a multiple of {G} groups")
-    bc = tuple(shape[:-1]) + (G, N)
-    d = _ScanDims(bs, T, Ch, G, N, bs, *_strides(x, "x", shape, lead, dtype, dev), *_strides(dt, "dt", shape, lead, dtype, dev),
-                  *_strides(B, "B", bc, lead, dtype, dev), *_strides(C, "C", bc, lead, dtype, dev),
-                  *((0, 0) if z is None else _strides(z, "z", shape, lead, dtype, dev)), _type(x), int(bool(softplus)))
+    bc = (bs, T, G, N) if lead == 2 else (bs, G, N)
+    st = _strides if lead == 2 else _strides1
+    d = _ScanDims(bs, T, Ch, G, N, bs, *st(x, "x", shape, dtype, dev), *st(dt, "dt", shape, dtype, dev), *st(B, "B", bc, dtype, dev),
+                  *st(C, "C", bc, dtype, dev), *((0, 0) if z is None else st(z, "z", shape, dtype, dev)), _type(x), 1 if softplus else 0)
     _require(A, "A", (Ch, N), torch.float32, dev)
     _optional(D, "D", (Ch,), torch.float32, dev)
     _optional(dt_bias, "dt_bias", (Ch,), torch.float32, dev)
@@ -394,7 +404,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, S0=None, cu_seq
 # ------------------------------------------------------------------------------------------------ norm
 def _norm_rows(t, name, shape, dtype, dev):
     """Element stride between the rows of a tensor [..., C]: its channels dense, its other dimensions evenly spaced."""
-    if _is(t, shape, dtype, dev):
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
         return shape[-1]
     _need_rows(t, name, shape, len(shape) - 1, dtype, dev)
     if t.numel() == 0:

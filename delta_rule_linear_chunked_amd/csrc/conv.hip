@@ -112,12 +112,20 @@ __device__ __forceinline__ void conv_tail(const ConvParams& p, int n, int c) {
     *reinterpret_cast<V*>(static_cast<InT*>(p.state_T) + (s * (W - 1) + j) * p.C + c) = v[j];
 }
 
+// Neighbouring channel blocks share the cache lines of rows that are not aligned, neighbouring runs the inputs between them: consecutive
+// logical blocks go to one XCD (workgroups are dealt over eight). Of `total` blocks; past them: nothing to do.
+__device__ __forceinline__ int logical_block(int total) {
+  const int per = (total + 7) / 8;
+  return (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+}
+
 template <typename InT, int VEC, int W>
 __global__ __launch_bounds__(64 * CONV_WAVES) void conv_fwd_kernel(const ConvParams p) {
   using V = typename Vec<InT, VEC>::type;
   constexpr int AHEAD = 8;  // tokens whose loads are issued together
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blk = p.block0 + blockIdx.x, cb = blk % p.cblocks;
+  const int at = logical_block(p.nblocks), blk = p.block0 + at, cb = blk % p.cblocks;
+  if (at >= p.nblocks) return;
   const int c = (cb * 64 + lane) * VEC;
   if (blk >= p.nmain) {
     const int n = (blk - p.nmain) / p.cblocks * CONV_WAVES + wave;
@@ -137,10 +145,16 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_fwd_kernel(const ConvPar
     if (q.n >= 0) {
       float e[W][VEC];
       k.window(x, q.a, q.start, state_row(p.sidx, p.nslots, q.n), e);
+      V next[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) next[i] = k.load(x, min(q.a + i, q.b - 1));
       for (int a = q.a; a < q.b; a += AHEAD) {
         V raw[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) raw[i] = k.load(x, min(a + i, q.b - 1));
+        for (int i = 0; i < AHEAD; ++i) raw[i] = next[i];
+        if (a + AHEAD < q.b)
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) next[i] = k.load(x, min(a + AHEAD + i, q.b - 1));
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
           if (a + i < q.b) {
@@ -160,35 +174,50 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_fwd_kernel(const ConvPar
   }
 }
 
+// A wave takes `run` sequences one after the other on one block of channels (the weights are twice a token's inputs and outputs),
+// the next one's inputs loaded ahead.
 template <typename InT, int VEC, int W>
 __global__ __launch_bounds__(256) void conv_step_kernel(const ConvParams p) {
   using V = typename Vec<InT, VEC>::type;
   const int cb = blockIdx.x % p.cblocks;
-  const int n = blockIdx.x / p.cblocks * CONV_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = (cb * 64 + (threadIdx.x & 63)) * VEC;
-  if (n >= p.nseq || c >= p.C) return;
-  const int64_t s = state_row(p.sidx, p.nslots, n);
-  V* y = reinterpret_cast<V*>(static_cast<InT*>(p.y) + (int64_t)n * p.C + c);
-  if (s < 0) {  // no stored state
-    *y = V{};
-    return;
-  }
-  V* st = reinterpret_cast<V*>(static_cast<InT*>(p.state_T) + s * (W - 1) * p.C + c);
-  V r[W];
+  const int n0 = (blockIdx.x / p.cblocks * CONV_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * p.run;
+  const int c = (cb * 64 + (threadIdx.x & 63)) * VEC, n1 = min(n0 + p.run, p.nseq);
+  if (n0 >= n1 || c >= p.C) return;
+  V next[W];
+  int64_t snext;
+  auto fetch = [&](int n) {
+    snext = state_row(p.sidx, p.nslots, n);
+    if (snext < 0) return;
+    const InT* st = static_cast<const InT*>(p.state_T) + snext * (W - 1) * p.C + c;
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) r[j] = *reinterpret_cast<const V*>(reinterpret_cast<const InT*>(st) + (int64_t)j * p.C);
-  r[W - 1] = *reinterpret_cast<const V*>(static_cast<const InT*>(p.x) + n * p.x_bs + c);
+    for (int j = 0; j < W - 1; ++j) next[j] = *reinterpret_cast<const V*>(st + (int64_t)j * p.C);
+    next[W - 1] = *reinterpret_cast<const V*>(static_cast<const InT*>(p.x) + n * p.x_bs + c);
+  };
+  fetch(n0);
   const Conv<InT, VEC, W> k(p, c);
-  float e[W][VEC], u[VEC];
+  for (int n = n0; n < n1; ++n) {
+    V r[W];
+    const int64_t s = snext;
 #pragma unroll
-  for (int j = 0; j < W; ++j) unpack<VEC, InT>(r[j], e[j]);
-  k.dot(e, u);
-  if (p.silu)
+    for (int j = 0; j < W; ++j) r[j] = next[j];
+    if (n + 1 < n1) fetch(n + 1);
+    V* y = reinterpret_cast<V*>(static_cast<InT*>(p.y) + (int64_t)n * p.C + c);
+    if (s < 0) {  // no stored state
+      *y = V{};
+      continue;
+    }
+    float e[W][VEC], u[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
+    for (int j = 0; j < W; ++j) unpack<VEC, InT>(r[j], e[j]);
+    k.dot(e, u);
+    if (p.silu)
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<V*>(reinterpret_cast<InT*>(st) + (int64_t)j * p.C) = r[j + 1];
-  *y = pack<VEC, InT>(u);
+      for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
+    InT* st = static_cast<InT*>(p.state_T) + s * (W - 1) * p.C + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<V*>(st + (int64_t)j * p.C) = r[j + 1];
+    *y = pack<VEC, InT>(u);
+  }
 }
 
 // Gradient of a token's sum before the activation: dy, with silu times sigmoid(u) (1 + u sigmoid(-u)).
@@ -210,7 +239,8 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvPar
   constexpr int AHEAD = 8;
   __shared__ float s_part[CONV_WAVES - 1][W + 1][64 * VEC];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blk = blockIdx.x, cb = blk % p.cblocks;
+  const int blk = logical_block(p.nblocks), cb = blk % p.cblocks;
+  if (blk >= p.nblocks) return;
   const int c = (cb * 64 + lane) * VEC;
   if (blk >= p.nmain) {  // the gradient of sequence n's starting state
     const int n = (blk - p.nmain) / p.cblocks * CONV_WAVES + wave;
@@ -281,15 +311,25 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvPar
 #pragma unroll
           for (int v = 0; v < VEC; ++v) du[j][v] = 0.f;
         const int stop = q.b + W - 1;  // (tokens past the sequence's end have no gradient)
+        V xn[AHEAD], gn[AHEAD];
+        auto fetch = [&](int a) {
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int at_t = min(a + i, q.end - 1);
+            xn[i] = k.load(x, at_t);
+            gn[i] = V{};
+            if (k.in) gn[i] = *reinterpret_cast<const V*>(dy + (int64_t)at_t * p.C);
+          }
+        };
+        fetch(q.a);
         for (int a = q.a; a < stop; a += AHEAD) {
           V xr[AHEAD], gr[AHEAD];
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i) {
-            const int at_t = min(a + i, q.end - 1);
-            xr[i] = k.load(x, at_t);
-            gr[i] = V{};
-            if (k.in) gr[i] = *reinterpret_cast<const V*>(dy + (int64_t)at_t * p.C);
+            xr[i] = xn[i];
+            gr[i] = gn[i];
           }
+          if (a + AHEAD < stop) fetch(a + AHEAD);
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i) {
             const int tt = a + i;
@@ -376,6 +416,7 @@ __global__ __launch_bounds__(1024) void conv_dw_kernel(const ConvParams p, int p
 }
 
 static int64_t run_blocks(const ConvParams& p) { return ((int64_t)p.nbatch * p.runs + CONV_WAVES - 1) / CONV_WAVES; }
+static dim3 eights(int64_t n) { return dim3((unsigned)((n + 7) / 8 * 8)); }
 static int64_t seq_blocks(const ConvParams& p) { return ((int64_t)p.nseq + CONV_WAVES - 1) / CONV_WAVES; }
 
 template <typename InT, int VEC, int W>
@@ -385,18 +426,19 @@ static hipError_t launch_fwd_t(ConvParams p, hipStream_t s) {
   p.block0 = 0;
   // the states' own launch where the tokens' still read the states that it writes
   const bool apart = tail > 0 && p.state == p.state_T;
-  const int64_t first = apart ? main : main + tail;
-  if (first > 0)
-    hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), dim3((unsigned)first), dim3(64 * CONV_WAVES), 0, s, p);
+  p.nblocks = (int32_t)(apart ? main : main + tail);
+  if (p.nblocks > 0) hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
   if (apart) {
     p.block0 = p.nmain;
-    hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), dim3((unsigned)tail), dim3(64 * CONV_WAVES), 0, s, p);
+    p.nblocks = (int32_t)tail;
+    hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
   }
   return hipGetLastError();
 }
 template <typename InT, int VEC, int W>
 static hipError_t launch_step_t(const ConvParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((conv_step_kernel<InT, VEC, W>), dim3((unsigned)(seq_blocks(p) * p.cblocks)), dim3(256), 0, s, p);
+  const int64_t waves = ((int64_t)p.nseq + p.run - 1) / p.run;
+  hipLaunchKernelGGL((conv_step_kernel<InT, VEC, W>), dim3((unsigned)((waves + CONV_WAVES - 1) / CONV_WAVES * p.cblocks)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 template <typename InT, int VEC, int W>
@@ -404,8 +446,8 @@ static hipError_t launch_bwd_t(ConvParams p, hipStream_t s) {
   const int64_t main = run_blocks(p) * p.cblocks, tail = p.dstate ? seq_blocks(p) * p.cblocks : 0;
   p.nmain = (int32_t)main;
   p.block0 = 0;
-  if (main + tail > 0)
-    hipLaunchKernelGGL((conv_bwd_kernel<InT, VEC, W>), dim3((unsigned)(main + tail)), dim3(64 * CONV_WAVES), 0, s, p);
+  p.nblocks = (int32_t)(main + tail);
+  if (p.nblocks > 0) hipLaunchKernelGGL((conv_bwd_kernel<InT, VEC, W>), eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((conv_dw_kernel<W>), dim3((unsigned)(((W + 1) * (int64_t)p.C + 63) / 64)), dim3(1024), 0, s, p, (int)run_blocks(p));

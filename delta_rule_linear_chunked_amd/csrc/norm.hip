@@ -237,19 +237,19 @@ __global__ __launch_bounds__(NormShape<WAVES>::NT) void norm_bwd_kernel(const No
   }
 }
 
-// out[c] = sum over the rows of part [rows, C]: 64 channels x 16 row groups a workgroup.
+// out[c] = sum over the rows of part [rows, C]: 16 channels x 64 row groups a workgroup.
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const NormParams p) {
-  __shared__ float s[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
+  __shared__ float s[64][16];
+  const int i = threadIdx.x & 15, c = blockIdx.x * 16 + i, g = threadIdx.x >> 4;
   float v = 0.f;
   if (c < p.C)
-    for (int r = g; r < p.nwg; r += 16) v += p.part[(int64_t)r * p.C + c];
-  s[g][threadIdx.x & 63] = v;
+    for (int r = g; r < p.nwg; r += 64) v += p.part[(int64_t)r * p.C + c];
+  s[g][i] = v;
   __syncthreads();
   if (g == 0 && c < p.C) {
     float a = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) a += s[k][threadIdx.x];
+    for (int k = 0; k < 64; ++k) a += s[k][i];
     p.dw[c] = a;
   }
 }
@@ -299,7 +299,7 @@ hipError_t launch_norm_bwd(const NormParams& p, bool bf16, bool vec, hipStream_t
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((p.C + 63) / 64)), dim3(1024), 0, s, p);
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((p.C + 15) / 16)), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 

@@ -90,10 +90,10 @@ struct ConvParams {
   int64_t T, x_ts, x_bs;
   int32_t C, nbatch, nseq;
   int32_t silu;
-  int32_t run;             // tokens of a wave
+  int32_t run;             // tokens of a wave; step: sequences
   int32_t cblocks;         // channel blocks of 64 vectors
   int32_t runs;            // runs of one batch row
-  int32_t block0, nmain;   // first logical block of this launch; blocks below nmain walk tokens, the others states
+  int32_t block0, nblocks, nmain;  // logical blocks of this launch: the first, their number; those below nmain walk tokens, the others states
   // backward
   const void* dy;
   const void* dstate_T;    // may be null

@@ -84,6 +84,7 @@ int64_t env_int(const char* name) {
   const char* e = getenv(name);
   return e ? atoll(e) : 0;
 }
+int64_t env_or(const char* name, int64_t d) { const int64_t v = env_int(name); return v ? v : d; }
 template <class P>
 void set_opts(P& p, const dr_opts* o) {
   if (o == nullptr) return;
@@ -130,14 +131,14 @@ dr::ConvParams conv_params(const dr_conv_dims* d, int64_t vec, bool backward) {
   // tokens of a wave: as many as still leave 16 waves to a CU, so that the inputs read twice stay few
   const int64_t most = backward ? 64 : 32;
   int64_t run = 8;
-  while (run < most && d->batch * ceil_div(d->seqlen, 2 * run) * p.cblocks >= 4096) run *= 2;
+  while (run < most && d->batch * ceil_div(d->seqlen, 2 * run) * p.cblocks >= env_or("DR_TUNE_RUN", 4096)) run *= 2;
   p.run = (int32_t)run;
   p.runs = (int32_t)ceil_div(d->seqlen, run);
   return p;
 }
 int64_t conv_blocks(const dr::ConvParams& p) { return ceil_div((int64_t)p.nbatch * p.runs, dr::CONV_WAVES); }
 bool conv_fits(const dr::ConvParams& p) {
-  return dr::launch_fits((conv_blocks(p) + ceil_div(p.nseq, dr::CONV_WAVES)) * p.cblocks, 64 * dr::CONV_WAVES);
+  return dr::launch_fits((conv_blocks(p) + ceil_div(p.nseq, dr::CONV_WAVES)) * p.cblocks + 8, 64 * dr::CONV_WAVES);
 }
 // (a run may be as short as 8 tokens and a workgroup's share of the channels as narrow as one vector block)
 int64_t conv_space(const dr_conv_dims* d) {
@@ -363,6 +364,8 @@ int dr_conv_step(const void* x, const float* weight, const float* bias, void* st
   const bool bf16 = dims->in_dtype == DR_BF16, vec = conv_vectors(dims, {x, state, y});
   dr::ConvParams p = conv_params(dims, dr::conv_vec(bf16, vec, false), false);
   if (!dr::launch_fits(ceil_div(p.nseq, dr::CONV_WAVES) * p.cblocks, 256)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
+  p.run = 1;
+  while (p.run < 8 && (int64_t)p.nseq * p.cblocks >= 2 * env_or("DR_TUNE_STEP", 2048) * p.run) p.run *= 2;
   set_opts(p, opts);
   p.x = x; p.w = weight; p.bias = bias; p.state_T = state; p.y = y;
   return done(dr::launch_conv_step(p, (int)dims->width, bf16, vec, stream), "convolution step");
