@@ -38,36 +38,44 @@ template <typename InT, int VEC, int W>
 struct Conv {
   using V = typename Vec<InT, VEC>::type;
   const ConvParams& p;
-  int c;
+  int c;          // the lane's first channel; lanes past the last channels have those again and store nothing
   bool in;
+  uint32_t off;   // its bytes
   float w[W][VEC], bias[VEC];
-  __device__ __forceinline__ Conv(const ConvParams& p_, int c_) : p(p_), c(c_), in(c_ < p_.C) {
+  __device__ __forceinline__ Conv(const ConvParams& p_, int c_) : p(p_), c(min(c_, p_.C - VEC)), in(c_ < p_.C), off((uint32_t)c * sizeof(InT)) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      bias[v] = in && p.bias ? p.bias[c + v] : 0.f;
+      bias[v] = p.bias ? p.bias[c + v] : 0.f;
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][v] = in ? p.w[(int64_t)(c + v) * W + j] : 0.f;
+      for (int j = 0; j < W; ++j) w[j][v] = p.w[(int64_t)(c + v) * W + j];
     }
   }
-  // x of token t of batch row `row` (in range)
-  __device__ __forceinline__ V load(const InT* x, int64_t t) const {
-    V r = V{};
-    if (in) r = *reinterpret_cast<const V*>(x + t * p.x_ts);
-    return r;
+  // the lane's channels of a row (uniform)
+  __device__ __forceinline__ V load(const void* rows, int64_t row, int64_t stride) const {
+    return *reinterpret_cast<const V*>(byte_at(static_cast<const InT*>(rows) + row * stride, off));
   }
-  // input number k (0: the oldest) of the state of sequence n
+  __device__ __forceinline__ void store(void* rows, int64_t row, int64_t stride, const V& v) const {
+    if (in) *reinterpret_cast<V*>(byte_at(static_cast<InT*>(rows) + row * stride, off)) = v;
+  }
+  // a row of an output that no cache will hold until it is read (whole lines: stores of single channels got slower that way)
+  template <bool STREAM>
+  __device__ __forceinline__ void put(void* rows, int64_t row, int64_t stride, const V& v) const {
+    if constexpr (STREAM) {
+      if (in) __builtin_nontemporal_store(v, reinterpret_cast<V*>(byte_at(static_cast<InT*>(rows) + row * stride, off)));
+    } else {
+      store(rows, row, stride, v);
+    }
+  }
+  // input number k (0: the oldest) of row `srow` of the states
   __device__ __forceinline__ V old(int64_t srow, int k) const {
-    V r = V{};
-    if (in && p.state && srow >= 0)
-      r = *reinterpret_cast<const V*>(static_cast<const InT*>(p.state) + (srow * (W - 1) + k) * p.C + c);
-    return r;
+    return p.state && srow >= 0 ? load(p.state, srow * (W - 1) + k, p.C) : V{};
   }
   // the W - 1 inputs in front of token a of a sequence that starts at `start`
   __device__ __forceinline__ void window(const InT* x, int a, int start, int64_t srow, float (&e)[W][VEC]) const {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       const int t = a - (W - 1) + j;
-      unpack<VEC, InT>(t >= start ? load(x, t) : old(srow, t - start + W - 1), e[j]);
+      unpack<VEC, InT>(t >= start ? load(x, t, p.x_ts) : old(srow, t - start + W - 1), e[j]);
     }
   }
   __device__ __forceinline__ void dot(const float (&e)[W][VEC], float (&u)[VEC]) const {
@@ -99,17 +107,16 @@ __device__ __forceinline__ void conv_tail(const ConvParams& p, int n, int c) {
     row = 0;
   }
   const int64_t s = state_row(p.sidx, p.nslots, n);
-  const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
+  const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs;
   V v[W - 1];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int t = end - (W - 1) + j;
-    v[j] = t >= start ? k.load(x, t) : k.old(s, t - start + W - 1);
+    v[j] = t >= start ? k.load(x, t, p.x_ts) : k.old(s, t - start + W - 1);
   }
-  if (s < 0 || !k.in) return;
+  if (s < 0) return;
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    *reinterpret_cast<V*>(static_cast<InT*>(p.state_T) + (s * (W - 1) + j) * p.C + c) = v[j];
+  for (int j = 0; j < W - 1; ++j) k.store(p.state_T, s * (W - 1) + j, p.C, v[j]);
 }
 
 // Neighbouring channel blocks share the cache lines of rows that are not aligned, neighbouring runs the inputs between them: consecutive
@@ -119,10 +126,10 @@ __device__ __forceinline__ int logical_block(int total) {
   return (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
 }
 
-template <typename InT, int VEC, int W>
+template <typename InT, int VEC, int W, bool SILU, bool STREAM>
 __global__ __launch_bounds__(64 * CONV_WAVES) void conv_fwd_kernel(const ConvParams p) {
   using V = typename Vec<InT, VEC>::type;
-  constexpr int AHEAD = 8;  // tokens whose loads are issued together
+  constexpr int AHEAD = 8;  // tokens whose loads are issued together, a batch in front of their use
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int at = logical_block(p.nblocks), blk = p.block0 + at, cb = blk % p.cblocks;
   if (at >= p.nblocks) return;
@@ -138,35 +145,40 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_fwd_kernel(const ConvPar
   const int t0 = (rid - row * p.runs) * p.run;
   const int t1 = (int)(p.T - t0 < p.run ? p.T : t0 + p.run);
   const Conv<InT, VEC, W> k(p, c);
-  const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
-  InT* y = static_cast<InT*>(p.y) + (int64_t)row * p.T * p.C + c;
+  const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs;
+  InT* y = static_cast<InT*>(p.y) + (int64_t)row * p.T * p.C;
   for (int t = t0; t < t1;) {
     const RunPiece q = piece_at(p, row, t, t1);
     if (q.n >= 0) {
       float e[W][VEC];
-      k.window(x, q.a, q.start, state_row(p.sidx, p.nslots, q.n), e);
-      V next[AHEAD];
+      V next[AHEAD], raw[AHEAD];
+      auto fetch = [&](int a) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) next[i] = k.load(x, min(q.a + i, q.b - 1));
+        for (int i = 0; i < AHEAD; ++i) next[i] = k.load(x, min(a + i, q.b - 1), p.x_ts);
+      };
+      auto token = [&](int at_t, int i) {
+        unpack<VEC, InT>(raw[i], e[W - 1]);
+        float u[VEC];
+        k.dot(e, u);
+        if constexpr (SILU)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
+        k.template put<STREAM>(y, at_t, p.C, pack<VEC, InT>(u));
+        k.slide(e);
+      };
+      fetch(q.a);
+      k.window(x, q.a, q.start, state_row(p.sidx, p.nslots, q.n), e);
       for (int a = q.a; a < q.b; a += AHEAD) {
-        V raw[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) raw[i] = next[i];
-        if (a + AHEAD < q.b)
+        if (a + AHEAD < q.b) fetch(a + AHEAD);
+        if (a + AHEAD <= q.b) {
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) next[i] = k.load(x, min(a + AHEAD + i, q.b - 1));
+          for (int i = 0; i < AHEAD; ++i) token(a + i, i);
+        } else {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          if (a + i < q.b) {
-            unpack<VEC, InT>(raw[i], e[W - 1]);
-            float u[VEC];
-            k.dot(e, u);
-            if (p.silu)
-#pragma unroll
-              for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
-            if (k.in) *reinterpret_cast<V*>(y + (int64_t)(a + i) * p.C) = pack<VEC, InT>(u);
-            k.slide(e);
-          }
+          for (int i = 0; i < AHEAD; ++i)
+            if (a + i < q.b) token(a + i, i);
         }
       }
     }
@@ -183,27 +195,25 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const ConvParams p) {
   const int n0 = (blockIdx.x / p.cblocks * CONV_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * p.run;
   const int c = (cb * 64 + (threadIdx.x & 63)) * VEC, n1 = min(n0 + p.run, p.nseq);
   if (n0 >= n1 || c >= p.C) return;
+  const Conv<InT, VEC, W> k(p, c);
   V next[W];
   int64_t snext;
   auto fetch = [&](int n) {
     snext = state_row(p.sidx, p.nslots, n);
     if (snext < 0) return;
-    const InT* st = static_cast<const InT*>(p.state_T) + snext * (W - 1) * p.C + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) next[j] = *reinterpret_cast<const V*>(st + (int64_t)j * p.C);
-    next[W - 1] = *reinterpret_cast<const V*>(static_cast<const InT*>(p.x) + n * p.x_bs + c);
+    for (int j = 0; j < W - 1; ++j) next[j] = k.load(p.state_T, snext * (W - 1) + j, p.C);
+    next[W - 1] = k.load(p.x, n, p.x_bs);
   };
   fetch(n0);
-  const Conv<InT, VEC, W> k(p, c);
   for (int n = n0; n < n1; ++n) {
     V r[W];
     const int64_t s = snext;
 #pragma unroll
     for (int j = 0; j < W; ++j) r[j] = next[j];
     if (n + 1 < n1) fetch(n + 1);
-    V* y = reinterpret_cast<V*>(static_cast<InT*>(p.y) + (int64_t)n * p.C + c);
     if (s < 0) {  // no stored state
-      *y = V{};
+      k.store(p.y, n, p.C, V{});
       continue;
     }
     float e[W][VEC], u[VEC];
@@ -213,30 +223,32 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const ConvParams p) {
     if (p.silu)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
-    InT* st = static_cast<InT*>(p.state_T) + s * (W - 1) * p.C + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<V*>(st + (int64_t)j * p.C) = r[j + 1];
-    *y = pack<VEC, InT>(u);
+    for (int j = 0; j < W - 1; ++j) k.store(p.state_T, s * (W - 1) + j, p.C, r[j + 1]);
+    k.store(p.y, n, p.C, pack<VEC, InT>(u));
   }
 }
 
 // Gradient of a token's sum before the activation: dy, with silu times sigmoid(u) (1 + u sigmoid(-u)).
-template <int VEC>
-__device__ __forceinline__ void conv_du(const float (&u)[VEC], const float (&dy)[VEC], int silu, float (&du)[VEC]) {
+template <int VEC, bool SILU>
+__device__ __forceinline__ void conv_du(const float (&u)[VEC], const float (&dy)[VEC], float (&du)[VEC]) {
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    const float sg = sigmoid_f(u[v]);
-    du[v] = silu ? dy[v] * (sg * fmaf(u[v], 1.f - sg, 1.f)) : dy[v];
+    du[v] = dy[v];
+    if constexpr (SILU) {
+      const float sg = sigmoid_f(u[v]);
+      du[v] *= sg * fmaf(u[v], 1.f - sg, 1.f);
+    }
   }
 }
 
 // An input reaches the outputs of its own and the next W - 1 tokens of its sequence: the gradients du of W consecutive
 // tokens slide through registers behind the inputs, and token t completes the gradient of input t - W + 1. The
 // gradients of the weights stay in registers over the run; a workgroup adds its four runs'.
-template <typename InT, int VEC, int W>
+template <typename InT, int VEC, int W, bool SILU, bool STREAM>
 __global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvParams p) {
   using V = typename Vec<InT, VEC>::type;
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 4;
   __shared__ float s_part[CONV_WAVES - 1][W + 1][64 * VEC];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blk = logical_block(p.nblocks), cb = blk % p.cblocks;
@@ -252,8 +264,8 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvPar
       end = min(max(p.cu[n + 1], start), (int)p.T);
       row = 0;
     }
-    const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
-    const InT* dy = static_cast<const InT*>(p.dy) + (int64_t)row * p.T * p.C + c;
+    const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs;
+    const InT* dy = static_cast<const InT*>(p.dy) + (int64_t)row * p.T * p.C;
     float e[W][VEC], ds[W - 1][VEC];
     k.window(x, start, start, n, e);
 #pragma unroll
@@ -261,29 +273,24 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvPar
 #pragma unroll
       for (int v = 0; v < VEC; ++v) ds[j][v] = 0.f;
       const int L = end - start;
-      if (j >= L && p.dstate_T && k.in)
-        unpack<VEC, InT>(*reinterpret_cast<const V*>(static_cast<const InT*>(p.dstate_T) + ((int64_t)n * (W - 1) + j - L) * p.C + c), ds[j]);
+      if (j >= L && p.dstate_T) unpack<VEC, InT>(k.load(p.dstate_T, (int64_t)n * (W - 1) + j - L, p.C), ds[j]);
     }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i)
       if (start + i < end) {
         float u[VEC], g[VEC], du[VEC];
-        unpack<VEC, InT>(k.load(x, start + i), e[W - 1]);
+        unpack<VEC, InT>(k.load(x, start + i, p.x_ts), e[W - 1]);
         k.dot(e, u);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) g[v] = 0.f;
-        if (k.in) unpack<VEC, InT>(*reinterpret_cast<const V*>(dy + (int64_t)(start + i) * p.C), g);
-        conv_du<VEC>(u, g, p.silu, du);
+        unpack<VEC, InT>(k.load(dy, start + i, p.C), g);
+        conv_du<VEC, SILU>(u, g, du);
 #pragma unroll
         for (int j = i; j < W - 1; ++j)
 #pragma unroll
           for (int v = 0; v < VEC; ++v) ds[j][v] = fmaf(k.w[j - i][v], du[v], ds[j][v]);
         k.slide(e);
       }
-    if (k.in)
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        *reinterpret_cast<V*>(static_cast<InT*>(p.dstate) + ((int64_t)n * (W - 1) + j) * p.C + c) = pack<VEC, InT>(ds[j]);
+    for (int j = 0; j < W - 1; ++j) k.store(p.dstate, (int64_t)n * (W - 1) + j, p.C, pack<VEC, InT>(ds[j]));
     return;
   }
   const Conv<InT, VEC, W> k(p, c);
@@ -297,77 +304,79 @@ __global__ __launch_bounds__(64 * CONV_WAVES) void conv_bwd_kernel(const ConvPar
   if (row < p.nbatch) {
     const int t0 = (rid - row * p.runs) * p.run;
     const int t1 = (int)(p.T - t0 < p.run ? p.T : t0 + p.run);
-    const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs + c;
-    const int64_t at = (int64_t)row * p.T * p.C + c;
-    const InT* dy = static_cast<const InT*>(p.dy) + at;
-    InT* dx = static_cast<InT*>(p.dx) + at;
+    const InT* x = static_cast<const InT*>(p.x) + row * p.x_bs;
+    const InT* dy = static_cast<const InT*>(p.dy) + (int64_t)row * p.T * p.C;
+    InT* dx = static_cast<InT*>(p.dx) + (int64_t)row * p.T * p.C;
     for (int t = t0; t < t1;) {
       const RunPiece q = piece_at(p, row, t, t1);
       if (q.n >= 0) {
         float e[W][VEC], du[W][VEC];  // du[j]: of token t - W + 1 + j
+        V xn[AHEAD], gn[AHEAD], xr[AHEAD], gr[AHEAD];
+        auto fetch = [&](int a) {
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int at_t = min(a + i, q.end - 1);
+            xn[i] = k.load(x, at_t, p.x_ts);
+            gn[i] = k.load(dy, at_t, p.C);
+          }
+        };
+        // token tt, in the run and the sequence (USED), behind the run (its weights' gradients are another's), or behind the
+        // sequence (no gradient); then the gradient of input tt - W + 1, which is complete
+        auto token = [&](int tt, int i, auto used) {
+          constexpr bool USED = decltype(used)::value;
+          k.slide(du);
+          if (USED || tt < q.end) {
+            float u[VEC], g[VEC];
+            unpack<VEC, InT>(xr[i], e[W - 1]);
+            unpack<VEC, InT>(gr[i], g);
+            k.dot(e, u);
+            conv_du<VEC, SILU>(u, g, du[W - 1]);
+            if (USED || tt < q.b)
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][v] = fmaf(du[W - 1][v], e[j][v], dw[j][v]);
+                dw[W][v] += du[W - 1][v];
+              }
+            k.slide(e);
+          } else {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) du[W - 1][v] = 0.f;
+          }
+          const int i0 = tt - (W - 1);
+          if (i0 < q.a) return;
+          float g[VEC];
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) g[v] = 0.f;
+          if (i0 >= q.end - (W - 1) && p.dstate_T)
+            unpack<VEC, InT>(k.load(p.dstate_T, (int64_t)q.n * (W - 1) + i0 - (q.end - (W - 1)), p.C), g);
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) g[v] = fmaf(k.w[W - 1 - j][v], du[j][v], g[v]);
+          k.template put<STREAM>(dx, i0, p.C, pack<VEC, InT>(g));
+        };
+        fetch(q.a);
         k.window(x, q.a, q.start, q.n, e);
 #pragma unroll
         for (int j = 0; j < W; ++j)
 #pragma unroll
           for (int v = 0; v < VEC; ++v) du[j][v] = 0.f;
-        const int stop = q.b + W - 1;  // (tokens past the sequence's end have no gradient)
-        V xn[AHEAD], gn[AHEAD];
-        auto fetch = [&](int a) {
-#pragma unroll
-          for (int i = 0; i < AHEAD; ++i) {
-            const int at_t = min(a + i, q.end - 1);
-            xn[i] = k.load(x, at_t);
-            gn[i] = V{};
-            if (k.in) gn[i] = *reinterpret_cast<const V*>(dy + (int64_t)at_t * p.C);
-          }
-        };
-        fetch(q.a);
+        const int stop = q.b + W - 1;
         for (int a = q.a; a < stop; a += AHEAD) {
-          V xr[AHEAD], gr[AHEAD];
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i) {
             xr[i] = xn[i];
             gr[i] = gn[i];
           }
           if (a + AHEAD < stop) fetch(a + AHEAD);
+          if (a + AHEAD <= q.b) {
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) {
-            const int tt = a + i;
-            if (tt < stop) {
-              k.slide(du);
-              if (tt < q.end) {
-                float u[VEC], g[VEC];
-                unpack<VEC, InT>(xr[i], e[W - 1]);
-                unpack<VEC, InT>(gr[i], g);
-                k.dot(e, u);
-                conv_du<VEC>(u, g, p.silu, du[W - 1]);
-                if (tt < q.b)
+            for (int i = 0; i < AHEAD; ++i) token(a + i, i, std::true_type{});
+          } else {
 #pragma unroll
-                  for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][v] = fmaf(du[W - 1][v], e[j][v], dw[j][v]);
-                    dw[W][v] += du[W - 1][v];
-                  }
-                k.slide(e);
-              } else {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) du[W - 1][v] = 0.f;
-              }
-              const int i0 = tt - (W - 1);  // this input's gradient is complete
-              if (i0 >= q.a) {
-                float g[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) g[v] = 0.f;
-                if (i0 >= q.end - (W - 1) && p.dstate_T && k.in)
-                  unpack<VEC, InT>(*reinterpret_cast<const V*>(static_cast<const InT*>(p.dstate_T) +
-                                                               ((int64_t)q.n * (W - 1) + i0 - (q.end - (W - 1))) * p.C + c), g);
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-#pragma unroll
-                  for (int v = 0; v < VEC; ++v) g[v] = fmaf(k.w[W - 1 - j][v], du[j][v], g[v]);
-                if (k.in) *reinterpret_cast<V*>(dx + (int64_t)i0 * p.C) = pack<VEC, InT>(g);
-              }
-            }
+            for (int i = 0; i < AHEAD; ++i)
+              if (a + i < stop) token(a + i, i, std::false_type{});
           }
         }
       }
@@ -427,11 +436,14 @@ static hipError_t launch_fwd_t(ConvParams p, hipStream_t s) {
   // the states' own launch where the tokens' still read the states that it writes
   const bool apart = tail > 0 && p.state == p.state_T;
   p.nblocks = (int32_t)(apart ? main : main + tail);
-  if (p.nblocks > 0) hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
+  constexpr bool S = VEC > 1;
+  const auto kernel = S && p.streamed ? (p.silu ? conv_fwd_kernel<InT, VEC, W, true, S> : conv_fwd_kernel<InT, VEC, W, false, S>)
+                                      : (p.silu ? conv_fwd_kernel<InT, VEC, W, true, false> : conv_fwd_kernel<InT, VEC, W, false, false>);
+  if (p.nblocks > 0) hipLaunchKernelGGL(kernel, eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
   if (apart) {
     p.block0 = p.nmain;
     p.nblocks = (int32_t)tail;
-    hipLaunchKernelGGL((conv_fwd_kernel<InT, VEC, W>), eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
+    hipLaunchKernelGGL(kernel, eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
   }
   return hipGetLastError();
 }
@@ -447,7 +459,10 @@ static hipError_t launch_bwd_t(ConvParams p, hipStream_t s) {
   p.nmain = (int32_t)main;
   p.block0 = 0;
   p.nblocks = (int32_t)(main + tail);
-  if (p.nblocks > 0) hipLaunchKernelGGL((conv_bwd_kernel<InT, VEC, W>), eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
+  constexpr bool S = VEC > 1;
+  const auto kernel = S && p.streamed ? (p.silu ? conv_bwd_kernel<InT, VEC, W, true, S> : conv_bwd_kernel<InT, VEC, W, false, S>)
+                                      : (p.silu ? conv_bwd_kernel<InT, VEC, W, true, false> : conv_bwd_kernel<InT, VEC, W, false, false>);
+  if (p.nblocks > 0) hipLaunchKernelGGL(kernel, eights(p.nblocks), dim3(64 * CONV_WAVES), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((conv_dw_kernel<W>), dim3((unsigned)(((W + 1) * (int64_t)p.C + 63) / 64)), dim3(1024), 0, s, p, (int)run_blocks(p));

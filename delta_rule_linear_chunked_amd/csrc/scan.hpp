@@ -1,6 +1,8 @@
 // Selective scan, short convolution and norm: parameter blocks, what host and kernels agree on, launches.
 #pragma once
 
+#include <type_traits>
+
 #include "decay.hpp"
 
 namespace dr {
@@ -8,6 +10,13 @@ namespace dr {
 // ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
+// p + off bytes: with a uniform p the memory instruction adds the lane's 32 bits by itself.
+template <typename T>
+__device__ __forceinline__ T* byte_at(T* p, uint32_t off) {
+  using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(p) + off);
+}
+
 // VEC consecutive elements as one load or store (bf16: 8 in 16 bytes, fp32: 4), or one element.
 template <typename T, int VEC>
 struct Vec {
@@ -90,6 +99,7 @@ struct ConvParams {
   int64_t T, x_ts, x_bs;
   int32_t C, nbatch, nseq;
   int32_t silu;
+  int32_t streamed;        // outputs larger than the L2 caches: stored around them
   int32_t run;             // tokens of a wave; step: sequences
   int32_t cblocks;         // channel blocks of 64 vectors
   int32_t runs;            // runs of one batch row

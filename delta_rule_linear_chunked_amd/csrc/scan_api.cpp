@@ -127,6 +127,8 @@ dr::ConvParams conv_params(const dr_conv_dims* d, int64_t vec, bool backward) {
   p.nbatch = (int32_t)d->batch;
   p.nseq = (int32_t)d->num_seqs;
   p.silu = d->activation;
+  // (4 x 4096 x 2048 in bf16, 64 MiB: 30 us, 35 with ordinary stores)
+  p.streamed = d->batch * d->seqlen * d->channels * esize(d->in_dtype) > (int64_t)32 << 20;
   p.cblocks = (int32_t)ceil_div(d->channels, 64 * vec);
   // tokens of a wave: as many as still leave 16 waves to a CU, so that the inputs read twice stay few
   const int64_t most = backward ? 64 : 32;

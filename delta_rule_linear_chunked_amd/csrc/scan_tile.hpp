@@ -8,8 +8,6 @@
 // neither B nor d x is ever handed around, and a state costs the vector units its exponential, one product and two sums.
 #pragma once
 
-#include <type_traits>
-
 #include "scan.hpp"
 
 namespace dr {
@@ -65,12 +63,6 @@ __device__ __forceinline__ uint32_t raw_bits(const __bf16* p) { return *reinterp
 template <typename InT>
 __device__ __forceinline__ float raw_value(uint32_t v) {
   return __builtin_bit_cast(float, sizeof(InT) == 2 ? v << 16 : v);
-}
-
-template <typename T>
-__device__ __forceinline__ T* byte_at(T* p, uint32_t off) {
-  using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
-  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(p) + off);
 }
 
 // An input [tokens, channels] as a wave reads it: a uniform pointer to the tile's first token, moved on with the tile,
