@@ -5,6 +5,8 @@
 // read once and every output is written once; the weights stay in registers over the rows of a workgroup.
 // 8 bits: p = h w does not contain the mean, so codes and the row's scale come from p exactly as the state cache's from
 // a state, and the statistic only multiplies the scale.
+#include <type_traits>
+
 #include "scan.hpp"
 #include "state_code.hpp"
 
@@ -52,11 +54,11 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int wave)
   return v;
 }
 
-template <typename InT, int VEC, int WAVES, int OUT>
+template <typename InT, int VEC, int WAVES, int ELEMS, int OUT>
 __global__ __launch_bounds__(NormShape<WAVES>::NT) void norm_fwd_kernel(const NormParams p) {
   using Sh = NormShape<WAVES>;
   using V = typename Vec<InT, VEC>::type;
-  constexpr int NV = NORM_ELEMS / VEC, LANES = Sh::LANES;
+  constexpr int NV = ELEMS / VEC, LANES = Sh::LANES;
   __shared__ float s_sum[WAVES][1];
   __shared__ uint32_t s_max[WAVES];
   const int lane = threadIdx.x % LANES, wave = (threadIdx.x % LANES) >> 6, C = p.C;
@@ -151,13 +153,13 @@ __global__ __launch_bounds__(NormShape<WAVES>::NT) void norm_fwd_kernel(const No
 }
 
 // dx = dh + r (w dy - h r^2 mean(w dy h)); each workgroup's sum of dy h r over its rows for dw.
-template <typename InT, int VEC, int WAVES>
+template <typename InT, int VEC, int WAVES, int ELEMS>
 __global__ __launch_bounds__(NormShape<WAVES>::NT) void norm_bwd_kernel(const NormParams p) {
   using Sh = NormShape<WAVES>;
   using V = typename Vec<InT, VEC>::type;
-  constexpr int NV = NORM_ELEMS / VEC, LANES = Sh::LANES;
+  constexpr int NV = ELEMS / VEC, LANES = Sh::LANES;
   __shared__ float s_sum[WAVES][2];
-  __shared__ float s_dw[WAVES == 1 ? 3 : 1][WAVES == 1 ? 64 * NORM_ELEMS : 1];
+  __shared__ float s_dw[WAVES == 1 ? 3 : 1][WAVES == 1 ? 64 * ELEMS : 1];
   const int lane = threadIdx.x % LANES, wave = (threadIdx.x % LANES) >> 6, C = p.C;
   float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
@@ -254,41 +256,47 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const NormParams p) {
   }
 }
 
-template <typename InT, int VEC, int WAVES>
-static hipError_t launch_fwd_w(const NormParams& p, int out, hipStream_t s) {
-  const dim3 grid((unsigned)norm_groups(p.rows, p.C, 2048)), block(NormShape<WAVES>::NT);
-  if (out == 0)
-    hipLaunchKernelGGL((norm_fwd_kernel<InT, VEC, WAVES, 0>), grid, block, 0, s, p);
-  else if (out == 1)
-    hipLaunchKernelGGL((norm_fwd_kernel<InT, VEC, WAVES, 1>), grid, block, 0, s, p);
+// f(waves of a row, elements of a lane), as constants
+template <typename F>
+static void with_shape(const NormParams& p, F&& f) {
+  using std::integral_constant;
+  if (p.few)
+    norm_waves(p.C, p.few) == 4 ? f(integral_constant<int, 4>{}, integral_constant<int, NORM_FEW>{})
+                                 : f(integral_constant<int, 16>{}, integral_constant<int, NORM_FEW>{});
+  else if (norm_waves(p.C, p.few) == 1)
+    f(integral_constant<int, 1>{}, integral_constant<int, NORM_ELEMS>{});
+  else if (norm_waves(p.C, p.few) == 4)
+    f(integral_constant<int, 4>{}, integral_constant<int, NORM_ELEMS>{});
   else
-    hipLaunchKernelGGL((norm_fwd_kernel<InT, VEC, WAVES, 2>), grid, block, 0, s, p);
-  return hipGetLastError();
+    f(integral_constant<int, 16>{}, integral_constant<int, NORM_ELEMS>{});
 }
 template <typename InT, int VEC>
-static hipError_t launch_fwd_v(const NormParams& p, int out, hipStream_t s) {
-  switch (norm_waves(p.C)) {
-    case 1: return launch_fwd_w<InT, VEC, 1>(p, out, s);
-    case 4: return launch_fwd_w<InT, VEC, 4>(p, out, s);
-    default: return launch_fwd_w<InT, VEC, 16>(p, out, s);
-  }
+static void launch_fwd_v(const NormParams& p, int out, hipStream_t s) {
+  with_shape(p, [&](auto waves, auto elems) {
+    constexpr int W = decltype(waves)::value, E = decltype(elems)::value;
+    const dim3 grid((unsigned)p.nwg), block(NormShape<W>::NT);
+    if (out == 0)
+      hipLaunchKernelGGL((norm_fwd_kernel<InT, VEC, W, E, 0>), grid, block, 0, s, p);
+    else if (out == 1)
+      hipLaunchKernelGGL((norm_fwd_kernel<InT, VEC, W, E, 1>), grid, block, 0, s, p);
+    else
+      hipLaunchKernelGGL((norm_fwd_kernel<InT, VEC, W, E, 2>), grid, block, 0, s, p);
+  });
 }
 hipError_t launch_norm_fwd(const NormParams& p, int out, bool bf16, bool vec, hipStream_t s) {
-  if (bf16) return vec ? launch_fwd_v<__bf16, 8>(p, out, s) : launch_fwd_v<__bf16, 1>(p, out, s);
-  return vec ? launch_fwd_v<float, 4>(p, out, s) : launch_fwd_v<float, 1>(p, out, s);
+  if (bf16)
+    vec ? launch_fwd_v<__bf16, 8>(p, out, s) : launch_fwd_v<__bf16, 1>(p, out, s);
+  else
+    vec ? launch_fwd_v<float, 4>(p, out, s) : launch_fwd_v<float, 1>(p, out, s);
+  return hipGetLastError();
 }
 
-template <typename InT, int VEC, int WAVES>
-static void launch_bwd_w(const NormParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((norm_bwd_kernel<InT, VEC, WAVES>), dim3((unsigned)p.nwg), dim3(NormShape<WAVES>::NT), 0, s, p);
-}
 template <typename InT, int VEC>
 static void launch_bwd_v(const NormParams& p, hipStream_t s) {
-  switch (norm_waves(p.C)) {
-    case 1: return launch_bwd_w<InT, VEC, 1>(p, s);
-    case 4: return launch_bwd_w<InT, VEC, 4>(p, s);
-    default: return launch_bwd_w<InT, VEC, 16>(p, s);
-  }
+  with_shape(p, [&](auto waves, auto elems) {
+    constexpr int W = decltype(waves)::value, E = decltype(elems)::value;
+    hipLaunchKernelGGL((norm_bwd_kernel<InT, VEC, W, E>), dim3((unsigned)p.nwg), dim3(NormShape<W>::NT), 0, s, p);
+  });
 }
 hipError_t launch_norm_bwd(const NormParams& p, bool bf16, bool vec, hipStream_t s) {
   if (p.nwg > 0) {

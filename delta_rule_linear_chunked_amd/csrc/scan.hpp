@@ -137,15 +137,26 @@ struct NormParams {
   void* dx;
   float* part;        // [workgroups, C]
   float* dw;
-  int32_t nwg;        // workgroups of the backward's first kernel
+  int32_t nwg;        // workgroups (of the backward's first kernel)
+  int32_t few;        // norm_few
 };
 constexpr int NORM_ELEMS = 32;  // of a row in a lane's registers
+constexpr int NORM_FEW = 8;     // with few rows
 constexpr int NORM_MOST = 32768;
+// Few rows leave most of the GPU idle: then four times as many waves take a row, with a quarter of it in each lane. Measured, in
+// us, one (four) waves a row: 1 x 2048 3.8 (2.9), 1333 x 1531 e4m3 12.8 (8.3), 8192 x 2048 int8 26.4 (21.0); above 2048 channels
+// four (sixteen): 256 x 4096 int8 5.6 (5.1), 4096 x 4096 26.6 (40.0). The backward's workgroups each leave a row of sums:
+// 64 x 2048 7.1 (5.8), 512 x 2048 8.1 (10.9).
+constexpr bool norm_few(int64_t rows, int64_t C, bool backward) {
+  return C > 64 * NORM_FEW && C <= 1024 * NORM_FEW && rows <= (C <= 256 * NORM_FEW && !backward ? 8192 : 256);
+}
 // Waves of a row.
-constexpr int norm_waves(int64_t C) { return C <= 64 * NORM_ELEMS ? 1 : C <= 256 * NORM_ELEMS ? 4 : 16; }
+constexpr int norm_waves(int64_t C, bool few) {
+  return (C <= 64 * NORM_ELEMS ? 1 : C <= 256 * NORM_ELEMS ? 4 : 16) * (few ? 4 : 1);
+}
 // Workgroups: rows are dealt to at most so many, each of which keeps the weights (backward: its sums) in registers.
-constexpr int64_t norm_groups(int64_t rows, int64_t C, int64_t most) {
-  const int64_t per = norm_waves(C) == 1 ? 4 : 1, n = (rows + per - 1) / per;
+constexpr int64_t norm_groups(int64_t rows, int64_t C, bool few, int64_t most) {
+  const int64_t per = norm_waves(C, few) == 1 ? 4 : 1, n = (rows + per - 1) / per;
   return n < most ? n : most;
 }
 hipError_t launch_norm_fwd(const NormParams& p, int out, bool bf16, bool vec, hipStream_t s);

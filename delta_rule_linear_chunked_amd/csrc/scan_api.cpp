@@ -84,7 +84,6 @@ int64_t env_int(const char* name) {
   const char* e = getenv(name);
   return e ? atoll(e) : 0;
 }
-int64_t env_or(const char* name, int64_t d) { const int64_t v = env_int(name); return v ? v : d; }
 template <class P>
 void set_opts(P& p, const dr_opts* o) {
   if (o == nullptr) return;
@@ -133,7 +132,7 @@ dr::ConvParams conv_params(const dr_conv_dims* d, int64_t vec, bool backward) {
   // tokens of a wave: as many as still leave 16 waves to a CU, so that the inputs read twice stay few
   const int64_t most = backward ? 64 : 32;
   int64_t run = 8;
-  while (run < most && d->batch * ceil_div(d->seqlen, 2 * run) * p.cblocks >= env_or("DR_TUNE_RUN", 4096)) run *= 2;
+  while (run < most && d->batch * ceil_div(d->seqlen, 2 * run) * p.cblocks >= 4096) run *= 2;
   p.run = (int32_t)run;
   p.runs = (int32_t)ceil_div(d->seqlen, run);
   return p;
@@ -182,38 +181,42 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
   return DR_OK;
 }
 
-// Segments. A wave walks a segment of 64 channels x 16 states. Alone on its SIMD it takes 0.46 us a token (every instruction
-// waits for the one before), two take 0.58 together and four 1.0: k waves max(1, 0.25 + 0.5 k) times the time of one. A sequence that is cut
-// costs the segments' own states, 0.75 of the main pass (backward: the reverse part of the first pass), two launches
-// and a walk over the segments: in units of a token's time
-//   max(1, 0.25 + 0.5 waves / 1024) x (tokens of a segment) x (1 or 1.75) + (0 or 20 + segments)
-// 4 x 4096 tokens, 2048 channels, 16 states, bf16: 128 tokens 256 us, 256 285, 512 429, 1024 837, whole 1873.
-// With a workgroup's waves along the tokens (forward only) the decays are formed once; a workgroup fills a CU and takes 5.5 us (12 units) for 128 tokens of
-// 32 channels x 16 states.
+// Segments and kernels, by times in us as measured (bf16, 16 states, with z).
+// A wave walks a segment of 32 channels x 16 states: 0.195 a token, also where two share a SIMD for half of the time, and k waves a
+// SIMD take 0.8 k times as long. A sequence that is cut costs 0.73 of the main pass again (the segments' own states), what
+// 20 tokens of each segment cost, and 5. 1 x 8192 tokens, 2048 channels: segments of 64 181, 128 161, 256 157, 512 198, 1024 360, whole 1569.
+// With a workgroup's waves along the tokens the decays are formed once: a workgroup takes 6.4 for 128 tokens of 32 channels x 16
+// states and fills a CU. 4 x 2048 tokens, 2048 channels: 105, in segments 145; 64 x 256 tokens: 239, a wave a sequence 149.
+// Backward: 0.74 a token, 0.13 of it again for a cut sequence and what 10 tokens cost. 1 x 8192 tokens, 2048 channels: segments of 64 405,
+// 128 365, 256 350, 512 539, whole 6190.
 dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
   dr::ScanPlan pl{};
-  const int64_t T = d->seqlen, per = d->channels / d->groups;
-  const int64_t tiles = d->groups * ceil_div(per, dr::SCAN_TILE), waves = tiles * (d->state_dim / 16);
-  const double again = backward ? 1.15 : 1.75;
-  double best = 0;
+  const int64_t T = d->seqlen, SL = d->state_dim / 16, tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE);
+  const double token = backward ? 0.74 : 0.195, again = backward ? 1.13 : 1.73, own = backward ? 10 : 20;
+  // (packed: as many whole segments as the tokens fill, and half of one at each sequence's end)
+  const double waves = (double)(tiles * SL), ends = packed ? 0.5 * d->num_seqs : 0, rows = packed ? 1 : (double)d->num_seqs;
+  auto load = [&](double n) {
+    const double k = std::ceil((rows * n + ends) * waves / 1024);
+    return k > 1 ? 0.8 * k : 1.0;
+  };
+  double best = load(1) * T * token;
   int64_t seg = ceil_div(T, 8) * 8;
-  const int64_t force = env_int("DR_SCAN_BLOCK");  // for tuning and tests: 1 always, 2 never
-  for (int64_t n = 1; n == 1 || (n * 16 < T + 16 && n <= 4096); n += 1 + n / 8) {
-    const int64_t s = ceil_div(ceil_div(T, n), 8) * 8, nseg = s > 0 ? ceil_div(T, s) : 1;
-    const double slots = packed && s > 0 ? (double)T / s + 0.5 * d->num_seqs : (double)d->num_seqs * nseg;
-    double load = 0.25 + 0.5 * slots * waves / 1024;
-    if (load < 1) load = 1;
-    const double join = nseg > 1 ? 20.0 + nseg : 0.0;
-    const double plain = load * s * (nseg > 1 ? again : 1.0) + join;
-    double rounds = std::ceil(slots * tiles / 256);
-    const double block = rounds * std::ceil((double)s * (d->state_dim / 16) / 128) * 12 + (nseg > 1 ? load * s * 0.75 + join : 0.0);
-    const bool by_block = !backward && force != 2 && (block < plain || force == 1);
-    const double cost = by_block ? block : plain;
-    if (best == 0 || cost < best) {
+  for (const int k : {1, 2, 3, 4, 6, 8}) {  // so many waves a SIMD
+    double n = std::floor((k * 1024 / waves - ends) / rows);
+    if (n > (double)(T / 16)) n = (double)(T / 16);
+    if (n < 2) continue;
+    const int64_t s = ceil_div(ceil_div(T, (int64_t)n), 8) * 8;
+    const double cost = load(std::ceil((double)T / s)) * (s + own) * token * again + 5;
+    if (cost < best) {
       best = cost;
       seg = s;
-      pl.block = by_block;
     }
+  }
+  const int64_t force = env_int("DR_SCAN_BLOCK");  // for tuning and tests: 1 wherever sequences are whole, 2 never
+  const double block = std::ceil((double)d->num_seqs * tiles / 256) * (ceil_div(T * SL, 128) * 6.4 + 1);
+  if (!backward && force != 2 && (block < best || force == 1)) {
+    pl.block = true;
+    seg = ceil_div(T, 8) * 8;
   }
   if (const int64_t s = env_int("DR_SCAN_SEG"))
     if (s > 0 && s <= INT32_MAX - 8) seg = ceil_div(s, 8) * 8;
@@ -221,6 +224,7 @@ dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
   pl.seg = seg;
   pl.nseg = ceil_div(T, seg);
   if (pl.nseg < 1) pl.nseg = 1;
+  if (pl.nseg > 1) pl.block = false;
   pl.slots = packed ? T / seg + d->num_seqs : d->num_seqs * pl.nseg;
   return pl;
 }
@@ -229,7 +233,7 @@ int64_t grad_blocks(const dr_scan_dims* d) { return ceil_div(d->channels / d->gr
 bool scan_fits(const dr_scan_dims* d, const dr::ScanPlan& pl, bool backward) {
   const int64_t tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE), N = d->state_dim;
   if (pl.slots > INT32_MAX || pl.seg > INT32_MAX) return false;
-  if (pl.block && !dr::launch_fits(pl.slots * d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE) + 8, 64 * dr::SCAN_BLOCK_WAVES)) return false;
+  if (pl.block && !dr::launch_fits(pl.slots * tiles + 8, 64 * dr::SCAN_BLOCK_WAVES)) return false;
   if (!dr::launch_fits(pl.slots * tiles, (int)(64 * (N / 16))) || !dr::launch_fits(d->num_seqs * ceil_div(d->channels * (N / 4), 256), 256))
     return false;
   return !backward || (dr::launch_fits(pl.slots * d->groups * grad_blocks(d), 256) &&
@@ -319,15 +323,17 @@ int check_norm(const dr_norm_dims* d) {
   st = check_stride(d->x_row_stride, 1, "x row");
   return st ? st : check_stride(d->residual_row_stride, 1, "residual row");
 }
-dr::NormParams norm_params(const dr_norm_dims* d) {
+dr::NormParams norm_params(const dr_norm_dims* d, bool backward) {
   dr::NormParams p{};
   p.rows = d->rows;
   p.C = (int32_t)d->channels;
   p.x_rs = d->x_row_stride;
   p.r_rs = d->residual_row_stride;
   p.eps = d->eps;
-  // (the backward's sums are held by the workgroups: two for each CU)
-  p.nwg = (int32_t)dr::norm_groups(d->rows, d->channels, 512);
+  const bool few = dr::norm_few(d->rows, d->channels, backward);
+  p.few = few;
+  // (two for each CU keep the backward's sums few)
+  p.nwg = (int32_t)dr::norm_groups(d->rows, d->channels, few, backward ? 512 : 2048);
   return p;
 }
 
@@ -367,7 +373,7 @@ int dr_conv_step(const void* x, const float* weight, const float* bias, void* st
   dr::ConvParams p = conv_params(dims, dr::conv_vec(bf16, vec, false), false);
   if (!dr::launch_fits(ceil_div(p.nseq, dr::CONV_WAVES) * p.cblocks, 256)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   p.run = 1;
-  while (p.run < 8 && (int64_t)p.nseq * p.cblocks >= 2 * env_or("DR_TUNE_STEP", 2048) * p.run) p.run *= 2;
+  while (p.run < 8 && (int64_t)p.nseq * p.cblocks >= 4096 * p.run) p.run *= 2;
   set_opts(p, opts);
   p.x = x; p.w = weight; p.bias = bias; p.state_T = state; p.y = y;
   return done(dr::launch_conv_step(p, (int)dims->width, bf16, vec, stream), "convolution step");
@@ -520,7 +526,7 @@ int dr_norm_fwd(const void* x, const void* residual, const float* weight, void* 
   const int64_t unit = 16 / e;
   const bool vec = dims->channels % unit == 0 && dims->x_row_stride % unit == 0 &&
                    (residual == nullptr || dims->residual_row_stride % unit == 0) && aligned16({x, residual, y, h});
-  dr::NormParams p = norm_params(dims);
+  dr::NormParams p = norm_params(dims, false);
   p.x = x; p.r = residual; p.w = weight; p.y = y; p.scales = scales; p.h = h;
   return done(dr::launch_norm_fwd(p, dims->out, dims->in_dtype == DR_BF16, vec, stream), "norm");
 }
@@ -530,7 +536,7 @@ int dr_norm_workspace(const dr_norm_dims* dims, int64_t* bytes) {
   const int st = check_norm(dims);
   if (st) return st;
   if (bytes == nullptr) return host_fail(DR_ERR_NULL, "`bytes` is NULL");
-  *bytes = round256((int64_t)norm_params(dims).nwg * dims->channels * 4);
+  *bytes = round256((int64_t)norm_params(dims, true).nwg * dims->channels * 4);
   return DR_OK;
 }
 
@@ -545,7 +551,7 @@ int dr_norm_bwd(const void* h, const float* weight, const void* dy, const void* 
   st = check_ptrs({{h, "h", e, some}, {weight, "weight", 16, true}, {dy, "dy", e, some}, {dh, "dh", e, false}, {dx, "dx", e, some},
                    {dweight, "dweight", 16, true}});
   if (st) return st;
-  dr::NormParams p = norm_params(dims);
+  dr::NormParams p = norm_params(dims, true);
   unsigned char* ws = nullptr;
   bool owned = false;
   st = dr::host_space("norm backward", round256((int64_t)p.nwg * p.C * 4), workspace, workspace_bytes, 16, stream, &ws, &owned);

@@ -1,4 +1,4 @@
-// Selective scan with a workgroup's waves along the tokens (gfx950): few channels and sequences, or few tokens.
+// Selective scan with a workgroup's waves along the tokens (gfx950): whole sequences, where a wave for each would leave the GPU idle.
 //
 // The exponentials are the scan's largest part, and cutting sequences into segments forms each of them twice. Here a workgroup has 32
 // channels and walks 128 tokens at a time (64 or 32 with more states), a tile of 16 tokens a wave (scan_tile.hpp): a wave forms its decays
@@ -35,9 +35,7 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
     h[j] = 0.f;
   }
   const float bias = p.bias ? p.bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
-  if (p.part) {
-    load_states(p.part + ((int64_t)slot * p.C + c) * N + n0, h);
-  } else if (p.S0) {
+  if (p.S0) {
     const int64_t r = state_row(p.sidx, p.nslots, sp.n);
     if (r >= 0) load_states(p.S0 + (r * p.C + c) * N + n0, h);
   }
@@ -206,7 +204,7 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
     }
     y += IT * (int64_t)p.C;
   }
-  if (ts == TS - 1 && sp.last && p.S && on) {
+  if (ts == TS - 1 && p.S && on) {
     const int64_t r = state_row(p.sidx, p.nslots, sp.n);
     if (r >= 0) store_states(p.S + (r * p.C + c) * N + n0, h);
   }
