@@ -522,6 +522,7 @@ int dr_norm_fwd(const void* x, const void* residual, const float* weight, void* 
   st = check_ptrs({{x, "x", e, true}, {residual, "residual", e, false}, {weight, "weight", 16, true}, {y, "y", codes ? 1 : e, true},
                    {scales, "scales", 16, codes}, {h, "h", e, false}});
   if (st) return st;
+  if (residual == nullptr && h != nullptr) return host_fail(DR_ERR_SHAPE, "h is the sum with a residual: there is none");
   if (!codes && scales != nullptr) return host_fail(DR_ERR_SHAPE, "scales are an output of the 8-bit formats");
   const int64_t unit = 16 / e;
   const bool vec = dims->channels % unit == 0 && dims->x_row_stride % unit == 0 &&

@@ -24,7 +24,8 @@
  * At most 2^31 - 1024 tokens and sequences per call, at most 2^20 channels (norm: 32768); a call whose launches would pass
  * 2^32 - 1 work items is refused (DR_ERR_UNSUPPORTED).
  * A NaN or an infinity stays in its channel and sequence (gradients: also in what is summed over them), except that the gradients of B and C sum over
- * channels and a norm's row is one.
+ * channels and a norm's row is one. In the scan a product that is not finite may also show one token early (two tokens' products d x B
+ * share a matrix instruction).
  */
 #ifndef DELTARULE_SCAN_H
 #define DELTARULE_SCAN_H
@@ -141,7 +142,7 @@ typedef struct dr_norm_dims {
 
 /*
  * x, residual [rows, C] (residual NULL: h is x), weight [C], y [rows, C].
- * h        [rows, C]: the sum as it was normalised, rounded to in_dtype; NULL without residual or if it is not wanted. May be
+ * h        [rows, C]: the sum as it was normalised, rounded to in_dtype; NULL if it is not wanted, and without residual. May be
  *          x or residual where that is dense.
  * 8 bits   p = h w (float32) is held as a row of the state cache is (dr_cache_format: int8, or e4m3 with a power of two), and
  *          scales[row] is that scale times 1 / sqrt(mean(h^2) + eps): y is code * scale, and the codes do not depend on the

@@ -124,6 +124,22 @@ def test_gradients(R, C, dtype):
     check_bwd(x, dtype, dh=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,C", [(257, 520), (257, 2047), (300, 2048), (257, 2056), (260, 8192)])
+def test_more_rows_than_few(R, C, dtype):
+    # (smaller calls of these widths give a row to more waves; below 2049 channels the forward pass does up to 8192 rows)
+    x = make(seed_of("many", R, C, dtype), R, C, dtype)
+    check_bwd(x, dtype)
+    R = 8193 if C <= 2048 else R
+    x = make(seed_of("many rows", R, C, dtype), R, C, dtype)
+    y, h = drl.norm_fwd(dev(x["x"], dtype), dev(x["w"]), dev(x["r"], dtype))
+    want = oracle.norm(x["h"], x["w"])
+    close(y, want, np.abs(want), NORM_K, "y")
+    assert torch.equal(h, dev(x["h"], dtype))
+    for fmt in ("int8", "e4m3"):
+        check_codes(drl.norm_fwd(h, dev(x["w"]), fmt=fmt), x["h"], x["w"], fmt)
+
+
 def test_gradients_in_place_and_of_nothing():
     x = make(2, 33, 64, "bf16")
     dh, dw = dev(x["dh"], "bf16"), torch.empty(64, device="cuda")
