@@ -53,43 +53,30 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
   B.init(p.B, sp.b * p.b_bs + sp.t0 * p.b_ts, p.b_ts, half, g * N + sl * 16 + (lane & 15));
   // C: lane l brings states 4 (l % 4) .. + 3 of token l / 4
   typedef typename Vec<InT, 4>::type V4;
+  auto c_at = [&](uint32_t l) { return ((l >> 2) * (uint32_t)p.c_ts + (uint32_t)(g * N + sl * 16) + 4 * (l & 3)) * (uint32_t)sizeof(InT); };
   const InT* Ca = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + sp.t0 * p.c_ts;
-  const uint32_t c_off = (uint32_t)((lane >> 2) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)) * sizeof(InT);
   InT* y = LOCAL ? nullptr : static_cast<InT*>(p.y) + (sp.b * p.T + sp.t0) * (int64_t)p.C;
-  const uint32_t y_off = (uint32_t)(half * p.C + c) * sizeof(InT);
   float sumd = 0.f;
   uint32_t xn[O], dn[O], zn[O], bn[O];
   V4 cn{};
-  auto fetch = [&](int left) {
-    if (left >= K) {
-      X.whole(xn);
-      T.whole(dn);
-      B.whole(bn);
-      if constexpr (!LOCAL) {
-        Z.whole(zn);
-        cn = *reinterpret_cast<const V4*>(byte_at(Ca, c_off));
-      }
-      whole_tile();
-    } else {
-      X.part(xn, left);
-      T.part(dn, left);
-      B.part(bn, left);
-      if constexpr (!LOCAL) {
-        Z.part(zn, left);
-        cn = *reinterpret_cast<const V4*>(Ca + ((int64_t)min(lane >> 2, left - 1) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)));
-      }
-    }
-    X.at += K * X.ts;
-    T.at += K * T.ts;
-    B.at += K * B.ts;
+  // a whole tile, the next one if there is one, the same again if not (loads under a condition would be waited for where its branches meet)
+  auto fetch = [&](int step) {
+    X.at += step * X.ts;
+    T.at += step * T.ts;
+    B.at += step * B.ts;
+    X.whole(xn);
+    T.whole(dn);
+    B.whole(bn);
     if constexpr (!LOCAL) {
-      Z.at += K * Z.ts;
-      Ca += K * p.c_ts;
+      Z.at += step * Z.ts;
+      Ca += step * p.c_ts;
+      Z.whole(zn);
+      cn = *reinterpret_cast<const V4*>(byte_at(Ca, c_at(fresh(lane))));
     }
   };
-  if (len > 0) fetch(len);
   int buf = 0;
-  for (int t = 0; t < len; t += K, buf ^= 1) {
+  auto tokens = [&](int t, auto cut) {
+    constexpr bool CUT = decltype(cut)::value;
     float xv[O], dv[O], zv[O], dx[O], bo[O], v[O];
 #pragma unroll
     for (int i = 0; i < O; ++i) {
@@ -98,7 +85,7 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
       float own = soft ? sf : raw;
       here(own);
       // (tokens past the end: a decay of one and nothing added)
-      const bool inside = t + K <= len || t + 2 * i + half < len;
+      const bool inside = !CUT || t + 2 * i + half < len;
       dv[i] = inside ? own : 0.f;
       dx[i] = inside ? dv[i] * xv[i] : 0.f;
       bo[i] = operand<InT>(bn[i], lane);
@@ -111,7 +98,7 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
       *reinterpret_cast<f32x4*>(&s_c[sl][lane >> 2][4 * (lane & 3)]) = f32x4{f[0], f[1], f[2], f[3]};
       __builtin_amdgcn_wave_barrier();
     }
-    if (t + K < len) fetch(len - t - K);
+    if constexpr (!CUT) fetch(t + 2 * K <= len ? K : 0);
     f32x16 in = outer_pair(bo[0], dx[0]);
 #pragma unroll
     for (int i = 0; i < O; ++i) {
@@ -163,10 +150,32 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
         }
         o = fmaf(D, xv[i], o);
         const float sg = zv[i] * sigmoid_f(zv[i]);
-        if (on && (t + K <= len || t + 2 * i + half < len)) *byte_at(row, y_off) = (InT)(o * (gate ? sg : 1.f));
+        if (on && (!CUT || t + 2 * i + half < len)) *byte_at(row, (fresh(c) + (fresh(half) ? (uint32_t)p.C : 0u)) * (uint32_t)sizeof(InT)) = (InT)(o * (gate ? sg : 1.f));
       }
       y += K * (int64_t)p.C;
     }
+    buf ^= 1;
+  };
+  const int whole = len / K * K;
+  if (whole > 0) {
+    fetch(0);
+    for (int t = 0; t < whole; t += K) tokens(t, std::false_type{});
+  }
+  if (whole < len) {
+    const int step = whole > 0 ? K : 0, left = len - whole;
+    X.at += step * X.ts;
+    T.at += step * T.ts;
+    B.at += step * B.ts;
+    X.part(xn, left);
+    T.part(dn, left);
+    B.part(bn, left);
+    if constexpr (!LOCAL) {
+      Z.at += step * Z.ts;
+      Ca += step * p.c_ts;
+      Z.part(zn, left);
+      cn = *reinterpret_cast<const V4*>(Ca + ((int64_t)min(lane >> 2, left - 1) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)));
+    }
+    tokens(whole, std::true_type{});
   }
   if (!on) return;
   if constexpr (LOCAL) {

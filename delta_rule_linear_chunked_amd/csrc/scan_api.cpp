@@ -205,7 +205,7 @@ dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
     double n = std::floor((k * 1024 / waves - ends) / rows);
     if (n > (double)(T / 16)) n = (double)(T / 16);
     if (n < 2) continue;
-    const int64_t s = ceil_div(ceil_div(T, (int64_t)n), 8) * 8;
+    const int64_t s = ceil_div(ceil_div(T, (int64_t)n), 16) * 16;
     const double cost = load(std::ceil((double)T / s)) * (s + own) * token * again + 5;
     if (cost < best) {
       best = cost;

@@ -56,33 +56,24 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
   B.init(p.B, sp.b * p.b_bs + mine * p.b_ts, p.b_ts, half, g * N + sl * 16 + (lane & 15));
   // C: lane l brings states 4 (l % 4) .. + 3 of token l / 4
   typedef typename Vec<InT, 4>::type V4;
+  auto c_at = [&](uint32_t l) { return ((l >> 2) * (uint32_t)p.c_ts + (uint32_t)(g * N + sl * 16) + 4 * (l & 3)) * (uint32_t)sizeof(InT); };
   const InT* Ca = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + mine * p.c_ts;
-  const uint32_t c_off = (uint32_t)((lane >> 2) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)) * sizeof(InT);
   InT* y = static_cast<InT*>(p.y) + (sp.b * p.T + mine) * (int64_t)p.C;
-  const uint32_t y_off = (uint32_t)(half * p.C + c) * sizeof(InT);
   uint32_t xn[O], dn[O], bn[O];
   V4 cn;
-  auto fetch = [&](int left) {  // (waves whose tile lies past the end read its last token)
-    if (left >= K) {
-      X.whole(xn);
-      T.whole(dn);
-      B.whole(bn);
-      cn = *reinterpret_cast<const V4*>(byte_at(Ca, c_off));
-      whole_tile();
-    } else {
-      X.part(xn, left);
-      T.part(dn, left);
-      B.part(bn, left);
-      cn = *reinterpret_cast<const V4*>(Ca + ((int64_t)min(lane >> 2, left - 1) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)));
-    }
-    X.at += IT * X.ts;
-    T.at += IT * T.ts;
-    B.at += IT * B.ts;
-    Ca += IT * p.c_ts;
+  auto fetch = [&](int step) {  // (as for a wave on its own)
+    X.at += step * X.ts;
+    T.at += step * T.ts;
+    B.at += step * B.ts;
+    Ca += step * p.c_ts;
+    X.whole(xn);
+    T.whole(dn);
+    B.whole(bn);
+    cn = *reinterpret_cast<const V4*>(byte_at(Ca, c_at(fresh(lane))));
   };
-  if (len > 0) fetch(len - ts * K);
   int par = 0;
-  for (int t0 = 0; t0 < len; t0 += IT, par ^= 1) {
+  auto tokens = [&](int t0, auto cut) {
+    constexpr bool CUT = decltype(cut)::value;
     const int t = t0 + ts * K;
     float xv[O], dv[O], dx[O], bo[O];
     {
@@ -98,7 +89,7 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
       float own = soft ? sf : raw;
       here(own);
       // (tokens past the end: a decay of one and nothing added)
-      const bool inside = t + K <= len || t + 2 * i + half < len;
+      const bool inside = !CUT || t + 2 * i + half < len;
       dv[i] = inside ? own : 0.f;
       dx[i] = inside ? dv[i] * xv[i] : 0.f;
       bo[i] = operand<InT>(bn[i], lane);
@@ -146,19 +137,17 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
       }
     }
     uint32_t zn[O];
-    if (len - t >= K) {
-      Z.whole(zn);
-      whole_tile();
-    } else {
+    if constexpr (CUT)
       Z.part(zn, len - t);
-    }
+    else
+      Z.whole(zn);
     Z.at += IT * Z.ts;
     float v[O];
     f32x16 in = outer_pair(bo[0], dx[0]);
 #pragma unroll
     for (int i = 0; i < O; ++i) {
       tile_step();
-      if (i == O / 2 && t0 + IT < len) fetch(len - t - IT);  // (half of the decays are no longer held)
+      if (!CUT && i == O / 2) fetch(t0 + 2 * IT <= len ? IT : 0);  // (half of the decays are no longer held)
       float s[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -200,9 +189,27 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
       }
       o = fmaf(D, xv[i], o);
       const float zv = raw_value<InT>(zn[i]), sg = zv * sigmoid_f(zv);
-      if (on && (t + K <= len || t + 2 * i + half < len)) *byte_at(row, y_off) = (InT)(o * (gate ? sg : 1.f));
+      if (on && (!CUT || t + 2 * i + half < len)) *byte_at(row, (fresh(c) + (fresh(half) ? (uint32_t)p.C : 0u)) * (uint32_t)sizeof(InT)) = (InT)(o * (gate ? sg : 1.f));
     }
     y += IT * (int64_t)p.C;
+    par ^= 1;
+  };
+  const int whole = len / IT * IT;
+  if (whole > 0) {
+    fetch(0);
+    for (int t0 = 0; t0 < whole; t0 += IT) tokens(t0, std::false_type{});
+  }
+  if (whole < len) {  // (waves whose tile lies past the end read the last token)
+    const int step = whole > 0 ? IT : 0, left = len - whole - ts * K;
+    X.at += step * X.ts;
+    T.at += step * T.ts;
+    B.at += step * B.ts;
+    Ca += step * p.c_ts;
+    X.part(xn, left);
+    T.part(dn, left);
+    B.part(bn, left);
+    cn = *reinterpret_cast<const V4*>(Ca + ((int64_t)min(lane >> 2, left - 1) * p.c_ts + g * N + sl * 16 + 4 * (lane & 3)));
+    tokens(whole, std::true_type{});
   }
   if (ts == TS - 1 && p.S && on) {
     const int64_t r = state_row(p.sidx, p.nslots, sp.n);

@@ -56,38 +56,24 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
   float* ckd = p.ckd + (int64_t)slot * cps * p.C + c;
   float sumd = 0.f;
   uint32_t xn[O], dn[O], zn[O], yn[O], bn[O], cn[O];
-  auto fetch = [&](int left) {
-    if (left >= K) {
-      X.whole(xn);
-      T.whole(dn);
-      B.whole(bn);
-      if constexpr (BOTH) {
-        Z.whole(zn);
-        Y.whole(yn);
-        Cr.whole(cn);
-      }
-      whole_tile();
-    } else {
-      X.part(xn, left);
-      T.part(dn, left);
-      B.part(bn, left);
-      if constexpr (BOTH) {
-        Z.part(zn, left);
-        Y.part(yn, left);
-        Cr.part(cn, left);
-      }
-    }
-    X.at += K * X.ts;
-    T.at += K * T.ts;
-    B.at += K * B.ts;
+  auto fetch = [&](int step) {  // (as in the forward pass)
+    X.at += step * X.ts;
+    T.at += step * T.ts;
+    B.at += step * B.ts;
+    X.whole(xn);
+    T.whole(dn);
+    B.whole(bn);
     if constexpr (BOTH) {
-      Z.at += K * Z.ts;
-      Y.at += K * Y.ts;
-      Cr.at += K * Cr.ts;
+      Z.at += step * Z.ts;
+      Y.at += step * Y.ts;
+      Cr.at += step * Cr.ts;
+      Z.whole(zn);
+      Y.whole(yn);
+      Cr.whole(cn);
     }
   };
-  if (len > 0) fetch(len);
-  for (int t = 0; t < len; t += K) {
+  auto tokens = [&](int t, auto cut) {
+    constexpr bool CUT = decltype(cut)::value;
     float dv[O], dx[O], gy[O], bo[O], co[O];
 #pragma unroll
     for (int i = 0; i < O; ++i) {
@@ -95,7 +81,7 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
       float own = soft ? sf : raw;
       here(own);
       // (tokens past the end: a decay of one, nothing in or out)
-      const bool inside = t + K <= len || t + 2 * i + half < len;
+      const bool inside = !CUT || t + 2 * i + half < len;
       dv[i] = inside ? own : 0.f;
       dx[i] = inside ? dv[i] * raw_value<InT>(xn[i]) : 0.f;
       bo[i] = operand<InT>(bn[i], lane);
@@ -107,12 +93,12 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
         co[i] = operand<InT>(cn[i], lane);
       }
     }
-    if (t + K < len) fetch(len - t - K);
+    if constexpr (!CUT) fetch(t + 2 * K <= len ? K : 0);
     f32x16 in = outer_pair(bo[0], dx[0]), out = BOTH ? outer_pair(co[0], gy[0]) : f32x16{};
 #pragma unroll
     for (int i = 0; i < O; ++i) {
       tile_step();
-      if (i % (O / 2) == 0 && (i == 0 || t + SCAN_CHUNK < len)) {
+      if (i % (O / 2) == 0 && (i == 0 || !CUT || t + SCAN_CHUNK < len)) {
         if (on && (t > 0 || i > 0)) store_states(ck, h);  // (a segment begins at zero)
         float lo, hi;
         both_halves(sumd, lo, hi);
@@ -140,6 +126,29 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
       }
       if constexpr (BOTH) here(R);
     }
+  };
+  const int whole = len / K * K;
+  if (whole > 0) {
+    fetch(0);
+    for (int t = 0; t < whole; t += K) tokens(t, std::false_type{});
+  }
+  if (whole < len) {
+    const int step = whole > 0 ? K : 0, left = len - whole;
+    X.at += step * X.ts;
+    T.at += step * T.ts;
+    B.at += step * B.ts;
+    X.part(xn, left);
+    T.part(dn, left);
+    B.part(bn, left);
+    if constexpr (BOTH) {
+      Z.at += step * Z.ts;
+      Y.at += step * Y.ts;
+      Cr.at += step * Cr.ts;
+      Z.part(zn, left);
+      Y.part(yn, left);
+      Cr.part(cn, left);
+    }
+    tokens(whole, std::true_type{});
   }
   if constexpr (BOTH) {
     float lo, hi;
@@ -196,24 +205,37 @@ __device__ __forceinline__ float pair16(float a, float b) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// A workgroup: 4 waves, each 32 channels x 16 states (SL waves share channels), one segment.
+// A workgroup: 4 waves, each 32 channels x 16 states, one segment. With 16 states nothing but the sums of dB and dC passes between
+// waves, and they meet once for every two chunks; with more, SL waves share their channels' inputs and add their parts of
+// the sums over states.
 template <int N>
 struct GradShape {
-  static constexpr int SL = N / 16;           // slices of states
-  static constexpr int CB = 4 / SL;           // channel blocks
-  static constexpr int CH = 32 * CB;          // channels
-  static constexpr int ROWS = 256 / CH;       // token rows that the threads cover at once
-  static constexpr int PP = SCAN_CHUNK / ROWS;  // (token, channel) pairs of a thread
+  static constexpr int SL = N / 16;                      // slices of states
+  static constexpr int CB = 4 / SL;                      // channel blocks
+  static constexpr int CH = 32 * CB;                     // channels
+  static constexpr int ROWS = 2 * SL;                    // token rows of a chunk that the lanes of a channel cover at once
+  static constexpr int PP = SCAN_CHUNK / ROWS;           // (token, channel) pairs of a lane
+  static constexpr int F = 2;                            // chunks between two meetings of the workgroup
 };
+// What lanes of a channel block wrote to LDS is seen by its other lanes (one wave's LDS accesses are in order).
+template <int SL>
+__device__ __forceinline__ void block_sync() {
+  if constexpr (SL == 1) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
 template <int N, typename InT, bool GATE>
 __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   using Sh = GradShape<N>;
-  constexpr int K = SCAN_CHUNK, CH = Sh::CH, SL = Sh::SL, PP = Sh::PP, ROWS = Sh::ROWS;
+  constexpr int K = SCAN_CHUNK, CH = Sh::CH, SL = Sh::SL, CB = Sh::CB, PP = Sh::PP, ROWS = Sh::ROWS, F = Sh::F;
   __shared__ __align__(16) float s_d[K][CH], s_dx[K][CH], s_dy[K][CH];
-  __shared__ __align__(16) float s_b[K][N], s_c[K][N];
+  __shared__ __align__(16) float s_in[4][K][32];  // a wave's 16 states of B and of C
   __shared__ float s_u[SL][K][CH], s_e[SL][K][CH], s_y[GATE ? SL : 1][GATE ? K : 1][GATE ? CH : 1];
-  __shared__ __align__(16) float s_bc[4][K][32];
-  // what a thread needs of its pairs again at the end of a chunk, and its starting state, wait here instead of in registers
+  __shared__ __align__(16) float s_bc[2][F][4][K][32];
+  // what a lane needs of its pairs again at the end of a chunk, and its starting state, wait here instead of in registers
   __shared__ __align__(16) float s_own[GATE ? 4 : 2][PP][256], s_hs[2][256][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int sl = wave % SL, cb = wave / SL;
@@ -226,16 +248,14 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   // as the lane of states and gradients: 4 channels, 2 states
   const int ng = lane >> 3, cg = lane & 7;
   const int l_ch = cb * 32 + cg * 4, n0 = sl * 16 + ng * 2;
-  int lc[4];  // (channels past the group's count as its last)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) lc[i] = g * p.Cg + min(in0 + l_ch + i, p.Cg - 1);
-  const int lim = max(p.Cg - 1 - in0 - l_ch, 0);
+  // channel i of lane l (those past the group's count as its last)
+  auto chan = [&](uint32_t l, int i) { return g * p.Cg + min(in0 + cb * 32 + (int)(l & 7) * 4 + i, p.Cg - 1); };
   float A[4][2], carry[4][2], dA[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t at = (int64_t)lc[i] * N + n0 + j;
+      const int64_t at = (int64_t)chan(lane, i) * N + n0 + j;
       A[i][j] = p.A[at] * LOG2E;
       dA[i][j] = 0.f;
       const float* from = p.part ? p.part + (int64_t)slot * C * N : p.S0 ? p.S0 + (int64_t)sp.n * C * N : nullptr;
@@ -243,118 +263,126 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       const float* back = p.part ? p.rpart + (int64_t)slot * C * N : p.dST ? p.dST + (int64_t)sp.n * C * N : nullptr;
       carry[i][j] = back ? back[at] : 0.f;
     }
-  // as the thread of (token, channel) pairs: one channel, PP tokens of a chunk
-  const int pc = tid % CH, prow = tid / CH;
+  // as the lane of (token, channel) pairs: one channel, PP tokens of a chunk
+  const int pc = cb * 32 + (lane & 31), prow = (lane >> 5) + 2 * sl;
   const bool on = in0 + pc < p.Cg;
-  const int c = g * p.Cg + min(in0 + pc, p.Cg - 1);
-  const float bias = p.bias ? p.bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
   // Addresses: a uniform pointer for the chunk, moved back by a chunk after each, and 32-bit offsets of the lane that stay
   // (token strides are limited to 2^24 elements, groups to 2^16).
   const int last = len > 0 ? (len - 1) / K * K : 0;
   const int64_t row0 = sp.b * p.T + sp.t0, x_ts = p.x_ts, dt_ts = p.dt_ts, z_ts = p.z_ts;
-  const InT* xb = static_cast<const InT*>(p.x) + sp.b * p.x_bs + (sp.t0 + last) * x_ts;
-  const InT* db = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + (sp.t0 + last) * dt_ts;
-  const InT* zb = GATE ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + (sp.t0 + last) * z_ts : nullptr;
-  int64_t row = row0 + last, next = row;  // of the outputs, of dy
+  const InT* xb = static_cast<const InT*>(p.x) + sp.b * p.x_bs + (sp.t0 + last + 2 * sl) * x_ts;
+  const InT* db = static_cast<const InT*>(p.dt) + sp.b * p.dt_bs + (sp.t0 + last + 2 * sl) * dt_ts;
+  const InT* zb = GATE ? static_cast<const InT*>(p.z) + sp.b * p.z_bs + (sp.t0 + last + 2 * sl) * z_ts : nullptr;
+  int64_t row = row0 + last + 2 * sl, next = row;  // of the outputs, of dy
   constexpr uint32_t E = sizeof(InT);
-  const uint32_t xo = (uint32_t)(prow * x_ts + c) * E, dto = (uint32_t)(prow * dt_ts + c) * E, zo = GATE ? (uint32_t)(prow * z_ts + c) * E : 0u;
-  const uint32_t oo = (uint32_t)(prow * C + c) * E, cko = ((uint32_t)lc[0] * N + n0) * 4;
+  // bytes to the channel of lane l's pairs, and one row on in the upper lanes
+  auto pair_at = [&](uint32_t l, int64_t ts) { return (uint32_t)(g * p.Cg + min(in0 + cb * 32 + (int)(l & 31), p.Cg - 1)) * E + (l & 32 ? (uint32_t)ts * E : 0u); };
+  const float bias = p.bias ? p.bias[pair_at(lane, 0) / E] : 0.f, D = p.D ? p.D[pair_at(lane, 0) / E] : 0.f;
   int64_t chunk = (int64_t)slot * cps + last / K;
-  constexpr int BCN = 2 * K * N / 256;  // elements of B and C of a thread: B's first, then C's (a wave has one of them)
-  static_assert(2 * K * N % 256 == 0 && K * N % 64 == 0, "whole waves");
-  uint32_t bco[BCN];
-#pragma unroll
-  for (int i = 0; i < BCN; ++i) {
-    const int e = (tid + i * 256) % (K * N);
-    const bool isC = (wave * 64 + i * 256) / (K * N) == 1;
-    bco[i] = (uint32_t)(e / N * (isC ? p.c_ts : p.b_ts) + g * N + e % N) * E;
-  }
+  // B and C: lane l brings states 2 (l % 8), + 1 of token l / 8
+  typedef uint32_t Raw2 __attribute__((ext_vector_type(2 * sizeof(InT) / 4)));
+  const InT* Bb = static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + last) * p.b_ts + g * N + sl * 16;
+  const InT* Cb = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + (sp.t0 + last) * p.c_ts + g * N + sl * 16;
   const bool soft = p.softplus != 0;
   float accD = 0.f, accb = 0.f;
-  InT xn[PP], dn[PP], zn[PP], yn[PP];
-  float hn[4][2], dsum[4];
-  InT bn[BCN];
-  auto fetch = [&](int t) {  // (rows past the end are read from the last one and not used; those of B and C are zeros)
+  uint32_t xn[PP], dn[PP], zn[PP], yn[PP];
+  f32x2 hn[4];
+  float dsum[4];
+  Raw2 bn, cn;
+  // (first: the segment's last chunk, whose rows past the end are read from the last one and not used; those of B and C are zeros)
+  auto fetch = [&](int t, auto first) {
     const InT *xr = xb, *dr = db, *zr = zb, *yr = static_cast<const InT*>(p.dy) + next * C;
-    if (t + K <= len) {
+    const uint32_t l = fresh(lane), brow = l >> 3;
+    const uint32_t bo = (brow * (uint32_t)p.b_ts + 2 * (l & 7)) * E, co = (brow * (uint32_t)p.c_ts + 2 * (l & 7)) * E;
+    if (!decltype(first)::value || t + K <= len) {
+      const uint32_t xo = pair_at(l, x_ts), dto = pair_at(l, dt_ts), zo = GATE ? pair_at(l, z_ts) : 0u, oo = pair_at(l, C);
 #pragma unroll
       for (int i = 0; i < PP; ++i) {
-        xn[i] = *byte_at(xr, xo);
-        dn[i] = *byte_at(dr, dto);
-        if constexpr (GATE) zn[i] = *byte_at(zr, zo);
-        yn[i] = *byte_at(yr, oo);
+        xn[i] = raw_bits(byte_at(xr, xo));
+        dn[i] = raw_bits(byte_at(dr, dto));
+        if constexpr (GATE) zn[i] = raw_bits(byte_at(zr, zo));
+        yn[i] = raw_bits(byte_at(yr, oo));
         xr += ROWS * x_ts;
         dr += ROWS * dt_ts;
         if constexpr (GATE) zr += ROWS * z_ts;
         yr += ROWS * (int64_t)C;
       }
+      bn = *reinterpret_cast<const Raw2*>(byte_at(Bb, bo));
+      cn = *reinterpret_cast<const Raw2*>(byte_at(Cb, co));
       whole_tile();
     } else {
 #pragma unroll
       for (int i = 0; i < PP; ++i) {
-        const int64_t r = min(prow + i * ROWS, len - 1 - t);
-        xn[i] = xr[r * x_ts + c];
-        dn[i] = dr[r * dt_ts + c];
-        if constexpr (GATE) zn[i] = zr[r * z_ts + c];
-        yn[i] = yr[r * C + c];
+        const int64_t r = min((int)(l >> 5) + 2 * sl + i * ROWS, len - 1 - t) - 2 * sl;
+        const int c = (int)(pair_at(l, 0) / E);
+        xn[i] = raw_bits(xr + (r * x_ts + c));
+        dn[i] = raw_bits(dr + (r * dt_ts + c));
+        if constexpr (GATE) zn[i] = raw_bits(zr + (r * z_ts + c));
+        yn[i] = raw_bits(yr + (r * C + c));
+      }
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(Raw2) / 4); ++i) bn[i] = cn[i] = 0;
+      if (t + (int)brow < len) {
+        bn = *reinterpret_cast<const Raw2*>(byte_at(Bb, bo));
+        cn = *reinterpret_cast<const Raw2*>(byte_at(Cb, co));
       }
     }
     xb -= K * x_ts;
     db -= K * dt_ts;
     if constexpr (GATE) zb -= K * z_ts;
     next -= K;
-#pragma unroll
-    for (int i = 0; i < BCN; ++i) {
-      const bool isC = (wave * 64 + i * 256) / (K * N) == 1;
-      const InT* from = isC ? static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + (sp.t0 + t) * p.c_ts : static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + t) * p.b_ts;
-      bn[i] = InT(0);
-      if (t + K <= len || t + (tid + i * 256) % (K * N) / N < len) bn[i] = *byte_at(from, bco[i]);
-    }
+    Bb -= K * p.b_ts;
+    Cb -= K * p.c_ts;
     const float *ck = p.ck + chunk * C * N, *ckd = p.ckd + chunk * C;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dsum[i] = 0.f;
-      hn[i][0] = hn[i][1] = 0.f;
-      if (t > 0) {
-        const uint32_t o = min(i, lim);
-        dsum[i] = *byte_at(ckd, ((uint32_t)lc[0] + o) * 4);
-        const f32x2 v = *reinterpret_cast<const f32x2*>(byte_at(ck, cko + o * (4 * N)));
-        hn[i][0] = v[0];
-        hn[i][1] = v[1];
-      }
+    for (int i = 0; i < 4; ++i) {  // (a segment's first chunk has none: not used there)
+      const uint32_t ch = (uint32_t)chan(l, i) * 4;
+      dsum[i] = *byte_at(ckd, ch);
+      hn[i] = *reinterpret_cast<const f32x2*>(byte_at(ck, ch * N + (sl * 16 + (l >> 3) * 2) * 4));
     }
     --chunk;
   };
   // this workgroup's part of dB and dC: 2 N values to a token
-  float* pbc = p.pBC + (((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0 + last) * p.G + g) * (2 * N);
-  const uint32_t pbo = ((uint32_t)(tid / (2 * N)) * p.G * (2 * N) + tid % (2 * N)) * 4;
-  if (len > 0) fetch(last);
+  float* pbc = p.pBC + (((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0) * p.G + g) * (2 * N);
+  if (len > 0) fetch(last, std::true_type{});
+  int met = 0;  // chunks since the last meeting, and which half of s_bc they use
+  int part = 0;
   for (int t = last; len > 0 && t >= 0; t -= K) {
-    __syncthreads();  // (the chunk before has been written out)
+    block_sync<SL>();  // (the chunk before has been written out)
 #pragma unroll
     for (int i = 0; i < PP; ++i) {
       const int r = prow + i * ROWS;
-      const bool here = on && t + r < len;
-      const float xv = (float)xn[i], raw = (float)dn[i] + bias, sf = softplus_f(raw), sr = sigmoid_f(raw);
-      const float dv = soft ? sf : raw;
-      float gv = (float)yn[i];
+      const bool inside = on && t + r < len;
+      const float xv = raw_value<InT>(xn[i]), raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw), sr = sigmoid_f(raw);
+      float dv = soft ? sf : raw, gv = raw_value<InT>(yn[i]);
       s_own[0][i][tid] = xv;
       s_own[1][i][tid] = soft ? sr : 1.f;
       if constexpr (GATE) {
-        const float zv = (float)zn[i];
+        const float zv = raw_value<InT>(zn[i]);
         s_own[2][i][tid] = zv;
         s_own[3][i][tid] = gv;
         gv *= zv * sigmoid_f(zv);
       }
+      here(dv);
+      here(gv);
       // tokens past the end and channels past the group's: a decay of one, nothing in or out
-      s_d[r][pc] = here ? dv : 0.f;
-      s_dx[r][pc] = here ? dv * xv : 0.f;
-      s_dy[r][pc] = here ? gv : 0.f;
+      s_d[r][pc] = inside ? dv : 0.f;
+      s_dx[r][pc] = inside ? dv * xv : 0.f;
+      s_dy[r][pc] = inside ? gv : 0.f;
     }
+    {
+      f32x2 v[2];
 #pragma unroll
-    for (int i = 0; i < BCN; ++i) {
-      const int q = tid + i * 256;
-      (q < K * N ? &s_b[0][0] : &s_c[0][0] - K * N)[q] = (float)bn[i];
+      for (int i = 0; i < 2; ++i)
+        if constexpr (sizeof(InT) == 4) {
+          v[0][i] = __builtin_bit_cast(float, (uint32_t)bn[i]);
+          v[1][i] = __builtin_bit_cast(float, (uint32_t)cn[i]);
+        } else {
+          v[0][i] = __builtin_bit_cast(float, i ? (uint32_t)bn[0] & 0xffff0000u : (uint32_t)bn[0] << 16);
+          v[1][i] = __builtin_bit_cast(float, i ? (uint32_t)cn[0] & 0xffff0000u : (uint32_t)cn[0] << 16);
+        }
+      *reinterpret_cast<f32x2*>(&s_in[wave][ng][2 * cg]) = v[0];
+      *reinterpret_cast<f32x2*>(&s_in[wave][ng][16 + 2 * cg]) = v[1];
     }
     // the state in front of the chunk
     float a[K][4][2], h[K + 1][4][2];
@@ -362,14 +390,14 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
     for (int j = 0; j < 2; ++j) {
       const f32x4 hs = *reinterpret_cast<const f32x4*>(&s_hs[j][tid][0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[0][i][j] = fmaf(__builtin_amdgcn_exp2f(dsum[i] * A[i][j]), hs[i], hn[i][j]);
+      for (int i = 0; i < 4; ++i) h[0][i][j] = t > 0 ? fmaf(__builtin_amdgcn_exp2f(dsum[i] * A[i][j]), hs[i], hn[i][j]) : hs[i];
     }
-    __syncthreads();
+    block_sync<SL>();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (k % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+      if (k % 2 == 0) tile_step();
       const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[k][l_ch]), dx = *reinterpret_cast<const f32x4*>(&s_dx[k][l_ch]);
-      const f32x2 b = *reinterpret_cast<const f32x2*>(&s_b[k][n0]);
+      const f32x2 b = *reinterpret_cast<const f32x2*>(&s_in[wave][k][ng * 2]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -381,11 +409,11 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
       // the next chunk's loads start where half of this one's states and decays are no longer held
-      if (k == K / 2 - 1 && t > 0) fetch(t - K);
-      __builtin_amdgcn_sched_barrier(0);
+      if (k == K / 2 - 1 && t > 0) fetch(t - K, std::false_type{});
+      tile_step();
       const f32x4 d = *reinterpret_cast<const f32x4*>(&s_d[k][l_ch]), dx = *reinterpret_cast<const f32x4*>(&s_dx[k][l_ch]);
       const f32x4 gy = *reinterpret_cast<const f32x4*>(&s_dy[k][l_ch]);
-      const f32x2 b = *reinterpret_cast<const f32x2*>(&s_b[k][n0]), cc = *reinterpret_cast<const f32x2*>(&s_c[k][n0]);
+      const f32x2 b = *reinterpret_cast<const f32x2*>(&s_in[wave][k][ng * 2]), cc = *reinterpret_cast<const f32x2*>(&s_in[wave][k][16 + ng * 2]);
       float u[4], e[4], yo[4], vb[2] = {0.f, 0.f}, vc[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -421,13 +449,14 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       }
       // sums over channels
       const float b0 = sum8(vb[0]), b1 = sum8(vb[1]), c0 = sum8(vc[0]), c1 = sum8(vc[1]);
-      if (cg == 0) *reinterpret_cast<f32x4*>(&s_bc[wave][k][ng * 4]) = f32x4{b0, b1, c0, c1};
+      if (cg == 0) *reinterpret_cast<f32x4*>(&s_bc[part][met][wave][k][ng * 4]) = f32x4{b0, b1, c0, c1};
     }
-    __syncthreads();
+    block_sync<SL>();
 #pragma unroll
     for (int i = 0; i < PP; ++i) {
       const int r = prow + i * ROWS;
       if (t + r >= len || !on) continue;
+      const uint32_t oo = pair_at(fresh(lane), C);
       float u = 0.f, e = 0.f, yo = 0.f;
 #pragma unroll
       for (int s = 0; s < SL; ++s) {
@@ -447,31 +476,39 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       accD = fmaf(gv, xv, accD);
       accb += draw;
     }
-#pragma unroll
-    for (int i = 0; i < BCN; ++i) {
-      const int q = tid + i * 256, r = q / (2 * N), m = q / N & 1, n = q % N;
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < Sh::CB; ++w) v += s_bc[w * SL + n / 16][r][(n % 16) / 2 * 4 + 2 * m + (n & 1)];
-      if (t + r < len) *byte_at(pbc + i * (256 / (2 * N)) * (int64_t)p.G * (2 * N), pbo) = v;
-    }
     row -= K;
-    pbc -= K * (int64_t)p.G * (2 * N);
+    // the channel blocks' sums of dB and dC for the chunks since the last meeting; the next ones go to the other half of s_bc, and
+    // this one is used again only behind the next meeting
+    if (++met == F || t == 0) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < F * K * 2 * N / 256; ++i) {
+        const int q = tid + i * 256, f = q / (K * 2 * N), r = q / (2 * N) % K, m = q / N & 1, n = q % N;
+        const int tok = t + (met - 1 - f) * K + r;
+        if (f >= met || tok >= len) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < CB; ++w) v += s_bc[part][f][w * SL + n / 16][r][(n % 16) / 2 * 4 + 2 * m + (n & 1)];
+        pbc[(int64_t)tok * p.G * (2 * N) + m * N + n] = v;
+      }
+      met = 0;
+      part ^= 1;
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (in0 + l_ch + i >= p.Cg) continue;
-      const int64_t at = (int64_t)lc[i] * N + n0 + j;
+      const int64_t at = (int64_t)chan(lane, i) * N + n0 + j;
       p.pA[(int64_t)slot * C * N + at] = dA[i][j];
       if (sp.first && p.dS0) p.dS0[(int64_t)sp.n * C * N + at] = carry[i][j];
     }
-  // D and the bias: the token rows of a channel
+  // D and the bias: the lanes of a channel
   __syncthreads();
   float* red = &s_u[0][0][0];
-  red[tid] = accD;
-  red[256 + tid] = accb;
+  red[prow * CH + pc] = accD;
+  red[256 + prow * CH + pc] = accb;
   __syncthreads();
   if (prow == 0 && on) {
     float vD = 0.f, vb = 0.f;
@@ -480,6 +517,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       vD += red[r * CH + pc];
       vb += red[256 + r * CH + pc];
     }
+    const int c = g * p.Cg + in0 + pc;
     p.pD[(int64_t)slot * 2 * C + c] = vD;
     p.pD[(int64_t)slot * 2 * C + C + c] = vb;
   }

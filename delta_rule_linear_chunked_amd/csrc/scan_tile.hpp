@@ -34,6 +34,13 @@ __device__ __forceinline__ void here(float (&v)[8]) {
 // Ends the branch of a whole tile's loads: without it the compiler joins them with those of a cut tile, whose addresses are the lanes'
 // own, and forms 64-bit addresses for both.
 __device__ __forceinline__ void whole_tile() { asm volatile("; whole tile" ::: "memory"); }
+// A lane's offset (or number) as a value of its own: what is computed from it is computed where it is used. Loads from a uniform pointer
+// want 32-bit offsets beside them; those that a loop keeps are kept as 64 bits and added for each load (scan 220 -> XXX us), or spilled, and
+// the reload of a spilled register waits for every load in front of it (gradients 340 -> 257 us).
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 // A value of the lower half's token and of the upper half's, in both halves.
 __device__ __forceinline__ void both_halves(float v, float& low, float& high) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
@@ -66,29 +73,30 @@ __device__ __forceinline__ float raw_value(uint32_t v) {
 }
 
 // An input [tokens, channels] as a wave reads it: a uniform pointer to the tile's first token, moved on with the tile,
-// and the lane's offset in it, 32 bits of bytes (token strides are at most 2^24 elements), which the loads add by themselves.
+// and the lane's offset in it, 32 bits of bytes (token strides are at most 2^24 elements), which the loads add by themselves; formed for
+// each tile (see fresh).
 template <typename InT>
 struct Rows {
   const InT* at;
   int64_t ts;
-  uint32_t off;
   int half, col;
   __device__ __forceinline__ void init(const void* base, int64_t first, int64_t ts_, int half_, int col_) {
     at = static_cast<const InT*>(base) + first;
     ts = ts_;
     half = half_;
     col = col_;
-    off = (uint32_t)(half * ts_ + col_) * sizeof(InT);
   }
   // own tokens 2 i + half; `left`: tokens from the tile's first to the end (those past it are read from the last and not used)
   __device__ __forceinline__ void whole(uint32_t (&v)[TILE_OWN]) const {
     const InT* q = at;
+    const uint32_t o = fresh(col) * sizeof(InT) + (fresh(half) ? (uint32_t)ts * sizeof(InT) : 0u);
 #pragma unroll
-    for (int i = 0; i < TILE_OWN; ++i, q += 2 * ts) v[i] = raw_bits(byte_at(q, off));
+    for (int i = 0; i < TILE_OWN; ++i, q += 2 * ts) v[i] = raw_bits(byte_at(q, o));
   }
   __device__ __forceinline__ void part(uint32_t (&v)[TILE_OWN], int left) const {
+    const int h = (int)fresh(half), c = (int)fresh(col);
 #pragma unroll
-    for (int i = 0; i < TILE_OWN; ++i) v[i] = raw_bits(at + ((int64_t)min(2 * i + half, left - 1) * ts + col));
+    for (int i = 0; i < TILE_OWN; ++i) v[i] = raw_bits(at + ((int64_t)min(2 * i + h, left - 1) * ts + c));
   }
 };
 
