@@ -139,18 +139,24 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
         __syncthreads();
       }
       InT* row = y;
+      if constexpr (SL > 1) row += 2 * sl * (int64_t)p.C;
+      // (of SL pairs a wave has one; in a whole tile lanes past the last channel write that one's outputs again: stores under a condition
+      // would be waited for with the next tile's inputs)
 #pragma unroll
-      for (int i = 0; i < O; ++i, row += 2 * (int64_t)p.C) {
-        if (SL > 1 && i % SL != sl) continue;
-        float o = v[i];
+      for (int q = 0; q < O / SL; ++q, row += 2 * SL * (int64_t)p.C) {
+        float o = v[q], x = xv[q], z = zv[q];
         if constexpr (SL > 1) {
           o = 0.f;
 #pragma unroll
-          for (int w = 0; w < SL; ++w) o += s_y[buf][w][i][lane];
+          for (int w = 0; w < SL; ++w) {
+            o += s_y[buf][w][q * SL + sl][lane];
+            x = w == 0 || sl == w ? xv[q * SL + w] : x;
+            z = w == 0 || sl == w ? zv[q * SL + w] : z;
+          }
         }
-        o = fmaf(D, xv[i], o);
-        const float sg = zv[i] * sigmoid_f(zv[i]);
-        if (on && (!CUT || t + 2 * i + half < len)) *byte_at(row, (fresh(c) + (fresh(half) ? (uint32_t)p.C : 0u)) * (uint32_t)sizeof(InT)) = (InT)(o * (gate ? sg : 1.f));
+        o = fmaf(D, x, o);
+        const float sg = z * sigmoid_f(z);
+        if (!CUT || (on && t + 2 * (q * SL + sl) + half < len)) *byte_at(row, (fresh(c) + (fresh(half) ? (uint32_t)p.C : 0u)) * (uint32_t)sizeof(InT)) = (InT)(o * (gate ? sg : 1.f));
       }
       y += K * (int64_t)p.C;
     }
@@ -159,6 +165,7 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
   const int whole = len / K * K;
   if (whole > 0) {
     fetch(0);
+    arrived();
     for (int t = 0; t < whole; t += K) tokens(t, std::false_type{});
   }
   if (whole < len) {

@@ -178,18 +178,23 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
       __syncthreads();
     }
     InT* row = y;
+    if constexpr (SL > 1) row += 2 * sl * (int64_t)p.C;
 #pragma unroll
-    for (int i = 0; i < O; ++i, row += 2 * (int64_t)p.C) {
-      if (SL > 1 && i % SL != sl) continue;
-      float o = v[i];
+    for (int q = 0; q < O / SL; ++q, row += 2 * SL * (int64_t)p.C) {  // (as for a wave on its own)
+      float o = v[q], x = xv[q];
+      uint32_t raw = zn[q];
       if constexpr (SL > 1) {
         o = 0.f;
 #pragma unroll
-        for (int s = 0; s < SL; ++s) o += s_y[ts * SL + s][i][lane];
+        for (int s = 0; s < SL; ++s) {
+          o += s_y[ts * SL + s][q * SL + sl][lane];
+          x = s == 0 || sl == s ? xv[q * SL + s] : x;
+          raw = s == 0 || sl == s ? zn[q * SL + s] : raw;
+        }
       }
-      o = fmaf(D, xv[i], o);
-      const float zv = raw_value<InT>(zn[i]), sg = zv * sigmoid_f(zv);
-      if (on && (!CUT || t + 2 * i + half < len)) *byte_at(row, (fresh(c) + (fresh(half) ? (uint32_t)p.C : 0u)) * (uint32_t)sizeof(InT)) = (InT)(o * (gate ? sg : 1.f));
+      o = fmaf(D, x, o);
+      const float zv = raw_value<InT>(raw), sg = zv * sigmoid_f(zv);
+      if (!CUT || (on && t + 2 * (q * SL + sl) + half < len)) *byte_at(row, (fresh(c) + (fresh(half) ? (uint32_t)p.C : 0u)) * (uint32_t)sizeof(InT)) = (InT)(o * (gate ? sg : 1.f));
     }
     y += IT * (int64_t)p.C;
     par ^= 1;
@@ -197,6 +202,7 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
   const int whole = len / IT * IT;
   if (whole > 0) {
     fetch(0);
+    arrived();
     for (int t0 = 0; t0 < whole; t0 += IT) tokens(t0, std::false_type{});
   }
   if (whole < len) {  // (waves whose tile lies past the end read the last token)

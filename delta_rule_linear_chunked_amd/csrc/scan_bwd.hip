@@ -99,10 +99,11 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
     for (int i = 0; i < O; ++i) {
       tile_step();
       if (i % (O / 2) == 0 && (i == 0 || !CUT || t + SCAN_CHUNK < len)) {
-        if (on && (t > 0 || i > 0)) store_states(ck, h);  // (a segment begins at zero)
+        // (lanes and waves that share a channel write the same; stores under a condition would be waited for with the next tile's inputs)
+        store_states(ck, h);
         float lo, hi;
         both_halves(sumd, lo, hi);
-        if (on && sl == 0 && half == 0) *ckd = lo + hi;
+        *ckd = lo + hi;
         ck += (int64_t)p.C * N;
         ckd += p.C;
       }
@@ -130,6 +131,7 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
   const int whole = len / K * K;
   if (whole > 0) {
     fetch(0);
+    arrived();
     for (int t = 0; t < whole; t += K) tokens(t, std::false_type{});
   }
   if (whole < len) {
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   typedef uint32_t Raw2 __attribute__((ext_vector_type(2 * sizeof(InT) / 4)));
   const InT* Bb = static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + last) * p.b_ts + g * N + sl * 16;
   const InT* Cb = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + (sp.t0 + last) * p.c_ts + g * N + sl * 16;
-  const bool soft = p.softplus != 0;
+  const bool soft = p.softplus != 0, full = in0 + CH <= p.Cg;
   float accD = 0.f, accb = 0.f;
   uint32_t xn[PP], dn[PP], zn[PP], yn[PP];
   f32x2 hn[4];
@@ -345,6 +347,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   // this workgroup's part of dB and dC: 2 N values to a token
   float* pbc = p.pBC + (((int64_t)(blk - g * p.cblocks) * p.nbatch * p.T + row0) * p.G + g) * (2 * N);
   if (len > 0) fetch(last, std::true_type{});
+  arrived();
   int met = 0;  // chunks since the last meeting, and which half of s_bc they use
   int part = 0;
   for (int t = last; len > 0 && t >= 0; t -= K) {
@@ -452,10 +455,8 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       if (cg == 0) *reinterpret_cast<f32x4*>(&s_bc[part][met][wave][k][ng * 4]) = f32x4{b0, b1, c0, c1};
     }
     block_sync<SL>();
-#pragma unroll
-    for (int i = 0; i < PP; ++i) {
+    auto outputs = [&](int i) {
       const int r = prow + i * ROWS;
-      if (t + r >= len || !on) continue;
       const uint32_t oo = pair_at(fresh(lane), C);
       float u = 0.f, e = 0.f, yo = 0.f;
 #pragma unroll
@@ -475,6 +476,15 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       }
       accD = fmaf(gv, xv, accD);
       accb += draw;
+    };
+    if (full && t + K <= len) {
+#pragma unroll
+      for (int i = 0; i < PP; ++i) outputs(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PP; ++i)
+        if (t + prow + i * ROWS < len && on) outputs(i);
+      arrived();
     }
     row -= K;
     // the channel blocks' sums of dB and dC for the chunks since the last meeting; the next ones go to the other half of s_bc, and
