@@ -182,22 +182,22 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
 }
 
 // Segments and kernels, by times in us as measured (bf16, 16 states, with z).
-// A wave walks a segment of 32 channels x 16 states: 0.195 a token, also where two share a SIMD for half of the time, and k waves a
-// SIMD take 0.8 k times as long. A sequence that is cut costs 0.73 of the main pass again (the segments' own states), what
-// 20 tokens of each segment cost, and 5. 1 x 8192 tokens, 2048 channels: segments of 64 181, 128 161, 256 157, 512 198, 1024 360, whole 1569.
-// With a workgroup's waves along the tokens the decays are formed once: a workgroup takes 6.4 for 128 tokens of 32 channels x 16
-// states and fills a CU. 4 x 2048 tokens, 2048 channels: 105, in segments 145; 64 x 256 tokens: 239, a wave a sequence 149.
-// Backward: 0.74 a token, 0.13 of it again for a cut sequence and what 10 tokens cost. 1 x 8192 tokens, 2048 channels: segments of 64 405,
-// 128 365, 256 350, 512 539, whole 6190.
+// A wave walks a segment of 32 channels x 16 states: 0.17 a token, also where two share a SIMD for half of the time, and k waves a
+// SIMD take 0.85 k times as long. A sequence that is cut costs 0.6 of the main pass again (the segments' own states), what
+// 20 tokens of each segment cost, and 8. 1 x 8192 tokens, 2048 channels: segments of 64 171, 128 147, 256 144, 512 169, 1024 306, whole 1396.
+// With a workgroup's waves along the tokens the decays are formed once: a workgroup takes 6 for 128 tokens of 32 channels x 16
+// states and fills a CU. 4 x 2048 tokens, 2048 channels: 103, in segments 129; 64 x 256 tokens: 213, a wave a sequence 133.
+// Backward: 0.62 a token, 0.1 of it again for a cut sequence and what 10 tokens cost. 1 x 8192 tokens, 2048 channels: segments of 64 366,
+// 128 323, 256 308, 512 454, whole 5066.
 dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
   dr::ScanPlan pl{};
   const int64_t T = d->seqlen, SL = d->state_dim / 16, tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE);
-  const double token = backward ? 0.74 : 0.195, again = backward ? 1.13 : 1.73, own = backward ? 10 : 20;
+  const double token = backward ? 0.62 : 0.17, again = backward ? 1.1 : 1.6, own = backward ? 10 : 20;
   // (packed: as many whole segments as the tokens fill, and half of one at each sequence's end)
   const double waves = (double)(tiles * SL), ends = packed ? 0.5 * d->num_seqs : 0, rows = packed ? 1 : (double)d->num_seqs;
   auto load = [&](double n) {
     const double k = std::ceil((rows * n + ends) * waves / 1024);
-    return k > 1 ? 0.8 * k : 1.0;
+    return k > 1 ? 0.85 * k : 1.0;
   };
   double best = load(1) * T * token;
   int64_t seg = ceil_div(T, 8) * 8;
@@ -206,14 +206,14 @@ dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
     if (n > (double)(T / 16)) n = (double)(T / 16);
     if (n < 2) continue;
     const int64_t s = ceil_div(ceil_div(T, (int64_t)n), 16) * 16;
-    const double cost = load(std::ceil((double)T / s)) * (s + own) * token * again + 5;
+    const double cost = load(std::ceil((double)T / s)) * (s + own) * token * again + 8;
     if (cost < best) {
       best = cost;
       seg = s;
     }
   }
   const int64_t force = env_int("DR_SCAN_BLOCK");  // for tuning and tests: 1 wherever sequences are whole, 2 never
-  const double block = std::ceil((double)d->num_seqs * tiles / 256) * (ceil_div(T * SL, 128) * 6.4 + 1);
+  const double block = std::ceil((double)d->num_seqs * tiles / 256) * (ceil_div(T * SL, 128) * 6.0 + 1);
   if (!backward && force != 2 && (block < best || force == 1)) {
     pl.block = true;
     seg = ceil_div(T, 8) * 8;
