@@ -3,7 +3,10 @@
 // A few operations per value: bound by memory. A lane has one 16-byte piece of the channels (or one channel where rows are
 // not aligned), a wave a run of consecutive tokens whose last inputs slide through registers, so an input is read once
 // (and the width - 1 in front of a run again). A run that holds the ends of packed sequences is walked in
-// pieces, one per sequence.
+// pieces, one per sequence. Loads are issued a batch of tokens in front of their use.
+//
+// 4 x 4096 x 2048 bf16: 30 us (134 MB, 26 at the copy rate). Backward, packed, fp32, 1531 channels (rows not aligned: single channels): 32 us and
+// 4 for the sums of dw (28). Step, 512 sequences x 4096 channels: 9.7 us a call (33 MB, 6.5).
 #include "scan.hpp"
 
 namespace dr {

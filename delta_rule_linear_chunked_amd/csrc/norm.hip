@@ -5,6 +5,10 @@
 // read once and every output is written once; the weights stay in registers over the rows of a workgroup.
 // 8 bits: p = h w does not contain the mean, so codes and the row's scale come from p exactly as the state cache's from
 // a state, and the statistic only multiplies the scale.
+//
+// Bound by memory where there are rows enough: 16384 x 2048 bf16 with residual and codes 56 us (235 MB, 46 at the copy rate), backward 49 and 5 for the
+// sums of dw (268 MB, 52); 1333 x 1531 fp32 with e4m3 codes 9.3 (27 MB, 5.2), one row 2.4. Stores around the caches: between 10% less and
+// 10% more time from 128 MiB on, without a rule, so they are ordinary.
 #include <type_traits>
 
 #include "scan.hpp"
