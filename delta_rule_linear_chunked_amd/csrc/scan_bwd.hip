@@ -11,8 +11,8 @@
 // the tokens in reverse. A lane's square of channels and states shares the two kinds of sums between lanes evenly: over states (dx,
 // dd, y) across the lanes' rows, over channels (dB, dC) within eight lanes.
 //
-// 2 x 4096 x 2048, 16 states, bf16: 346 us, of them states 104, join 10, gradients 246 (the vector units issue 84% of the time, about
-// 1550 instructions for a chunk of 32 channels x 16 states: 830 of the formulas, 290 sums across lanes, 430 inputs, outputs and
+// 2 x 4096 x 2048, 16 states, bf16: 341 us, of them states 104, join 10, gradients 240 (the vector units issue 84% of the time, about
+// 1480 instructions for a chunk of 32 channels x 16 states: 830 of the formulas, 250 sums across lanes, 400 inputs, outputs and
 // addresses), dB and dC 9, dA and the rest 5. Checkpoints are 134 MB, written and read; one for every 4th token would halve the registers of a chunk and
 // double that.
 #include "scan_tile.hpp"
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   __shared__ float s_u[SL][K][CH], s_e[SL][K][CH], s_y[GATE ? SL : 1][GATE ? K : 1][GATE ? CH : 1];
   __shared__ __align__(16) float s_bc[2][F][4][K][32];
   // what a lane needs of its pairs again at the end of a chunk, and its starting state, wait here instead of in registers
-  __shared__ __align__(16) float s_own[GATE ? 4 : 2][PP][256], s_hs[2][256][4];
+  __shared__ __align__(16) float s_own[GATE ? 3 : 2][PP][256], s_hs[2][256][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int sl = wave % SL, cb = wave / SL;
   const int per = p.G * p.cblocks;
@@ -367,9 +367,9 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       s_own[1][i][tid] = soft ? sr : 1.f;
       if constexpr (GATE) {
         const float zv = raw_value<InT>(zn[i]);
-        s_own[2][i][tid] = zv;
-        s_own[3][i][tid] = gv;
-        gv *= zv * sigmoid_f(zv);
+        const float sz = sigmoid_f(zv);
+        s_own[2][i][tid] = gv * (sz * fmaf(zv, 1.f - sz, 1.f));  // dy silu'(z)
+        gv *= zv * sz;
       }
       here(dv);
       here(gv);
@@ -452,11 +452,16 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
         *to = lane & 8 ? r1 : r0;
       }
       if constexpr (GATE) {  // (one channel a row of 16 lanes: 0, 1, 2, 3)
-        const float v = dpp_add<0x128>(pair16(pair32(yo[0], yo[2]), pair32(yo[1], yo[3])));
+        float v = dpp_add<0x128>(pair16(pair32(yo[0], yo[2]), pair32(yo[1], yo[3])));
+        here(v);  // (in the branch below a sum across lanes is two instructions)
         if (!(lane & 8)) s_y[sl][k][l_ch + 2 * (lane >> 5) + ((lane >> 4) & 1)] = v;
       }
       // sums over channels
-      const float b0 = sum8(vb[0]), b1 = sum8(vb[1]), c0 = sum8(vc[0]), c1 = sum8(vc[1]);
+      float b0 = sum8(vb[0]), b1 = sum8(vb[1]), c0 = sum8(vc[0]), c1 = sum8(vc[1]);
+      here(b0);
+      here(b1);
+      here(c0);
+      here(c1);
       if (cg == 0) *reinterpret_cast<f32x4*>(&s_bc[part][met][wave][k][ng * 4]) = f32x4{b0, b1, c0, c1};
     }
     block_sync<SL>();
@@ -476,8 +481,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       *byte_at(static_cast<InT*>(p.ddt) + base, oo) = (InT)draw;
       *byte_at(static_cast<InT*>(p.dx) + base, oo) = (InT)fmaf(u, s_d[r][pc], D * gv);
       if constexpr (GATE) {
-        const float zv = s_own[2][i][tid], sz = sigmoid_f(zv);
-        *byte_at(static_cast<InT*>(p.dz) + base, oo) = (InT)(s_own[3][i][tid] * fmaf(D, xv, yo) * (sz * fmaf(zv, 1.f - sz, 1.f)));
+        *byte_at(static_cast<InT*>(p.dz) + base, oo) = (InT)(s_own[2][i][tid] * fmaf(D, xv, yo));
       }
       accD = fmaf(gv, xv, accD);
       accb += draw;

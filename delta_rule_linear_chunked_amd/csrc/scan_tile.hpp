@@ -36,7 +36,7 @@ __device__ __forceinline__ void here(float (&v)[8]) {
 __device__ __forceinline__ void whole_tile() { asm volatile("; whole tile" ::: "memory"); }
 // A lane's offset (or number) as a value of its own: what is computed from it is computed where it is used. Loads from a uniform pointer
 // want 32-bit offsets beside them; those that a loop keeps are kept as 64 bits and added for each load, or spilled, and the reload of a
-// spilled register waits for every load in front of it (gradients of 2 x 4096 x 2048: 340 us so, 247 without).
+// spilled register waits for every load in front of it (gradients of 2 x 4096 x 2048: 340 us so, 240 without).
 __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   asm volatile("" : "+v"(v));
   return v;
