@@ -185,6 +185,7 @@ struct ScanParams {
   int32_t C, G, Cg;        // channels, groups, channels of a group
   int32_t tiles;           // channel tiles of a group
   int32_t nseq, nbatch;
+  int32_t run;         // sequences of a workgroup in a step
   int32_t softplus;
   int32_t seg;             // tokens of a segment
   int32_t nseg;            // fixed length: segments of a sequence; packed: more than 1 if any may have more

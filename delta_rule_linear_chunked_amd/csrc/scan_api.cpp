@@ -468,10 +468,14 @@ int dr_scan_step(const void* x, const void* dt, const float* A, const void* B, c
   st = check_ptrs({{x, "x", e, true}, {dt, "dt", e, true}, {A, "A", 16, true}, {B, "B", 16, true}, {C, "C", 16, true},
                    {D, "D", 16, false}, {z, "z", e, false}, {dt_bias, "dt_bias", 16, false}, {S, "S", 16, true}, {y, "y", e, true}});
   if (st) return st;
-  if (!dr::launch_fits(dims->num_seqs * ceil_div(dims->channels, dr::scan_step_channels((int)dims->state_dim)), 256))
+  const int64_t groups = dims->num_seqs * ceil_div(dims->channels, dr::scan_step_channels((int)dims->state_dim));
+  if (!dr::launch_fits(groups, 256))
     return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   dr::ScanParams p = scan_params(dims);
   set_opts(p, opts);
+  // sequences of a workgroup: 512 x 4096 channels, 16 states: 1 64.8 us, 2 52.6, 4 51.1, 8 53.1; 8 sequences: 3.2, 3.6, 4.4, 6.0
+  p.run = 1;
+  while (p.run < 4 && groups >= 4096 * p.run) p.run *= 2;
   p.x = x; p.dt = dt; p.A = A; p.B = B; p.Cm = C; p.D = D; p.z = z; p.bias = dt_bias; p.S = S; p.y = y;
   return done(dr::launch_scan_step(p, (int)dims->state_dim, dims->in_dtype == DR_BF16, stream), "selective scan step");
 }

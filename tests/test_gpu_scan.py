@@ -94,7 +94,7 @@ def test_views_and_pools():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("N,S,C,G", [(16, 1, 1, 1), (16, 5, 130, 2), (32, 3, 65, 1), (64, 4, 48, 3), (16, 70, 64, 1)])
+@pytest.mark.parametrize("N,S,C,G", [(16, 1, 1, 1), (16, 5, 130, 2), (32, 3, 65, 1), (64, 4, 48, 3), (16, 70, 64, 1), (16, 4099, 66, 1), (64, 2600, 40, 2)])
 def test_step(N, S, C, G, dtype):
     # four tokens one by one from rows of a pool, against the definition over all of them
     T = 4
