@@ -6,7 +6,7 @@
 // pieces, one per sequence. Loads are issued a batch of tokens in front of their use.
 //
 // 4 x 4096 x 2048 bf16: 30 us (134 MB, 26 at the copy rate). Backward, packed, fp32, 1531 channels (rows not aligned: single channels): 32 us and
-// 4 for the sums of dw (28). Step, 512 sequences x 4096 channels: 9.7 us a call (33 MB, 6.5).
+// 4 for the sums of dw (28). Step, 512 sequences x 4096 channels: 9.1 us in a graph (33 MB, 6.5).
 #include "scan.hpp"
 
 namespace dr {
@@ -59,6 +59,9 @@ struct Conv {
   }
   __device__ __forceinline__ void store(void* rows, int64_t row, int64_t stride, const V& v) const {
     if (in) *reinterpret_cast<V*>(byte_at(static_cast<InT*>(rows) + row * stride, off)) = v;
+  }
+  __device__ __forceinline__ void store_same(void* rows, int64_t row, int64_t stride, const V& v) const {
+    *reinterpret_cast<V*>(byte_at(static_cast<InT*>(rows) + row * stride, off)) = v;
   }
   // a row of an output that no cache will hold until it is read (whole lines: stores of single channels got slower that way)
   template <bool STREAM>
@@ -197,39 +200,49 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const ConvParams p) {
   const int cb = blockIdx.x % p.cblocks;
   const int n0 = (blockIdx.x / p.cblocks * CONV_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * p.run;
   const int c = (cb * 64 + (threadIdx.x & 63)) * VEC, n1 = min(n0 + p.run, p.nseq);
-  if (n0 >= n1 || c >= p.C) return;
+  if (n0 >= n1) return;
+  // (every lane stays: those past the last channels have the last ones again and store the same; `rows` is read from lanes by number)
   const Conv<InT, VEC, W> k(p, c);
+  const int lane = threadIdx.x & 63;
+  int rows = -1;  // lane i: of sequence n0 + i (at most 64 of them)
+  if (n0 + lane < n1) rows = (int)state_row(p.sidx, p.nslots, n0 + lane);
   V next[W];
-  int64_t snext;
-  auto fetch = [&](int n) {
-    snext = state_row(p.sidx, p.nslots, n);
-    if (snext < 0) return;
+  auto fetch = [&](int n) {  // (one without a stored state reads its input in its place)
+    const int s = __builtin_amdgcn_readlane(rows, n - n0);
+    const InT* x = static_cast<const InT*>(p.x) + n * p.x_bs;
+    const InT* old = s >= 0 ? static_cast<const InT*>(p.state_T) + (int64_t)s * (W - 1) * p.C : x;
+    const int64_t stride = s >= 0 ? p.C : 0;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) next[j] = k.load(p.state_T, snext * (W - 1) + j, p.C);
-    next[W - 1] = k.load(p.x, n, p.x_bs);
+    for (int j = 0; j < W - 1; ++j) next[j] = k.load(old, j, stride);
+    next[W - 1] = k.load(x, 0, 0);
   };
-  fetch(n0);
-  for (int n = n0; n < n1; ++n) {
+  auto token = [&](int n, auto more) {
     V r[W];
-    const int64_t s = snext;
-#pragma unroll
-    for (int j = 0; j < W; ++j) r[j] = next[j];
-    if (n + 1 < n1) fetch(n + 1);
-    if (s < 0) {  // no stored state
-      k.store(p.y, n, p.C, V{});
-      continue;
-    }
     float e[W][VEC], u[VEC];
 #pragma unroll
-    for (int j = 0; j < W; ++j) unpack<VEC, InT>(r[j], e[j]);
+    for (int j = 0; j < W; ++j) {
+      r[j] = next[j];
+      unpack<VEC, InT>(r[j], e[j]);
+    }
+    if constexpr (decltype(more)::value) fetch(n + 1);
     k.dot(e, u);
     if (p.silu)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) u[v] *= sigmoid_f(u[v]);
+    const int s = __builtin_amdgcn_readlane(rows, n - n0);
+    if (s >= 0) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) k.store(p.state_T, s * (W - 1) + j, p.C, r[j + 1]);
-    k.store(p.y, n, p.C, pack<VEC, InT>(u));
-  }
+      for (int j = 0; j < W - 1; ++j) k.store_same(p.state_T, (int64_t)s * (W - 1) + j, p.C, r[j + 1]);
+      k.store_same(p.y, n, p.C, pack<VEC, InT>(u));
+    } else {  // no stored state
+      k.store_same(p.y, n, p.C, V{});
+      arrived();
+    }
+  };
+  fetch(n0);
+  arrived();
+  for (int n = n0; n + 1 < n1; ++n) token(n, std::true_type{});
+  token(n1 - 1, std::false_type{});
 }
 
 // Gradient of a token's sum before the activation: dy, with silu times sigmoid(u) (1 + u sigmoid(-u)).

@@ -66,6 +66,10 @@ __device__ __forceinline__ float softplus_f(float v) {
   return fmaf(s, q, fmaxf(v, 0.f));
 }
 
+// Waits for what is in flight. Loads and stores are counted together: where paths with different numbers of stores meet, a wait for the loads
+// in front of them waits for the stores as well; with nothing in flight on one of the paths the number is the other's.
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // (vmcnt 0)
+
 // Row of a state pool that sequence n has; -1: none.
 __device__ __forceinline__ int64_t state_row(const int32_t* idx, int64_t slots, int64_t n) {
   if (!idx) return n;
@@ -250,6 +254,7 @@ __device__ __forceinline__ SlotSpan slot_span(const ScanParams& p, int slot) {
 constexpr int SCAN_TILE = 32;        // channels of a wave
 constexpr int SCAN_BLOCK_WAVES = 8;  // waves of a workgroup of scan_block.hip
 hipError_t launch_scan_block(const ScanParams& p, int n, bool bf16, hipStream_t s);
+constexpr int SCAN_STEP_RUN = 4;  // most sequences of a workgroup in a step
 constexpr int scan_step_channels(int n) { return 1024 / n; }  // channels of a workgroup of the step (4 states a lane)
 hipError_t launch_scan_plan(const ScanParams& p, hipStream_t s);
 hipError_t launch_scan_fwd(ScanParams p, const ScanPlan& pl, int n, bool bf16, hipStream_t s);

@@ -22,8 +22,10 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const ScanParams p) {
   const bool gate = p.z != nullptr;
   const InT* zs = static_cast<const InT*>(gate ? p.z : p.x);
   const int64_t zst = gate ? p.z_bs : p.x_bs;
+  // lane i: of sequence n0 + i. Read from lanes by number: the first channel's, which are there wherever a wave has a channel at all.
+  static_assert(LPC >= SCAN_STEP_RUN, "a sequence for each of them");
   const int lane = threadIdx.x & 63;
-  int rows = -1;  // lane i: of sequence n0 + i (at most 64 of them)
+  int rows = -1;
   if (n0 + lane < n1) rows = (int)state_row(p.sidx, p.nslots, n0 + lane);
   // the next sequence's inputs are loaded ahead of their use; one without a stored state reads A in its place
   f32x4 hn;

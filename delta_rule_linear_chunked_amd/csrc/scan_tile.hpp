@@ -41,9 +41,6 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   asm volatile("" : "+v"(v));
   return v;
 }
-// Waits for what is in flight. Loads and stores are counted together: where paths with different numbers of stores meet, a wait for the loads
-// in front of them waits for the stores as well; with nothing in flight on one of the paths the number is the other's.
-__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // (vmcnt 0)
 // A value of the lower half's token and of the upper half's, in both halves.
 __device__ __forceinline__ void both_halves(float v, float& low, float& high) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);

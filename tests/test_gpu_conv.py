@@ -95,7 +95,7 @@ def test_views_and_pools(C, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("N,C,W", [(1, 1, 2), (1, 512, 4), (5, 130, 3), (9, 264, 4), (70, 256, 4)])
+@pytest.mark.parametrize("N,C,W", [(1, 1, 2), (1, 512, 4), (5, 130, 3), (9, 264, 4), (70, 256, 4), (4099, 66, 4), (8195, 258, 3)])
 def test_step(N, C, W, dtype):
     # tokens one by one equal the convolution of all of them, bit for bit; unnamed rows stay
     T = 6
