@@ -327,6 +327,33 @@ def test_no_tokens(B, T):
     assert drl.norm_fwd(x, c["b"], fmt="int8")[1].shape == x.shape[:-1]
 
 
+@pytest.mark.parametrize("C", [66, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_steps_with_slots_outside_the_pool(dtype, C):
+    # more sequences than a wave has at a time, every third without a stored state: zeros there, the others as by themselves,
+    # and rows that nobody names stay
+    S, N = 4099, 16
+    t = scan_tensors(make_scan(seed_of("outside", dtype, C), 1, S, C, 1, N, dtype, n=1), dtype)
+    one = {k: (t[k] if k in ("A", "D", "bias") else t[k][0]) for k in SCAN_IN}
+    idx = np.random.default_rng(6).permutation(S + 5)[:S].astype(np.int32)
+    idx[::3] = np.where(np.arange(0, S, 3) % 2, -1, S + 5)
+    kept = torch.from_numpy(np.flatnonzero((idx >= 0) & (idx < S + 5))).cuda()
+    rows = torch.from_numpy(idx).cuda()[kept].long()
+    pool = torch.randn(S + 5, C, N, device="cuda")
+    window = torch.randn(S + 5, 3, C, device="cuda").to(t["x"].dtype)
+    w, b = torch.randn(C, 4, device="cuda"), torch.randn(C, device="cuda")
+    before, wbefore, own, wown = pool.clone(), window.clone(), pool[rows].clone(), window[rows].clone()
+    a = lambda f: [f(one[k]) for k in ("x", "dt")] + [one["A"]] + [f(one[k]) for k in ("B", "C")]  # noqa: E731
+    more = lambda f: dict(D=one["D"], z=f(one["z"]), dt_bias=one["bias"])  # noqa: E731
+    y = drl.scan_step(*a(lambda v: v), pool, **more(lambda v: v), state_idx=i32(idx))
+    u = drl.conv_step(one["x"], w, window, b, state_idx=i32(idx))
+    pick = lambda v: v[kept].contiguous()  # noqa: E731
+    assert torch.equal(y[kept], drl.scan_step(*a(pick), own, **more(pick))) and torch.equal(u[kept], drl.conv_step(pick(one["x"]), w, wown, b))
+    assert not y[::3].any() and not u[::3].any()
+    before[rows], wbefore[rows] = own, wown
+    assert torch.equal(pool, before) and torch.equal(window, wbefore)
+
+
 # ------------------------------------------------------------------------------------------------ all of them together
 def test_serving_run():
     # Four users: prompts of 1 to 100 tokens packed through norm, projections, convolution and scan into the users' slots,
