@@ -214,8 +214,8 @@ struct ScanParams {
   float* dbias;
   float* dS0;              // may be null
   float* rpart;            // [slots, C, N] as part, of the reverse pass
-  float* ck;               // [slots, seg / 8, C, N] local states at chunk starts
-  float* ckd;              // [slots, seg / 8, C] sums of the slot's steps before them
+  float* ck;               // [chunks, C, N] local states at chunk starts (slot_chunk)
+  float* ckd;              // [chunks, C] sums of the slot's steps before them
   float* pA;               // [slots, C, N] partial sums of dA
   float* pD;               // [slots, 2, C] of dD and of ddt_bias
   float* pBC;              // [channel blocks of a group, tokens, G, 2, N] partial sums of dB and dC
@@ -251,6 +251,16 @@ __device__ __forceinline__ SlotSpan slot_span(const ScanParams& p, int slot) {
   s.last = s.t0 + s.len >= end;
   return s;
 }
+constexpr int SCAN_CHUNK = 8;        // tokens whose states the gradient pass holds at once
+// Chunks of 8 tokens: the first one of a slot, and the number that all slots take. Packed slots lie one behind the other in the row: one
+// of L tokens from t0 takes (L + 7) / 8 chunks, at most one more than lie between t0 / 8 and (t0 + L) / 8, so each
+// slot in front adds one, however short it is (a whole segment's room for each would be sequences x T where they are not cut).
+__device__ __forceinline__ int64_t slot_chunk(const ScanParams& p, int slot, const SlotSpan& s) {
+  return p.cu ? s.t0 / SCAN_CHUNK + slot : (int64_t)slot * (p.seg / SCAN_CHUNK);
+}
+constexpr int64_t scan_chunks(int64_t T, int64_t slots, int64_t seg, bool packed) {
+  return packed ? T / SCAN_CHUNK + slots : slots * (seg / SCAN_CHUNK);
+}
 constexpr int SCAN_TILE = 32;        // channels of a wave
 constexpr int SCAN_BLOCK_WAVES = 8;  // waves of a workgroup of scan_block.hip
 hipError_t launch_scan_block(const ScanParams& p, int n, bool bf16, hipStream_t s);
@@ -260,7 +270,6 @@ hipError_t launch_scan_plan(const ScanParams& p, hipStream_t s);
 hipError_t launch_scan_fwd(ScanParams p, const ScanPlan& pl, int n, bool bf16, hipStream_t s);
 hipError_t launch_scan_step(const ScanParams& p, int n, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(ScanParams p, int n, bool bf16, hipStream_t s);
-constexpr int SCAN_CHUNK = 8;     // tokens whose states the gradient pass holds at once
 constexpr int scan_grad_channels(int n) { return 2048 / n; }  // channels of a workgroup of the gradient pass
 
 }  // namespace dr

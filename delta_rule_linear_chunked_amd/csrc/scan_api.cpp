@@ -259,7 +259,7 @@ Space scan_space(const dr_scan_dims* d, const dr::ScanPlan& pl, bool packed, boo
   }
   if (packed) s.tab = s.take((pl.slots + 2 * d->num_seqs + 2) * 4);
   if (backward) {
-    const int64_t chunks = pl.slots * (pl.seg / dr::SCAN_CHUNK);
+    const int64_t chunks = dr::scan_chunks(d->seqlen, pl.slots, pl.seg, packed);
     s.ck = s.take(chunks * cn * 4);
     s.ckd = s.take(chunks * C * 4);
     s.pA = s.take(pl.slots * cn * 4);
@@ -269,8 +269,8 @@ Space scan_space(const dr_scan_dims* d, const dr::ScanPlan& pl, bool packed, boo
   return s;
 }
 // Whether the sizes of a workspace stay within 64 bits.
-bool scan_space_fits(const dr_scan_dims* d, const dr::ScanPlan& pl) {
-  const double chunks = (double)pl.slots * (double)(pl.seg / 8 + 4);
+bool scan_space_fits(const dr_scan_dims* d, const dr::ScanPlan& pl, bool packed) {
+  const double chunks = packed ? (double)d->seqlen / 8 + 5 * (double)pl.slots : (double)pl.slots * (double)(pl.seg / 8 + 4);
   return chunks * (double)d->channels * (double)d->state_dim * 8 < 4e18 &&
          (double)grad_blocks(d) * (double)d->batch * (double)d->seqlen * (double)d->groups * (double)d->state_dim * 8 < 4e18;
 }
@@ -423,7 +423,7 @@ int dr_scan_workspace(const dr_scan_dims* dims, int packed, int backward, int64_
   if (st) return st;
   if (bytes == nullptr) return host_fail(DR_ERR_NULL, "`bytes` is NULL");
   const dr::ScanPlan pl = plan_scan(dims, packed != 0, backward != 0);
-  if (!scan_space_fits(dims, pl)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
+  if (!scan_space_fits(dims, pl, packed != 0)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   *bytes = scan_space(dims, pl, packed != 0, backward != 0).size;
   return DR_OK;
 }
@@ -444,7 +444,7 @@ int dr_scan_fwd(const void* x, const void* dt, const float* A, const void* B, co
   if (!st) st = dr::host_check_offsets(cu_seqlens, dims->num_seqs, dims->seqlen, stream);
   if (st || dims->num_seqs == 0) return st;
   const dr::ScanPlan pl = plan_scan(dims, packed, false);
-  if (!scan_fits(dims, pl, false) || !scan_space_fits(dims, pl)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
+  if (!scan_fits(dims, pl, false) || !scan_space_fits(dims, pl, packed)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   const Space sp = scan_space(dims, pl, packed, false);
   unsigned char* ws = nullptr;
   bool owned = false;
@@ -500,7 +500,7 @@ int dr_scan_bwd(const void* x, const void* dt, const float* A, const void* B, co
   if (!st) st = dr::host_check_offsets(cu_seqlens, dims->num_seqs, dims->seqlen, stream);
   if (st) return st;
   const dr::ScanPlan pl = plan_scan(dims, packed, true);
-  if (!scan_fits(dims, pl, true) || !scan_space_fits(dims, pl)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
+  if (!scan_fits(dims, pl, true) || !scan_space_fits(dims, pl, packed)) return host_fail(DR_ERR_UNSUPPORTED, kTooLarge);
   const Space sp = scan_space(dims, pl, packed, true);
   unsigned char* ws = nullptr;
   bool owned = false;

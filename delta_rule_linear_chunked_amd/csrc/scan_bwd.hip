@@ -56,9 +56,9 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
     Cr.init(p.Cm, sp.b * p.c_bs + sp.t0 * p.c_ts, p.c_ts, half, g * N + sl * 16 + (lane & 15));
     Y.init(p.dy, (sp.b * p.T + sp.t0) * (int64_t)p.C, p.C, half, c);
   }
-  const int64_t cps = p.seg / SCAN_CHUNK;
-  float* ck = p.ck + ((int64_t)slot * cps * p.C + c) * N + n0;
-  float* ckd = p.ckd + (int64_t)slot * cps * p.C + c;
+  const int64_t chunk0 = slot_chunk(p, slot, sp);
+  float* ck = p.ck + (chunk0 * p.C + c) * N + n0;
+  float* ckd = p.ckd + chunk0 * p.C + c;
   float sumd = 0.f;
   uint32_t xn[O], dn[O], zn[O], yn[O], bn[O], cn[O];
   auto fetch = [&](int step) {  // (as in the forward pass)
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   const int g = blk / p.cblocks, in0 = (blk - g * p.cblocks) * CH;  // the group, the first channel within it
   const SlotSpan sp = slot_span(p, slot);
   if (sp.n < 0) return;
-  const int len = sp.len, cps = p.seg / K, C = p.C;
+  const int len = sp.len, C = p.C;
   // as the lane of states and gradients: 4 channels, 2 states
   const int ng = lane >> 3, cg = lane & 7;
   const int l_ch = cb * 32 + cg * 4, n0 = sl * 16 + ng * 2;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   // bytes to the channel of lane l's pairs, and one row on in the upper lanes
   auto pair_at = [&](uint32_t l, int64_t ts) { return (uint32_t)(g * p.Cg + min(in0 + cb * 32 + (int)(l & 31), p.Cg - 1)) * E + (l & 32 ? (uint32_t)ts * E : 0u); };
   const float bias = p.bias ? p.bias[pair_at(lane, 0) / E] : 0.f, D = p.D ? p.D[pair_at(lane, 0) / E] : 0.f;
-  int64_t chunk = (int64_t)slot * cps + last / K;
+  int64_t chunk = slot_chunk(p, slot, sp) + last / K;
   // B and C: lane l brings states 2 (l % 8), + 1 of token l / 8
   typedef uint32_t Raw2 __attribute__((ext_vector_type(2 * sizeof(InT) / 4)));
   const InT* Bb = static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + last) * p.b_ts + g * N + sl * 16;
