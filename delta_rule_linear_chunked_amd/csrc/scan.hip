@@ -38,7 +38,7 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
   }
   const float bias = p.bias ? p.bias[c] : 0.f, D = !LOCAL && p.D ? p.D[c] : 0.f;
   if constexpr (!LOCAL) {
-    if (p.part) {
+    if (p.part && !sp.whole()) {
       load_states(p.part + ((int64_t)slot * p.C + c) * N + n0, h);
     } else if (p.S0) {
       const int64_t r = state_row(p.sidx, p.nslots, sp.n);
@@ -208,6 +208,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const ScanParams p) {
   if (e >= p.C * (N / 4)) return;
   const int c = e / (N / 4), j = e - c * (N / 4);
   const int first = p.cu ? p.slot_first[n] : n * p.nseg, past = p.cu ? p.slot_first[n + 1] : first + p.nseg;
+  if (past - first == 1) return;  // (a sequence that is not cut starts from S0 itself)
   f32x4 A = *reinterpret_cast<const f32x4*>(p.A + (int64_t)c * N + 4 * j), h = {0, 0, 0, 0};
   const int64_t r = state_row(p.sidx, p.nslots, n);
   if (p.S0 && r >= 0) h = *reinterpret_cast<const f32x4*>(p.S0 + (r * p.C + c) * N + 4 * j);

@@ -230,6 +230,8 @@ struct SlotSpan {
   int n, b, len;
   int64_t t0;
   bool first, last;
+  // (only then may a slot read the states that its call starts from: they may be the final ones, which a sequence's last slot writes)
+  __device__ __forceinline__ bool whole() const { return first && last; }
 };
 __device__ __forceinline__ SlotSpan slot_span(const ScanParams& p, int slot) {
   SlotSpan s;

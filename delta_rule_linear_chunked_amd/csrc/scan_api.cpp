@@ -189,30 +189,65 @@ int check_scan(const dr_scan_dims* d, const void* cu, bool step) {
 // states and fills a CU. 4 x 2048 tokens, 2048 channels: 103, in segments 129; 64 x 256 tokens: 213, a wave a sequence 133.
 // Backward: 0.62 a token, 0.1 of it again for a cut sequence and what 10 tokens cost. 1 x 8192 tokens, 2048 channels: segments of 64 366,
 // 128 323, 256 308, 512 454, whole 5066.
-dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
-  dr::ScanPlan pl{};
-  const int64_t T = d->seqlen, SL = d->state_dim / 16, tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE);
-  const double token = backward ? 0.62 : 0.17, again = backward ? 1.1 : 1.6, own = backward ? 10 : 20;
+struct ScanCost {
+  double token, again;
+  double waves;  // of a segment
+};
+// So many segments as give every SIMD 1 to 8 waves, or whole sequences.
+double few_segments(const dr_scan_dims* d, const ScanCost& c, bool packed, double own, int64_t* seg) {
+  const int64_t T = d->seqlen;
   // (packed: as many whole segments as the tokens fill, and half of one at each sequence's end)
-  const double waves = (double)(tiles * SL), ends = packed ? 0.5 * d->num_seqs : 0, rows = packed ? 1 : (double)d->num_seqs;
+  const double ends = packed ? 0.5 * d->num_seqs : 0, rows = packed ? 1 : (double)d->num_seqs;
   auto load = [&](double n) {
-    const double k = std::ceil((rows * n + ends) * waves / 1024);
+    const double k = std::ceil((rows * n + ends) * c.waves / 1024);
     return k > 1 ? 0.85 * k : 1.0;
   };
-  double best = load(1) * (ceil_div(T, 16) * 16) * token;  // (whole tiles: 37 tokens, 2048 channels 11.6, along the tokens 9.2; 24 tokens 8.9, 9.3)
-  int64_t seg = ceil_div(T, 8) * 8;
+  double best = load(1) * (ceil_div(T, 16) * 16) * c.token;  // (whole tiles: 37 tokens, 2048 channels 11.6, along the tokens 9.2; 24 tokens 8.9, 9.3)
+  *seg = ceil_div(T, 8) * 8;
   for (const int k : {1, 2, 3, 4, 6, 8}) {  // so many waves a SIMD
-    double n = std::floor((k * 1024 / waves - ends) / rows);
+    double n = std::floor((k * 1024 / c.waves - ends) / rows);
     if (n > (double)(T / 16)) n = (double)(T / 16);
     if (n < 2) continue;
     const int64_t s = ceil_div(ceil_div(T, (int64_t)n), 16) * 16;
-    const double cost = load(std::ceil((double)T / s)) * (s + own) * token * again + 8;
+    const double cost = load(std::ceil((double)T / s)) * (s + own) * c.token * c.again + 8;
     if (cost < best) {
       best = cost;
-      seg = s;
+      *seg = s;
     }
   }
+  return best;
+}
+// A packed row whose sequences' ends alone fill the GPU. The host knows its tokens and the number of its sequences, not their lengths. One of them may
+// hold nearly all tokens, so a row that is not cut counts as one walk over all of them, and segments as if every sequence were cut: the
+// tokens, and 20 more for each slot, at the rate of a full GPU, one segment behind them, and 0.25 for each step of a join over the
+// whole row. Slots: at each sequence's end half a segment, and no fewer than there are sequences.
+// 32768 tokens, 2048 channels, 64 sequences: segments of 64 507, 128 456, 256 458, 512 552, 1024 601; backward 1426, 1360, 1359, 1475, 1637.
+// 300 sequences, one of them with 20000 tokens: 601, 506, 459, 493, 759, whole 3714; backward 1654, 1536, 1477, 1434, 1528, whole 14979.
+// 2000 sequences, none cut: 497, whole 483; backward 2185, whole 1879 (the states' pass forms what a segment sends forward for each).
+double many_segments(const dr_scan_dims* d, const ScanCost& c, int64_t* seg) {
+  const double T = (double)d->seqlen, n = (double)d->num_seqs;
+  double best = std::ceil(T / 16) * 16 * c.token;
+  *seg = ceil_div(d->seqlen, 8) * 8;
+  for (int64_t s = 16; s < d->seqlen; s *= 2) {
+    if (T / s * c.waves > 8192) continue;  // (8 waves a SIMD; more would only add to the join)
+    const double slots = std::fmax(n, T / s + 0.5 * n);
+    const double cost = (0.85 * (T + 20 * slots) * c.waves / 1024 + s + 20) * c.token * c.again + 0.25 * T / s + 8;
+    if (cost < best) {
+      best = cost;
+      *seg = s;
+    }
+  }
+  return best;
+}
+dr::ScanPlan plan_scan(const dr_scan_dims* d, bool packed, bool backward) {
+  dr::ScanPlan pl{};
+  const int64_t T = d->seqlen, SL = d->state_dim / 16, tiles = d->groups * ceil_div(d->channels / d->groups, dr::SCAN_TILE);
+  const ScanCost c{backward ? 0.62 : 0.17, backward ? 1.1 : 1.6, (double)(tiles * SL)};
+  int64_t seg;
+  const bool many = packed && 0.5 * d->num_seqs * c.waves >= 1024;
+  const double best = many ? many_segments(d, c, &seg) : few_segments(d, c, packed, backward ? 10 : 20, &seg);
   const int64_t force = env_int("DR_SCAN_BLOCK");  // for tuning and tests: 1 wherever sequences are whole, 2 never
+  // (packed: as if each sequence had all tokens, so that a row of several comes here only where it is short)
   const double block = std::ceil((double)d->num_seqs * tiles / 256) * (ceil_div(T * SL, 128) * 6.0 + 1);
   if (!backward && force != 2 && (block < best || force == 1)) {
     pl.block = true;

@@ -160,7 +160,7 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
   if constexpr (BOTH) {
     float lo, hi;
     both_halves(sumd, lo, hi);
-    if (!on) return;
+    if (!on || sp.whole()) return;
     const int64_t at = ((int64_t)slot * p.C + c) * N + n0;
     store_states(p.part + at, h);
     store_states(p.rpart + at, R);
@@ -177,6 +177,7 @@ __global__ __launch_bounds__(256) void scan_join2_kernel(const ScanParams p) {
   if (e >= p.C * (N / 4)) return;
   const int c = e / (N / 4), j = e - c * (N / 4);
   const int first = p.cu ? p.slot_first[n] : n * p.nseg, past = p.cu ? p.slot_first[n + 1] : first + p.nseg;
+  if (past - first == 1) return;  // (a sequence that is not cut has S0 and dS_T themselves)
   const bool back = blockIdx.y == 1;
   f32x4 A = *reinterpret_cast<const f32x4*>(p.A + (int64_t)c * N + 4 * j), v = {0, 0, 0, 0};
   const float* from = back ? p.dST : p.S0;
@@ -258,6 +259,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   // channel i of lane l (those past the group's count as its last)
   auto chan = [&](uint32_t l, int i) { return g * p.Cg + min(in0 + cb * 32 + (int)(l & 7) * 4 + i, p.Cg - 1); };
   float A[4][2], carry[4][2], dA[4][2];
+  const bool cut = p.part && !sp.whole();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -265,9 +267,9 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
       const int64_t at = (int64_t)chan(lane, i) * N + n0 + j;
       A[i][j] = p.A[at] * LOG2E;
       dA[i][j] = 0.f;
-      const float* from = p.part ? p.part + (int64_t)slot * C * N : p.S0 ? p.S0 + (int64_t)sp.n * C * N : nullptr;
+      const float* from = cut ? p.part + (int64_t)slot * C * N : p.S0 ? p.S0 + (int64_t)sp.n * C * N : nullptr;
       s_hs[j][tid][i] = from ? from[at] : 0.f;
-      const float* back = p.part ? p.rpart + (int64_t)slot * C * N : p.dST ? p.dST + (int64_t)sp.n * C * N : nullptr;
+      const float* back = cut ? p.rpart + (int64_t)slot * C * N : p.dST ? p.dST + (int64_t)sp.n * C * N : nullptr;
       carry[i][j] = back ? back[at] : 0.f;
     }
   // as the lane of (token, channel) pairs: one channel, PP tokens of a chunk

@@ -23,3 +23,12 @@ def test_gradients_workspace_grows_with_tokens_and_not_with_sequences_times_toke
 def test_largest_packed_sizes_are_answered(lib):
     # 2^20 sequences in a row of 2^26 tokens: the sizes are those of the tokens, not refused as those of their product
     assert need(lib, "dr_scan_workspace", scan(T=1 << 26, C=4096, S=64, N=1 << 20), 1, 1) > 0
+
+
+@pytest.mark.parametrize("T,C,S", [(32768, 2048, 16), (8192, 1024, 32), (20000, 512, 64)])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_rows_of_many_sequences_are_cut(lib, T, C, S, backward):
+    # the lengths are not known on the host, and one sequence may hold nearly all tokens: whatever the number of the others, it is walked in
+    # segments of at most 2048 tokens, each of which has a state in the workspace
+    for n in (1, 2, 16, 64, 126, 127, 128, 200, 252, 253, 256, 300, 1000, 4096):
+        assert need(lib, "dr_scan_workspace", scan(T=T, C=C, S=S, N=n), 1, backward) >= (n + T // 2048) * C * S * 4, n
