@@ -46,7 +46,8 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
     }
   }
   const int len = sp.len;
-  const bool soft = p.softplus != 0, gate = !LOCAL && p.z != nullptr;
+  const float least = step_least(p.softplus != 0);
+  const bool gate = !LOCAL && p.z != nullptr;
   Rows<InT> X, T, Z, B;
   X.init(p.x, sp.b * p.x_bs + sp.t0 * p.x_ts, p.x_ts, half, c);
   T.init(p.dt, sp.b * p.dt_bs + sp.t0 * p.dt_ts, p.dt_ts, half, c);
@@ -85,8 +86,7 @@ __global__ __launch_bounds__(64 * SL) void scan_kernel(const ScanParams p) {
 #pragma unroll
     for (int i = 0; i < O; ++i) {
       xv[i] = raw_value<InT>(xn[i]);
-      const float raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw);
-      float own = soft ? sf : raw;
+      float own = step_f(raw_value<InT>(dn[i]) + bias, least);
       here(own);
       // (tokens past the end: a decay of one and nothing added)
       const bool inside = !CUT || t + 2 * i + half < len;

@@ -52,18 +52,24 @@ constexpr float LN2 = 0.6931471805599453f;
 __device__ __forceinline__ float sigmoid_f(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * LOG2E));
 }
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1].
+// A step d: softplus(v), or v itself. softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1].
 // log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: a small step (1e-3 and less is usual) keeps its relative precision, which log of
 // the rounded 1 + e would lose. 2 atanh(s) / s as a polynomial of s^2 in [0, 1/9], a Chebyshev fit of degree 4, off by 8e-9 of it.
-__device__ __forceinline__ float softplus_f(float v) {
-  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * LOG2E);
+// The rounding of the exponent p alone is |v| / 2 ULP of a small step (8 at -16): what -|v| differs from p LN2 by is put back. (For
+// infinities that is no number, and the smaller one of it and 1 is taken; e is 0.)
+// `least` is 0, or -infinity for v itself: it takes e to 0 and the maximum to v.
+__device__ __forceinline__ float step_least(bool softplus) { return softplus ? 0.f : -__builtin_inff(); }
+__device__ __forceinline__ float step_f(float v, float least) {
+  const float p = fmaf(-fabsf(v), LOG2E, least), left = fmaf(-p, LN2, -fabsf(v));
+  float e = __builtin_amdgcn_exp2f(p);
+  e = fmaf(e, fminf(left, 1.f), e);
   const float s = e * __builtin_amdgcn_rcpf(2.f + e), z = s * s;
   float q = 0.28174657f;
   q = fmaf(q, z, 0.27961419f);
   q = fmaf(q, z, 0.40024854f);
   q = fmaf(q, z, 0.66666316f);
   q = fmaf(q, z, 2.00000001f);
-  return fmaf(s, q, fmaxf(v, 0.f));
+  return fmaf(s, q, fmaxf(v, least));
 }
 
 // Waits for what is in flight. Loads and stores are counted together: where paths with different numbers of stores meet, a wait for the loads

@@ -47,7 +47,8 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
     s_carry[0][sl][1][lane] = f32x4{h[4], h[5], h[6], h[7]};
   }
   const int len = sp.len;
-  const bool soft = p.softplus != 0, gate = p.z != nullptr;
+  const float least = step_least(p.softplus != 0);
+  const bool gate = p.z != nullptr;
   const int64_t mine = sp.t0 + ts * K;  // the wave's tile; IT tokens further on after each
   Rows<InT> X, T, Z, B;
   X.init(p.x, sp.b * p.x_bs + mine * p.x_ts, p.x_ts, half, c);
@@ -88,8 +89,7 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
 #pragma unroll
     for (int i = 0; i < O; ++i) {
       xv[i] = raw_value<InT>(xn[i]);
-      const float raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw);
-      float own = soft ? sf : raw;
+      float own = step_f(raw_value<InT>(dn[i]) + bias, least);
       here(own);
       // (tokens past the end: a decay of one and nothing added)
       const bool inside = !CUT || t + 2 * i + half < len;

@@ -43,7 +43,8 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
   }
   const float bias = p.bias ? p.bias[c] : 0.f;
   const int len = sp.len;
-  const bool soft = p.softplus != 0, gate = BOTH && p.z != nullptr;
+  const float least = step_least(p.softplus != 0);
+  const bool gate = BOTH && p.z != nullptr;
   Rows<InT> X, T, Z, B, Y, Cr;
   X.init(p.x, sp.b * p.x_bs + sp.t0 * p.x_ts, p.x_ts, half, c);
   T.init(p.dt, sp.b * p.dt_bs + sp.t0 * p.dt_ts, p.dt_ts, half, c);
@@ -82,8 +83,7 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
     float dv[O], dx[O], gy[O], bo[O], co[O];
 #pragma unroll
     for (int i = 0; i < O; ++i) {
-      const float raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw);
-      float own = soft ? sf : raw;
+      float own = step_f(raw_value<InT>(dn[i]) + bias, least);
       here(own);
       // (tokens past the end: a decay of one, nothing in or out)
       const bool inside = !CUT || t + 2 * i + half < len;
@@ -292,6 +292,7 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
   typedef uint32_t Raw2 __attribute__((ext_vector_type(2 * sizeof(InT) / 4)));
   const InT* Bb = static_cast<const InT*>(p.B) + sp.b * p.b_bs + (sp.t0 + last) * p.b_ts + g * N + sl * 16;
   const InT* Cb = static_cast<const InT*>(p.Cm) + sp.b * p.c_bs + (sp.t0 + last) * p.c_ts + g * N + sl * 16;
+  const float least = step_least(p.softplus != 0);
   const bool soft = p.softplus != 0, full = in0 + CH <= p.Cg;
   float accD = 0.f, accb = 0.f;
   uint32_t xn[PP], dn[PP], zn[PP], yn[PP];
@@ -363,8 +364,8 @@ __global__ __launch_bounds__(256, 2) void scan_grad_kernel(const ScanParams p) {
     for (int i = 0; i < PP; ++i) {
       const int r = prow + i * ROWS;
       const bool inside = on && t + r < len;
-      const float xv = raw_value<InT>(xn[i]), raw = raw_value<InT>(dn[i]) + bias, sf = softplus_f(raw), sr = sigmoid_f(raw);
-      float dv = soft ? sf : raw, gv = raw_value<InT>(yn[i]);
+      const float xv = raw_value<InT>(xn[i]), raw = raw_value<InT>(dn[i]) + bias, sr = sigmoid_f(raw);
+      float dv = step_f(raw, least), gv = raw_value<InT>(yn[i]);
       s_own[0][i][tid] = xv;
       s_own[1][i][tid] = soft ? sr : 1.f;
       if constexpr (GATE) {

@@ -19,6 +19,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const ScanParams p) {
   const f32x4 A = *reinterpret_cast<const f32x4*>(p.A + (int64_t)c * N + j);
   const int g = c / p.Cg;
   const float bias = p.bias ? p.bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
+  const float least = step_least(p.softplus != 0);
   const bool gate = p.z != nullptr;
   const InT* zs = static_cast<const InT*>(gate ? p.z : p.x);
   const int64_t zst = gate ? p.z_bs : p.x_bs;
@@ -48,7 +49,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const ScanParams p) {
     unpack<4, InT>(Bn, B);
     unpack<4, InT>(Cn, C);
     if constexpr (decltype(more)::value) fetch(n + 1);
-    const float d = p.softplus ? softplus_f(raw) : raw, dx = d * x;
+    const float d = step_f(raw, least), dx = d * x;
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
