@@ -95,7 +95,8 @@ __global__ __launch_bounds__(64 * SCAN_BLOCK_WAVES, 1) void scan_block_kernel(co
       const bool inside = !CUT || t + 2 * i + half < len;
       dv[i] = inside ? own : 0.f;
       dx[i] = inside ? dv[i] * xv[i] : 0.f;
-      bo[i] = operand<InT>(bn[i], lane);
+      own_token(dv[i], dx[i]);
+      bo[i] = inside ? operand<InT>(bn[i], lane) : 0.f;
       sumd += dv[i];
     }
     // from zero

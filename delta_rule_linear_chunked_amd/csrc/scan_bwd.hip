@@ -20,9 +20,10 @@
 namespace dr {
 
 // Local states at every 8th token and behind the segment, the sums of d there, and (BOTH) the reverse part: tiles as in the
-// forward pass, dy C by the matrix units as d x B is.
+// forward pass, dy C by the matrix units as d x B is. (A product that is not finite may reach the other token of its pair: both lie between the same
+// checkpoints. In fp32 three waves a SIMD, 168 registers.)
 template <int SL, typename InT, bool BOTH>
-__global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p) {
+__global__ __launch_bounds__(64 * SL, BOTH && sizeof(InT) == 4 ? 3 : 1) void scan_states_kernel(const ScanParams p) {
   constexpr int N = 16 * SL, K = TILE_TOK, O = TILE_OWN;
   static_assert(K == 2 * SCAN_CHUNK, "two checkpoints to a tile");
   const int lane = threadIdx.x & 63, sl = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
@@ -89,13 +90,13 @@ __global__ __launch_bounds__(64 * SL) void scan_states_kernel(const ScanParams p
       const bool inside = !CUT || t + 2 * i + half < len;
       dv[i] = inside ? own : 0.f;
       dx[i] = inside ? dv[i] * raw_value<InT>(xn[i]) : 0.f;
-      bo[i] = operand<InT>(bn[i], lane);
+      bo[i] = inside ? operand<InT>(bn[i], lane) : 0.f;
       if constexpr (BOTH) {
         const float zv = raw_value<InT>(zn[i]), sg = zv * sigmoid_f(zv);
         float out = raw_value<InT>(yn[i]) * (gate ? sg : 1.f);
         here(out);
         gy[i] = inside ? out : 0.f;
-        co[i] = operand<InT>(cn[i], lane);
+        co[i] = inside ? operand<InT>(cn[i], lane) : 0.f;
       }
     }
     if constexpr (!CUT) fetch(t + 2 * K <= len ? K : 0);

@@ -21,6 +21,12 @@ __device__ __forceinline__ f32x16 outer_pair(float states, float channels) {
   for (int i = 0; i < 16; ++i) z[i] = 0.f;
   return __builtin_amdgcn_mfma_f32_32x32x2f32(states, channels, z, 0, 0, 0);
 }
+// Two tokens share that instruction, and the zeros in the other one's places times a d x that is not finite would make the other's sum NaN, the
+// earlier one's too. Such a d x goes in as a finite number, and its own token's decay is made NaN, so that the state is from there on.
+__device__ __forceinline__ void own_token(float& d, float& dx) {
+  d = fmaf(dx, 0.f, d);
+  dx = __builtin_amdgcn_fmed3f(dx, -3.402823466e38f, 3.402823466e38f);
+}
 // Between the pairs of a tile: what a pair loads and forms is not moved in front of the pairs before it, where it would only hold registers.
 __device__ __forceinline__ void tile_step() {
   asm volatile("" ::: "memory");

@@ -24,8 +24,8 @@
  * At most 2^31 - 1024 tokens and sequences per call, at most 2^20 channels (norm: 32768); a call whose launches would pass
  * 2^32 - 1 work items is refused (DR_ERR_UNSUPPORTED).
  * A NaN or an infinity stays in its channel and sequence (gradients: also in what is summed over them), except that the gradients of B and C sum over
- * channels and a norm's row is one. In the scan a product that is not finite may also show one token early (two tokens' products d x B
- * share a matrix instruction).
+ * channels and a norm's row is one. Outputs of the tokens before it are not touched. In the scan's forward pass a d x that is not finite
+ * makes its channel's states NaN from its token on.
  */
 #ifndef DELTARULE_SCAN_H
 #define DELTARULE_SCAN_H
