@@ -6,7 +6,9 @@
 // pieces, one per sequence. Loads are issued a batch of tokens in front of their use.
 //
 // 4 x 4096 x 2048 bf16: 30 us (134 MB, 26 at the copy rate). Backward, packed, fp32, 1531 channels (rows not aligned: single channels): 32 us and
-// 4 for the sums of dw (28). Step, 512 sequences x 4096 channels: 9.1 us in a graph (33 MB, 6.5).
+// 4 for the sums of dw (28). Step, 4096 channels, bf16, in a graph: 1 sequence 3.6 us, 64 5.1, 256 6.4, 512
+// 8.7-9.5 (33 MB, 6.5), 2048 24.4 (26): some 4 us of a launch and its rounds of loads, then memory. Backward, bf16, 4 x 2048 x 2048 35.6 us
+// (19.5 at the copy rate), 4 x 8192 x 2048 92.8 (78).
 #include "scan.hpp"
 
 namespace dr {

@@ -2,12 +2,14 @@
 // gradients.
 //
 // A row stays in registers (32 elements a lane; one wave for up to 2048 channels, 4 or 16 above), so x and the residual are
-// read once and every output is written once; the weights stay in registers over the rows of a workgroup.
+// read once and every output is written once; the weights stay in registers over the rows of a workgroup. Above 8192 channels (few rows
+// aside) 1024 threads leave each 128 registers, too few: 14 to 26 of them wait in scratch forward, 97 to 197 backward.
 // 8 bits: p = h w does not contain the mean, so codes and the row's scale come from p exactly as the state cache's from
 // a state, and the statistic only multiplies the scale.
 //
 // Bound by memory where there are rows enough: 16384 x 2048 bf16 with residual and codes 56 us (235 MB, 46 at the copy rate), backward 49 and 5 for the
-// sums of dw (268 MB, 52); 1333 x 1531 fp32 with e4m3 codes 9.3 (27 MB, 5.2), one row 2.4. Stores around the caches: between 10% less and
+// sums of dw (268 MB, 52); 1333 x 1531 fp32 with e4m3 codes 9.3 (27 MB, 5.2), one row 2.4. In a graph, bf16: values 16384 x 2048 54 (52), 4096 x 16384 102 (104), backward
+// 4096 x 8192 62 (52), 4096 x 16384 416 (104: the registers above). Stores around the caches: between 10% less and
 // 10% more time from 128 MiB on, without a rule, so they are ordinary.
 #include <type_traits>
 

@@ -8,8 +8,8 @@
 // C and y), then each segment's start by a walk over the segments, whose decay is exp(A sum d); or a workgroup's waves
 // go along the tokens (scan_block.hip).
 //
-// 64 x 256 tokens x 2048 channels, 16 states, bf16: 130 us, four waves a SIMD. Packed, fp32, 32 states (5.2 million token-channels): segments'
-// states 53 us, main pass 58, join 10, plan 5; the vector units issue 73 and 77% of the time. Loads and stores of whole tiles stand under no
+// 64 x 256 tokens x 2048 channels, 16 states, bf16: 136 us, four waves a SIMD. Packed, fp32, 32 states (5.2 million token-channels): segments'
+// states 54 us, main pass 60, join 10, plan 5; the vector units issue 73 and 77% of the time. Loads and stores of whole tiles stand under no
 // condition (1 x 8192 x 2048: main pass 0.195 us a token with them under conditions, 0.17 without).
 #include "scan_tile.hpp"
 

@@ -4,8 +4,8 @@
 // channels and walks 128 tokens at a time (64 or 32 with more states), a tile of 16 tokens a wave (scan_tile.hpp): a wave forms its decays
 // once and holds them in registers (16 tokens x 8 states a lane), runs them from zero for its own end state, hands that and the
 // decays' product on through LDS, and behind one barrier runs them again from the state that the waves before it leave.
-// A workgroup fills a CU (226 registers, 78 KB of LDS): two waves a SIMD, whose vector units issue 75% of the time. 4 x 4096 x 2048, 16 states, bf16:
-// 193 us a call; in segments of 256 tokens 257. The tensors alone would take 52 at the copy rate, an exponential (two issues), a
+// A workgroup fills a CU (230 registers, 78 KB of LDS): two waves a SIMD, whose vector units issue 75% of the time. 4 x 4096 x 2048, 16 states, bf16:
+// 196 us a call; in segments of 256 tokens 257. The tensors alone would take 52 at the copy rate, an exponential (two issues), a
 // product and two sums for each state 68, softplus and gate about 30 more.
 #include "scan_tile.hpp"
 

@@ -13,8 +13,8 @@
 //
 // 2 x 4096 x 2048, 16 states, bf16: 341 us, of them states 104, join 10, gradients 240 (the vector units issue 84% of the time, about
 // 1480 instructions for a chunk of 32 channels x 16 states: 830 of the formulas, 250 sums across lanes, 400 inputs, outputs and
-// addresses), dB and dC 9, dA and the rest 5. Checkpoints are 134 MB, written and read; one for every 4th token would halve the registers of a chunk and
-// double that.
+// addresses), dB and dC 9, dA and the rest 5. With a gate 9 to 11 registers wait in scratch over the loop of chunks; none are reloaded in it. Checkpoints are
+// 134 MB, written and read (one for every 4th token would double that; not tried).
 #include "scan_tile.hpp"
 
 namespace dr {
